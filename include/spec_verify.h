@@ -55,16 +55,24 @@ enum {
   SPEC_OK = 0,
   SPEC_ERR_ARG = 1,          /* null pointer, size out of range, bad temperature */
   SPEC_ERR_DTYPE = 2,        /* unknown dtype code */
-  SPEC_ERR_ALIGN = 3,        /* reserved: misaligned inputs take the slow path */
+  SPEC_ERR_ALIGN = 3,        /* a cache or output pointer that must be 16-byte aligned is not
+                                (misaligned inputs take a slow path instead) */
   SPEC_ERR_TOKEN_RANGE = 4,  /* (device) a draft/node token outside [0, V) */
   SPEC_ERR_CUDA = 5,         /* a CUDA runtime error; see spec_last_error_message */
   SPEC_ERR_TIMEOUT = 6,      /* (device) a bounded wait ran out */
   SPEC_ERR_PARENT = 7,       /* parent[] is not a tree: parent[0] != -1 or parent[c] >= c */
-  SPEC_ERR_UNSUPPORTED = 8   /* no usable GPU / cluster launch not possible */
+  SPEC_ERR_UNSUPPORTED = 8,  /* no usable GPU / cluster launch not possible */
+  SPEC_ERR_PAGE = 9,         /* (device) a cache page id outside [0, pages) */
+  SPEC_ERR_NONFINITE = 10    /* (device) a non-finite key or value given to the cache */
 };
 
-/* Logit element types. */
-enum { SPEC_F32 = 0, SPEC_BF16 = 1 };
+/* Element types: logits are SPEC_F32 or SPEC_BF16; the cache operators also
+ * take SPEC_F16. */
+enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 };
+
+/* Code types of a key/value cache: e4m3 (finite range +-448; the NaN codes
+ * are not used) and signed 8-bit integers. */
+enum { SPEC_E4M3 = 0, SPEC_I8 = 1 };
 
 /* Size limits. */
 #define SPEC_MAX_DRAFTS 255      /* K of a chain */
@@ -73,6 +81,7 @@ enum { SPEC_F32 = 0, SPEC_BF16 = 1 };
 #define SPEC_MAX_TOPK 32         /* k of spec_topk / spec_eagle2_expand */
 #define SPEC_EAGLE_MAX_CANDIDATES 4096 /* F * k of one expansion step */
 #define SPEC_EAGLE_MAX_NODES 8192      /* M of spec_eagle2_rerank */
+#define SPEC_MAX_NEW_TOKENS 65536      /* N of spec_cache_attention */
 
 /* Counters a caller may ask spec_verify_ex to accumulate (device memory,
  * zeroed by the caller, added to atomically by every call that receives it).
@@ -437,11 +446,160 @@ int spec_eagle2_rerank(const float *node_values, const int32_t *node_parents,
                        int32_t *out_tokens, int32_t *out_index, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * One layer of the target's pass over drafted tokens, around a paged
+ * key/value cache in 8 bits.  The drafted tokens of a sequence (one token, a
+ * chain, a tree's nodes as spec_tree_mask lists them, or a part of a prompt)
+ * take the cache slots behind its context: node i has slot ctx_len + i.
+ *
+ *   spec_qk_norm_rope     norms and rotation of their queries and keys, at
+ *                         position ctx_len + depth (spec_tree_mask's out_depth)
+ *   spec_cache_write      their keys and values into the cache
+ *   spec_cache_attention  attention over context and tree (spec_tree_mask's
+ *                         out_mask)
+ *   spec_cache_commit     after the verification: the accepted path's rows
+ *                         move together, the context grows
+ *   spec_cache_read       reads cached rows back
+ *
+ * A chain needs no commit: its accepted tokens already stand behind the
+ * context, which grows by n_accepted + 1.
+ *
+ * The cache: codes of one byte in blocks (pages of one kv head), and one fp32
+ * scale for each block; a value is code * scale.  Slot s of sequence b is row
+ * s % page_size of page page_table[b * pages_per_seq + s / page_size].  Table
+ * entries past the slots that a call uses are not read, and rows past them may
+ * hold anything.  The scales that spec_cache_write and spec_cache_commit give
+ * are powers of two: the least with amax <= qmax * scale (qmax: 448 for e4m3,
+ * 127 for int8) over the block's new rows, at least 2^-100.  A caller's own
+ * codes may come with any non-negative finite scales (value scales below 2^-100
+ * count as 0 in the attention).
+ *
+ * Errors on the device (spec_get_status): a sequence whose slots do not fit
+ * its pages (SPEC_ERR_ARG) or a page id outside [0, pages) (SPEC_ERR_PAGE) has
+ * NaN outputs, or is not written (only the bad page's rows, where its others
+ * are good).
+ */
+typedef struct {
+  void *k, *v;              /* codes [pages, kv_heads, page_size, head_dim], 16-byte aligned */
+  float *k_scale, *v_scale; /* [pages, kv_heads] */
+  int32_t pages, kv_heads;
+  int32_t page_size;        /* 16, 32, 64 or 128 */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t kind;             /* SPEC_E4M3 or SPEC_I8 */
+} spec_cache_t;
+
+/* A tensor [B, N, heads, head_dim] on the device with the head contiguous and
+ * its other strides in elements (any sign and order; rows that are 16-byte
+ * aligned throughout are read with vectors). */
+typedef struct {
+  void *data;
+  int64_t stride_b, stride_n, stride_h;
+} spec_heads_t;
+
+/*
+ * spec_qk_norm_rope — norms of queries and keys for each head, and the
+ * position rotation, in one pass:
+ *   y = x * (mean(x^2) + eps)^(-1/2) * weight      (norm = 1; weights may be NULL)
+ *   (y_a, y_b) -> (y_a cos f - y_b sin f, y_b cos f + y_a sin f),
+ *   f = position * inv_freq[i]
+ * for i < rot / 2, where (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with
+ * pairs = 1; elements from rot on are not rotated.  Angles are reduced exactly
+ * (64-bit fractions of a turn), however far the position.
+ *   q, k          [B, N, Hq, D] and [B, N, Hk, D]; either may be absent (head
+ *                 count 0); out_q, out_k as q, k; an output may be its input
+ *                 (same pointer and strides), other overlaps are not allowed
+ *   weights       [D] of the same dtype, or NULL
+ *   base          [B] int32 or NULL (0); offset [B, N] int32 or NULL (n):
+ *                 the position of token (b, n) is base[b] + offset[b, n]
+ *   inv_freq      HOST array [rot / 2] of double, finite
+ *   dtype         SPEC_F32, SPEC_BF16 or SPEC_F16 (arithmetic in fp32, one
+ *                 rounding at the end)
+ *   D even, 2 to 512; rot even, 0 to D; eps >= 0
+ */
+int spec_qk_norm_rope(const spec_heads_t *q, const spec_heads_t *k, const spec_heads_t *out_q,
+                      const spec_heads_t *out_k, const void *q_weight, const void *k_weight,
+                      const int32_t *base, const int32_t *offset, int B, int N, int Hq, int Hk, int D,
+                      int dtype, int norm, float eps, const double *inv_freq, int rot, int pairs,
+                      void *stream);
+
+/*
+ * spec_cache_write — quantises the first counts[b] of N new rows of each
+ * sequence into slots ctx_len[b] ... of the cache.  A block that holds no slot
+ * before ctx_len[b] takes the scale of its new rows; any other block's scale
+ * grows where its new rows need it, and all its other rows are then rounded to
+ * the new scale.  Codes are nearest, ties to even.
+ *   k, v          [B, N, kv_heads, head_dim], dtype
+ *   ctx_len       [B] int32; counts [B] int32 (0 to N) or NULL (N)
+ * Two sequences must not write to one page.  Infinities are stored as +-qmax,
+ * NaN as 0, and spec_get_status then returns SPEC_ERR_NONFINITE.
+ */
+int spec_cache_write(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                     const int32_t *ctx_len, const int32_t *counts, const spec_heads_t *k,
+                     const spec_heads_t *v, int B, int N, int dtype, void *stream);
+
+/*
+ * spec_cache_read — reads slots start[b] ... start[b] + counts[b] - 1 back
+ * as code * scale, rounded once to dtype.
+ *   start [B] int32 or NULL (0); counts [B] int32 (0 to N) or NULL (N)
+ *   out_k, out_v  [B, N, kv_heads, head_dim], contiguous, 16-byte aligned;
+ *                 rows from counts[b] on are 0
+ */
+int spec_cache_read(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                    const int32_t *start, const int32_t *counts, void *out_k, void *out_v, int B, int N,
+                    int dtype, void *stream);
+
+/*
+ * spec_cache_attention — softmax attention of counts[b] new tokens of each
+ * sequence over its context and over one another:
+ *   out = sum_j p_j v_j, p = softmax(scale * q . k_j) over the slots that the
+ *   token sees: all slots before ctx_len[b], and of the new tokens' slots
+ *   those that its mask names, or, without a mask, those up to its own.
+ * Query head h uses kv head h / (Hq / kv_heads).
+ *   q             [B, N, Hq, head_dim], SPEC_BF16 or SPEC_F16
+ *   ctx_len       [B] int32; counts [B] int32 (0 to N) or NULL (N)
+ *   mask          [B, N, ceil(N / 32)] bit words as spec_tree_mask gives them,
+ *                 or NULL; bits of tokens from counts[b] on are ignored
+ *   out           [B, N, Hq, head_dim] contiguous, 16-byte aligned, dtype;
+ *                 0 for tokens from counts[b] on and where a token sees nothing
+ *   lse           [B, N, Hq] float or NULL: the natural logarithm of the sum of
+ *                 exp(scale * q . k_j); -inf where nothing is seen
+ * 0 <= N <= SPEC_MAX_NEW_TOKENS; N = 1 is a decoding step.  Scores, sums and
+ * the output are held in fp32.
+ */
+int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                         const int32_t *ctx_len, const int32_t *counts, const spec_heads_t *q,
+                         const uint32_t *mask, int B, int N, int Hq, int dtype, float scale, void *out,
+                         float *lse, void *stream);
+
+/*
+ * spec_cache_commit — after a tree verification: the rows of the accepted
+ * path move together behind the context, and the context grows.
+ *   parent        [N] (per_sequence = 0) or [B, N] (1), node_tokens [B, N],
+ *                 path [B, path_len], length [B]: as given to and by the tree
+ *                 verification (path_len = max_depth + 1); the path's nodes
+ *                 are the root and those with tokens path[0 .. length - 2]
+ *                 (of several with equal tokens, whose rows are equal, those
+ *                 above the last one's lowest index)
+ *   out_index     [B, path_len] int32: their node ids, then -1
+ *   out_ctx_len   [B] int32: ctx_len[b] + length[b] (not ctx_len's own memory)
+ * The row of node out_index[b, i] moves from slot ctx_len[b] + out_index[b, i]
+ * to slot ctx_len[b] + i; a block's scale only grows, as in spec_cache_write
+ * (its other rows are rounded to the new scale).  A length of -1 (an error of
+ * the verification) leaves the sequence as it is; a path that is not in the
+ * tree does too, and makes spec_get_status return SPEC_ERR_PARENT.
+ */
+int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                      const int32_t *ctx_len, const int32_t *parent, int per_sequence,
+                      const int32_t *node_tokens, const int32_t *path, const int32_t *length, int B,
+                      int N, int path_len, int32_t *out_index, int32_t *out_ctx_len, void *stream);
+
+/*
  * spec_get_status — waits for `stream`, then returns (and clears) the first
  * device-side error recorded by calls on it: SPEC_OK, SPEC_ERR_TOKEN_RANGE,
  * SPEC_ERR_PARENT, SPEC_ERR_TIMEOUT, SPEC_ERR_ARG (a lengths[] entry of
- * spec_ngram_propose out of range), or SPEC_ERR_CUDA for an asynchronous
- * CUDA error.  While a SPEC_ERR_TIMEOUT is recorded and not yet read, every
+ * spec_ngram_propose out of range, or slots that do not fit a sequence's
+ * pages), SPEC_ERR_PAGE, SPEC_ERR_NONFINITE, or SPEC_ERR_CUDA for an
+ * asynchronous CUDA error.  While a SPEC_ERR_TIMEOUT is recorded and not yet read, every
  * verification on the stream (chains, point-mass drafts, trees) writes -1
  * for its outputs (n_accepted or length -1, tokens -1) instead of values
  * drawn from statistics a stopped wait may have left incomplete.

@@ -15,11 +15,12 @@ import torch
 from . import build as _build
 
 SPEC_OK = 0
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
+SPEC_E4M3, SPEC_I8 = 0, 1
 STATUS_NAMES = {
     0: "SPEC_OK", 1: "SPEC_ERR_ARG", 2: "SPEC_ERR_DTYPE", 3: "SPEC_ERR_ALIGN",
     4: "SPEC_ERR_TOKEN_RANGE", 5: "SPEC_ERR_CUDA", 6: "SPEC_ERR_TIMEOUT",
-    7: "SPEC_ERR_PARENT", 8: "SPEC_ERR_UNSUPPORTED",
+    7: "SPEC_ERR_PARENT", 8: "SPEC_ERR_UNSUPPORTED", 9: "SPEC_ERR_PAGE", 10: "SPEC_ERR_NONFINITE",
 }
 
 _lib = None
@@ -36,6 +37,16 @@ class StatsStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_ulonglong) for n in
                 ("sequences", "accepted", "bonus", "resampled", "residual_fallbacks", "errors",
                  "near_boundary")]
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int32) for n in ("pages", "kv_heads", "page_size", "head_dim", "kind")]
+
+
+class HeadsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
 
 STATS_COUNTERS = len(StatsStruct._fields_)
 
@@ -68,6 +79,11 @@ def library():
     lib.spec_verify_points.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, u64, vp, vp, vp]
     lib.spec_eagle2_expand.argtypes = [vp, vp, i32, i32, i32, i32, f32, i32, vp, vp, vp, i32, i32, i32, vp, vp]
     lib.spec_eagle2_rerank.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.spec_qk_norm_rope.argtypes = [vp] * 8 + [i32] * 7 + [f32, vp, i32, i32, vp]
+    lib.spec_cache_write.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
+    lib.spec_cache_read.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
+    lib.spec_cache_attention.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp]
+    lib.spec_cache_commit.argtypes = [vp, vp, i32, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.spec_get_status.argtypes = [vp]
     lib.spec_error_string.argtypes = [i32]
     lib.spec_error_string.restype = ctypes.c_char_p
@@ -81,7 +97,8 @@ def library():
     for name in ("spec_verify", "spec_verify_ex", "spec_verify_host", "spec_verify_tree_greedy",
                  "spec_tree_max_depth", "spec_tree_mask", "spec_ngram_propose", "spec_topk",
                  "spec_eagle2_expand", "spec_eagle2_rerank", "spec_get_status", "spec_verify_noalloc",
-                 "spec_noalloc_get_status", "spec_debug_noalloc_status"):
+                 "spec_noalloc_get_status", "spec_debug_noalloc_status", "spec_qk_norm_rope", "spec_cache_write",
+                 "spec_cache_read", "spec_cache_attention", "spec_cache_commit"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -481,6 +498,231 @@ def spec_eagle2_rerank(node_values, node_parents, node_tokens, m, *, stream=None
                                     _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _stream(stream))
     _check(st, "spec_eagle2_rerank")
     return tuple(out)
+
+
+_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+_KINDS = {torch.float8_e4m3fn: SPEC_E4M3, torch.int8: SPEC_I8}
+
+
+class SpecCache:
+    """A paged key/value cache in 8 bits: codes k, v [pages, kv_heads, page_size, head_dim] (float8_e4m3fn or int8)
+    and scales k_scale, v_scale [pages, kv_heads] float32, all contiguous on one GPU; a value is code * scale.
+    ``SpecCache.empty`` makes one.  The tensors stay the caller's: the cache only holds references."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "struct", "ref")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or k.dtype not in _KINDS:
+            raise ValueError("k must be [pages, kv_heads, page_size, head_dim] float8_e4m3fn or int8")
+        pages, heads, page, dim = k.shape
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("v must have the shape and dtype of k")
+        if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
+            raise ValueError("k_scale and v_scale must be [pages, kv_heads]")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise TypeError("k_scale and v_scale must be float32")
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not (t.is_cuda and t.is_contiguous() and t.device == k.device):
+                raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of k")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
+                                  page, dim, _KINDS[k.dtype])
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_size, head_dim, dtype=torch.float8_e4m3fn, device="cuda"):
+        """A cache of zeros."""
+        shape = (pages, kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        return cls(k, v, *(torch.ones((pages, kv_heads), device=device) for _ in range(2)))
+
+
+def _heads(t, name, dtype, B, N, H, D):
+    """A [B, N, H, D] tensor with a contiguous head as HeadsStruct."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != (B, N, H, D):
+        raise ValueError(f"{name} must be [{B}, {N}, {H}, {D}], got {list(t.shape)}")
+    s = t.stride()
+    if s[3] != 1 and D > 1:
+        raise ValueError(f"{name}: a head's elements must be contiguous")
+    return HeadsStruct(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _index(t, name, shape, device):
+    """A contiguous int32 tensor of this shape on this device, or None, as a pointer."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _table(cache, page_table, B):
+    if not isinstance(cache, SpecCache):
+        raise TypeError("cache must be a SpecCache")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages_per_seq]")
+    return _index(page_table, "page_table", (B, page_table.shape[1]), cache.device), page_table.shape[1]
+
+
+def _code(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _call(fn, where, device, stream, *args):
+    """One library call on `device` and the stream."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    _check(st, where)
+
+
+def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True, q_weight=None, k_weight=None,
+                      eps=1e-6, pairs=False, out_q=None, out_k=None, stream=None):
+    """Norms of queries and keys for each head and the position rotation, in one pass.
+
+    q [B, N, Hq, D], k [B, N, Hk, D] (either may be None) in float32, bfloat16 or float16, any strides with a
+    contiguous head; weights [D] of the same dtype or None.  inv_freq: float64 host tensor [rot / 2] or None (no
+    rotation); the position of token (b, n) is base[b] + offset[b, n] (int32; None: 0 and n).  pairs: neighbouring
+    elements are rotated together, not the two halves.  Returns (out_q, out_k); out_q may be q, out_k may be k."""
+    lib = library()
+    x = q if q is not None else k
+    if x is None or x.dim() != 4:
+        raise ValueError("q and k must be [B, N, heads, head_dim]")
+    B, N, _, D = x.shape
+    code = _code(x, "q" if q is not None else "k")
+    heads, srcs, dsts, outs, weights = [0, 0], [None, None], [None, None], [None, None], [None, None]
+    for i, (t, out, w, name) in enumerate(((q, out_q, q_weight, "q"), (k, out_k, k_weight, "k"))):
+        if t is None:
+            continue
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, N, heads, head_dim]")
+        H = t.shape[2]
+        if t.device != x.device:
+            raise ValueError("q and k must be on one device")
+        src = _heads(t, name, x.dtype, B, N, H, D)
+        out = torch.empty((B, N, H, D), dtype=t.dtype, device=t.device) if out is None else out
+        if out.device != x.device:
+            raise ValueError(f"out_{name} must be on the device of {name}")
+        dst = _heads(out, "out_" + name, x.dtype, B, N, H, D)
+        if w is not None:
+            if w.dtype != x.dtype or tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != x.device:
+                raise ValueError(f"{name}_weight must be a contiguous [{D}] tensor of {x.dtype} on {x.device}")
+            weights[i] = w.data_ptr()
+        heads[i], srcs[i], dsts[i], outs[i] = H, src, dst, out
+    freq, rot = None, 0
+    if inv_freq is not None:
+        if inv_freq.device.type != "cpu" or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous 1-d float64 tensor on the host")
+        freq, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    ref = [None if s is None else ctypes.byref(s) for s in srcs + dsts]
+    _call(lib.spec_qk_norm_rope, "spec_qk_norm_rope", x.device, stream, *ref, *weights, _index(base, "base", (B,), x.device),
+          _index(offset, "offset", (B, N), x.device), B, N, heads[0], heads[1], D, code, int(norm), eps, freq, rot, int(pairs))
+    return tuple(outs)
+
+
+def spec_cache_write(cache, page_table, ctx_len, k, v, *, counts=None, stream=None):
+    """Quantises the first counts[b] rows (None: all N) of k, v [B, N, kv_heads, head_dim] into the cache's slots
+    from ctx_len[b] on.  page_table [B, pages_per_seq], ctx_len and counts [B], all int32."""
+    lib = library()
+    if k.dim() != 4:
+        raise ValueError("k must be [B, N, kv_heads, head_dim]")
+    B, N = k.shape[:2]
+    table, per = _table(cache, page_table, B)
+    c = cache.struct
+    code = _code(k, "k")
+    ks, vs = (_heads(t, name, k.dtype, B, N, c.kv_heads, c.head_dim) for t, name in ((k, "k"), (v, "v")))
+    if k.device != cache.device or v.device != cache.device:
+        raise ValueError("k and v must be on the cache's device")
+    if ctx_len is None:
+        raise ValueError("ctx_len is missing")
+    _call(lib.spec_cache_write, "spec_cache_write", cache.device, stream, cache.ref, table, per,
+          _index(ctx_len, "ctx_len", (B,), cache.device), _index(counts, "counts", (B,), cache.device), ctypes.byref(ks),
+          ctypes.byref(vs), B, N, code)
+
+
+def spec_cache_read(cache, page_table, start, counts, N, *, dtype=torch.bfloat16, out_k=None, out_v=None, stream=None):
+    """Reads counts[b] rows (None: N) from slot start[b] (None: 0) on.  Returns (k, v), [B, N, kv_heads, head_dim] of
+    dtype, 0 from counts[b] on."""
+    lib = library()
+    B = page_table.shape[0]
+    table, per = _table(cache, page_table, B)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    c = cache.struct
+    outs = []
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is None:
+            t = torch.empty((B, N, c.kv_heads, c.head_dim), dtype=dtype, device=cache.device)
+        _heads(t, name, dtype, B, N, c.kv_heads, c.head_dim)
+        if not t.is_contiguous() or t.device != cache.device:
+            raise ValueError(f"{name} must be contiguous and on the cache's device")
+        outs.append(t)
+    _call(lib.spec_cache_read, "spec_cache_read", cache.device, stream, cache.ref, table, per,
+          _index(start, "start", (B,), cache.device), _index(counts, "counts", (B,), cache.device), outs[0].data_ptr(),
+          outs[1].data_ptr(), B, N, _DTYPES[dtype])
+    return tuple(outs)
+
+
+def spec_cache_attention(q, cache, page_table, ctx_len, *, counts=None, mask=None, scale=None, out=None, want_lse=False,
+                         stream=None):
+    """Attention of the new tokens' queries q [B, N, Hq, head_dim] (bfloat16 or float16) over the cache: each sees
+    its sequence's slots before ctx_len[b], and of the new tokens' slots ctx_len[b] ... those that its row of mask
+    [B, N, ceil(N / 32)] (spec_tree_mask) names, or, without a mask, those up to its own.  scale: head_dim ** -0.5
+    by default.  Returns (out [B, N, Hq, head_dim], lse [B, N, Hq] float32 or None)."""
+    lib = library()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, head_dim]")
+    B, N, Hq, D = q.shape
+    table, per = _table(cache, page_table, B)
+    device = cache.device
+    if D != cache.struct.head_dim or q.device != device:
+        raise ValueError("q must have the cache's head_dim and be on its device")
+    code = _code(q, "q")
+    qs = _heads(q, "q", q.dtype, B, N, Hq, D)
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != device:
+        raise ValueError("out must be contiguous, on the cache's device, and of the shape and dtype of q")
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=device) if want_lse else None
+    if ctx_len is None:
+        raise ValueError("ctx_len is missing")
+    _call(lib.spec_cache_attention, "spec_cache_attention", device, stream, cache.ref, table, per,
+          _index(ctx_len, "ctx_len", (B,), device), _index(counts, "counts", (B,), device), ctypes.byref(qs),
+          _index(mask, "mask", (B, N, (N + 31) // 32), device), B, N, Hq, code, D ** -0.5 if scale is None else scale,
+          out.data_ptr(), None if lse is None else lse.data_ptr())
+    return out, lse
+
+
+def spec_cache_commit(cache, page_table, ctx_len, parent, node_tokens, path, length, *, stream=None):
+    """Moves the rows of each tree's accepted path together behind the context.  parent [N] or [B, N], node_tokens
+    [B, N]; path [B, max_depth + 1] and length [B] as the tree verification gives them.  Returns (node ids
+    [B, max_depth + 1], then -1; the new context lengths [B])."""
+    lib = library()
+    if node_tokens.dim() != 2 or path.dim() != 2:
+        raise ValueError("node_tokens must be [B, N] and path [B, max_depth + 1]")
+    B, N = node_tokens.shape
+    P = path.shape[1]
+    table, per = _table(cache, page_table, B)
+    device = cache.device
+    each = parent.dim() == 2
+    if any(t is None for t in (ctx_len, length)):
+        raise ValueError("ctx_len or length is missing")
+    index = torch.empty((B, P), dtype=torch.int32, device=device)
+    new_len = torch.empty((B,), dtype=torch.int32, device=device)
+    _call(lib.spec_cache_commit, "spec_cache_commit", device, stream, cache.ref, table, per,
+          _index(ctx_len, "ctx_len", (B,), device), _index(parent, "parent", (B, N) if each else (N,), device), int(each),
+          _index(node_tokens, "node_tokens", (B, N), device), _index(path, "path", (B, P), device),
+          _index(length, "length", (B,), device), B, N, P, index.data_ptr(), new_len.data_ptr())
+    return index, new_len
 
 
 def spec_selftest_wait(stream=None) -> int:

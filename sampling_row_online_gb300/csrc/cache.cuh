@@ -1,0 +1,679 @@
+// Kernels around the paged 8-bit key/value cache: the norms and the rotation
+// of queries and keys, the quantised write, the read-back, and the commit of
+// an accepted path.  All of them are bound by memory traffic or, at the sizes
+// of a decoding step, by the latency of a few dependent loads; none holds a
+// contraction.
+//
+// A block is one page of one kv head: page_size rows of D codes, contiguous,
+// with one fp32 scale; a value is code * scale.  The scales that these
+// kernels give are powers of two (the least with amax <= qmax * scale, at
+// least 2^-100).  So the division of a value by its scale is exact, an e4m3
+// code that moves to a larger scale changes its exponent only (no second
+// rounding unless it becomes subnormal), and the stored bits are a function
+// of the inputs that any fp32 arithmetic reproduces.
+#pragma once
+
+#include <cstdint>
+
+#include "device.cuh"
+#include "ptx.cuh"
+
+namespace spec {
+
+constexpr int DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2;  // SPEC_F32, SPEC_BF16, SPEC_F16
+constexpr int KIND_E4M3 = 0, KIND_I8 = 1;           // SPEC_E4M3, SPEC_I8
+constexpr int MAX_PAGE = 128;                       // page_size <= 128
+constexpr int MAX_ROPE = 256;                       // rotated pairs per head
+
+struct CacheView {  // spec_cache_t and the call's page table
+  unsigned char *k, *v;       // codes [pages, Hk, page, D]
+  float *k_scale, *v_scale;   // [pages, Hk]
+  const int32_t *table;       // [B, per]
+  int pages, Hk, page, log_page, D, kind, per;
+};
+
+// ------------------------------------------------------------- elements
+// Eight elements of a row as loaded: one 16-byte vector, or two for fp32.
+template <int DT>
+struct Raw8 {
+  uint4 v[DT == DT_F32 ? 2 : 1];
+};
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+  float2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float one_element(const void *base, long long i) {
+  if (DT == DT_F32) return static_cast<const float *>(base)[i];
+  const uint16_t h = static_cast<const uint16_t *>(base)[i];
+  if (DT == DT_BF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  return f16x2_to_f32(h).x;
+}
+template <int DT>
+__device__ __forceinline__ void put_element(void *base, long long i, float x) {
+  if (DT == DT_F32) static_cast<float *>(base)[i] = x;
+  else if (DT == DT_BF16) static_cast<uint16_t *>(base)[i] = static_cast<uint16_t>(f32_to_bf16x2(x, 0.f));
+  else static_cast<uint16_t *>(base)[i] = static_cast<uint16_t>(f32_to_f16x2(x, 0.f));
+}
+
+// The eight elements from element offset i; VEC: 16-byte aligned there.
+template <int DT, bool VEC>
+__device__ __forceinline__ Raw8<DT> load8(const void *base, long long i) {
+  Raw8<DT> r;
+  if constexpr (VEC) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + i * (DT == DT_F32 ? 4 : 2));
+    r.v[0] = p[0];
+    if constexpr (DT == DT_F32) r.v[1] = p[1];
+  } else if constexpr (DT == DT_F32) {
+    const uint32_t *p = static_cast<const uint32_t *>(base) + i;
+    r.v[0] = make_uint4(p[0], p[1], p[2], p[3]);
+    r.v[1] = make_uint4(p[4], p[5], p[6], p[7]);
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(base) + i;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = p[2 * j] | static_cast<uint32_t>(p[2 * j + 1]) << 16;
+    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8<DT> &r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+  if constexpr (DT == DT_F32) {
+    const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = __uint_as_float(w[j]);
+      x[4 + j] = __uint_as_float(u[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (DT == DT_BF16) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      } else {
+        const float2 f = f16x2_to_f32(w[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+    }
+  }
+}
+// One rounding, from fp32 to the output's type.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> pack8(const float (&x)[8]) {
+  Raw8<DT> r;
+  if constexpr (DT == DT_F32) {
+    r.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    r.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = DT == DT_BF16 ? f32_to_bf16x2(x[2 * j], x[2 * j + 1]) : f32_to_f16x2(x[2 * j], x[2 * j + 1]);
+    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store8(void *base, long long i, const Raw8<DT> &r) {
+  if constexpr (VEC) {
+    uint4 *p = reinterpret_cast<uint4 *>(static_cast<char *>(base) + i * (DT == DT_F32 ? 4 : 2));
+    p[0] = r.v[0];
+    if constexpr (DT == DT_F32) p[1] = r.v[1];
+  } else {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+    if constexpr (DT == DT_F32) {
+      const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+      uint32_t *p = static_cast<uint32_t *>(base) + i;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = w[j];
+        p[4 + j] = u[j];
+      }
+    } else {
+      uint16_t *p = static_cast<uint16_t *>(base) + i;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[2 * j] = static_cast<uint16_t>(w[j]);
+        p[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- codes
+// Four codes of a word as fp32.
+__device__ __forceinline__ void decode4(int kind, uint32_t w, float (&x)[4]) {
+  if (kind == KIND_E4M3) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    const float2 f = f16x2_to_f32(lo), g = f16x2_to_f32(hi);
+    x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j)));
+  }
+}
+// Four fp32 values (already divided by the scale) as codes: nearest, ties to
+// even; infinities become +-qmax, NaN 0.
+__device__ __forceinline__ uint32_t encode4(int kind, float a, float b, float c, float d) {
+  if (kind == KIND_E4M3) {
+    a = a == a ? a : 0.f, b = b == b ? b : 0.f, c = c == c ? c : 0.f, d = d == d ? d : 0.f;
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return lo | static_cast<uint32_t>(hi) << 16;
+  }
+  const float x[4] = {a, b, c, d};
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)  // __float2int_rn saturates and gives 0 for NaN
+    w |= static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x[j]))) & 0xff) << (8 * j);
+  return w;
+}
+// The least power of two with amax <= qmax * scale, at least 2^-100, from the
+// bits of amax: 448 = 1.75 * 2^8, 127 = 1.984375 * 2^6.
+__device__ __forceinline__ float scale_for(int kind, uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  const uint32_t m = amax_bits & 0x7fffffu;
+  const int s = kind == KIND_E4M3 ? e - 8 + (m > 0x600000u) : e - 6 + (m > 0x7e0000u);
+  return __uint_as_float(static_cast<uint32_t>(max(s, -100) + 127) << 23);
+}
+
+// The page of block `blk` of sequence b, or -1 (and a status bit).
+__device__ __forceinline__ int page_of(const CacheView &c, int b, int blk, int32_t *status) {
+  const int id = c.table[static_cast<long long>(b) * c.per + blk];
+  if (static_cast<unsigned>(id) < static_cast<unsigned>(c.pages)) return id;
+  atomicOr(status, ST_PAGE);
+  return -1;
+}
+
+// Rounds the rows of a block outside [lo, hi) to a larger scale (ratio =
+// old / new < 1), 16 codes at a time.
+template <int NTH>
+__device__ __forceinline__ void rescale_block(unsigned char *blk, int kind, int page, int D, int lo, int hi, float ratio) {
+  const int per_row = D / 16;
+  for (int c = threadIdx.x; c < page * per_row; c += NTH) {
+    const int row = c / per_row;
+    if (row >= lo && row < hi) continue;
+    uint4 *at = reinterpret_cast<uint4 *>(blk) + c;
+    uint4 w = *at;
+    uint32_t *u = &w.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+      decode4(kind, u[j], x);
+      u[j] = encode4(kind, x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
+    }
+    *at = w;
+  }
+}
+
+// Maximum over a block of NTH threads of non-negative fp32 bits.
+template <int NTH>
+__device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t *s) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if (NTH == 32) return x;
+  __syncthreads();  // the previous use of s is over
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = s[0];
+#pragma unroll
+  for (int i = 1; i < NTH / 32; ++i) x = max(x, s[i]);
+  return x;
+}
+
+// ------------------------------------------------- quantised cache write
+struct CacheWriteParams {
+  CacheView c;
+  const void *src[2];          // keys, values: [B, N, Hk, D] with strides in elements
+  long long sb[2], sn[2], sh[2];
+  const int32_t *ctx, *counts;
+  int N;
+  int32_t *status;
+};
+
+// One CTA per (block that the new rows may touch, kv head and tensor,
+// sequence).  The new rows of the block are read once and kept in registers
+// (at most 64 elements a thread), their maximum gives the scale, and the
+// codes follow: 3 bytes of traffic per 16-bit element, the floor.  The block
+// is re-read only where its scale grows under rows that it already holds.
+template <int DT, int NTH, bool VEC>
+__global__ void __launch_bounds__(NTH) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
+  __shared__ uint32_t s_max[NTH / 32];
+  const CacheView &c = p.c;
+  const int b = blockIdx.z, h = blockIdx.y >> 1, t = blockIdx.y & 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int start = p.ctx[b], count = p.counts ? p.counts[b] : p.N;
+  if (start < 0 || count < 0 || count > p.N || static_cast<long long>(start) + count > static_cast<long long>(c.per) * c.page) {
+    if (threadIdx.x == 0) atomicOr(p.status, ST_SLOTS);
+    return;
+  }
+  const int blk = (start >> c.log_page) + blockIdx.x;
+  const int first = blk << c.log_page;  // of the block; may pass the last slot, then nothing is left below
+  const int lo = max(start, first), hi = min(start + count, first + c.page);
+  if (hi <= lo) return;
+  const int page = page_of(c, b, blk, p.status);
+  if (page < 0) return;
+  const long long id = static_cast<long long>(page) * c.Hk + h;
+  float *scale_at = (t ? c.v_scale : c.k_scale) + id;
+  unsigned char *codes = (t ? c.v : c.k) + id * c.page * c.D;
+  const bool empty = first >= start;  // the block holds nothing before the new rows
+  const float old = empty ? 0.f : *scale_at;
+
+  constexpr int MOST = 8;  // chunks of eight elements per thread
+  const int per_row = c.D / 8, chunks = (hi - lo) * per_row;
+  const long long base = b * p.sb[t] + h * p.sh[t];
+  Raw8<DT> raw[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int k = threadIdx.x + i * NTH;
+    if (k < chunks)
+      raw[i] = load8<DT, VEC>(p.src[t], base + (lo - start + k / per_row) * p.sn[t] + (k % per_row) * 8);
+  }
+  uint32_t amax = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    if (threadIdx.x + i * NTH < chunks) {
+      float x[8];
+      unpack8<DT>(raw[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __float_as_uint(x[j]) & 0x7fffffffu;
+        if (a < 0x7f800000u) amax = max(amax, a);
+        else bad = true;
+      }
+    }
+  }
+  if (bad) atomicOr(p.status, ST_NONFINITE);
+  amax = block_max<NTH>(amax, s_max);
+  const float scale = fmaxf(scale_for(c.kind, amax), old);
+  if (threadIdx.x == 0) *scale_at = scale;  // every thread has read the old one before the maximum's barrier
+  const float inv = 1.f / scale;            // exact for powers of two
+  const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int k = threadIdx.x + i * NTH;
+    if (k < chunks) {
+      float x[8];
+      unpack8<DT>(raw[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = pow2 ? x[j] * inv : x[j] / scale;
+      uint2 w;
+      w.x = encode4(c.kind, x[0], x[1], x[2], x[3]);
+      w.y = encode4(c.kind, x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<uint2 *>(codes + static_cast<long long>(lo - first + k / per_row) * c.D + (k % per_row) * 8) = w;
+    }
+  }
+  if (!empty && scale > old) rescale_block<NTH>(codes, c.kind, c.page, c.D, lo - first, hi - first, old / scale);
+}
+
+// ------------------------------------------------------------- read-back
+struct CacheReadParams {
+  CacheView c;
+  void *out[2];  // [B, N, Hk, D]
+  const int32_t *start, *counts;
+  int N;
+  int32_t *status;
+};
+
+// One CTA per (block, kv head, sequence): the block's rows of both tensors,
+// 16 codes to a thread; rows past the count are zero, a sequence that does
+// not fit its pages and the rows of a bad page are NaN.
+template <int DT>
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p) {
+  const CacheView &c = p.c;
+  const int b = blockIdx.z, h = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  int start = p.start ? p.start[b] : 0, count = p.counts ? p.counts[b] : p.N;
+  float fill = 0.f;
+  if (start < 0 || count < 0 || count > p.N || static_cast<long long>(start) + count > static_cast<long long>(c.per) * c.page) {
+    if (threadIdx.x == 0) atomicOr(p.status, ST_SLOTS);
+    start = count = 0;
+    fill = __uint_as_float(0x7fc00000u);
+  }
+  const int blk = (start >> c.log_page) + blockIdx.x;
+  const long long first = static_cast<long long>(blk) << c.log_page;
+  const int lo = static_cast<int>(max(static_cast<long long>(start), first) - start);  // rows of the output
+  const int hi = static_cast<int>(min(static_cast<long long>(p.N), first + c.page - start));
+  const int held = min(hi, count);
+  int page = -1;
+  if (held > lo && (page = page_of(c, b, blk, p.status)) < 0) fill = __uint_as_float(0x7fc00000u);
+  const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
+  const int per_row = c.D / 16;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float scale = (t ? c.v_scale : c.k_scale)[id];
+    const unsigned char *codes = (t ? c.v : c.k) + id * c.page * c.D;
+    for (int k = threadIdx.x; k < (hi - lo) * per_row; k += 256) {
+      const int row = lo + k / per_row, d = (k % per_row) * 16;
+      float x[16];
+      if (row < held && page >= 0) {
+        const uint4 w = ldg_na(reinterpret_cast<const uint4 *>(codes + (start + row - first) * c.D + d));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y[4];
+          decode4(c.kind, u[j], y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * j + e] = y[e] * scale;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = row < held || count == 0 ? fill : 0.f;
+      }
+      const long long o = ((static_cast<long long>(b) * p.N + row) * c.Hk + h) * c.D + d;
+      float lo8[8], hi8[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lo8[j] = x[j], hi8[j] = x[8 + j];
+      store8<DT, true>(p.out[t], o, pack8<DT>(lo8));
+      store8<DT, true>(p.out[t], o + 8, pack8<DT>(hi8));
+    }
+  }
+}
+
+// --------------------------------------------- commit of an accepted path
+struct CacheCommitParams {
+  CacheView c;
+  const int32_t *ctx, *parent, *tokens, *path, *length;
+  int N, P, parent_stride;  // parent_stride: 0 (one tree) or N
+  int32_t *out_index, *out_ctx;
+  int32_t *status;
+};
+constexpr int COMMIT_MAX_NODES = 1024;
+
+// One CTA per (kv head, tensor, sequence).  The nodes of the accepted path:
+// every thread walks from its nodes towards the root comparing tokens (the
+// token of depth d is path[d - 1]) and the lowest index that arrives wins;
+// equal token paths hold equal rows, so which of several is taken does not
+// matter.  Node i of the path moves from slot ctx + index[i] to ctx + i.
+// index[i] >= i, so the destination blocks are taken in ascending order and
+// no block is overwritten before its rows have been read.
+__global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
+  __shared__ int s_par[COMMIT_MAX_NODES], s_tok[COMMIT_MAX_NODES], s_path[COMMIT_MAX_NODES], s_index[COMMIT_MAX_NODES];
+  __shared__ uint32_t s_max[8];
+  __shared__ int s_node, s_bad, s_first;
+  const CacheView &c = p.c;
+  const int h = blockIdx.x >> 1, t = blockIdx.x & 1, b = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int len = p.length[b], ctx = p.ctx[b];
+  if (threadIdx.x == 0) s_node = INT32_MAX, s_bad = 0, s_first = INT32_MAX;
+  const bool fits = len >= 1 && len <= min(p.P, p.N);
+  for (int i = threadIdx.x; i < p.N; i += 256) {
+    s_par[i] = p.parent[static_cast<long long>(b) * p.parent_stride + i];
+    s_tok[i] = p.tokens[static_cast<long long>(b) * p.N + i];
+  }
+  if (fits)
+    for (int i = threadIdx.x; i < len - 1; i += 256) s_path[i] = p.path[static_cast<long long>(b) * p.P + i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.N; i += 256)
+    if (i == 0 ? s_par[i] != -1 : s_par[i] < 0 || s_par[i] >= i) s_bad = 1;
+  __syncthreads();
+  if (fits && !s_bad)
+    for (int i = threadIdx.x; i < p.N; i += 256) {
+      int at = i, d = len - 1;
+      while (d > 0 && at > 0 && s_tok[at] == s_path[d - 1]) at = s_par[at], --d;
+      if (d == 0 && at == 0) atomicMin(&s_node, i);
+    }
+  __syncthreads();
+  // length -1 marks an error that the verification has reported already
+  const bool tree_ok = fits && !s_bad && s_node != INT32_MAX;
+  const bool slots_ok = ctx >= 0 && (!tree_ok || static_cast<long long>(ctx) + s_node < static_cast<long long>(c.per) * c.page);
+  const bool ok = tree_ok && slots_ok;
+  if (threadIdx.x == 0) {
+    if (!tree_ok && len != -1) atomicOr(p.status, ST_PARENT);
+    if (!slots_ok) atomicOr(p.status, ST_SLOTS);
+    if (ok)
+      for (int at = s_node, d = len - 1; d >= 0; at = s_par[at], --d) {
+        s_index[d] = at;
+        if (at != d) s_first = d;
+      }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < p.P; i += 256)
+      p.out_index[static_cast<long long>(b) * p.P + i] = ok && i < len ? s_index[i] : -1;
+    if (threadIdx.x == 0) p.out_ctx[b] = ok ? ctx + len : ctx;
+  }
+  if (!ok || s_first >= len) return;
+
+  constexpr int MOST = MAX_PAGE * 128 / 16 / 256;  // vectors of 16 codes per thread
+  unsigned char *base = t ? c.v : c.k;
+  float *scales = t ? c.v_scale : c.k_scale;
+  const int per_row = c.D / 16;
+  for (int row = s_first; row < len;) {
+    const int blk = (ctx + row) >> c.log_page, in = (ctx + row) & (c.page - 1);
+    const int n = min(len - row, c.page - in);
+    const int page = page_of(c, b, blk, p.status);
+    const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
+    const float old = scales[id];
+    uint4 raw[MOST];
+    float from[MOST];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const int k = threadIdx.x + i * 256;
+      from[i] = -1.f;  // nothing to move
+      if (k >= n * per_row) continue;
+      const int slot = ctx + s_index[row + k / per_row];
+      const int src = page_of(c, b, slot >> c.log_page, p.status);
+      if (src < 0) continue;
+      const long long sid = static_cast<long long>(src) * c.Hk + h;
+      from[i] = scales[sid];
+      raw[i] = *reinterpret_cast<const uint4 *>(base + (sid * c.page + (slot & (c.page - 1))) * c.D + (k % per_row) * 16);
+      const uint32_t *u = &raw[i].x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x[4];
+        decode4(c.kind, u[j], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a = __float_as_uint(x[e] * from[i]) & 0x7fffffffu;
+          if (a < 0x7f800000u) amax = max(amax, a);
+        }
+      }
+    }
+    amax = block_max<256>(amax, s_max);
+    // a block's scale never shrinks here: the rows of other nodes still stand in it
+    const float scale = fmaxf(scale_for(c.kind, amax), old);
+    __syncthreads();  // every thread has read the block's old scale and rows
+    if (page >= 0) {
+      unsigned char *codes = base + id * c.page * c.D;
+      if (threadIdx.x == 0) scales[id] = scale;
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        const int k = threadIdx.x + i * 256;
+        if (k >= n * per_row || from[i] < 0.f) continue;
+        uint32_t *u = &raw[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x[4];
+          decode4(c.kind, u[j], x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = x[e] * from[i] / scale;
+          u[j] = encode4(c.kind, x[0], x[1], x[2], x[3]);
+        }
+        *reinterpret_cast<uint4 *>(codes + static_cast<long long>(in + k / per_row) * c.D + (k % per_row) * 16) = raw[i];
+      }
+      if (scale > old) rescale_block<256>(codes, c.kind, c.page, c.D, in, in + n, old / scale);
+    }
+    __syncthreads();  // the next block's rows may come from this one's scale (its own page)
+    row += n;
+  }
+}
+
+// ------------------------------- norms of queries and keys with the rotation
+struct NormRopeParams {
+  const void *src[2];  // queries, keys
+  void *dst[2];
+  const void *weight[2];
+  long long ssb[2], ssn[2], ssh[2], dsb[2], dsn[2], dsh[2];  // strides in elements
+  int heads[2];
+  const int32_t *base, *offset;
+  int B, N, D, rot, per_cta;  // per_cta: tokens per CTA
+  int norm, pairs, lanes;     // lanes: threads per row (a power of two, <= 32)
+  float eps;
+  unsigned long long freq[MAX_ROPE];  // 2^64 turns per position, modulo 2^64
+};
+
+// Several tokens to a CTA, `lanes` threads to a row (one head of one token).
+// A thread takes units of the row: eight elements of the first half with the
+// eight that they are rotated with (halves), or eight elements by themselves
+// (neighbouring pairs, and what is not rotated).  The rotation's angle is
+// exact: pos * freq modulo 2^64 is the fraction of a turn in 64 bits, from
+// which 24 go into sincospi; a table of the CTA's tokens holds cos and sin, so
+// that all heads share them.
+template <int DT, int VE, int MAXU>
+__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
+  const int half = p.rot / 2;
+  const long long tokens = static_cast<long long>(p.B) * p.N;
+  const long long first = static_cast<long long>(blockIdx.x) * p.per_cta;
+  const int here = static_cast<int>(min(static_cast<long long>(p.per_cta), tokens - first));
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < here * half; i += 256) {
+    const long long tok = first + i / half;
+    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
+    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : n);
+    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[i % half];
+    // signed fraction of a turn times two, in units of pi
+    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+    float s, c;
+    sincospif(x, &s, &c);
+    s_trig[i] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int heads = p.heads[0] + p.heads[1];
+  const int lane = threadIdx.x & (p.lanes - 1);
+  const int npair = p.pairs ? 0 : half / VE;         // units of two vectors
+  const int units = npair + (p.D - 2 * npair * VE) / VE;
+  const int nrot = p.pairs ? p.rot / VE : npair;     // units that are rotated
+  const int rows = here * heads, step = 256 / p.lanes;
+  // every thread runs the same number of turns: the row sums are shuffles
+  for (int row0 = 0; row0 < rows; row0 += step) {
+    const int row = row0 + threadIdx.x / p.lanes;
+    const bool live = row < rows;
+    const int tk = live ? row / heads : 0, hh = live ? row % heads : 0;
+    const int w = hh >= p.heads[0], h = hh - (w ? p.heads[0] : 0);
+    const long long tok = first + tk;
+    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
+    const long long from = b * p.ssb[w] + n * p.ssn[w] + h * p.ssh[w];
+    const long long to = b * p.dsb[w] + n * p.dsn[w] + h * p.dsh[w];
+    float x[MAXU][2][VE];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < MAXU; ++i) {
+      const int u = lane + i * p.lanes;
+      if (live && u < units) {
+        const int at = u < npair ? u * VE : 2 * npair * VE + (u - npair) * VE;
+        if constexpr (VE == 8) {
+          unpack8<DT>(load8<DT, true>(p.src[w], from + at), x[i][0]);
+          if (u < npair) unpack8<DT>(load8<DT, true>(p.src[w], from + at + half), x[i][1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            x[i][0][j] = one_element<DT>(p.src[w], from + at + j);
+            if (u < npair) x[i][1][j] = one_element<DT>(p.src[w], from + at + half + j);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          sum = fmaf(x[i][0][j], x[i][0][j], sum);
+          if (u < npair) sum = fmaf(x[i][1][j], x[i][1][j], sum);
+        }
+      }
+    }
+    float r = 1.f;
+    if (p.norm) {
+      for (int o = p.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+    }
+    if (!live) continue;
+    const void *weight = p.weight[w];
+    const float2 *trig = s_trig + tk * half;
+#pragma unroll
+    for (int i = 0; i < MAXU; ++i) {
+      const int u = lane + i * p.lanes;
+      if (u >= units) continue;
+      const int at = u < npair ? u * VE : 2 * npair * VE + (u - npair) * VE;
+      const bool two = u < npair;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[i][0][j] *= r, x[i][1][j] *= r;
+      if (weight) {
+        if constexpr (VE == 8) {
+          float g[8];
+          unpack8<DT>(load8<DT, true>(weight, at), g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[i][0][j] *= g[j];
+          if (two) {
+            unpack8<DT>(load8<DT, true>(weight, at + half), g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][1][j] *= g[j];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            x[i][0][j] *= one_element<DT>(weight, at + j);
+            if (two) x[i][1][j] *= one_element<DT>(weight, at + half + j);
+          }
+        }
+      }
+      if (two) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float2 cs = trig[at + j];
+          const float a = x[i][0][j], c = x[i][1][j];
+          x[i][0][j] = a * cs.x - c * cs.y;
+          x[i][1][j] = c * cs.x + a * cs.y;
+        }
+      } else if (u < nrot) {
+        if constexpr (VE > 1) {
+#pragma unroll
+          for (int j = 0; j < VE; j += 2) {
+            const float2 cs = trig[(at + j) / 2];
+            const float a = x[i][0][j], c = x[i][0][j + 1];
+            x[i][0][j] = a * cs.x - c * cs.y;
+            x[i][0][j + 1] = c * cs.x + a * cs.y;
+          }
+        }
+      }
+      if constexpr (VE == 8) {
+        store8<DT, true>(p.dst[w], to + at, pack8<DT>(x[i][0]));
+        if (two) store8<DT, true>(p.dst[w], to + at + half, pack8<DT>(x[i][1]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          put_element<DT>(p.dst[w], to + at + j, x[i][0][j]);
+          if (two) put_element<DT>(p.dst[w], to + at + half + j, x[i][1][j]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace spec

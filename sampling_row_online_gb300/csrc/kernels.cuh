@@ -41,6 +41,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "device.cuh"
 #include "philox.cuh"
 #include "ptx.cuh"
 
@@ -51,16 +52,12 @@ constexpr int NWARP = NT / 32;
 constexpr int VECS_PER_THREAD = 2;      // 16-byte vectors per thread per tile
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_CLUSTER = 16;
-constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;  // 1 s bound on any wait
 
 // Streaming items are handed out by up to NSHARD ticket counters, one per
 // 128-byte line: shard k hands out items k, k + ns, k + 2 ns, ... to the CTAs
 // k, k + ns, ... of the row kernel.
 constexpr int NSHARD = 32;
 constexpr int TICKET_STRIDE = 32;  // ints
-
-// device status bits (per stream)
-constexpr int ST_TOKEN = 1, ST_PARENT = 2, ST_TIMEOUT = 4;
 
 enum Kind : int { KIND_SAMPLE = 0, KIND_GREEDY_CHAIN = 1, KIND_TREE = 2, KIND_TREE_SAMPLE = 3 };
 constexpr int MAX_TREE_NODES = 1024;
@@ -321,17 +318,12 @@ __device__ __forceinline__ const unsigned char *draft_row(const Params &p, int b
          (static_cast<size_t>(b) * p.K + i) * p.V * Elem<DT>::BYTES;
 }
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // After the dependent-launch wait: a bounded wait of this call's streaming
 // kernel (or of any earlier call on the same status word not yet read) ran
 // out, so the row statistics may be incomplete; the call's outputs are then
 // -1 rather than values drawn from them.
 __device__ __forceinline__ bool stream_timed_out(const Params &p) {
   return (*reinterpret_cast<const volatile int32_t *>(p.status) & ST_TIMEOUT) != 0;
-}
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ======================================================================
@@ -377,19 +369,6 @@ struct ItemCursor {
     }
   }
 };
-
-// Bounded wait on an mbarrier phase; false if it ran out.  The warp sleeps
-// in hardware between polls.
-// Also bounded in polls (each suspends at most ~20 us), should the clock
-// not advance.
-constexpr int WAIT_LIMIT_POLLS = 1 << 17;
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-  const uint64_t t0 = clock_ns();
-  for (int polls = 0; !mbar_try_wait_sleep(bar, parity, 20000u); ++polls)
-    if (clock_ns() - t0 > WAIT_LIMIT_NS || polls > WAIT_LIMIT_POLLS) return false;
-  return true;
-}
 
 // Online (max, sum 2^((z - max) c)) state of one row in one thread; the sum
 // is kept as two lanes for the packed fp32x2 adds.  mc = max(m c, -FLT_MAX)

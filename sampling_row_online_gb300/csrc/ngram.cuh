@@ -42,7 +42,6 @@ namespace spec {
 constexpr int NGRAM_MAX_N = 64;   // largest n_max
 constexpr int NGRAM_U = 4;        // 4-token groups each lane loads per round
 constexpr int NGRAM_REG_BINS = 8; // register histogram: n_max - n_min < 8
-constexpr int ST_LENGTH = 8;      // device status: lengths[b] outside [0, L]
 
 // per-thread hit bookkeeping
 enum NgramMode : int { NGRAM_MAXKEY = 0, NGRAM_REGHIST = 1, NGRAM_SMEMHIST = 2 };

@@ -2,7 +2,6 @@
 // (cluster size, slices, tiles, stages), per-stream workspaces and the C ABI
 // declared in include/spec_verify.h.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
@@ -15,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.cuh"
 #include "eagle2.cuh"
 #include "ngram.cuh"
@@ -31,6 +31,8 @@ void noalloc_forget();  // spec_verify_noalloc's cached device addresses (define
 // now reports cudaErrorLaunchFailure without launching.  0: off.
 std::atomic<int> g_fail_launch{0};
 
+}  // namespace
+
 cudaError_t launch_kernel(const cudaLaunchConfig_t *cfg, const void *fn, void **args) {
   int n = g_fail_launch.load();
   while (n > 0 && !g_fail_launch.compare_exchange_weak(n, n - 1)) {
@@ -38,13 +40,6 @@ cudaError_t launch_kernel(const cudaLaunchConfig_t *cfg, const void *fn, void **
   if (n == 1) return cudaErrorLaunchFailure;  // this launch is the injected failure
   return cudaLaunchKernelExC(cfg, fn, args);
 }
-
-// An NVTX range around each entry point (free when no tool is attached), so
-// that profilers can attribute kernels to calls.
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
 
 int fail(int code, const std::string &msg) {
   g_last_error = msg;
@@ -56,6 +51,8 @@ int cuda_fail(cudaError_t e, const char *what) {
   return SPEC_ERR_CUDA;
 }
 
+namespace {
+
 // Status word (one 256-byte slot) followed by the item tickets.
 constexpr size_t CONTROL_BYTES = 256 + sizeof(int) * NSHARD * TICKET_STRIDE;
 inline int *tickets_of(int32_t *status) {
@@ -63,21 +60,6 @@ inline int *tickets_of(int32_t *status) {
 }
 
 // ------------------------------------------------------------ workspaces
-// Per (device, stream): the status word (never reallocated), the row
-// partials of the current call (float4 per job and slice, grow-only), and a
-// staging area for the host-buffer entry point.
-struct Workspace {
-  int device = -1;
-  cudaStream_t stream = nullptr;
-  int32_t *status = nullptr;  // status word, then the item tickets (zeroed once)
-  float4 *partials = nullptr;
-  size_t cap_parts = 0;
-  unsigned char *stage = nullptr;
-  size_t stage_cap = 0;
-  int *ngram_done = nullptr;  // n-gram drafter: finished-CTA counters, zero between calls
-  size_t ngram_cap = 0;
-};
-
 std::mutex g_mu;
 std::vector<Workspace *> g_ws;
 
@@ -92,7 +74,9 @@ Workspace *find_ws(int device, cudaStream_t stream, bool create) {
   return w;
 }
 
-int get_ws(cudaStream_t stream, size_t nparts, Workspace **out) {
+}  // namespace
+
+int get_ws(cudaStream_t stream, size_t nparts, Workspace **out, size_t nattn) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -115,9 +99,24 @@ int get_ws(cudaStream_t stream, size_t nparts, Workspace **out) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(partials)");
     w->cap_parts = nparts;
   }
+  if (w->attn_cap < nattn) {
+    if (w->attn_done) {
+      e = cudaFree(w->attn_done);  // synchronises the device: no call still uses it
+      w->attn_done = nullptr;
+      w->attn_cap = 0;
+      if (e != cudaSuccess) return cuda_fail(e, "cudaFree(attention counters)");
+    }
+    if ((e = cudaMalloc(&w->attn_done, sizeof(int) * nattn)) != cudaSuccess)
+      return cuda_fail(e, "cudaMalloc(attention counters)");
+    if ((e = cudaMemsetAsync(w->attn_done, 0, sizeof(int) * nattn, stream)) != cudaSuccess)
+      return cuda_fail(e, "cudaMemsetAsync(attention counters)");
+    w->attn_cap = nattn;
+  }
   *out = w;
   return SPEC_OK;
 }
+
+namespace {
 
 // ------------------------------------------------------------ geometry
 constexpr int DEFAULT_STAGES = 2;               // tile ring depth
@@ -204,6 +203,8 @@ int occupancy(const void *fn, int smem, int C, int *result) {
   return SPEC_OK;
 }
 
+}  // namespace
+
 int num_sms() {
   static int sms[64] = {0};
   int dev = 0;
@@ -215,6 +216,8 @@ int num_sms() {
   }
   return sms[dev];
 }
+
+namespace {
 
 bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
@@ -993,6 +996,10 @@ int read_status_word(int32_t *word) {
   if (bits & ST_TIMEOUT) return fail(SPEC_ERR_TIMEOUT, "a bounded wait on the device ran out");
   if (bits & ST_PARENT) return fail(SPEC_ERR_PARENT, "parent[] is not a tree of the given depth");
   if (bits & ST_LENGTH) return fail(SPEC_ERR_ARG, "lengths[b] outside [0, L]");
+  if (bits & ST_SLOTS)
+    return fail(SPEC_ERR_ARG, "a sequence's context length and token count do not fit its pages");
+  if (bits & ST_PAGE) return fail(SPEC_ERR_PAGE, "a page id is outside [0, pages)");
+  if (bits & ST_NONFINITE) return fail(SPEC_ERR_NONFINITE, "a non-finite key or value was given to the cache");
   return fail(SPEC_ERR_TOKEN_RANGE, "a draft or node token is outside [0, V)");
 }
 }  // namespace
@@ -1082,6 +1089,8 @@ const char *spec_error_string(int status) {
     case SPEC_ERR_TIMEOUT: return "SPEC_ERR_TIMEOUT";
     case SPEC_ERR_PARENT: return "SPEC_ERR_PARENT";
     case SPEC_ERR_UNSUPPORTED: return "SPEC_ERR_UNSUPPORTED";
+    case SPEC_ERR_PAGE: return "SPEC_ERR_PAGE";
+    case SPEC_ERR_NONFINITE: return "SPEC_ERR_NONFINITE";
     default: return "SPEC_ERR_UNKNOWN";
   }
 }
@@ -1099,6 +1108,7 @@ void spec_shutdown(void) {
     if (w->partials) cudaFree(w->partials);
     if (w->stage) cudaFree(w->stage);
     if (w->ngram_done) cudaFree(w->ngram_done);
+    if (w->attn_done) cudaFree(w->attn_done);
     delete w;
   }
   g_ws.clear();
