@@ -34,6 +34,7 @@ struct AttnParams {
   CacheView c;
   const void *q;              // [B, N, Hq, D], strides in elements
   long long q_sb, q_sn, q_sh;
+  int q_vec;                  // rows of q are 16-byte aligned
   void *out;                  // [B, N, Hq, D]
   float *lse;                 // [B, N, Hq] or NULL
   const int32_t *ctx, *counts;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   using L = StreamLayout<D>;
   constexpr int CH = D / 64, NT8 = D / 8;                // 16-byte chunks of a key row per lane; column tiles
   constexpr float VFIX = KIND == KIND_E4M3 ? 256.f : 1.f;  // fp16 codes are value / VFIX
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Segment s_seg[2 * AW];
   __shared__ int s_has[2 * AW];
   __shared__ long long s_start[AW + 1];  // first step of each warp's stretch

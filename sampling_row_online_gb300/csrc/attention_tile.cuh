@@ -1,0 +1,774 @@
+// Attention over the 8-bit cache where a kv head has many query rows (chains
+// times grouped heads, trees, parts of a prompt): tensor cores with the
+// accumulators in tensor memory.  The mathematics is attention.cuh's.
+#pragma once
+
+#include "attention.cuh"
+
+namespace spec {
+
+// ------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t *at, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Arrives on the barrier once all products issued so far by this thread are done.
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// D (tensor memory, fp32) = A B^T (+ D): A in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Columns of this warp's 32 lanes: thread = lane, register = column.  What a
+// load names may be used after the wait that names it.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// f(group, registers) for the 16-column groups of a range, each loaded while
+// the one before it is worked on.
+template <int GROUPS, class F>
+__device__ __forceinline__ void tmem_each16(uint32_t at, F f) {
+  uint32_t r[2][16];
+  tmem_ld16(at, r[0]);
+#pragma unroll
+  for (int q = 0; q < GROUPS; ++q) {
+    tc_wait_ld(r[q & 1]);
+    if (q + 1 < GROUPS) tmem_ld16(at + 16 * (q + 1), r[(q + 1) & 1]);
+    f(q, r[q & 1]);
+  }
+}
+// Shared-memory operand of 128-byte swizzled rows (8 rows of 128 bytes to an
+// atom of 1024); `lead` is the distance of neighbouring 64-element blocks where
+// the rows run along the contracted axis (0 otherwise).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t at, uint32_t lead) {
+  return static_cast<uint64_t>((at & 0x3ffffu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+// Generic writes to shared memory become visible to the tensor cores.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// ======================================================================
+// A persistent CTA per SM.  The list of all work is (sequence, kv head, tile of
+// 128 rows, tile of 128 tokens); every CTA takes an equal stretch of it.  Its
+// tiles alternate between two groups of 128 softmax threads, A and B, each
+// with its own scores, weights, accumulator, maximum and sum: they meet only at
+// the end of a segment (a row tile of a kv head), so one group's softmax runs
+// under the other's products.
+//
+//   copy warp    pages -> raw ring (bulk copies of 8-bit codes), scales -> ring
+//   conversion   raw codes -> fp16 tiles in the swizzled operand layout
+//   product warp S = Q K^T, O += P V (P in tensor memory, over S)
+//   softmax      one row per thread: S -> P, lazy rescaling of O, the output
+//
+// Codes cannot be an operand next to fp16 (one instruction takes one type), and
+// e4m3 queries and weights would cost the precision that the cache has.
+constexpr int TQ = 128, TK = 128;    // rows, tokens of a tile
+constexpr int T_SOFT = 256;          // softmax threads
+constexpr int T_CONV = 128;          // conversion threads
+constexpr int T_NT = T_SOFT + T_CONV + 128;  // and a warp each for products and copies, and two idle ones
+// Registers: 128 a thread at launch, then 176 for the softmax, 96 for the
+// conversion and 64 for the rest: 256 * 176 + 128 * 96 + 128 * 64 = 512 * 128.
+constexpr int T_REG_SOFT = 176, T_REG_CONV = 96, T_REG_REST = 64;
+static_assert(T_SOFT * T_REG_SOFT + T_CONV * T_REG_CONV + 128 * T_REG_REST <= T_NT * 128, "register split");
+constexpr int T_RAW = 4;             // raw slots: keys and values of two tiles
+constexpr int T_SCALES = 8;          // tiles of scales: more than the copy warp can be ahead
+
+template <int D>
+struct TileLayout {
+  static constexpr int OP = 128 * D * 2;            // an fp16 operand tile
+  static constexpr int RAWB = 128 * D;              // a raw tile
+  static constexpr int Q = 0, K = OP, V = 3 * OP, RAW = 5 * OP;
+  static constexpr int SCALES = RAW + T_RAW * RAWB;  // [T_SCALES][8] (key scale, log2 of the value scale)
+  static constexpr int ML = SCALES + T_SCALES * 64;  // [2][128] (offset, sum) of the groups
+  static constexpr int BARS = ML + 2048;
+  static constexpr int MISC = BARS + 40 * 8;
+  static constexpr int SMEM = MISC + 64;
+  static constexpr int PIECE = 128 * D + 256;       // floats: out, offset, sum
+};
+
+struct TileBars {
+  uint64_t raw_full[T_RAW], raw_empty[T_RAW], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t sc_full[T_SCALES], q_full, meet;
+};
+static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
+
+struct TileCursor {
+  int b, h, rt, j, n, tiles, ctx, cnt;  // n: token tiles of this row tile
+};
+__device__ __forceinline__ int token_tiles(const AttnParams &p, int ctx, int cnt, int rt) {
+  // without a mask a row tile sees no further than its last node
+  const int last = p.mask ? cnt : min(((rt + 1) * TQ - 1) / p.G + 1, cnt);
+  return (ctx + last + TK - 1) / TK;
+}
+__device__ __forceinline__ void tile_enter(const AttnParams &p, TileCursor &u) {
+  for (;; ++u.b) {
+    const Seq s = sequence(p, u.b);
+    if (s.cnt <= 0) continue;
+    u.ctx = s.ctx, u.cnt = s.cnt;
+    u.tiles = (s.cnt * p.G + TQ - 1) / TQ;
+    return;
+  }
+}
+__device__ __forceinline__ void tile_next(const AttnParams &p, TileCursor &u) {  // the next segment
+  u.j = 0;
+  if (++u.rt == u.tiles) {
+    u.rt = 0;
+    if (++u.h == p.c.Hk) {
+      u.h = 0;
+      ++u.b;
+      tile_enter(p, u);
+    }
+  }
+  u.n = token_tiles(p, u.ctx, u.cnt, u.rt);
+}
+
+// Sixteen codes as fp16, in order.
+template <int KIND, bool SAFE>
+__device__ __forceinline__ void codes_to_f16(uint4 w, uint4 &lo, uint4 &hi) {
+  uint32_t u[4] = {w.x, w.y, w.z, w.w}, r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (KIND == KIND_E4M3) {
+      if (SAFE) {  // any bits give finite numbers: rows past the last slot may hold anything
+        r[2 * i] = e4m3_halves(prmt(u[i], 0, 0x1404));
+        r[2 * i + 1] = e4m3_halves(prmt(u[i], 0, 0x3424));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r[2 * i]) : "r"(0x5c005c00u));  // 256
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r[2 * i + 1]) : "r"(0x5c005c00u));
+      } else {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(r[2 * i]), "=r"(r[2 * i + 1])
+            : "r"(u[i]));
+      }
+    } else {
+      const uint32_t x = u[i] ^ 0x80808080u;
+      r[2 * i] = prmt(x, 0x64646464u, 0x4140);
+      r[2 * i + 1] = prmt(x, 0x64646464u, 0x4342);
+      asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r[2 * i]) : "r"(0x64806480u));
+      asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r[2 * i + 1]) : "r"(0x64806480u));
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// A raw tile [128][D] into panels of 64 columns of 128-byte swizzled rows.
+template <int D, int KIND, bool SAFE>
+__device__ __forceinline__ void convert_tile(const unsigned char *raw, unsigned char *to, int tid) {
+  constexpr int PER = D / 16;
+#pragma unroll 4
+  for (int k = tid; k < 128 * PER; k += T_CONV) {
+    const int row = k / PER, c = k % PER;
+    uint4 x[2];
+    codes_to_f16<KIND, SAFE>(lds128(raw + k * 16), x[0], x[1]);
+    unsigned char *base = to + (c >> 2) * 16384 + row * 128;
+    const int chunk = 2 * (c & 3), odd = c >> 2;  // the second panel starts with its odd chunk: no bank conflict
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = i ^ odd;
+      *reinterpret_cast<uint4 *>(base + ((chunk + e) ^ (row & 7)) * 16) = e ? x[1] : x[0];
+    }
+  }
+}
+
+template <int D, int KIND, int DT>
+__global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constant__ AttnParams p) {
+  using L = TileLayout<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  TileBars &bar = *reinterpret_cast<TileBars *>(smem + L::BARS);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::MISC);
+  volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::MISC + 4);
+  int *s_seq = reinterpret_cast<int *>(smem + L::MISC + 8);
+  long long *s_base = reinterpret_cast<long long *>(smem + L::MISC + 16);
+  long long *s_scan = reinterpret_cast<long long *>(smem + L::ML);
+  const CacheView &c = p.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = T_NT / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the list of all work, and this CTA's stretch of it
+  const auto work_of = [&](int b) -> long long {
+    const Seq s = sequence(p, b);
+    if (s.cnt <= 0) return 0;
+    const int tiles = (s.cnt * p.G + TQ - 1) / TQ;
+    long long w = 0;
+    if (p.mask) w = static_cast<long long>(tiles) * token_tiles(p, s.ctx, s.cnt, 0);
+    else
+      for (int t = 0; t < tiles; ++t) w += token_tiles(p, s.ctx, s.cnt, t);
+    return w * c.Hk;
+  };
+  long long total = 0, nc = 0, my0 = 0, my1 = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += T_NT) {
+      const int b = b0 + tid;
+      const long long w = b < p.B ? work_of(b) : 0;
+      long long x = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      long long before = run;
+      for (int i = 0; i < NW; ++i) {
+        if (i < warp) before += s_scan[i];
+        run += s_scan[i];
+      }
+      const long long first = before + x - w;
+      if (pass == 1 && w > 0 && my0 >= first && my0 < first + w) *s_seq = b, *s_base = first;
+    }
+    if (pass == 0) {
+      total = run;
+      nc = min(static_cast<long long>(gridDim.x), total);
+      if (static_cast<long long>(blockIdx.x) >= nc) break;
+      my0 = total * blockIdx.x / nc, my1 = total * (blockIdx.x + 1) / nc;
+    }
+  }
+  fill_rest<DT, T_NT>(p, D);
+  if (my1 <= my0) return;
+  if (tid == 0) {
+    for (int i = 0; i < T_RAW; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], T_CONV / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], T_CONV / 32), mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], T_CONV / 32), mbar_init(&bar.v_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1);
+    }
+    for (int i = 0; i < T_SCALES; ++i) mbar_init(&bar.sc_full[i], 1);
+    mbar_init(&bar.q_full, T_SOFT / 32);
+    mbar_init(&bar.meet, T_SOFT / 32);
+    fence_mbar_init();
+  }
+  if (warp == (T_SOFT + T_CONV) / 32) tmem_alloc(s_tmem, 512);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
+
+  TileCursor at;
+  at.b = *s_seq;
+  tile_enter(p, at);
+  {
+    long long r = my0 - *s_base;
+    at.rt = at.h = 0;
+    long long head = 0;  // tiles of one kv head
+    if (p.mask) head = static_cast<long long>(at.tiles) * token_tiles(p, at.ctx, at.cnt, 0);
+    else
+      for (int t = 0; t < at.tiles; ++t) head += token_tiles(p, at.ctx, at.cnt, t);
+    at.h = static_cast<int>(r / head);
+    r %= head;
+    for (;;) {
+      at.n = token_tiles(p, at.ctx, at.cnt, at.rt);
+      if (r < at.n) break;
+      r -= at.n;
+      ++at.rt;
+    }
+    at.j = static_cast<int>(r);
+  }
+  const int count = static_cast<int>(my1 - my0);
+  const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
+    return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
+  };
+  const auto arrive = [&](uint64_t *b) {  // once for the warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+  bool ok = true;
+
+  if (warp < T_SOFT / 32) {
+    // ------------------------------------------------------------ softmax
+    more_registers<T_REG_SOFT>();
+    const int grp = warp >> 2, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
+    const uint32_t tS = tmem + lanes + grp * 128, tO = tmem + lanes + 256 + grp * 128, tOther = tmem + lanes + 256 + (grp ^ 1) * 128;
+    float2 *ml = reinterpret_cast<float2 *>(smem + L::ML);
+    const float2 *scales = reinterpret_cast<const float2 *>(smem + L::SCALES);
+    const float NINF = __uint_as_float(0xff800000u);
+    uint32_t meets = 0, uses = 0, segs = 0;  // phases: meetings, tiles of this group, segments
+    const auto meet = [&]() {      // both groups
+      arrive(&bar.meet);
+      const bool good = wait(&bar.meet, meets & 1);
+      ++meets;
+      return good;
+    };
+    float *const mine = p.pieces + static_cast<long long>(blockIdx.x) * 2 * L::PIECE;
+    int i = 0;
+    while (ok && i < count) {
+      // ---- a segment: its queries
+      const int rows = min(TQ, at.cnt * p.G - at.rt * TQ), row = at.rt * TQ + r, node = row / p.G;
+      float fac;
+      {
+        const bool live = r < rows;
+        const long long base = live ? at.b * p.q_sb + node * p.q_sn + (at.h * p.G + row % p.G) * p.q_sh + grp * (D / 2) : 0;
+        Raw8<DT> raw[D / 16];
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          if (live) raw[k] = p.q_vec ? load8<DT, true>(p.q, base + 8 * k) : load8<DT, false>(p.q, base + 8 * k);
+          else raw[k].v[0] = make_uint4(0, 0, 0, 0);
+          float x[8];
+          unpack8<DT>(raw[k], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        }
+        float *halves = reinterpret_cast<float *>(ml);
+        halves[grp * 128 + r] = amax;
+        if (!(ok = meet())) break;
+        amax = fmaxf(amax, halves[(grp ^ 1) * 128 + r]);
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        fac = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          float x[8];
+          unpack8<DT>(raw[k], x);
+          const uint4 w = make_uint4(f32_to_f16x2(x[0] * down, x[1] * down), f32_to_f16x2(x[2] * down, x[3] * down),
+                                     f32_to_f16x2(x[4] * down, x[5] * down), f32_to_f16x2(x[6] * down, x[7] * down));
+          const int chunk = grp * (D / 16) + k;  // of 8 elements
+          *reinterpret_cast<uint4 *>(smem + L::Q + (chunk >> 3) * 16384 + r * 128 + ((chunk & 7) ^ (r & 7)) * 16) = w;
+        }
+        fence_async_smem();
+        arrive(&bar.q_full);
+      }
+      const int s0 = at.j, end = min(at.n - at.j, count - i) + i;
+      float m = NINF, base = 0.f, l = 0.f, m0 = NINF, l0 = 0.f;
+      const uint32_t uses0 = uses;
+      for (int k = i + ((i ^ grp) & 1); k < end; k += 2, ++uses) {
+        const int tok0 = (s0 + k - i) * TK;
+        if (!(ok = wait(&bar.sc_full[k % T_SCALES], (k / T_SCALES) & 1) && wait(&bar.s_full[grp], uses & 1))) break;
+        tc_after_sync();
+        const bool edge = tok0 + TK > at.ctx;  // new tokens, or slots past the last one
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        if (edge) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n0 = tok0 + 32 * q - at.ctx;  // node of the first column
+            const auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+            uint32_t bits;
+            if (p.mask) {
+              const uint32_t *words = p.mask + (static_cast<long long>(at.b) * p.N + min(node, p.N - 1)) * p.W;
+              const int w = n0 >> 5;  // rounds down
+              const uint32_t a = w >= 0 && w < p.W ? words[w] : w < 0 ? ~0u : 0u;
+              const uint32_t b = w + 1 >= 0 && w + 1 < p.W ? words[w + 1] : w + 1 < 0 ? ~0u : 0u;
+              bits = __funnelshift_r(a, b, n0 & 31);
+            } else {
+              bits = low(node + 1 - n0);
+            }
+            vis[q] = bits & low(at.cnt - n0);
+          }
+        }
+        const float2 *sc_at = scales + (k % T_SCALES) * 8;
+        const bool again = __any_sync(0xffffffffu, m == NINF);  // the first tile of a segment has no offset yet
+        uint32_t pk[64];
+        float sum = 0.f, sum0 = 0.f;
+        // turn 0: weights under the offset so far; turn 1, where one of them
+        // would pass 2^15: after the offset has moved
+#pragma unroll 1
+        for (int turn = again ? 1 : 0; turn < 2; ++turn) {
+          if (turn == 1) {
+            float top = NINF, top0 = NINF;
+            tmem_each16<8>(tS, [&](int q, const uint32_t(&s)[16]) {
+              const float2 sc = sc_at[q];
+              const bool zero = sc.y == NINF;
+              const float f = fac * sc.x, lv = zero ? 0.f : sc.y;
+              const uint32_t seen = vis[q >> 1] >> (16 * (q & 1));
+              float t = NINF;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x = fmaf(__uint_as_float(s[e]), f, lv);
+                if (edge && !((seen >> e) & 1)) x = NINF;
+                t = fmaxf(t, x);
+              }
+              if (zero) top0 = fmaxf(top0, t);
+              else top = fmaxf(top, t);
+            });
+            const float nm = fmaxf(m, top - WEIGHT_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
+            const float nm0 = fmaxf(m0, top0);
+            l *= a;
+            l0 *= ex2(m0 - (nm0 == NINF ? 0.f : nm0));
+            m = nm, base = nb, m0 = nm0;
+            if (uses != uses0) {  // O holds the products of this segment's earlier tiles
+              if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
+              tc_after_sync();
+              tmem_each16<D / 16>(tO, [&](int q, uint32_t(&o)[16]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                tmem_st16(tO + 16 * q, o);
+              });
+              tc_wait_st();
+            }
+          }
+          sum = 0.f, sum0 = 0.f;
+          float over = NINF;
+          tmem_each16<8>(tS, [&](int q, const uint32_t(&s)[16]) {
+            const float2 sc = sc_at[q];
+            const bool zero = sc.y == NINF;
+            const float f = fac * sc.x, off = zero ? (m0 == NINF ? 0.f : -m0) : sc.y - base;
+            const uint32_t seen = vis[q >> 1] >> (16 * (q & 1));
+            float2 part = make_float2(0.f, 0.f);
+            float hi = NINF;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(f, f), make_float2(off, off));
+              if (edge) {
+                if (!((seen >> e) & 1)) x.x = NINF;
+                if (!((seen >> (e + 1)) & 1)) x.y = NINF;
+              }
+              hi = fmaxf(hi, fmaxf(x.x, x.y));
+              x.x = ex2(x.x), x.y = ex2(x.y);
+              part = add2(part, x);
+              pk[8 * q + e / 2] = f32_to_f16x2(x.x, x.y);
+            }
+            if (zero) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pk[8 * q + e] = 0u;
+              sum0 += part.x + part.y;
+              if (hi > (m0 == NINF ? NINF : 15.f)) over = 100.f;
+            } else {
+              sum = fmaf(part.x + part.y, ex2(-sc.y), sum);
+              over = fmaxf(over, hi);
+            }
+          });
+          if (turn == 0 && !__any_sync(0xffffffffu, over > WEIGHT_UP + WEIGHT_SLACK)) break;
+        }
+        if (!ok) break;
+        l += sum;
+        l0 += sum0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(tS + 16 * q, pk + 16 * q);
+        tc_wait_st();
+        tc_before_sync();
+        arrive(&bar.p_full[grp]);
+      }
+      if (!ok) break;
+      // ---- the end of the segment: both groups' parts meet
+      if (l0 > 0.f) {  // blocks without values: joined so that neither sum overflows
+        const float nm = fmaxf(m, m0 - 60.f), nb = nm == NINF ? 0.f : nm;
+        l = l * ex2(m - nb) + l0 * ex2(m0 - nb);
+        // what the accumulator is scaled by follows from the offset that it was made with
+        base = ex2(m - nb);
+        m = nm;
+      } else {
+        base = 1.f;
+      }
+      const bool any = uses != uses0;
+      if (any) {
+        if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
+        tc_after_sync();
+      } else if (!(ok = wait(&bar.q_full, segs & 1))) {
+        break;
+      }  // the other group has read the maxima that ml overwrites
+      ++segs;
+      // the other group's accumulator is scaled by its own factor: it goes with m and l
+      float *adj = reinterpret_cast<float *>(smem + L::Q);  // all products with the queries are done by the first meeting
+      ml[grp * 128 + r] = make_float2(m, l);
+      if (!(ok = meet())) break;
+      adj[grp * 128 + r] = base;
+      tc_before_sync();
+      if (!(ok = meet())) break;
+      tc_after_sync();
+      const float2 other = ml[(grp ^ 1) * 128 + r];
+      const float adj_o = adj[(grp ^ 1) * 128 + r];
+      const int both = end - i >= 2;
+      const float M = fmaxf(m, other.x), bm = M == NINF ? 0.f : M;
+      float aw = ex2(m - bm), bw = ex2(other.x - bm);
+      const float sum = l * aw + other.y * bw;
+      aw *= base, bw *= adj_o;
+      const bool whole = s0 == 0 && s0 + end - i == at.n;
+      const int which = s0 > 0 ? 0 : 1;
+      const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      aw *= inv, bw *= inv;
+      float *piece = mine + which * L::PIECE;
+      const long long orow = (static_cast<long long>(at.b) * p.N + node) * (c.Hk * p.G) + at.h * p.G + row % p.G;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {  // this group writes its half of the columns
+        const int col = grp * (D / 2) + 16 * q;
+        uint32_t x[16], y[16];
+        float z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = y[e] = 0;
+        if (any) tmem_ld16(tO + col, x);
+        if (!any || both) tmem_ld16(tOther + col, y);
+        tc_wait_ld(x);
+        tc_wait_ld(y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = __uint_as_float(x[e]) * aw + __uint_as_float(y[e]) * bw;
+        if (r < rows) {
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              const float w[8] = {z[e], z[e + 1], z[e + 2], z[e + 3], z[e + 4], z[e + 5], z[e + 6], z[e + 7]};
+              store8<DT, true>(p.out, orow * D + col + e, pack8<DT>(w));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              reinterpret_cast<float4 *>(piece)[((col + e) / 4) * 128 + r] = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+          }
+        }
+      }
+      tc_before_sync();
+      if (r < rows && grp == 0) {
+        if (whole) {
+          if (p.lse) p.lse[orow] = sum == 0.f ? NINF : (M + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          piece[128 * D + r] = M, piece[128 * D + 128 + r] = sum;
+        }
+      }
+      if (!whole) __threadfence();
+      if (!(ok = meet())) break;  // the accumulators are free
+      if (!whole) {
+        // a segment that several CTAs share: the last to arrive merges, in order
+        const long long f0 = my0 + i - s0, f1 = f0 + at.n - 1;
+        const auto holder = [&](long long f) {
+          long long k = f * nc / total;
+          while (total * k / nc > f) --k;
+          while (total * (k + 1) / nc <= f) ++k;
+          return static_cast<int>(k);
+        };
+        const int c0 = holder(f0), n = holder(f1) - c0 + 1;
+        if (tid == 0) {
+          *s_last = atomicAdd(p.done + c0, 1) == n - 1;
+          __threadfence();
+        }
+        if (!(ok = meet())) break;
+        if (*s_last) {
+          __threadfence();
+          if (r < rows) {
+            const auto part = [&](int e) { return p.pieces + (static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * L::PIECE; };
+            float M2 = NINF;
+            for (int e = 0; e < n; ++e) M2 = fmaxf(M2, __ldcg(part(e) + 128 * D + r));
+            const float b2 = M2 == NINF ? 0.f : M2;
+            float sum2 = 0.f;
+            for (int e = 0; e < n; ++e) sum2 = fmaf(ex2(__ldcg(part(e) + 128 * D + r) - b2), __ldcg(part(e) + 128 * D + 128 + r), sum2);
+            const float inv2 = sum2 == 0.f ? 0.f : 1.f / sum2;
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              const int col = grp * (D / 2) + 16 * q;
+              float z[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[e] = 0.f;
+              for (int e = 0; e < n; ++e) {
+                const float a = ex2(__ldcg(part(e) + 128 * D + r) - b2);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(e)) + (col / 4 + g) * 128 + r);
+                  z[4 * g] = fmaf(a, x.x, z[4 * g]), z[4 * g + 1] = fmaf(a, x.y, z[4 * g + 1]);
+                  z[4 * g + 2] = fmaf(a, x.z, z[4 * g + 2]), z[4 * g + 3] = fmaf(a, x.w, z[4 * g + 3]);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 16; e += 8) {
+                float w[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) w[g] = z[e + g] * inv2;
+                store8<DT, true>(p.out, orow * D + col + e, pack8<DT>(w));
+              }
+            }
+            if (grp == 0 && p.lse) p.lse[orow] = sum2 == 0.f ? NINF : (M2 + log2f(sum2)) * 0.6931471805599453f;
+          }
+          if (tid == 0) p.done[c0] = 0;  // zero again for the next call
+        }
+        if (!(ok = meet())) break;  // s_last may be written again
+      }
+      i = end;
+      if (i < count) tile_next(p, at);
+    }
+  } else if (warp < (T_SOFT + T_CONV) / 32) {
+    // --------------------------------------------------------- conversion
+    fewer_registers<T_REG_CONV>();
+    const int ct = tid - T_SOFT;
+    int left = at.n - at.j;  // tiles of the segment from here on
+    TileCursor u = at;
+    for (int i = 0; ok && i < count; ++i) {
+      if (left == 0) tile_next(p, u), left = u.n;
+      const int j = u.n - left;
+      --left;
+      const bool safe = (j + 1) * TK <= u.ctx + u.cnt;  // every row of the tile has been written
+      const uint32_t buf = i & 1, ph = (i >> 1) & 1;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int slot = (2 * i + t) % T_RAW;
+        if (!(ok = wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1) && wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1))) break;
+        const unsigned char *raw = smem + L::RAW + slot * L::RAWB;
+        unsigned char *to = smem + (t ? L::V : L::K) + buf * L::OP;
+        if (safe) convert_tile<D, KIND, false>(raw, to, ct);
+        else convert_tile<D, KIND, true>(raw, to, ct);
+        fence_async_smem();
+        arrive(t ? &bar.v_full[buf] : &bar.k_full[buf]);
+        if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
+      }
+    }
+  } else {
+    fewer_registers<T_REG_REST>();
+    if (warp == (T_SOFT + T_CONV) / 32) {
+    // ----------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t ID_S = 1u << 4 | (TK / 8) << 17 | (TQ / 16) << 24;           // fp16 x fp16 -> fp32
+      constexpr uint32_t ID_O = 1u << 4 | 1u << 16 | (D / 8) << 17 | (TQ / 16) << 24;  // values run along the tokens
+      const uint32_t base = smem_u32(smem);
+      TileCursor u = at;
+      int left = at.n - at.j, segs = 0, seg0 = 0, pv = 0;  // pv: the next tile whose second product is due
+      int pv_first = 0;                                    // first tile of pv's segment
+      const auto second = [&]() {
+        const uint32_t g = pv & 1, ph = (pv >> 1) & 1;
+        ok = mbar_wait_bounded(&bar.p_full[g], ph) && mbar_wait_bounded(&bar.v_full[g], ph);
+        if (!ok) return;
+        tc_after_sync();
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k)
+          tc_mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k, tc_desc(base + L::V + g * L::OP + k * 2048, 16384), ID_O,
+                    k > 0 || pv - pv_first >= 2);
+        tc_commit(&bar.v_empty[g]);
+        tc_commit(&bar.o_done[g]);
+        ++pv;
+      };
+      for (int i = 0; ok && i < count; ++i) {
+        if (left == 0) {
+          tile_next(p, u), left = u.n;
+          while (ok && pv < i) second();  // the queries change when the segment is done
+          seg0 = i;
+          ++segs;
+          pv_first = i;
+        } else if (i - pv == 2) {
+          second();
+        }
+        if (!ok) break;
+        const uint32_t g = i & 1, ph = (i >> 1) & 1;
+        if (i == seg0) ok = mbar_wait_bounded(&bar.q_full, segs & 1);
+        ok = ok && mbar_wait_bounded(&bar.k_full[g], ph);
+        if (!ok) break;
+        tc_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(tmem + g * 128, tc_desc(base + L::Q + (k >> 2) * 16384 + (k & 3) * 32, 0),
+                    tc_desc(base + L::K + g * L::OP + (k >> 2) * 16384 + (k & 3) * 32, 0), ID_S, k > 0);
+        tc_commit(&bar.k_empty[g]);
+        tc_commit(&bar.s_full[g]);
+        --left;
+      }
+      while (ok && pv < count) second();
+    }
+    } else if (warp == (T_SOFT + T_CONV) / 32 + 1) {
+    // -------------------------------------------------------------- copies
+    TileCursor u = at;
+    int left = at.n - at.j, issued = 0;
+    // lane g < 8 looks after the tokens 16 g of a tile
+    const auto page_id = [&](const TileCursor &v, int j) {
+      const int tok = j * TK + 16 * (lane & 7);
+      return tok < v.ctx + v.cnt ? c.table[static_cast<long long>(v.b) * c.per + (tok >> c.log_page)] : 0;
+    };
+    int page = page_id(u, u.j);
+    for (int i = 0; ok && i < count; ++i) {
+      const int j = u.n - left, tok = j * TK + 16 * (lane & 7), len = u.ctx + u.cnt;
+      const bool there = lane < 8 && tok < len, bad = there && static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages);
+      const long long id = static_cast<long long>(bad ? 0 : page) * c.Hk + u.h;
+      if (bad) atomicOr(p.status, ST_PAGE);
+      float ks = 0.f, vs = 1.f;
+      if (there) ks = c.k_scale[id], vs = c.v_scale[id];
+      // the next tile's pages, while this one's copies wait for their slots
+      TileCursor v = u;
+      if (--left == 0 && i + 1 < count) tile_next(p, v), left = v.n;
+      const int next = i + 1 < count ? page_id(v, v.n - left) : 0;
+      // one copy for each page: its first 16 tokens in the tile stand for it
+      const int in = tok & (c.page - 1);
+      const bool lead = there && (in == 0 || (lane & 7) == 0);
+      const uint32_t bytes = static_cast<uint32_t>(min(c.page, TK) * D);
+      const uint32_t pages = __popc(__ballot_sync(0xffffffffu, lead));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int slot = (2 * i + t) % T_RAW;
+        if (!(ok = wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], bytes * pages);
+        __syncwarp();
+        if (lead)
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           smem_u32(smem + L::RAW + slot * L::RAWB + 16 * (lane & 7) * D)),
+                       "l"((t ? c.v : c.k) + (id * c.page + in) * D), "r"(bytes), "r"(smem_u32(&bar.raw_full[slot]))
+                       : "memory");
+        issued = 2 * i + t + 1;
+      }
+      if (!ok) break;
+      if (lane < 8) {
+        const float lv = bad ? __uint_as_float(0x7fc00000u) : vs <= LEAST_V_SCALE ? __uint_as_float(0xff800000u) : lg2(vs);
+        reinterpret_cast<float2 *>(smem + L::SCALES)[(i % T_SCALES) * 8 + lane] = make_float2(bad ? __uint_as_float(0x7fc00000u) : ks, lv);
+      }
+      arrive(&bar.sc_full[i % T_SCALES]);
+      u = v;
+      page = next;
+    }
+    // no copy outlives the CTA, even after a wait that ran out
+    for (int k = max(0, issued - T_RAW); k < issued; ++k) wait(&bar.raw_full[k % T_RAW], (k / T_RAW) & 1);
+    }
+  }
+  if (!ok) atomicOr(p.status, ST_TIMEOUT);
+  tc_before_sync();
+  __syncthreads();
+  if (warp == (T_SOFT + T_CONV) / 32) {
+    tc_after_sync();
+    tmem_free(tmem, 512);
+  }
+}
+
+}  // namespace spec

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "attention.cuh"
+#include "attention_tile.cuh"
 #include "cache.cuh"
 #include "host.h"
 #include "spec_verify.h"
@@ -88,20 +89,23 @@ const void *pick_norm_rope(bool vec, bool pairs) {
                : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16>);
 }
 
+// The attention's kernel, its block and shared memory, and the floats of a piece.
+struct AttnChoice {
+  const void *fn;
+  int threads, smem;
+  size_t piece;
+};
 template <int D, int KIND, int DT>
-int set_stream(const void **fn, int *smem) {
-  *fn = reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT>);
-  *smem = StreamLayout<D>::SMEM;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_stream_kernel<D, KIND, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamLayout<D>::SMEM);
-  return e == cudaSuccess ? static_cast<int>(SPEC_OK) : cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
+AttnChoice choose_attn(bool tile) {
+  if (tile) return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, TileLayout<D>::SMEM, TileLayout<D>::PIECE};
+  return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT>), ANT, StreamLayout<D>::SMEM, StreamLayout<D>::PIECE / 4};
 }
-int pick_stream(int D, int kind, int dtype, const void **fn, int *smem) {
+AttnChoice choose_attn(int D, int kind, int dtype, bool tile) {
   const bool bf = dtype == SPEC_BF16;
-  if (D == 128 && kind == SPEC_E4M3) return bf ? set_stream<128, KIND_E4M3, DT_BF16>(fn, smem) : set_stream<128, KIND_E4M3, DT_F16>(fn, smem);
-  if (D == 128) return bf ? set_stream<128, KIND_I8, DT_BF16>(fn, smem) : set_stream<128, KIND_I8, DT_F16>(fn, smem);
-  if (kind == SPEC_E4M3) return bf ? set_stream<64, KIND_E4M3, DT_BF16>(fn, smem) : set_stream<64, KIND_E4M3, DT_F16>(fn, smem);
-  return bf ? set_stream<64, KIND_I8, DT_BF16>(fn, smem) : set_stream<64, KIND_I8, DT_F16>(fn, smem);
+  if (D == 128 && kind == SPEC_E4M3) return bf ? choose_attn<128, KIND_E4M3, DT_BF16>(tile) : choose_attn<128, KIND_E4M3, DT_F16>(tile);
+  if (D == 128) return bf ? choose_attn<128, KIND_I8, DT_BF16>(tile) : choose_attn<128, KIND_I8, DT_F16>(tile);
+  if (kind == SPEC_E4M3) return bf ? choose_attn<64, KIND_E4M3, DT_BF16>(tile) : choose_attn<64, KIND_E4M3, DT_F16>(tile);
+  return bf ? choose_attn<64, KIND_I8, DT_BF16>(tile) : choose_attn<64, KIND_I8, DT_F16>(tile);
 }
 
 }  // namespace
@@ -255,18 +259,18 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   p.mask = mask;
   p.B = B, p.N = N, p.W = (N + 31) / 32, p.G = Hq / p.c.Hk;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const void *fn = nullptr;
-  int smem = 0;
-  if ((st = pick_stream(p.c.D, p.c.kind, dtype, &fn, &smem))) return st;
+  p.q_vec = vectors(*q, 2);
+  const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G > 16);
+  const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   const int grid = num_sms();
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const size_t piece = 16 * static_cast<size_t>(p.c.D) + 32;
-  if ((st = get_ws(stream, (2 * grid * piece + 3) / 4, &w, static_cast<size_t>(grid)))) return st;
+  if ((st = get_ws(stream, (2 * grid * k.piece + 3) / 4, &w, static_cast<size_t>(grid)))) return st;
   p.pieces = reinterpret_cast<float *>(w->partials);
   p.done = w->attn_done;
   p.status = w->status;
-  return launch(fn, dim3(static_cast<unsigned>(grid)), ANT, smem, stream, &p, "attn_stream_kernel launch");
+  return launch(k.fn, dim3(static_cast<unsigned>(grid)), k.threads, k.smem, stream, &p, "attention kernel launch");
 }
 
 int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len,
