@@ -59,19 +59,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// f(group, registers) for the 16-column groups of a range, each loaded while
-// the one before it is worked on.
-template <int GROUPS, class F>
-__device__ __forceinline__ void tmem_each16(uint32_t at, F f) {
-  uint32_t r[2][16];
-  tmem_ld16(at, r[0]);
-#pragma unroll
-  for (int q = 0; q < GROUPS; ++q) {
-    tc_wait_ld(r[q & 1]);
-    if (q + 1 < GROUPS) tmem_ld16(at + 16 * (q + 1), r[(q + 1) & 1]);
-    f(q, r[q & 1]);
-  }
-}
 // Shared-memory operand of 128-byte swizzled rows (8 rows of 128 bytes to an
 // atom of 1024); `lead` is the distance of neighbouring 64-element blocks where
 // the rows run along the contracted axis (0 otherwise).
@@ -124,14 +111,23 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // e4m3 queries and weights would cost the precision that the cache has.
 constexpr int TQ = 128, TK = 128;    // rows, tokens of a tile
 constexpr int T_SOFT = 256;          // softmax threads
-constexpr int T_CONV = 128;          // conversion threads
+constexpr int T_CONV = 256;          // conversion threads
 constexpr int T_NT = T_SOFT + T_CONV + 128;  // and a warp each for products and copies, and two idle ones
-// Registers: 128 a thread at launch, then 176 for the softmax, 96 for the
-// conversion and 64 for the rest: 256 * 176 + 128 * 96 + 128 * 64 = 512 * 128.
-constexpr int T_REG_SOFT = 176, T_REG_CONV = 96, T_REG_REST = 64;
-static_assert(T_SOFT * T_REG_SOFT + T_CONV * T_REG_CONV + 128 * T_REG_REST <= T_NT * 128, "register split");
+// Registers: 96 a thread at launch, then 136 for the softmax, 72 for the
+// conversion and 64 for the rest: 256 * 136 + 256 * 72 + 128 * 64 = 640 * 96.
+constexpr int T_REG = 96, T_REG_SOFT = 136, T_REG_CONV = 72, T_REG_REST = 64;
+static_assert(T_SOFT * T_REG_SOFT + T_CONV * T_REG_CONV + 128 * T_REG_REST <= T_NT * T_REG, "register split");
 constexpr int T_RAW = 4;             // raw slots: keys and values of two tiles
 constexpr int T_SCALES = 8;          // tiles of scales: more than the copy warp can be ahead
+
+// A bounded wait in a few instructions (the roles' code shares the
+// instruction cache): 50000 polls of at most 20 us each.
+__device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+  for (int polls = 0; polls < 50000; ++polls)
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return false;
+}
 
 template <int D>
 struct TileLayout {
@@ -213,19 +209,21 @@ __device__ __forceinline__ void codes_to_f16(uint4 w, uint4 &lo, uint4 &hi) {
 // A raw tile [128][D] into panels of 64 columns of 128-byte swizzled rows.
 template <int D, int KIND, bool SAFE>
 __device__ __forceinline__ void convert_tile(const unsigned char *raw, unsigned char *to, int tid) {
-  constexpr int PER = D / 16;
-#pragma unroll 4
-  for (int k = tid; k < 128 * PER; k += T_CONV) {
-    const int row = k / PER, c = k % PER;
-    uint4 x[2];
-    codes_to_f16<KIND, SAFE>(lds128(raw + k * 16), x[0], x[1]);
-    unsigned char *base = to + (c >> 2) * 16384 + row * 128;
-    const int chunk = 2 * (c & 3), odd = c >> 2;  // the second panel starts with its odd chunk: no bank conflict
+  constexpr int PER = D / 16, TURNS = 128 * PER / T_CONV;
+  static_assert(T_CONV % (8 * PER) == 0, "a thread's rows are equal modulo 8");
+  uint4 w[TURNS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = i ^ odd;
-      *reinterpret_cast<uint4 *>(base + ((chunk + e) ^ (row & 7)) * 16) = e ? x[1] : x[0];
-    }
+  for (int k = 0; k < TURNS; ++k) w[k] = lds128(raw + (tid + k * T_CONV) * 16);
+  const int row = tid / PER, c = tid % PER, odd = c >> 2;
+  // the second panel starts with its odd chunk: no bank conflict
+  unsigned char *base = to + odd * 16384 + row * 128;
+  unsigned char *first = base + ((2 * (c & 3) + odd) ^ (row & 7)) * 16, *second = base + ((2 * (c & 3) + (odd ^ 1)) ^ (row & 7)) * 16;
+#pragma unroll
+  for (int k = 0; k < TURNS; ++k) {
+    uint4 x[2];
+    codes_to_f16<KIND, SAFE>(w[k], x[0], x[1]);
+    *reinterpret_cast<uint4 *>(first + k * (T_CONV / PER) * 128) = odd ? x[1] : x[0];
+    *reinterpret_cast<uint4 *>(second + k * (T_CONV / PER) * 128) = odd ? x[0] : x[1];
   }
 }
 
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   }
   const int count = static_cast<int>(my1 - my0);
   const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
-    return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
+    return __all_sync(0xffffffffu, tile_wait(b, parity));
   };
   const auto arrive = [&](uint64_t *b) {  // once for the warp
     __syncwarp();
@@ -359,13 +357,13 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const int rows = min(TQ, at.cnt * p.G - at.rt * TQ), row = at.rt * TQ + r, node = row / p.G;
       float fac;
       {
-        const bool live = r < rows;
-        const long long base = live ? at.b * p.q_sb + node * p.q_sn + (at.h * p.G + row % p.G) * p.q_sh + grp * (D / 2) : 0;
+        const bool mine_live = r < rows;
+        const long long base = mine_live ? at.b * p.q_sb + node * p.q_sn + (at.h * p.G + row % p.G) * p.q_sh + grp * (D / 2) : 0;
         Raw8<DT> raw[D / 16];
         float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          if (live) raw[k] = p.q_vec ? load8<DT, true>(p.q, base + 8 * k) : load8<DT, false>(p.q, base + 8 * k);
+          if (mine_live) raw[k] = p.q_vec ? load8<DT, true>(p.q, base + 8 * k) : load8<DT, false>(p.q, base + 8 * k);
           else raw[k].v[0] = make_uint4(0, 0, 0, 0);
           float x[8];
           unpack8<DT>(raw[k], x);
@@ -377,8 +375,9 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         if (!(ok = meet())) break;
         amax = fmaxf(amax, halves[(grp ^ 1) * 128 + r]);
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        fac = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+        // a negative scale turns the query around, so that scores only grow with the products
+        const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), p.scale_log2);
+        fac = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           float x[8];
@@ -394,109 +393,119 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const int s0 = at.j, end = min(at.n - at.j, count - i) + i;
       float m = NINF, base = 0.f, l = 0.f, m0 = NINF, l0 = 0.f;
       const uint32_t uses0 = uses;
+      const bool live = 32 * (warp & 3) < rows;  // this warp has rows to look after
       for (int k = i + ((i ^ grp) & 1); k < end; k += 2, ++uses) {
         const int tok0 = (s0 + k - i) * TK;
         if (!(ok = wait(&bar.sc_full[k % T_SCALES], (k / T_SCALES) & 1) && wait(&bar.s_full[grp], uses & 1))) break;
         tc_after_sync();
-        const bool edge = tok0 + TK > at.ctx;  // new tokens, or slots past the last one
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (edge) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
+        if (live) {
+          const float2 *sc_at = scales + (k % T_SCALES) * 8;
+          const bool edge = tok0 + TK > at.ctx;  // new tokens, or slots past the last one
+          // the slots that the row sees, of 32 columns
+          const auto seen32 = [&](int q) -> uint32_t {
             const int n0 = tok0 + 32 * q - at.ctx;  // node of the first column
             const auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-            uint32_t bits;
+            uint32_t bits = low(node + 1 - n0);
             if (p.mask) {
               const uint32_t *words = p.mask + (static_cast<long long>(at.b) * p.N + min(node, p.N - 1)) * p.W;
-              const int w = n0 >> 5;  // rounds down
-              const uint32_t a = w >= 0 && w < p.W ? words[w] : w < 0 ? ~0u : 0u;
-              const uint32_t b = w + 1 >= 0 && w + 1 < p.W ? words[w + 1] : w + 1 < 0 ? ~0u : 0u;
-              bits = __funnelshift_r(a, b, n0 & 31);
-            } else {
-              bits = low(node + 1 - n0);
+              const int w = n0 >> 5;  // rounds down; words before the first are context
+              const uint32_t x = w < 0 ? ~0u : w < p.W ? words[w] : 0u, y = w + 1 < 0 ? ~0u : w + 1 < p.W ? words[w + 1] : 0u;
+              bits = __funnelshift_r(x, y, n0 & 31);
             }
-            vis[q] = bits & low(at.cnt - n0);
-          }
-        }
-        const float2 *sc_at = scales + (k % T_SCALES) * 8;
-        const bool again = __any_sync(0xffffffffu, m == NINF);  // the first tile of a segment has no offset yet
-        uint32_t pk[64];
-        float sum = 0.f, sum0 = 0.f;
-        // turn 0: weights under the offset so far; turn 1, where one of them
-        // would pass 2^15: after the offset has moved
+            return bits & low(at.cnt - n0);
+          };
+          // the tile's maximum, per group of 16 tokens that share their scales
+          float top = NINF, top0 = NINF;
 #pragma unroll 1
-        for (int turn = again ? 1 : 0; turn < 2; ++turn) {
-          if (turn == 1) {
-            float top = NINF, top0 = NINF;
-            tmem_each16<8>(tS, [&](int q, const uint32_t(&s)[16]) {
-              const float2 sc = sc_at[q];
-              const bool zero = sc.y == NINF;
-              const float f = fac * sc.x, lv = zero ? 0.f : sc.y;
-              const uint32_t seen = vis[q >> 1] >> (16 * (q & 1));
-              float t = NINF;
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[2][16];
+            tmem_ld16(tS + 32 * q, s[0]);
+            tmem_ld16(tS + 32 * q + 16, s[1]);
+            tc_wait_ld(s[0]);
+            tc_wait_ld(s[1]);
+            if (edge) {
+              const uint32_t bits = seen32(q);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x = fmaf(__uint_as_float(s[e]), f, lv);
-                if (edge && !((seen >> e) & 1)) x = NINF;
-                t = fmaxf(t, x);
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1)) s[e >> 4][e & 15] = 0xff800000u;
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float t0 = NINF, t1 = NINF;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                t0 = fmaxf(fmaxf(t0, __uint_as_float(s[hf][e])), __uint_as_float(s[hf][e + 1]));
+                t1 = fmaxf(fmaxf(t1, __uint_as_float(s[hf][e + 2])), __uint_as_float(s[hf][e + 3]));
               }
-              if (zero) top0 = fmaxf(top0, t);
-              else top = fmaxf(top, t);
-            });
+              const float2 sc = sc_at[2 * q + hf];
+              const float t = fmaxf(t0, t1);
+              // a factor of 0 (no keys, no scale) leaves 0, also of nothing seen
+              if (sc.y == NINF) top0 = fmaxf(top0, t == NINF ? NINF : t * (fac * sc.x));
+              else top = fmaxf(top, t == NINF ? NINF : fmaf(t, fac * sc.x, sc.y));
+            }
+          }
+          // the offset moves only when a weight would pass 2^15
+          if (__any_sync(0xffffffffu, top > m + (WEIGHT_UP + WEIGHT_SLACK))) {
             const float nm = fmaxf(m, top - WEIGHT_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
-            const float nm0 = fmaxf(m0, top0);
             l *= a;
-            l0 *= ex2(m0 - (nm0 == NINF ? 0.f : nm0));
-            m = nm, base = nb, m0 = nm0;
+            m = nm, base = nb;
             if (uses != uses0) {  // O holds the products of this segment's earlier tiles
               if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
               tc_after_sync();
-              tmem_each16<D / 16>(tO, [&](int q, uint32_t(&o)[16]) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * q, o);
+                tc_wait_ld(o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
                 tmem_st16(tO + 16 * q, o);
-              });
-              tc_wait_st();
+              }
             }
           }
-          sum = 0.f, sum0 = 0.f;
-          float over = NINF;
-          tmem_each16<8>(tS, [&](int q, const uint32_t(&s)[16]) {
-            const float2 sc = sc_at[q];
-            const bool zero = sc.y == NINF;
-            const float f = fac * sc.x, off = zero ? (m0 == NINF ? 0.f : -m0) : sc.y - base;
-            const uint32_t seen = vis[q >> 1] >> (16 * (q & 1));
-            float2 part = make_float2(0.f, 0.f);
-            float hi = NINF;
+          if (__any_sync(0xffffffffu, top0 > m0)) {  // blocks without values count in a sum of their own
+            const float nm0 = fmaxf(m0, top0);
+            l0 *= ex2(m0 - (nm0 == NINF ? 0.f : nm0));
+            m0 = nm0;
+          }
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[2][16], pk[16];
+            tmem_ld16(tS + 32 * q, s[0]);
+            tmem_ld16(tS + 32 * q + 16, s[1]);
+            tc_wait_ld(s[0]);
+            tc_wait_ld(s[1]);
+            uint32_t bits = ~0u;
+            if (edge) bits = seen32(q);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(f, f), make_float2(off, off));
-              if (edge) {
-                if (!((seen >> e) & 1)) x.x = NINF;
-                if (!((seen >> (e + 1)) & 1)) x.y = NINF;
+            for (int hf = 0; hf < 2; ++hf) {
+              const float2 sc = sc_at[2 * q + hf];
+              const bool zero = sc.y == NINF;
+              const float f = fac * sc.x, off = zero ? (m0 == NINF ? 0.f : -m0) : sc.y - base;
+              float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float2 x = fma2(make_float2(__uint_as_float(s[hf][e]), __uint_as_float(s[hf][e + 1])), make_float2(f, f), make_float2(off, off));
+                x.x = ex2(x.x), x.y = ex2(x.y);
+                if (edge) {
+                  if (!((bits >> (16 * hf + e)) & 1)) x.x = 0.f;
+                  if (!((bits >> (16 * hf + e + 1)) & 1)) x.y = 0.f;
+                }
+                part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
+                pk[8 * hf + e / 2] = f32_to_f16x2(x.x, x.y);
               }
-              hi = fmaxf(hi, fmaxf(x.x, x.y));
-              x.x = ex2(x.x), x.y = ex2(x.y);
-              part = add2(part, x);
-              pk[8 * q + e / 2] = f32_to_f16x2(x.x, x.y);
-            }
-            if (zero) {
+              const float2 sum = add2(part[0], part[1]);
+              if (zero) {
+                l0 += sum.x + sum.y;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) pk[8 * q + e] = 0u;
-              sum0 += part.x + part.y;
-              if (hi > (m0 == NINF ? NINF : 15.f)) over = 100.f;
-            } else {
-              sum = fmaf(part.x + part.y, ex2(-sc.y), sum);
-              over = fmaxf(over, hi);
+                for (int e = 0; e < 8; ++e) pk[8 * hf + e] = 0u;
+              } else {
+                l = fmaf(sum.x + sum.y, ex2(-sc.y), l);
+              }
             }
-          });
-          if (turn == 0 && !__any_sync(0xffffffffu, over > WEIGHT_UP + WEIGHT_SLACK)) break;
+            tmem_st16(tS + 16 * q, pk);  // weights over scores that have been read
+          }
         }
-        if (!ok) break;
-        l += sum;
-        l0 += sum0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_st16(tS + 16 * q, pk + 16 * q);
         tc_wait_st();
         tc_before_sync();
         arrive(&bar.p_full[grp]);
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       --left;
       const bool safe = (j + 1) * TK <= u.ctx + u.cnt;  // every row of the tile has been written
       const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = (2 * i + t) % T_RAW;
         if (!(ok = wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1) && wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1))) break;
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       int pv_first = 0;                                    // first tile of pv's segment
       const auto second = [&]() {
         const uint32_t g = pv & 1, ph = (pv >> 1) & 1;
-        ok = mbar_wait_bounded(&bar.p_full[g], ph) && mbar_wait_bounded(&bar.v_full[g], ph);
+        ok = tile_wait(&bar.p_full[g], ph) && tile_wait(&bar.v_full[g], ph);
         if (!ok) return;
         tc_after_sync();
 #pragma unroll
@@ -696,8 +705,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         }
         if (!ok) break;
         const uint32_t g = i & 1, ph = (i >> 1) & 1;
-        if (i == seg0) ok = mbar_wait_bounded(&bar.q_full, segs & 1);
-        ok = ok && mbar_wait_bounded(&bar.k_full[g], ph);
+        if (i == seg0) ok = tile_wait(&bar.q_full, segs & 1);
+        ok = ok && tile_wait(&bar.k_full[g], ph);
         if (!ok) break;
         tc_after_sync();
 #pragma unroll
@@ -736,7 +745,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const bool lead = there && (in == 0 || (lane & 7) == 0);
       const uint32_t bytes = static_cast<uint32_t>(min(c.page, TK) * D);
       const uint32_t pages = __popc(__ballot_sync(0xffffffffu, lead));
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = (2 * i + t) % T_RAW;
         if (!(ok = wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1))) break;
