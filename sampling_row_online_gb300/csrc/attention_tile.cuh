@@ -120,12 +120,14 @@ static_assert(T_SOFT * T_REG_SOFT + T_CONV * T_REG_CONV + 128 * T_REG_REST <= T_
 constexpr int T_RAW = 4;             // raw slots: keys and values of two tiles
 constexpr int T_SCALES = 8;          // tiles of scales: more than the copy warp can be ahead
 
-// A bounded wait in a few instructions (the roles' code shares the
-// instruction cache): 50000 polls of at most 20 us each.
+// A bounded wait in a few instructions (the roles share the instruction cache
+// and the issue slots; a wait with a suspend hint polls with nanosleep, which
+// took 40 % of the issued instructions).  The limit is in polls, each of which
+// the hardware may hold for some time: tens of milliseconds at least.
 __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
-  for (int polls = 0; polls < 50000; ++polls)
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  for (int polls = 0; polls < 1 << 20; ++polls)
+    if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 
@@ -147,6 +149,11 @@ struct TileBars {
   uint64_t sc_full[T_SCALES], q_full, meet;
 };
 static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
+
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
 
 struct TileCursor {
   int b, h, rt, j, n, tiles, ctx, cnt;  // n: token tiles of this row tile
@@ -416,6 +423,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           };
           // the tile's maximum, per group of 16 tokens that share their scales
           float top = NINF, top0 = NINF;
+          const auto maxima = [&](auto at_edge) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t s[2][16];
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             tmem_ld16(tS + 32 * q + 16, s[1]);
             tc_wait_ld(s[0]);
             tc_wait_ld(s[1]);
-            if (edge) {
+            if constexpr (decltype(at_edge)::value) {
               const uint32_t bits = seen32(q);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -444,6 +452,9 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
               else top = fmaxf(top, t == NINF ? NINF : fmaf(t, fac * sc.x, sc.y));
             }
           }
+          };
+          if (edge) maxima(Flag<true>{});
+          else maxima(Flag<false>{});
           // the offset moves only when a weight would pass 2^15
           if (__any_sync(0xffffffffu, top > m + (WEIGHT_UP + WEIGHT_SLACK))) {
             const float nm = fmaxf(m, top - WEIGHT_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
@@ -468,6 +479,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             l0 *= ex2(m0 - (nm0 == NINF ? 0.f : nm0));
             m0 = nm0;
           }
+          const auto weights = [&](auto at_edge) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t s[2][16], pk[16];
@@ -476,7 +488,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             tc_wait_ld(s[0]);
             tc_wait_ld(s[1]);
             uint32_t bits = ~0u;
-            if (edge) bits = seen32(q);
+            if constexpr (decltype(at_edge)::value) bits = seen32(q);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const float2 sc = sc_at[2 * q + hf];
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
               for (int e = 0; e < 16; e += 2) {
                 float2 x = fma2(make_float2(__uint_as_float(s[hf][e]), __uint_as_float(s[hf][e + 1])), make_float2(f, f), make_float2(off, off));
                 x.x = ex2(x.x), x.y = ex2(x.y);
-                if (edge) {
+                if constexpr (decltype(at_edge)::value) {
                   if (!((bits >> (16 * hf + e)) & 1)) x.x = 0.f;
                   if (!((bits >> (16 * hf + e + 1)) & 1)) x.y = 0.f;
                 }
@@ -505,6 +517,9 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             }
             tmem_st16(tS + 16 * q, pk);  // weights over scores that have been read
           }
+          };
+          if (edge) weights(Flag<true>{});
+          else weights(Flag<false>{});
         }
         tc_wait_st();
         tc_before_sync();
