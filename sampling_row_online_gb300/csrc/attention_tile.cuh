@@ -97,7 +97,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // ======================================================================
 // A persistent CTA per SM.  The list of all work is (sequence, kv head, tile of
 // 128 rows, tile of 128 tokens); every CTA takes an equal stretch of it.  Its
-// tiles alternate between two groups of 128 softmax threads, A and B, each
+// tiles alternate between two groups of 256 softmax threads, A and B, each
 // with its own scores, weights, accumulator, maximum and sum: they meet only at
 // the end of a segment (a row tile of a kv head), so one group's softmax runs
 // under the other's products.
@@ -105,17 +105,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 //   copy warp    pages -> raw ring (bulk copies of 8-bit codes), scales -> ring
 //   conversion   raw codes -> fp16 tiles in the swizzled operand layout
 //   product warp S = Q K^T, O += P V (P in tensor memory, over S)
-//   softmax      one row per thread: S -> P, lazy rescaling of O, the output
+//   softmax      two threads per row, half of the tokens each: S -> P, lazy
+//                rescaling of O, the output
 //
 // Codes cannot be an operand next to fp16 (one instruction takes one type), and
 // e4m3 queries and weights would cost the precision that the cache has.
 constexpr int TQ = 128, TK = 128;    // rows, tokens of a tile
-constexpr int T_SOFT = 256;          // softmax threads
+constexpr int T_SOFT = 512;          // softmax threads: two groups, two threads per row
 constexpr int T_CONV = 256;          // conversion threads
 constexpr int T_NT = T_SOFT + T_CONV + 128;  // and a warp each for products and copies, and two idle ones
-// Registers: 96 a thread at launch, then 136 for the softmax, 72 for the
-// conversion and 64 for the rest: 256 * 136 + 256 * 72 + 128 * 64 = 640 * 96.
-constexpr int T_REG = 96, T_REG_SOFT = 136, T_REG_CONV = 72, T_REG_REST = 64;
+// Registers: 72 a thread at launch, then 88 for the softmax, 56 for the
+// conversion and 40 for the rest: 512 * 88 + 256 * 56 + 128 * 40 = 896 * 72.
+constexpr int T_REG = 72, T_REG_SOFT = 88, T_REG_CONV = 56, T_REG_REST = 40;
 static_assert(T_SOFT * T_REG_SOFT + T_CONV * T_REG_CONV + 128 * T_REG_REST <= T_NT * T_REG, "register split");
 constexpr int T_RAW = 4;             // raw slots: keys and values of two tiles
 constexpr int T_SCALES = 8;          // tiles of scales: more than the copy warp can be ahead
@@ -137,7 +138,7 @@ struct TileLayout {
   static constexpr int RAWB = 128 * D;              // a raw tile
   static constexpr int Q = 0, K = OP, V = 3 * OP, RAW = 5 * OP;
   static constexpr int SCALES = RAW + T_RAW * RAWB;  // [T_SCALES][8] (key scale, log2 of the value scale)
-  static constexpr int ML = SCALES + T_SCALES * 64;  // [2][128] (offset, sum) of the groups
+  static constexpr int ML = SCALES + T_SCALES * 64;  // [4][128] floats: maxima that a row's threads exchange
   static constexpr int BARS = ML + 2048;
   static constexpr int MISC = BARS + 40 * 8;
   static constexpr int SMEM = MISC + 64;
@@ -146,7 +147,7 @@ struct TileLayout {
 
 struct TileBars {
   uint64_t raw_full[T_RAW], raw_empty[T_RAW], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
-  uint64_t sc_full[T_SCALES], q_full, meet;
+  uint64_t sc_full[T_SCALES], pair[8], q_full, meet;
 };
 static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
 
@@ -298,9 +299,10 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], T_CONV / 32), mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.v_full[i], T_CONV / 32), mbar_init(&bar.v_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 8), mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < T_SCALES; ++i) mbar_init(&bar.sc_full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&bar.pair[i], 2);
     mbar_init(&bar.q_full, T_SOFT / 32);
     mbar_init(&bar.meet, T_SOFT / 32);
     fence_mbar_init();
@@ -344,14 +346,15 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   if (warp < T_SOFT / 32) {
     // ------------------------------------------------------------ softmax
     more_registers<T_REG_SOFT>();
-    const int grp = warp >> 2, r = tid & 127;
+    const int grp = (warp >> 2) & 1, half = warp >> 3, quarter = 2 * half + grp, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
-    const uint32_t tS = tmem + lanes + grp * 128, tO = tmem + lanes + 256 + grp * 128, tOther = tmem + lanes + 256 + (grp ^ 1) * 128;
-    float2 *ml = reinterpret_cast<float2 *>(smem + L::ML);
+    const uint32_t tS = tmem + lanes + grp * 128 + 64 * half, tO = tmem + lanes + 256;
+    float *xch = reinterpret_cast<float *>(smem + L::ML);
+    uint64_t *const pair = &bar.pair[warp & 7];  // this warp and the other half's of the same rows
     const float2 *scales = reinterpret_cast<const float2 *>(smem + L::SCALES);
     const float NINF = __uint_as_float(0xff800000u);
-    uint32_t meets = 0, uses = 0, segs = 0;  // phases: meetings, tiles of this group, segments
-    const auto meet = [&]() {      // both groups
+    uint32_t meets = 0, uses = 0, pairs = 0;  // phases: meetings, tiles of this group, exchanges
+    const auto meet = [&]() {                 // all softmax threads
       arrive(&bar.meet);
       const bool good = wait(&bar.meet, meets & 1);
       ++meets;
@@ -365,11 +368,11 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       float fac;
       {
         const bool mine_live = r < rows;
-        const long long base = mine_live ? at.b * p.q_sb + node * p.q_sn + (at.h * p.G + row % p.G) * p.q_sh + grp * (D / 2) : 0;
-        Raw8<DT> raw[D / 16];
+        const long long base = mine_live ? at.b * p.q_sb + node * p.q_sn + (at.h * p.G + row % p.G) * p.q_sh + quarter * (D / 4) : 0;
+        Raw8<DT> raw[D / 32];
         float amax = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
           if (mine_live) raw[k] = p.q_vec ? load8<DT, true>(p.q, base + 8 * k) : load8<DT, false>(p.q, base + 8 * k);
           else raw[k].v[0] = make_uint4(0, 0, 0, 0);
           float x[8];
@@ -377,21 +380,20 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
 #pragma unroll
           for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
-        float *halves = reinterpret_cast<float *>(ml);
-        halves[grp * 128 + r] = amax;
+        xch[quarter * 128 + r] = amax;
         if (!(ok = meet())) break;
-        amax = fmaxf(amax, halves[(grp ^ 1) * 128 + r]);
+        amax = fmaxf(fmaxf(xch[r], xch[128 + r]), fmaxf(xch[256 + r], xch[384 + r]));
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
         // a negative scale turns the query around, so that scores only grow with the products
         const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), p.scale_log2);
         fac = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(p.scale_log2);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
           float x[8];
           unpack8<DT>(raw[k], x);
           const uint4 w = make_uint4(f32_to_f16x2(x[0] * down, x[1] * down), f32_to_f16x2(x[2] * down, x[3] * down),
                                      f32_to_f16x2(x[4] * down, x[5] * down), f32_to_f16x2(x[6] * down, x[7] * down));
-          const int chunk = grp * (D / 16) + k;  // of 8 elements
+          const int chunk = quarter * (D / 32) + k;  // of 8 elements
           *reinterpret_cast<uint4 *>(smem + L::Q + (chunk >> 3) * 16384 + r * 128 + ((chunk & 7) ^ (r & 7)) * 16) = w;
         }
         fence_async_smem();
@@ -402,12 +404,12 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const uint32_t uses0 = uses;
       const bool live = 32 * (warp & 3) < rows;  // this warp has rows to look after
       for (int k = i + ((i ^ grp) & 1); k < end; k += 2, ++uses) {
-        const int tok0 = (s0 + k - i) * TK;
+        const int tok0 = (s0 + k - i) * TK + 64 * half;
         if (!(ok = wait(&bar.sc_full[k % T_SCALES], (k / T_SCALES) & 1) && wait(&bar.s_full[grp], uses & 1))) break;
         tc_after_sync();
         if (live) {
-          const float2 *sc_at = scales + (k % T_SCALES) * 8;
-          const bool edge = tok0 + TK > at.ctx;  // new tokens, or slots past the last one
+          const float2 *sc_at = scales + (k % T_SCALES) * 8 + 4 * half;
+          const bool edge = tok0 + 64 > at.ctx;  // new tokens, or slots past the last one
           // the slots that the row sees, of 32 columns
           const auto seen32 = [&](int q) -> uint32_t {
             const int n0 = tok0 + 32 * q - at.ctx;  // node of the first column
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           float top = NINF, top0 = NINF;
           const auto maxima = [&](auto at_edge) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t s[2][16];
             tmem_ld16(tS + 32 * q, s[0]);
             tmem_ld16(tS + 32 * q + 16, s[1]);
@@ -455,6 +457,12 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           };
           if (edge) maxima(Flag<true>{});
           else maxima(Flag<false>{});
+          // both halves go by the maximum of the whole tile
+          xch[256 * grp + 128 * half + r] = top;
+          arrive(pair);
+          if (!(ok = wait(pair, pairs & 1))) break;
+          ++pairs;
+          top = fmaxf(top, xch[256 * grp + 128 * (half ^ 1) + r]);
           // the offset moves only when a weight would pass 2^15
           if (__any_sync(0xffffffffu, top > m + (WEIGHT_UP + WEIGHT_SLACK))) {
             const float nm = fmaxf(m, top - WEIGHT_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
@@ -464,13 +472,14 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
               if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
               tc_after_sync();
 #pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
+              for (int q = 0; q < D / 32; ++q) {  // each half takes half of the columns
+                const uint32_t col = tO + grp * 128 + half * (D / 2) + 16 * q;
                 uint32_t o[16];
-                tmem_ld16(tO + 16 * q, o);
+                tmem_ld16(col, o);
                 tc_wait_ld(o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                tmem_st16(tO + 16 * q, o);
+                tmem_st16(col, o);
               }
             }
           }
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           }
           const auto weights = [&](auto at_edge) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t s[2][16], pk[16];
             tmem_ld16(tS + 32 * q, s[0]);
             tmem_ld16(tS + 32 * q + 16, s[1]);
@@ -527,53 +536,45 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       }
       if (!ok) break;
       // ---- the end of the segment: both groups' parts meet
-      if (l0 > 0.f) {  // blocks without values: joined so that neither sum overflows
-        const float nm = fmaxf(m, m0 - 60.f), nb = nm == NINF ? 0.f : nm;
-        l = l * ex2(m - nb) + l0 * ex2(m0 - nb);
-        // what the accumulator is scaled by follows from the offset that it was made with
-        base = ex2(m - nb);
-        m = nm;
-      } else {
-        base = 1.f;
-      }
-      const bool any = uses != uses0;
-      if (any) {
+      const bool has[2] = {end - i >= 2 || !(i & 1), end - i >= 2 || (i & 1)};  // the group had a tile
+      if (has[grp]) {
         if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
         tc_after_sync();
-      } else if (!(ok = wait(&bar.q_full, segs & 1))) {
-        break;
-      }  // the other group has read the maxima that ml overwrites
-      ++segs;
-      // the other group's accumulator is scaled by its own factor: it goes with m and l
-      float *adj = reinterpret_cast<float *>(smem + L::Q);  // all products with the queries are done by the first meeting
-      ml[grp * 128 + r] = make_float2(m, l);
-      if (!(ok = meet())) break;
-      adj[grp * 128 + r] = base;
+      }
       tc_before_sync();
       if (!(ok = meet())) break;
       tc_after_sync();
-      const float2 other = ml[(grp ^ 1) * 128 + r];
-      const float adj_o = adj[(grp ^ 1) * 128 + r];
-      const int both = end - i >= 2;
-      const float M = fmaxf(m, other.x), bm = M == NINF ? 0.f : M;
-      float aw = ex2(m - bm), bw = ex2(other.x - bm);
-      const float sum = l * aw + other.y * bw;
-      aw *= base, bw *= adj_o;
+      // all products with the queries are done: their place takes the sums
+      float4 *sums = reinterpret_cast<float4 *>(smem + L::Q);
+      sums[quarter * 128 + r] = make_float4(m, l, m0, l0);
+      if (!(ok = meet())) break;
+      float M = NINF, mg[2];
+      float4 each[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        each[e] = sums[e * 128 + r];
+        M = fmaxf(M, fmaxf(each[e].x, each[e].z - 60.f));  // blocks without values: neither sum overflows
+      }
+      mg[0] = each[0].x, mg[1] = each[1].x;
+      const float bm = M == NINF ? 0.f : M;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += each[e].y * ex2(each[e].x - bm) + each[e].w * ex2(each[e].z - bm);
       const bool whole = s0 == 0 && s0 + end - i == at.n;
       const int which = s0 > 0 ? 0 : 1;
       const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-      aw *= inv, bw *= inv;
+      const float aw = ex2(mg[0] - bm) * inv, bw = ex2(mg[1] - bm) * inv;
       float *piece = mine + which * L::PIECE;
       const long long orow = (static_cast<long long>(at.b) * p.N + node) * (c.Hk * p.G) + at.h * p.G + row % p.G;
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {  // this group writes its half of the columns
-        const int col = grp * (D / 2) + 16 * q;
+      for (int q = 0; q < D / 64; ++q) {  // a quarter of the columns each
+        const int col = quarter * (D / 4) + 16 * q;
         uint32_t x[16], y[16];
         float z[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = y[e] = 0;
-        if (any) tmem_ld16(tO + col, x);
-        if (!any || both) tmem_ld16(tOther + col, y);
+        if (has[0]) tmem_ld16(tO + col, x);
+        if (has[1]) tmem_ld16(tO + 128 + col, y);
         tc_wait_ld(x);
         tc_wait_ld(y);
 #pragma unroll
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         }
       }
       tc_before_sync();
-      if (r < rows && grp == 0) {
+      if (r < rows && quarter == 0) {
         if (whole) {
           if (p.lse) p.lse[orow] = sum == 0.f ? NINF : (M + log2f(sum)) * 0.6931471805599453f;
         } else {
@@ -628,8 +629,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             for (int e = 0; e < n; ++e) sum2 = fmaf(ex2(__ldcg(part(e) + 128 * D + r) - b2), __ldcg(part(e) + 128 * D + 128 + r), sum2);
             const float inv2 = sum2 == 0.f ? 0.f : 1.f / sum2;
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              const int col = grp * (D / 2) + 16 * q;
+            for (int q = 0; q < D / 64; ++q) {
+              const int col = quarter * (D / 4) + 16 * q;
               float z[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) z[e] = 0.f;
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
                 store8<DT, true>(p.out, orow * D + col + e, pack8<DT>(w));
               }
             }
-            if (grp == 0 && p.lse) p.lse[orow] = sum2 == 0.f ? NINF : (M2 + log2f(sum2)) * 0.6931471805599453f;
+            if (quarter == 0 && p.lse) p.lse[orow] = sum2 == 0.f ? NINF : (M2 + log2f(sum2)) * 0.6931471805599453f;
           }
           if (tid == 0) p.done[c0] = 0;  // zero again for the next call
         }
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         tc_after_sync();
 #pragma unroll
         for (int k = 0; k < TK / 16; ++k)
-          tc_mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k, tc_desc(base + L::V + g * L::OP + k * 2048, 16384), ID_O,
+          tc_mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 64 * (k >> 2) + 8 * (k & 3), tc_desc(base + L::V + g * L::OP + k * 2048, 16384), ID_O,
                     k > 0 || pv - pv_first >= 2);
         tc_commit(&bar.v_empty[g]);
         tc_commit(&bar.o_done[g]);
