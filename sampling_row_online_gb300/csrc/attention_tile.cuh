@@ -122,14 +122,23 @@ constexpr int T_RAW = 4;             // raw slots: keys and values of two tiles
 constexpr int T_SCALES = 8;          // tiles of scales: more than the copy warp can be ahead
 
 // A bounded wait in a few instructions (the roles share the instruction cache
-// and the issue slots; a wait with a suspend hint polls with nanosleep, which
-// took 40 % of the issued instructions).  The limit is in polls, each of which
-// the hardware may hold for some time: tens of milliseconds at least.
+// and the issue slots, of which polls without a pause took half).  REST: the
+// pause between polls, in nanoseconds.  The limit is in polls: tens of
+// milliseconds at least.
+template <int REST>
 __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
-  for (int polls = 0; polls < 1 << 20; ++polls)
+  for (int polls = 0; polls < 1 << 20; ++polls) {
     if (mbar_try_wait(bar, parity)) return true;
+    __nanosleep(REST);
+  }
   return false;
+}
+// A barrier of n threads of the CTA.  It has no limit: whoever gives up a wait
+// goes on to every barrier all the same, without waiting again.
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void mbar_arrive_many(uint64_t *bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
 template <int D>
@@ -147,7 +156,7 @@ struct TileLayout {
 
 struct TileBars {
   uint64_t raw_full[T_RAW], raw_empty[T_RAW], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
-  uint64_t sc_full[T_SCALES], pair[8], q_full, meet;
+  uint64_t sc_full[T_SCALES], q_full;
 };
 static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
 
@@ -217,21 +226,24 @@ __device__ __forceinline__ void codes_to_f16(uint4 w, uint4 &lo, uint4 &hi) {
 // A raw tile [128][D] into panels of 64 columns of 128-byte swizzled rows.
 template <int D, int KIND, bool SAFE>
 __device__ __forceinline__ void convert_tile(const unsigned char *raw, unsigned char *to, int tid) {
-  constexpr int PER = D / 16, TURNS = 128 * PER / T_CONV;
-  static_assert(T_CONV % (8 * PER) == 0, "a thread's rows are equal modulo 8");
+  constexpr int PER = D / 16, TURNS = 128 * PER / T_CONV, STEP = T_CONV / PER;  // rows per turn
+  static_assert(STEP % 8 == 0, "a thread's rows are equal modulo 8");
+  // eight neighbouring lanes take four 16-byte pieces of an even row and four
+  // of the odd row after it, in the other half where a row has two: their
+  // loads and their stores touch every bank once
+  const int odd = (tid >> 2) & 1, panel = D == 128 ? odd ^ ((tid >> 3) & 1) : 0, c = tid & 3;
+  const int row = (D == 128 ? (tid >> 4) : (tid >> 3)) * 2 + odd;
   uint4 w[TURNS];
 #pragma unroll
-  for (int k = 0; k < TURNS; ++k) w[k] = lds128(raw + (tid + k * T_CONV) * 16);
-  const int row = tid / PER, c = tid % PER, odd = c >> 2;
-  // the second panel starts with its odd chunk: no bank conflict
-  unsigned char *base = to + odd * 16384 + row * 128;
-  unsigned char *first = base + ((2 * (c & 3) + odd) ^ (row & 7)) * 16, *second = base + ((2 * (c & 3) + (odd ^ 1)) ^ (row & 7)) * 16;
+  for (int k = 0; k < TURNS; ++k) w[k] = lds128(raw + (row + k * STEP) * D + panel * 64 + c * 16);
+  unsigned char *base = to + panel * 16384 + row * 128;
+  unsigned char *first = base + ((2 * c) ^ (row & 7)) * 16, *second = base + ((2 * c + 1) ^ (row & 7)) * 16;
 #pragma unroll
   for (int k = 0; k < TURNS; ++k) {
     uint4 x[2];
     codes_to_f16<KIND, SAFE>(w[k], x[0], x[1]);
-    *reinterpret_cast<uint4 *>(first + k * (T_CONV / PER) * 128) = odd ? x[1] : x[0];
-    *reinterpret_cast<uint4 *>(second + k * (T_CONV / PER) * 128) = odd ? x[0] : x[1];
+    *reinterpret_cast<uint4 *>(first + k * STEP * 128) = x[0];
+    *reinterpret_cast<uint4 *>(second + k * STEP * 128) = x[1];
   }
 }
 
@@ -302,9 +314,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 8), mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < T_SCALES; ++i) mbar_init(&bar.sc_full[i], 1);
-    for (int i = 0; i < 8; ++i) mbar_init(&bar.pair[i], 2);
     mbar_init(&bar.q_full, T_SOFT / 32);
-    mbar_init(&bar.meet, T_SOFT / 32);
     fence_mbar_init();
   }
   if (warp == (T_SOFT + T_CONV) / 32) tmem_alloc(s_tmem, 512);
@@ -334,14 +344,16 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
     at.j = static_cast<int>(r);
   }
   const int count = static_cast<int>(my1 - my0);
+  // a wait that ran out: the role goes on without waiting, its loops end, and
+  // the call reports a timeout
+  bool lost = false;
   const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
-    return __all_sync(0xffffffffu, tile_wait(b, parity));
+    if (!lost && !__all_sync(0xffffffffu, tile_wait<40>(b, parity))) lost = true;
   };
   const auto arrive = [&](uint64_t *b) {  // once for the warp
     __syncwarp();
     if (lane == 0) mbar_arrive(b);
   };
-  bool ok = true;
 
   if (warp < T_SOFT / 32) {
     // ------------------------------------------------------------ softmax
@@ -350,19 +362,14 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
     const uint32_t tS = tmem + lanes + grp * 128 + 64 * half, tO = tmem + lanes + 256;
     float *xch = reinterpret_cast<float *>(smem + L::ML);
-    uint64_t *const pair = &bar.pair[warp & 7];  // this warp and the other half's of the same rows
     const float2 *scales = reinterpret_cast<const float2 *>(smem + L::SCALES);
     const float NINF = __uint_as_float(0xff800000u);
-    uint32_t meets = 0, uses = 0, pairs = 0;  // phases: meetings, tiles of this group, exchanges
-    const auto meet = [&]() {                 // all softmax threads
-      arrive(&bar.meet);
-      const bool good = wait(&bar.meet, meets & 1);
-      ++meets;
-      return good;
-    };
+    uint32_t uses = 0;                                       // tiles of this group
+    const auto meet = [&]() { named_sync(1, T_SOFT); };      // all softmax threads
+    const auto pair = [&]() { named_sync(2 + (warp & 7), 64); };  // this warp and the other half's of the same rows
     float *const mine = p.pieces + static_cast<long long>(blockIdx.x) * 2 * L::PIECE;
     int i = 0;
-    while (ok && i < count) {
+    while (i < count) {
       // ---- a segment: its queries
       const int rows = min(TQ, at.cnt * p.G - at.rt * TQ), row = at.rt * TQ + r, node = row / p.G;
       float fac;
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
         xch[quarter * 128 + r] = amax;
-        if (!(ok = meet())) break;
+        meet();
         amax = fmaxf(fmaxf(xch[r], xch[128 + r]), fmaxf(xch[256 + r], xch[384 + r]));
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
         // a negative scale turns the query around, so that scores only grow with the products
@@ -403,11 +410,14 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       float m = NINF, base = 0.f, l = 0.f, m0 = NINF, l0 = 0.f;
       const uint32_t uses0 = uses;
       const bool live = 32 * (warp & 3) < rows;  // this warp has rows to look after
-      for (int k = i + ((i ^ grp) & 1); k < end; k += 2, ++uses) {
+      const int k0 = i + ((i ^ grp) & 1);  // the group's first tile
+      if (!live && k0 < end) uses += (end - k0 + 1) / 2;
+      for (int k = k0; live && k < end; k += 2, ++uses) {
         const int tok0 = (s0 + k - i) * TK + 64 * half;
-        if (!(ok = wait(&bar.sc_full[k % T_SCALES], (k / T_SCALES) & 1) && wait(&bar.s_full[grp], uses & 1))) break;
+        wait(&bar.sc_full[k % T_SCALES], (k / T_SCALES) & 1);
+        wait(&bar.s_full[grp], uses & 1);
         tc_after_sync();
-        if (live) {
+        {
           const float2 *sc_at = scales + (k % T_SCALES) * 8 + 4 * half;
           const bool edge = tok0 + 64 > at.ctx;  // new tokens, or slots past the last one
           // the slots that the row sees, of 32 columns
@@ -459,9 +469,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           else maxima(Flag<false>{});
           // both halves go by the maximum of the whole tile
           xch[256 * grp + 128 * half + r] = top;
-          arrive(pair);
-          if (!(ok = wait(pair, pairs & 1))) break;
-          ++pairs;
+          pair();
           top = fmaxf(top, xch[256 * grp + 128 * (half ^ 1) + r]);
           // the offset moves only when a weight would pass 2^15
           if (__any_sync(0xffffffffu, top > m + (WEIGHT_UP + WEIGHT_SLACK))) {
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             l *= a;
             m = nm, base = nb;
             if (uses != uses0) {  // O holds the products of this segment's earlier tiles
-              if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
+              wait(&bar.o_done[grp], (uses - 1) & 1);
               tc_after_sync();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {  // each half takes half of the columns
@@ -532,22 +540,22 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         }
         tc_wait_st();
         tc_before_sync();
-        arrive(&bar.p_full[grp]);
+        __syncwarp();  // the first rows' warps arrive for those without rows, too
+        if (lane == 0) mbar_arrive_many(&bar.p_full[grp], (warp & 3) == 0 ? 4 - (rows - 1) / 32 : 1);
       }
-      if (!ok) break;
       // ---- the end of the segment: both groups' parts meet
       const bool has[2] = {end - i >= 2 || !(i & 1), end - i >= 2 || (i & 1)};  // the group had a tile
-      if (has[grp]) {
-        if (!(ok = wait(&bar.o_done[grp], (uses - 1) & 1))) break;
+      if (live && has[grp]) {
+        wait(&bar.o_done[grp], (uses - 1) & 1);
         tc_after_sync();
       }
       tc_before_sync();
-      if (!(ok = meet())) break;
+      meet();
       tc_after_sync();
       // all products with the queries are done: their place takes the sums
       float4 *sums = reinterpret_cast<float4 *>(smem + L::Q);
       sums[quarter * 128 + r] = make_float4(m, l, m0, l0);
-      if (!(ok = meet())) break;
+      meet();
       float M = NINF, mg[2];
       float4 each[4];
 #pragma unroll
@@ -568,6 +576,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const long long orow = (static_cast<long long>(at.b) * p.N + node) * (c.Hk * p.G) + at.h * p.G + row % p.G;
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {  // a quarter of the columns each
+        if (!live) break;
         const int col = quarter * (D / 4) + 16 * q;
         uint32_t x[16], y[16];
         float z[16];
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         }
       }
       if (!whole) __threadfence();
-      if (!(ok = meet())) break;  // the accumulators are free
+      meet();  // the accumulators are free
       if (!whole) {
         // a segment that several CTAs share: the last to arrive merges, in order
         const long long f0 = my0 + i - s0, f1 = f0 + at.n - 1;
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           *s_last = atomicAdd(p.done + c0, 1) == n - 1;
           __threadfence();
         }
-        if (!(ok = meet())) break;
+        meet();
         if (*s_last) {
           __threadfence();
           if (r < rows) {
@@ -655,7 +664,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           }
           if (tid == 0) p.done[c0] = 0;  // zero again for the next call
         }
-        if (!(ok = meet())) break;  // s_last may be written again
+        meet();  // s_last may be written again
       }
       i = end;
       if (i < count) tile_next(p, at);
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
     const int ct = tid - T_SOFT;
     int left = at.n - at.j;  // tiles of the segment from here on
     TileCursor u = at;
-    for (int i = 0; ok && i < count; ++i) {
+    for (int i = 0; i < count; ++i) {
       if (left == 0) tile_next(p, u), left = u.n;
       const int j = u.n - left;
       --left;
@@ -675,7 +684,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = (2 * i + t) % T_RAW;
-        if (!(ok = wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1) && wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1))) break;
+        wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1);
+        wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1);
         const unsigned char *raw = smem + L::RAW + slot * L::RAWB;
         unsigned char *to = smem + (t ? L::V : L::K) + buf * L::OP;
         if (safe) convert_tile<D, KIND, false>(raw, to, ct);
@@ -696,10 +706,13 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       TileCursor u = at;
       int left = at.n - at.j, segs = 0, seg0 = 0, pv = 0;  // pv: the next tile whose second product is due
       int pv_first = 0;                                    // first tile of pv's segment
+      const auto one = [&](uint64_t *b, uint32_t parity) {
+        if (!lost && !tile_wait<20>(b, parity)) lost = true;
+      };
       const auto second = [&]() {
         const uint32_t g = pv & 1, ph = (pv >> 1) & 1;
-        ok = tile_wait(&bar.p_full[g], ph) && tile_wait(&bar.v_full[g], ph);
-        if (!ok) return;
+        one(&bar.v_full[g], ph);
+        one(&bar.p_full[g], ph);
         tc_after_sync();
 #pragma unroll
         for (int k = 0; k < TK / 16; ++k)
@@ -709,21 +722,19 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         tc_commit(&bar.o_done[g]);
         ++pv;
       };
-      for (int i = 0; ok && i < count; ++i) {
+      for (int i = 0; i < count; ++i) {
         if (left == 0) {
           tile_next(p, u), left = u.n;
-          while (ok && pv < i) second();  // the queries change when the segment is done
+          while (pv < i) second();  // the queries change when the segment is done
           seg0 = i;
           ++segs;
           pv_first = i;
         } else if (i - pv == 2) {
           second();
         }
-        if (!ok) break;
         const uint32_t g = i & 1, ph = (i >> 1) & 1;
-        if (i == seg0) ok = tile_wait(&bar.q_full, segs & 1);
-        ok = ok && tile_wait(&bar.k_full[g], ph);
-        if (!ok) break;
+        if (i == seg0) one(&bar.q_full, segs & 1);
+        one(&bar.k_full[g], ph);
         tc_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -733,7 +744,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         tc_commit(&bar.s_full[g]);
         --left;
       }
-      while (ok && pv < count) second();
+      while (pv < count) second();
     }
     } else if (warp == (T_SOFT + T_CONV) / 32 + 1) {
     // -------------------------------------------------------------- copies
@@ -745,7 +756,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       return tok < v.ctx + v.cnt ? c.table[static_cast<long long>(v.b) * c.per + (tok >> c.log_page)] : 0;
     };
     int page = page_id(u, u.j);
-    for (int i = 0; ok && i < count; ++i) {
+    for (int i = 0; i < count; ++i) {
       const int j = u.n - left, tok = j * TK + 16 * (lane & 7), len = u.ctx + u.cnt;
       const bool there = lane < 8 && tok < len, bad = there && static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages);
       const long long id = static_cast<long long>(bad ? 0 : page) * c.Hk + u.h;
@@ -764,7 +775,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = (2 * i + t) % T_RAW;
-        if (!(ok = wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1))) break;
+        wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1);
+        if (lost) break;  // no copy into a slot that may be in use
         if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], bytes * pages);
         __syncwarp();
         if (lead)
@@ -774,7 +786,6 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
                        : "memory");
         issued = 2 * i + t + 1;
       }
-      if (!ok) break;
       if (lane < 8) {
         const float lv = bad ? __uint_as_float(0x7fc00000u) : vs <= LEAST_V_SCALE ? __uint_as_float(0xff800000u) : lg2(vs);
         reinterpret_cast<float2 *>(smem + L::SCALES)[(i % T_SCALES) * 8 + lane] = make_float2(bad ? __uint_as_float(0x7fc00000u) : ks, lv);
@@ -784,10 +795,11 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       page = next;
     }
     // no copy outlives the CTA, even after a wait that ran out
+    lost = false;
     for (int k = max(0, issued - T_RAW); k < issued; ++k) wait(&bar.raw_full[k % T_RAW], (k / T_RAW) & 1);
     }
   }
-  if (!ok) atomicOr(p.status, ST_TIMEOUT);
+  if (lost) atomicOr(p.status, ST_TIMEOUT);
   tc_before_sync();
   __syncthreads();
   if (warp == (T_SOFT + T_CONV) / 32) {
