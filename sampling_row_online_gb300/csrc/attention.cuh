@@ -6,12 +6,12 @@
 //
 // with codes ck, cv and one scale sk, sv per (page, kv head).  In base 2 and
 // with x = s log2e + log2(sv) the weights are w = 2^(x - m), m 13 below a
-// running maximum of x that is at most 2 behind, and
+// running maximum of x that is at most 2.9 behind, and
 //
 //   out = sum_j w_j cv_j / sum_j w_j / sv_j:
 //
 // the value's scale rides in the exponent, so the largest weight that meets
-// the codes lies in [2^13, 2^15] whatever the scales are (fp16 keeps its full
+// the codes lies in [2^13, 2^15.9] whatever the scales are (fp16 keeps its full
 // precision down to 2^-27 of it), and both scales cost nothing more than the
 // multiply-add that every score needs anyway.  Codes of both kinds
 // are exact in fp16 (e4m3 as code * 2^-8, by moving bits; int8 by an offset),
@@ -51,7 +51,7 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-constexpr float WEIGHT_UP = 13.f, WEIGHT_SLACK = 2.f;  // the largest weight is 2^13 to 2^15
+constexpr float WEIGHT_UP = 13.f, WEIGHT_SLACK = 2.9f;  // the largest weight is 2^13 to 2^15.9
 constexpr float LEAST_V_SCALE = 7.888609052210118e-31f;  // 2^-100: below it a block counts as zero
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
           ++at.step;
           continue;
         }
-        // the offset moves only when a weight would pass 2^15
+        // the offset moves only when a weight would pass 2^15.9
         bool up = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

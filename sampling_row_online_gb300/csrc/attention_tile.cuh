@@ -104,7 +104,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 //
 //   copy warp    pages -> raw ring (bulk copies of 8-bit codes), scales -> ring
 //   conversion   raw codes -> fp16 tiles in the swizzled operand layout
-//   product warp S = Q K^T, O += P V (P in tensor memory, over S)
+//   products     S = Q K^T, O += P V (P in tensor memory, over S)
 //   softmax      two threads per row, half of the tokens each: S -> P, lazy
 //                rescaling of O, the output
 //
@@ -112,8 +112,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // e4m3 queries and weights would cost the precision that the cache has.
 constexpr int TQ = 128, TK = 128;    // rows, tokens of a tile
 constexpr int T_SOFT = 512;          // softmax threads: two groups, two threads per row
-constexpr int T_CONV = 256;          // conversion threads
-constexpr int T_NT = T_SOFT + T_CONV + 128;  // and a warp each for products and copies, and two idle ones
+constexpr int T_CONV = 256;          // conversion threads: half for keys, half for values, so that neither waits for the other's buffer
+constexpr int T_NT = T_SOFT + T_CONV + 128;  // and a warp for each group's products, one for copies, an idle one
 // Registers: 72 a thread at launch, then 88 for the softmax, 56 for the
 // conversion and 40 for the rest: 512 * 88 + 256 * 56 + 128 * 40 = 896 * 72.
 constexpr int T_REG = 72, T_REG_SOFT = 88, T_REG_CONV = 56, T_REG_REST = 40;
@@ -130,7 +130,7 @@ __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
   for (int polls = 0; polls < 1 << 20; ++polls) {
     if (mbar_try_wait(bar, parity)) return true;
-    __nanosleep(REST);
+    if (REST) __nanosleep(REST);
   }
   return false;
 }
@@ -160,6 +160,10 @@ struct TileBars {
 };
 static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
 
+template <int V>
+struct Number {
+  static constexpr int value = V;
+};
 template <bool V>
 struct Flag {
   static constexpr bool value = V;
@@ -226,24 +230,28 @@ __device__ __forceinline__ void codes_to_f16(uint4 w, uint4 &lo, uint4 &hi) {
 // A raw tile [128][D] into panels of 64 columns of 128-byte swizzled rows.
 template <int D, int KIND, bool SAFE>
 __device__ __forceinline__ void convert_tile(const unsigned char *raw, unsigned char *to, int tid) {
-  constexpr int PER = D / 16, TURNS = 128 * PER / T_CONV, STEP = T_CONV / PER;  // rows per turn
-  static_assert(STEP % 8 == 0, "a thread's rows are equal modulo 8");
+  constexpr int PER = D / 16, STEP = T_CONV / 2 / PER, BATCH = 4;  // rows per turn, turns loaded at once
+  static_assert(STEP % 8 == 0 && 128 % (STEP * BATCH) == 0, "a thread's rows are equal modulo 8");
   // eight neighbouring lanes take four 16-byte pieces of an even row and four
   // of the odd row after it, in the other half where a row has two: their
   // loads and their stores touch every bank once
   const int odd = (tid >> 2) & 1, panel = D == 128 ? odd ^ ((tid >> 3) & 1) : 0, c = tid & 3;
   const int row = (D == 128 ? (tid >> 4) : (tid >> 3)) * 2 + odd;
-  uint4 w[TURNS];
-#pragma unroll
-  for (int k = 0; k < TURNS; ++k) w[k] = lds128(raw + (row + k * STEP) * D + panel * 64 + c * 16);
+  const unsigned char *from = raw + row * D + panel * 64 + c * 16;
   unsigned char *base = to + panel * 16384 + row * 128;
   unsigned char *first = base + ((2 * c) ^ (row & 7)) * 16, *second = base + ((2 * c + 1) ^ (row & 7)) * 16;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 128; k0 += STEP * BATCH) {
+    uint4 w[BATCH];
 #pragma unroll
-  for (int k = 0; k < TURNS; ++k) {
-    uint4 x[2];
-    codes_to_f16<KIND, SAFE>(w[k], x[0], x[1]);
-    *reinterpret_cast<uint4 *>(first + k * STEP * 128) = x[0];
-    *reinterpret_cast<uint4 *>(second + k * STEP * 128) = x[1];
+    for (int k = 0; k < BATCH; ++k) w[k] = lds128(from + (k0 + k * STEP) * D);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      uint4 x[2];
+      codes_to_f16<KIND, SAFE>(w[k], x[0], x[1]);
+      *reinterpret_cast<uint4 *>(first + (k0 + k * STEP) * 128) = x[0];
+      *reinterpret_cast<uint4 *>(second + (k0 + k * STEP) * 128) = x[1];
+    }
   }
 }
 
@@ -307,10 +315,10 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   fill_rest<DT, T_NT>(p, D);
   if (my1 <= my0) return;
   if (tid == 0) {
-    for (int i = 0; i < T_RAW; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], T_CONV / 32);
+    for (int i = 0; i < T_RAW; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], T_CONV / 64);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], T_CONV / 32), mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.v_full[i], T_CONV / 32), mbar_init(&bar.v_empty[i], 1);
+      mbar_init(&bar.k_full[i], T_CONV / 64), mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], T_CONV / 64), mbar_init(&bar.v_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 8), mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < T_SCALES; ++i) mbar_init(&bar.sc_full[i], 1);
@@ -347,9 +355,12 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   // a wait that ran out: the role goes on without waiting, its loops end, and
   // the call reports a timeout
   bool lost = false;
-  const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
-    if (!lost && !__all_sync(0xffffffffu, tile_wait<40>(b, parity))) lost = true;
+  const auto rest_wait = [&](auto rest, uint64_t *b, uint32_t parity) {  // warp-wide
+    constexpr int REST = decltype(rest)::value;
+    if (!lost && !__all_sync(0xffffffffu, tile_wait<REST>(b, parity))) lost = true;
   };
+  const auto wait = [&](uint64_t *b, uint32_t parity) { rest_wait(Number<0>{}, b, parity); };
+  const auto lazy_wait = [&](uint64_t *b, uint32_t parity) { rest_wait(Number<40>{}, b, parity); };  // where latency hides
   const auto arrive = [&](uint64_t *b) {  // once for the warp
     __syncwarp();
     if (lane == 0) mbar_arrive(b);
@@ -407,6 +418,11 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         arrive(&bar.q_full);
       }
       const int s0 = at.j, end = min(at.n - at.j, count - i) + i;
+      // A tile is weighed again, and the accumulator scaled, when the offset
+      // moves.  Over a long axis the largest weight starts at 2^8: fp16 then
+      // keeps its full precision down to 2^-22 of it, and the offset moves once
+      // or twice; at 2^13 some row of the tile's 128 moved it in half of the tiles.
+      const float up = at.n >= 8 ? 8.f : WEIGHT_UP;
       float m = NINF, base = 0.f, l = 0.f, m0 = NINF, l0 = 0.f;
       const uint32_t uses0 = uses;
       const bool live = 32 * (warp & 3) < rows;  // this warp has rows to look after
@@ -433,110 +449,103 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             }
             return bits & low(at.cnt - n0);
           };
-          // the tile's maximum, per group of 16 tokens that share their scales
-          float top = NINF, top0 = NINF;
-          const auto maxima = [&](auto at_edge) {
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            uint32_t s[2][16];
-            tmem_ld16(tS + 32 * q, s[0]);
-            tmem_ld16(tS + 32 * q + 16, s[1]);
-            tc_wait_ld(s[0]);
-            tc_wait_ld(s[1]);
-            if constexpr (decltype(at_edge)::value) {
-              const uint32_t bits = seen32(q);
+          // weights under the offset so far, and their largest exponent
+          uint32_t pk[32];
+          float sum = 0.f, hi = NINF;
+          bool any_zero = false;
+          const auto weights = [&](auto at_edge) {
+            sum = 0.f, hi = NINF;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((bits >> e) & 1)) s[e >> 4][e & 15] = 0xff800000u;
-            }
+            for (int q = 0; q < 2; ++q) {
+              uint32_t s[2][16];
+              tmem_ld16(tS + 32 * q, s[0]);
+              tmem_ld16(tS + 32 * q + 16, s[1]);
+              tc_wait_ld(s[0]);
+              tc_wait_ld(s[1]);
+              if constexpr (decltype(at_edge)::value) {
+                const uint32_t bits = seen32(q);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float t0 = NINF, t1 = NINF;
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                t0 = fmaxf(fmaxf(t0, __uint_as_float(s[hf][e])), __uint_as_float(s[hf][e + 1]));
-                t1 = fmaxf(fmaxf(t1, __uint_as_float(s[hf][e + 2])), __uint_as_float(s[hf][e + 3]));
+                for (int e = 0; e < 32; ++e)
+                  if (!((bits >> e) & 1)) s[e >> 4][e & 15] = 0xff800000u;
               }
-              const float2 sc = sc_at[2 * q + hf];
-              const float t = fmaxf(t0, t1);
-              // a factor of 0 (no keys, no scale) leaves 0, also of nothing seen
-              if (sc.y == NINF) top0 = fmaxf(top0, t == NINF ? NINF : t * (fac * sc.x));
-              else top = fmaxf(top, t == NINF ? NINF : fmaf(t, fac * sc.x, sc.y));
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {  // 16 tokens that share their scales
+                const float2 sc = sc_at[2 * q + hf];
+                const bool zero = sc.y == NINF;  // a block without values: every exponent becomes -inf
+                any_zero |= zero;
+                // a factor of 0 (no keys, no scale) must leave what is not seen at -inf
+                const float f = fmaxf(fac * sc.x, 1e-37f), off = sc.y - base;
+                float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  float2 x = fma2(make_float2(__uint_as_float(s[hf][e]), __uint_as_float(s[hf][e + 1])), make_float2(f, f), make_float2(off, off));
+                  hi = fmaxf(fmaxf(hi, x.x), x.y);
+                  x.x = ex2(x.x), x.y = ex2(x.y);
+                  part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
+                  pk[16 * q + 8 * hf + e / 2] = f32_to_f16x2(x.x, x.y);
+                }
+                const float2 both = add2(part[0], part[1]);
+                if (!zero) sum = fmaf(both.x + both.y, ex2(-sc.y), sum);
+              }
             }
-          }
           };
-          if (edge) maxima(Flag<true>{});
-          else maxima(Flag<false>{});
-          // both halves go by the maximum of the whole tile
-          xch[256 * grp + 128 * half + r] = top;
+          if (edge) weights(Flag<true>{});
+          else weights(Flag<false>{});
+          // both halves go by the whole tile's maximum
+          float *xmine = xch + 256 * grp + 128 * half + r, *xother = xch + 256 * grp + 128 * (half ^ 1) + r;
+          *xmine = hi + base;
           pair();
-          top = fmaxf(top, xch[256 * grp + 128 * (half ^ 1) + r]);
-          // the offset moves only when a weight would pass 2^15
+          const float top = fmaxf(hi + base, *xother);
           if (__any_sync(0xffffffffu, top > m + (WEIGHT_UP + WEIGHT_SLACK))) {
-            const float nm = fmaxf(m, top - WEIGHT_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
+            // the offset moves, and the tile is weighed again
+            const float nm = fmaxf(m, top - up), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
             l *= a;
             m = nm, base = nb;
             if (uses != uses0) {  // O holds the products of this segment's earlier tiles
               wait(&bar.o_done[grp], (uses - 1) & 1);
               tc_after_sync();
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {  // each half takes half of the columns
-                const uint32_t col = tO + grp * 128 + half * (D / 2) + 16 * q;
-                uint32_t o[16];
-                tmem_ld16(col, o);
-                tc_wait_ld(o);
+              for (int q = 0; q < D / 64; ++q) {  // each half takes half of the columns
+                const uint32_t col = tO + grp * 128 + half * (D / 2) + 32 * q;
+                uint32_t o[2][16];
+                tmem_ld16(col, o[0]);
+                tmem_ld16(col + 16, o[1]);
+                tc_wait_ld(o[0]);
+                tc_wait_ld(o[1]);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                tmem_st16(col, o);
+                for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = __float_as_uint(__uint_as_float(o[e >> 4][e & 15]) * a);
+                tmem_st16(col, o[0]);
+                tmem_st16(col + 16, o[1]);
               }
             }
+            if (edge) weights(Flag<true>{});
+            else weights(Flag<false>{});
           }
-          if (__any_sync(0xffffffffu, top0 > m0)) {  // blocks without values count in a sum of their own
-            const float nm0 = fmaxf(m0, top0);
-            l0 *= ex2(m0 - (nm0 == NINF ? 0.f : nm0));
-            m0 = nm0;
-          }
-          const auto weights = [&](auto at_edge) {
+          if (any_zero) {  // blocks without values count in a sum of their own
 #pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            uint32_t s[2][16], pk[16];
-            tmem_ld16(tS + 32 * q, s[0]);
-            tmem_ld16(tS + 32 * q + 16, s[1]);
-            tc_wait_ld(s[0]);
-            tc_wait_ld(s[1]);
-            uint32_t bits = ~0u;
-            if constexpr (decltype(at_edge)::value) bits = seen32(q);
+            for (int q = 0; q < 4; ++q) {
+              if (sc_at[q].y != NINF) continue;
+              const float f = fmaxf(fac * sc_at[q].x, 1e-37f);
+              const uint32_t bits = edge ? seen32(q >> 1) >> (16 * (q & 1)) : ~0u;
+              uint32_t s[16];
+              tmem_ld16(tS + 16 * q, s);
+              tc_wait_ld(s);
+              float t = m0;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const float2 sc = sc_at[2 * q + hf];
-              const bool zero = sc.y == NINF;
-              const float f = fac * sc.x, off = zero ? (m0 == NINF ? 0.f : -m0) : sc.y - base;
-              float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float2 x = fma2(make_float2(__uint_as_float(s[hf][e]), __uint_as_float(s[hf][e + 1])), make_float2(f, f), make_float2(off, off));
-                x.x = ex2(x.x), x.y = ex2(x.y);
-                if constexpr (decltype(at_edge)::value) {
-                  if (!((bits >> (16 * hf + e)) & 1)) x.x = 0.f;
-                  if (!((bits >> (16 * hf + e + 1)) & 1)) x.y = 0.f;
-                }
-                part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
-                pk[8 * hf + e / 2] = f32_to_f16x2(x.x, x.y);
+              for (int e = 0; e < 16; ++e) {
+                if (!((bits >> e) & 1)) s[e] = 0xff800000u;
+                t = fmaxf(t, __uint_as_float(s[e]) * f);
               }
-              const float2 sum = add2(part[0], part[1]);
-              if (zero) {
-                l0 += sum.x + sum.y;
+              const float nb = t == NINF ? 0.f : t;
+              l0 *= ex2(m0 - nb);
+              m0 = t;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) pk[8 * hf + e] = 0u;
-              } else {
-                l = fmaf(sum.x + sum.y, ex2(-sc.y), l);
-              }
+              for (int e = 0; e < 16; ++e) l0 += ex2(__uint_as_float(s[e]) * f - nb);
             }
-            tmem_st16(tS + 16 * q, pk);  // weights over scores that have been read
           }
-          };
-          if (edge) weights(Flag<true>{});
-          else weights(Flag<false>{});
+          l += sum;
+          tmem_st16(tS, pk);  // weights over scores that have been read
+          tmem_st16(tS + 16, pk + 16);
         }
         tc_wait_st();
         tc_before_sync();
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   } else if (warp < (T_SOFT + T_CONV) / 32) {
     // --------------------------------------------------------- conversion
     fewer_registers<T_REG_CONV>();
-    const int ct = tid - T_SOFT;
+    const int ct = (tid - T_SOFT) % (T_CONV / 2), t = (tid - T_SOFT) / (T_CONV / 2);  // keys or values
     int left = at.n - at.j;  // tiles of the segment from here on
     TileCursor u = at;
     for (int i = 0; i < count; ++i) {
@@ -681,72 +690,61 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       --left;
       const bool safe = (j + 1) * TK <= u.ctx + u.cnt;  // every row of the tile has been written
       const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        const int slot = (2 * i + t) % T_RAW;
-        wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1);
-        wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1);
-        const unsigned char *raw = smem + L::RAW + slot * L::RAWB;
-        unsigned char *to = smem + (t ? L::V : L::K) + buf * L::OP;
-        if (safe) convert_tile<D, KIND, false>(raw, to, ct);
-        else convert_tile<D, KIND, true>(raw, to, ct);
-        fence_async_smem();
-        arrive(t ? &bar.v_full[buf] : &bar.k_full[buf]);
-        if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
-      }
+      const int slot = (2 * i + t) % T_RAW;
+      lazy_wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1);
+      lazy_wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1);
+      const unsigned char *raw = smem + L::RAW + slot * L::RAWB;
+      unsigned char *to = smem + (t ? L::V : L::K) + buf * L::OP;
+      if (safe) convert_tile<D, KIND, false>(raw, to, ct);
+      else convert_tile<D, KIND, true>(raw, to, ct);
+      fence_async_smem();
+      arrive(t ? &bar.v_full[buf] : &bar.k_full[buf]);
+      if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
     }
   } else {
     fewer_registers<T_REG_REST>();
-    if (warp == (T_SOFT + T_CONV) / 32) {
+    const int extra = warp - (T_SOFT + T_CONV) / 32;
+    if (extra == 0 || extra == 2) {
     // ----------------------------------------------------------- products
+    // A warp for each group: the issue of one group's products and the waits
+    // around it hide behind the other group's.
     if (lane == 0) {
       constexpr uint32_t ID_S = 1u << 4 | (TK / 8) << 17 | (TQ / 16) << 24;           // fp16 x fp16 -> fp32
       constexpr uint32_t ID_O = 1u << 4 | 1u << 16 | (D / 8) << 17 | (TQ / 16) << 24;  // values run along the tokens
-      const uint32_t base = smem_u32(smem);
-      TileCursor u = at;
-      int left = at.n - at.j, segs = 0, seg0 = 0, pv = 0;  // pv: the next tile whose second product is due
-      int pv_first = 0;                                    // first tile of pv's segment
+      const int g = extra >> 1;
+      const uint32_t base = smem_u32(smem), tS = tmem + g * 128, tO = tmem + 256 + g * 128;
+      const uint64_t dQ = tc_desc(base + L::Q, 0), dK = tc_desc(base + L::K + g * L::OP, 0), dV = tc_desc(base + L::V + g * L::OP, 16384);
       const auto one = [&](uint64_t *b, uint32_t parity) {
-        if (!lost && !tile_wait<20>(b, parity)) lost = true;
+        if (!lost && !tile_wait<0>(b, parity)) lost = true;
       };
-      const auto second = [&]() {
-        const uint32_t g = pv & 1, ph = (pv >> 1) & 1;
-        one(&bar.v_full[g], ph);
-        one(&bar.p_full[g], ph);
-        tc_after_sync();
+      TileCursor u = at;
+      int i = g;  // this group's next tile
+      uint32_t ph = 0;
+      for (int seg0 = 0, seg1 = at.n - at.j, segs = 0;; tile_next(p, u), seg0 = seg1, seg1 += u.n, ++segs) {
+        one(&bar.q_full, segs & 1);
+        for (const int end = min(seg1, count), first = i; i < end; i += 2, ph ^= 1) {
+          one(&bar.k_full[g], ph);
+          tc_after_sync();
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
-          tc_mma_ts(tmem + 256 + g * 128, tmem + g * 128 + 64 * (k >> 2) + 8 * (k & 3), tc_desc(base + L::V + g * L::OP + k * 2048, 16384), ID_O,
-                    k > 0 || pv - pv_first >= 2);
-        tc_commit(&bar.v_empty[g]);
-        tc_commit(&bar.o_done[g]);
-        ++pv;
-      };
-      for (int i = 0; i < count; ++i) {
-        if (left == 0) {
-          tile_next(p, u), left = u.n;
-          while (pv < i) second();  // the queries change when the segment is done
-          seg0 = i;
-          ++segs;
-          pv_first = i;
-        } else if (i - pv == 2) {
-          second();
+          for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
+            const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            tc_mma_ss(tS, dQ + off, dK + off, ID_S, k > 0);
+          }
+          tc_commit(&bar.s_full[g]);
+          tc_commit(&bar.k_empty[g]);
+          one(&bar.v_full[g], ph);
+          one(&bar.p_full[g], ph);
+          tc_after_sync();
+#pragma unroll
+          for (int k = 0; k < TK / 16; ++k)  // 16 tokens at a time
+            tc_mma_ts(tO, tS + 64 * (k >> 2) + 8 * (k & 3), dV + (k * 2048 >> 4), ID_O, k > 0 || i != first);
+          tc_commit(&bar.o_done[g]);
+          tc_commit(&bar.v_empty[g]);
         }
-        const uint32_t g = i & 1, ph = (i >> 1) & 1;
-        if (i == seg0) one(&bar.q_full, segs & 1);
-        one(&bar.k_full[g], ph);
-        tc_after_sync();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_ss(tmem + g * 128, tc_desc(base + L::Q + (k >> 2) * 16384 + (k & 3) * 32, 0),
-                    tc_desc(base + L::K + g * L::OP + (k >> 2) * 16384 + (k & 3) * 32, 0), ID_S, k > 0);
-        tc_commit(&bar.k_empty[g]);
-        tc_commit(&bar.s_full[g]);
-        --left;
+        if (seg1 >= count) break;
       }
-      while (pv < count) second();
     }
-    } else if (warp == (T_SOFT + T_CONV) / 32 + 1) {
+    } else if (extra == 1) {
     // -------------------------------------------------------------- copies
     TileCursor u = at;
     int left = at.n - at.j, issued = 0;
@@ -775,7 +773,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = (2 * i + t) % T_RAW;
-        wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1);
+        lazy_wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1);
         if (lost) break;  // no copy into a slot that may be in use
         if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], bytes * pages);
         __syncwarp();
