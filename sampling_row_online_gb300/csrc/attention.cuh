@@ -63,25 +63,40 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 // (sign to the sign, the seven other bits to the top of exponent and mantissa;
 // subnormals stay exact), the lower bytes do not matter.
 __device__ __forceinline__ uint32_t e4m3_halves(uint32_t x) { return ((x >> 1) & 0x3f803f80u) | (x & 0x80008000u); }
-// int8 codes plus 128, each in the lower byte of a half, as fp16:
-// 0x6400 | u is 1024 + u.
-__device__ __forceinline__ uint32_t i8_halves(uint32_t x) {
-  const uint32_t u = (x & 0x00ff00ffu) | 0x64006400u;
+// int8 codes plus 128 in halves 0x6400 | u, which are 1024 + u, as fp16.
+__device__ __forceinline__ uint32_t i8_halves(uint32_t u) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));  // 1152
   return r;
 }
-// Codes j and j + 1 of the word w (j = 0 or 2).
-template <int KIND, int J>
-__device__ __forceinline__ uint32_t pair_of(uint32_t w) {
-  if (KIND == KIND_E4M3) return e4m3_halves(prmt(w, 0, J == 0 ? 0x1404 : 0x3424));
-  return i8_halves(prmt(w, 0, J == 0 ? 0x4140 : 0x4342));  // w: codes + 128 already
+// The two codes in the lower and in the upper half of a word as fp16 (int8:
+// plus 128 already, each in the lower byte of its half; e4m3: in the halves'
+// bytes).
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-// Code j of words a and b.
+// Codes 0, 1 and 2, 3 of a word (int8: plus 128).
 template <int KIND>
-__device__ __forceinline__ uint32_t pair_across(uint32_t a, uint32_t b, int j) {
-  if (KIND == KIND_E4M3) return e4m3_halves(prmt(a, b, 0x4400 + 0x1111 * j));
-  return i8_halves(prmt(a, b, 0x0400 + 0x1111 * j));
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (KIND == KIND_E4M3) {
+    e4m3_pairs(w, lo, hi);
+  } else {
+    lo = i8_halves(prmt(w, 0x64646464u, 0x4140));
+    hi = i8_halves(prmt(w, 0x64646464u, 0x4342));
+  }
+}
+// Codes j and j + 1 (j = 0 or 2) of the words a and b: (a_j, b_j) and
+// (a_j+1, b_j+1).
+template <int KIND, int J>
+__device__ __forceinline__ void pairs_across(uint32_t a, uint32_t b, uint32_t &lo, uint32_t &hi) {
+  if (KIND == KIND_E4M3) {
+    e4m3_pairs(prmt(a, b, J == 0 ? 0x5140 : 0x7362), lo, hi);
+  } else {
+    lo = i8_halves((prmt(a, b, J == 0 ? 0x0400 : 0x0602) & 0x00ff00ffu) | 0x64006400u);
+    hi = i8_halves((prmt(a, b, J == 0 ? 0x0501 : 0x0703) & 0x00ff00ffu) | 0x64006400u);
+  }
 }
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).
@@ -139,39 +154,49 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // ======================================================================
 // Few rows per kv head: each warp streams its own tokens.
 // ======================================================================
-// The work is the list of all (sequence, kv head, tile of 16 rows, step of 16
-// tokens), in that order, and every warp of the grid takes an equal stretch of
-// it, so ragged lengths need no schedule.  A warp copies the steps ahead into
-// a ring with cp.async; every lane reads back only what it copied itself, so
-// the loop has no barrier at all.  The m16n8k16 fragments allow any order of
-// the contracted index: a lane's 16 bytes of a key row serve four k-steps, and
-// its 16 bytes of each of four value rows serve 16 column tiles, so nothing is
-// exchanged and nothing is transposed; the weights go from the accumulators of
-// the first product to the operand of the second in registers.
+// The work is the list of all (sequence, kv head, step of 16 tokens), in that
+// order, and every warp of the grid takes an equal stretch of it, so ragged
+// lengths need no schedule.  A warp copies the steps ahead into a ring with
+// cp.async; every lane reads back only what it copied itself, so the loop has
+// no barrier at all.  The m16n8k16 fragments allow any order of the contracted
+// index: a lane's 16 bytes of a key row serve four k-steps, and its 16 bytes
+// of each of four value rows serve 16 column tiles, so nothing is exchanged
+// and nothing is transposed; the weights go from the accumulators of the first
+// product to the operand of the second in registers.  RT tiles of 16 rows
+// share the converted codes.
 //
-// A stretch that ends inside a segment (a row tile of a kv head) leaves a
-// piece (m, l, out); the CTA merges the pieces of its warps, and the last CTA
+// A stretch that ends inside a segment (the rows of a kv head) leaves a piece
+// (out, offset, sum); the CTA merges the pieces of its warps, and the last CTA
 // to arrive at a segment merges those of its CTAs in index order.
-constexpr int AW = 12;           // warps
+constexpr int AW = 8;            // warps
 constexpr int ANT = 32 * AW;
-constexpr int ASTAGES = 2;       // steps in flight per warp
+constexpr int ASTAGES = 4;       // steps in flight per warp
 constexpr int ASTEP = 16;        // tokens per step
+constexpr int ALEAST = 4;        // steps per warp at least, before more CTAs take part
 
-template <int D>
+template <int D, int RT>
 struct StreamLayout {
+  static constexpr int SUB = RT == 1 ? 2 : 1;                    // steps per turn of the loop
   static constexpr int KB = ASTEP * D, STAGE = 2 * KB + 256;     // codes of keys and values, scales
-  static constexpr int PIECE = (16 * D + 32) * 4;                // out, m, l
+  static constexpr int ROWS = 16 * RT;
+  static constexpr int PIECE = ROWS * D + 2 * ROWS;              // floats: out, offset, sum
   static constexpr int RING = AW * ASTAGES * STAGE;
-  static constexpr int SMEM = RING + AW * PIECE + 64;
-  static_assert(PIECE <= ASTAGES * STAGE, "a warp's last piece lies in its own ring");
+  // one tile of rows: its queries stay in registers, and the first pieces of
+  // the warps in shared memory; with two the queries take that room, and the
+  // first pieces go through the workspace
+  static constexpr int QBYTES = RT == 1 ? 0 : RT * (D / 16) * 512;  // fragments per warp
+  static constexpr int SMEM = RING + AW * (RT == 1 ? PIECE * 4 : QBYTES);
+  static constexpr int SHARED = 2 * PIECE;                       // floats per CTA that other CTAs read
+  static constexpr int WORK = SHARED + (RT == 1 ? 0 : AW * PIECE);
+  static_assert(PIECE * 4 <= ASTAGES * STAGE, "a warp's last piece lies in its own ring");
 };
 
-struct Segment {  // a row tile of a kv head, and the part of it that a piece covers
+struct Segment {  // the rows of a kv head, and the part of their steps that a piece covers
   long long at;   // first step in the list of all work
-  int b, h, tile, steps, s0, s1, ctx, cnt;
+  int b, h, steps, s0, s1, ctx, cnt;
 };
 
-// Writes one quarter row: 4 columns from `d` of row r.
+// Writes 4 columns from `d` of row r.
 template <int DT>
 __device__ __forceinline__ void put4(const AttnParams &p, const Segment &g, int D, int r, int d, float4 x) {
   const long long row = (static_cast<long long>(g.b) * p.N + r / p.G) * (p.c.Hk * p.G) + g.h * p.G + r % p.G;
@@ -186,11 +211,11 @@ __device__ __forceinline__ void put_lse(const AttnParams &p, const Segment &g, i
   p.lse[row] = l == 0.f ? __uint_as_float(0xff800000u) : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int KIND, int DT>
+template <int D, int KIND, int DT, int RT>
 __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_constant__ AttnParams p) {
-  using L = StreamLayout<D>;
-  constexpr int CH = D / 64, NT8 = D / 8;                // 16-byte chunks of a key row per lane; column tiles
-  constexpr float VFIX = KIND == KIND_E4M3 ? 256.f : 1.f;  // fp16 codes are value / VFIX
+  using L = StreamLayout<D, RT>;
+  constexpr int CH = D / 64, NT8 = D / 8, SUB = L::SUB;  // 16-byte chunks of a key row per lane; column tiles
+  const float NINF = __uint_as_float(0xff800000u);
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Segment s_seg[2 * AW];
   __shared__ int s_has[2 * AW];
@@ -205,17 +230,18 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   pdl_launch_dependents();
 
   // ---- the list of all work: total, and where this CTA's warps start
-  const auto work_of = [&](int b) -> long long {
-    const Seq s = sequence(p, b);
-    if (s.cnt <= 0) return 0;
-    return static_cast<long long>(c.Hk) * ((s.cnt * p.G + 15) / 16) * ((s.ctx + s.cnt + ASTEP - 1) / ASTEP);
-  };
   long long total = 0, nc = 0;
+  int rest = 0;  // some sequence has rows that no step writes
   for (int pass = 0; pass < 2; ++pass) {
     long long run = 0;
     for (int b0 = 0; b0 < p.B; b0 += ANT) {
       const int b = b0 + threadIdx.x;
-      const long long w = b < p.B ? work_of(b) : 0;
+      long long w = 0;
+      if (b < p.B) {
+        const Seq s = sequence(p, b);
+        if (s.cnt > 0) w = static_cast<long long>(c.Hk) * ((s.ctx + s.cnt + ASTEP - 1) / ASTEP);
+        rest |= s.cnt != p.N;
+      }
       long long x = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -238,25 +264,29 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     }
     if (pass == 0) {
       total = run;
-      nc = min(static_cast<long long>(gridDim.x), total);
+      nc = min(static_cast<long long>(gridDim.x), (total + AW * ALEAST - 1) / (AW * ALEAST));
       if (static_cast<long long>(blockIdx.x) < nc && threadIdx.x <= AW)
         s_start[threadIdx.x] = total * (static_cast<long long>(blockIdx.x) * AW + threadIdx.x) / (nc * AW);
-      __syncthreads();
+      rest = __syncthreads_or(rest);
       if (static_cast<long long>(blockIdx.x) >= nc) break;
     }
   }
-  fill_rest<DT, ANT>(p, D);
+  if (rest) fill_rest<DT, ANT>(p, D);
   if (static_cast<long long>(blockIdx.x) >= nc) return;
   __syncthreads();
 
-  const uint32_t ring = smem_u32(smem) + warp * ASTAGES * L::STAGE;
-  unsigned char *ring_ptr = smem + warp * ASTAGES * L::STAGE;
-  const long long my0 = s_start[warp], my1 = s_start[warp + 1];
+  unsigned char *const ring_ptr = smem + warp * ASTAGES * L::STAGE;
+  const uint32_t ring = smem_u32(ring_ptr);
+  float *const work = p.pieces + static_cast<long long>(blockIdx.x) * L::WORK;
+  float *const first_slot = RT == 1 ? reinterpret_cast<float *>(smem + L::RING) + warp * L::PIECE : work + L::SHARED + warp * L::PIECE;
+  uint4 *const q_slot = reinterpret_cast<uint4 *>(smem + L::RING + warp * L::QBYTES);
+  const long long my0 = s_start[warp];
+  const int mine = static_cast<int>(s_start[warp + 1] - my0);
   if (lane < 2) s_has[2 * warp + lane] = 0;
 
   // a place in the list of all work
   struct Cursor {
-    int b, h, tile, step, steps, tiles, ctx, cnt;
+    int b, h, step, steps, ctx, cnt;
   };
   const auto enter = [&](Cursor &u) {  // the sequence u.b, or the next one that has work
     for (;; ++u.b) {
@@ -264,66 +294,69 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       if (s.cnt <= 0) continue;
       u.ctx = s.ctx, u.cnt = s.cnt;
       u.steps = (s.ctx + s.cnt + ASTEP - 1) / ASTEP;
-      u.tiles = (s.cnt * p.G + 15) / 16;
       return;
     }
   };
   const auto next_segment = [&](Cursor &u) {
     u.step = 0;
-    if (++u.tile < u.tiles) return;
-    u.tile = 0;
     if (++u.h < c.Hk) return;
     u.h = 0;
     ++u.b;
     enter(u);
   };
-  if (my1 > my0) {
+  if (mine > 0) {
     Cursor at;  // what is consumed
     at.b = s_seq[warp];
     enter(at);
     {
-      long long r = my0 - s_base[warp];
+      const long long r = my0 - s_base[warp];
       at.step = static_cast<int>(r % at.steps);
-      r /= at.steps;
-      at.tile = static_cast<int>(r % at.tiles);
-      at.h = static_cast<int>(r / at.tiles);
+      at.h = static_cast<int>(r / at.steps);
     }
     Cursor is = at;  // what is copied ahead
-    long long copied = my0;
+    int copied = 0;
     int held_b = -1, held_p = 0, held = 0;  // page ids held_p + lane of sequence held_b
+    const unsigned char *kp = nullptr, *vp = nullptr;
+    const float *ksp = nullptr, *vsp = nullptr;
+    bool bad = false, fresh = true;  // fresh: another page, or its first step
 
     const auto copy_step = [&]() {
-      const int slot = static_cast<int>(copied - my0) % ASTAGES;
-      if (copied < my1) {
-        if (is.step == is.steps) next_segment(is);
-        const int tok = is.step * ASTEP, blk = tok >> c.log_page, in = tok & (c.page - 1);
-        if (is.b != held_b || blk < held_p || blk >= held_p + 32) {
-          held_b = is.b, held_p = blk;
-          const int blocks = (is.ctx + is.cnt + c.page - 1) >> c.log_page;
-          held = blk + lane < blocks ? c.table[static_cast<long long>(is.b) * c.per + blk + lane] : 0;
+      if (copied < mine) {
+        if (is.step == is.steps) next_segment(is), fresh = true;
+        const int tok = is.step * ASTEP, in = tok & (c.page - 1);
+        if (fresh || in == 0) {
+          const int blk = tok >> c.log_page;
+          if (is.b != held_b || blk < held_p || blk >= held_p + 32) {
+            held_b = is.b, held_p = blk;
+            const int blocks = (is.ctx + is.cnt + c.page - 1) >> c.log_page;
+            held = blk + lane < blocks ? c.table[static_cast<long long>(is.b) * c.per + blk + lane] : 0;
+          }
+          int page = __shfl_sync(0xffffffffu, held, blk - held_p);
+          bad = static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages);
+          if (bad) page = 0;
+          const long long id = static_cast<long long>(page) * c.Hk + is.h;
+          const long long off = (id * c.page + in) * D;
+          kp = c.k + off + (4 * (g >> 1) + (g & 1)) * D + 16 * t;
+          vp = c.v + off + 4 * t * D + g * NT8;
+          ksp = c.k_scale + id, vsp = c.v_scale + id;
+          fresh = false;
         }
-        int page = __shfl_sync(0xffffffffu, held, blk - held_p);
-        const bool bad = static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages);
-        if (bad) page = 0;
-        const long long id = static_cast<long long>(page) * c.Hk + is.h;
-        const long long off = (id * c.page + in) * D;
-        const uint32_t dst = ring + slot * L::STAGE;
-        const unsigned char *k = c.k + off + (4 * (g >> 1) + (g & 1)) * D + 16 * t;
+        const uint32_t dst = ring + copied % ASTAGES * L::STAGE;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, k + 2 * i * D + 64 * j);
-        const unsigned char *v = c.v + off + 4 * t * D + g * NT8;
+          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, kp + 2 * i * D + 64 * j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async<NT8>(dst + L::KB + (i * 32 + lane) * NT8, v + i * D);
+        for (int i = 0; i < 4; ++i) cp_async<NT8>(dst + L::KB + (i * 32 + lane) * NT8, vp + i * D);
         const uint32_t sc = dst + 2 * L::KB + lane * 8;
         if (!bad) {
-          cp_async<4>(sc, c.k_scale + id);
-          cp_async<4>(sc + 4, c.v_scale + id);
+          cp_async<4>(sc, ksp);
+          cp_async<4>(sc + 4, vsp);
         } else {  // a NaN scale makes the rows NaN
           if (lane == 0) atomicOr(p.status, ST_PAGE);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sc), "r"(0x7fc00000u), "r"(0x3f800000u) : "memory");
         }
+        kp += ASTEP * D, vp += ASTEP * D;
         ++is.step;
       }
       ++copied;
@@ -332,214 +365,324 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < ASTAGES; ++i) copy_step();
 
-    long long now = my0;
+    int now = 0;
     bool first_piece = true;
-    while (now < my1) {
+    while (now < mine) {
       if (at.step == at.steps) next_segment(at);
       Segment seg;
-      seg.b = at.b, seg.h = at.h, seg.tile = at.tile, seg.steps = at.steps, seg.ctx = at.ctx, seg.cnt = at.cnt;
-      seg.at = now - at.step, seg.s0 = at.step;
-      seg.s1 = static_cast<int>(min(static_cast<long long>(at.steps), at.step + (my1 - now)));
-      const int rows = min(16, at.cnt * p.G - at.tile * 16);
+      seg.b = at.b, seg.h = at.h, seg.steps = at.steps, seg.ctx = at.ctx, seg.cnt = at.cnt;
+      seg.at = my0 + now - at.step, seg.s0 = at.step;
+      seg.s1 = min(at.steps, at.step + mine - now);
+      const int rows = at.cnt * p.G;
 
       // queries as fp16 fragments with a power of two per row
-      uint32_t qf[CH * 4][4];
-      float fac[2];
+      uint32_t qf[RT == 1 ? CH * 4 : 1][4];
+      float fac[RT][2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int rr = g + 8 * half, r = at.tile * 16 + rr;
-        const bool live = rr < rows;
-        const long long base = live ? at.b * p.q_sb + (r / p.G) * p.q_sn + (at.h * p.G + r % p.G) * p.q_sh : 0;
-        float x[CH][16];
-        float amax = 0.f;
+      for (int rt = 0; rt < RT; ++rt) {
+        uint32_t f[CH * 4][4];
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
+        for (int half = 0; half < 2; ++half) {
+          const int r = 16 * rt + g + 8 * half;
+          const bool live = r < rows;
+          const long long base = live ? at.b * p.q_sb + (r / p.G) * p.q_sn + (at.h * p.G + r % p.G) * p.q_sh + 16 * t : 0;
+          float x[CH][16];
+          float amax = 0.f;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            x[i][j] = live ? one_element<DT>(p.q, base + 64 * i + 16 * t + j) : 0.f;
-            amax = fmaxf(amax, fabsf(x[i][j]));
+          for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              Raw8<DT> raw;
+              raw.v[0] = make_uint4(0, 0, 0, 0);
+              if (live) raw = p.q_vec ? load8<DT, true>(p.q, base + 64 * i + 8 * w) : load8<DT, false>(p.q, base + 64 * i + 8 * w);
+              float y[8];
+              unpack8<DT>(raw, y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                x[i][8 * w + j] = y[j];
+                amax = fmaxf(amax, fabsf(y[j]));
+              }
+            }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // amax * 2^-e lies in [1, 2)
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          fac[rt][half] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              f[i * 4 + w][half] = f32_to_f16x2(x[i][4 * w] * down, x[i][4 * w + 1] * down);
+              f[i * 4 + w][2 + half] = f32_to_f16x2(x[i][4 * w + 2] * down, x[i][4 * w + 3] * down);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < CH * 4; ++k) {
+          if constexpr (RT == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qf[k][j] = f[k][j];
+          } else {  // a lane reads back only its own
+            q_slot[(rt * CH * 4 + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
           }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // amax * 2^-e lies in [1, 2)
-        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        fac[half] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2 * VFIX;
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            qf[i * 4 + w][half] = f32_to_f16x2(x[i][4 * w] * down, x[i][4 * w + 1] * down);
-            qf[i * 4 + w][2 + half] = f32_to_f16x2(x[i][4 * w + 2] * down, x[i][4 * w + 3] * down);
-          }
+        }
       }
-      float o[NT8][4];
+      float o[RT][NT8][4];
+      // exponents' offset (as subtracted: 0 for -inf), sum; the same over blocks without values
+      float m[RT][2], base_m[RT][2], l[RT][2], m0[RT][2], l0[RT][2];
 #pragma unroll
-      for (int j = 0; j < NT8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float m[2], base_m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // exponents' offset (as subtracted: 0 for -inf), sum
-      float m0[2], l0[2] = {0.f, 0.f};  // maximum and sum over blocks without values
-      m[0] = m[1] = m0[0] = m0[1] = __uint_as_float(0xff800000u);
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int j = 0; j < NT8; ++j) o[rt][j][0] = o[rt][j][1] = o[rt][j][2] = o[rt][j][3] = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) m[rt][half] = m0[rt][half] = NINF, base_m[rt][half] = l[rt][half] = l0[rt][half] = 0.f;
+      }
 
-      for (int step = seg.s0; step < seg.s1; ++step, ++now) {
-        const int slot = static_cast<int>(now - my0) % ASTAGES;
-        cp_async_wait<ASTAGES - 1>();
-        const unsigned char *st = ring_ptr + slot * L::STAGE;
-        const float2 sc = *reinterpret_cast<const float2 *>(st + 2 * L::KB + lane * 8);
-        // scores: two tiles of 8 tokens; column n of tile i is token
+      for (int step = seg.s0; step < seg.s1;) {
+        const int nsub = min(SUB, seg.s1 - step);
+        cp_async_wait<ASTAGES - SUB>();
+        const unsigned char *st[SUB];
+        float2 sc[SUB];
+        // scores: two tiles of 8 tokens a step; column n of tile i is token
         // 4 (n / 2) + n % 2 + 2 i, so a lane holds tokens 4 t .. 4 t + 3
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float s[SUB][RT][2][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          st[u] = ring_ptr + (now + u) % ASTAGES * L::STAGE;
+          sc[u] = *reinterpret_cast<const float2 *>(st[u] + 2 * L::KB + lane * 8);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[u][rt][i][0] = s[u][rt][i][1] = s[u][rt][i][2] = s[u][rt][i][3] = 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-          uint4 a = lds128(st + (j * 32 + lane) * 16), b = lds128(st + ((CH + j) * 32 + lane) * 16);
-          uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+          uint32_t aw[SUB][2][4];
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 a = lds128(st[u] + ((i * CH + j) * 32 + lane) * 16);
+              aw[u][i][0] = a.x, aw[u][i][1] = a.y, aw[u][i][2] = a.z, aw[u][i][3] = a.w;
+            }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            if (KIND == KIND_I8) aw[w] ^= 0x80808080u, bw[w] ^= 0x80808080u;
-            mma16816(s[0], qf[4 * j + w], pair_of<KIND, 0>(aw[w]), pair_of<KIND, 2>(aw[w]));
-            mma16816(s[1], qf[4 * j + w], pair_of<KIND, 0>(bw[w]), pair_of<KIND, 2>(bw[w]));
-          }
-        }
-        const bool zero = sc.y <= LEAST_V_SCALE;  // no values in this block: it counts in the sum only
-        const float lv = zero ? 0.f : lg2(sc.y), rv = 1.f / sc.y;
-        const float f0 = fac[0] * sc.x, f1 = fac[1] * sc.x;
-        float x[2][4];  // row (g, g + 8), token 4 t + j
-        x[0][0] = fmaf(s[0][0], f0, lv), x[0][1] = fmaf(s[0][1], f0, lv), x[0][2] = fmaf(s[1][0], f0, lv), x[0][3] = fmaf(s[1][1], f0, lv);
-        x[1][0] = fmaf(s[0][2], f1, lv), x[1][1] = fmaf(s[0][3], f1, lv), x[1][2] = fmaf(s[1][2], f1, lv), x[1][3] = fmaf(s[1][3], f1, lv);
-        if ((step + 1) * ASTEP > at.ctx) {  // new tokens, or slots past the last one
+            uint32_t q[RT][4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int node = min((at.tile * 16 + g + 8 * half) / p.G, p.N - 1);
+            for (int rt = 0; rt < RT; ++rt) {
+              if constexpr (RT == 1) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int n = step * ASTEP + 4 * t + j - at.ctx;
-              bool seen = n < 0;
-              if (n >= 0 && n < at.cnt)
-                seen = p.mask ? (p.mask[(static_cast<long long>(at.b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
-              if (!seen) x[half][j] = __uint_as_float(0xff800000u);
+                for (int e = 0; e < 4; ++e) q[rt][e] = qf[4 * j + w][e];
+              } else {
+                const uint4 a = lds128(q_slot + (rt * CH * 4 + 4 * j + w) * 32 + lane);
+                q[rt][0] = a.x, q[rt][1] = a.y, q[rt][2] = a.z, q[rt][3] = a.w;
+              }
             }
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t b0, b1;
+                pairs_of<KIND>(KIND == KIND_I8 ? aw[u][i][w] ^ 0x80808080u : aw[u][i][w], b0, b1);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) mma16816(s[u][rt][i], q[rt], b0, b1);
+              }
           }
         }
-        if (zero) {
+        // new tokens, slots past the last one, or a step that is not there
+        const bool edge = (step + SUB) * ASTEP > at.ctx || nsub < SUB;
+        bool zero[SUB];
+        float lv[SUB], rv[SUB];
+        float x[SUB][RT][2][4];  // row g or g + 8, token 4 t + j
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float top = fmaxf(fmaxf(x[half][0], x[half][1]), fmaxf(x[half][2], x[half][3]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float nm = fmaxf(m0[half], top), nb = nm == __uint_as_float(0xff800000u) ? 0.f : nm;
-            l0[half] *= ex2(m0[half] - nb);
-            m0[half] = nm;
+        for (int u = 0; u < SUB; ++u) {
+          zero[u] = sc[u].y <= LEAST_V_SCALE;  // no values in this block: it counts in a sum of its own
+          lv[u] = zero[u] ? 0.f : lg2(sc[u].y), rv[u] = u < nsub ? 1.f / sc[u].y : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) l0[half] += ex2(x[half][j] - nb);
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float f = fac[rt][half] * sc[u].x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[u][rt][half][j] = fmaf(s[u][rt][j >> 1][2 * half + (j & 1)], f, lv[u]);
+            }
+        }
+        if (edge) {
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int node = min((16 * rt + g + 8 * half) / p.G, p.N - 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int n = (step + u) * ASTEP + 4 * t + j - at.ctx;
+                  bool seen = n < 0;
+                  if (n >= 0 && n < at.cnt)
+                    seen = p.mask ? (p.mask[(static_cast<long long>(at.b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
+                  if (!seen || u >= nsub) x[u][rt][half][j] = NINF;
+                }
+              }
+        }
+        bool any_zero = false;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) any_zero |= u < nsub && zero[u];
+        if (any_zero) {
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            if (u >= nsub || !zero[u]) continue;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                float(&y)[4] = x[u][rt][half];
+                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float nm = fmaxf(m0[rt][half], top), nb = nm == NINF ? 0.f : nm;
+                l0[rt][half] *= ex2(m0[rt][half] - nb);
+                m0[rt][half] = nm;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) l0[rt][half] += ex2(y[j] - nb), y[j] = NINF;
+              }
+            rv[u] = 0.f;
           }
-          copy_step();
-          ++at.step;
-          continue;
         }
         // the offset moves only when a weight would pass 2^15.9
         bool up = false;
+        float top[RT][2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float top = fmaxf(fmaxf(x[half][0], x[half][1]), fmaxf(x[half][2], x[half][3]));
-          up |= top > m[half] + (WEIGHT_UP + WEIGHT_SLACK);
-        }
-        if (__any_sync(0xffffffffu, up)) {
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            float top = fmaxf(fmaxf(x[half][0], x[half][1]), fmaxf(x[half][2], x[half][3]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float nm = fmaxf(m[half], top - WEIGHT_UP);
-            const float nb = nm == __uint_as_float(0xff800000u) ? 0.f : nm;
-            const float a = ex2(m[half] - nb);  // 0 from -inf
-            m[half] = nm, base_m[half] = nb, l[half] *= a;
+            float v = NINF;
 #pragma unroll
-            for (int j = 0; j < NT8; ++j) o[j][2 * half] *= a, o[j][2 * half + 1] *= a;
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v = fmaxf(v, x[u][rt][half][j]);
+            top[rt][half] = v;
+            up |= v > m[rt][half] + (WEIGHT_UP + WEIGHT_SLACK);
           }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float v = top[rt][half];
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+              const float nm = fmaxf(m[rt][half], v - WEIGHT_UP);
+              const float nb = nm == NINF ? 0.f : nm;
+              const float a = ex2(m[rt][half] - nb);  // 0 from -inf
+              m[rt][half] = nm, base_m[rt][half] = nb, l[rt][half] *= a;
+#pragma unroll
+              for (int j = 0; j < NT8; ++j) o[rt][j][2 * half] *= a, o[rt][j][2 * half + 1] *= a;
+            }
         }
-        float sum[2] = {0.f, 0.f};
+        uint32_t pf[SUB][RT][4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[half][j] = ex2(x[half][j] - base_m[half]);
-            sum[half] += x[half][j];
+          for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float(&y)[4] = x[u][rt][half];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = ex2(y[j] - base_m[rt][half]);
+              l[rt][half] = fmaf((y[0] + y[1]) + (y[2] + y[3]), rv[u], l[rt][half]);
+              pf[u][rt][half] = f32_to_f16x2(y[0], y[1]);
+              pf[u][rt][2 + half] = f32_to_f16x2(y[2], y[3]);
+            }
           }
-        l[0] = fmaf(sum[0], rv, l[0]);
-        l[1] = fmaf(sum[1], rv, l[1]);
-        const uint32_t pf[4] = {f32_to_f16x2(x[0][0], x[0][1]), f32_to_f16x2(x[1][0], x[1][1]),
-                                f32_to_f16x2(x[0][2], x[0][3]), f32_to_f16x2(x[1][2], x[1][3])};
-        uint32_t v[4][NT8 / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint4 a = lds128(st + L::KB + (i * 32 + lane) * 16);
-            v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
-          } else {
-            const uint2 a = *reinterpret_cast<const uint2 *>(st + L::KB + (i * 32 + lane) * 8);
-            v[i][0] = a.x, v[i][1] = a.y;
+        for (int u = 0; u < SUB; ++u) {
+          uint32_t v[4][NT8 / 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint4 a = lds128(st[u] + L::KB + (i * 32 + lane) * 16);
+              v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+            } else {
+              const uint2 a = *reinterpret_cast<const uint2 *>(st[u] + L::KB + (i * 32 + lane) * 8);
+              v[i][0] = a.x, v[i][1] = a.y;
+            }
+          }
+          if (edge) {  // rows that are not there may hold anything, NaN codes too
+            const int end = u < nsub ? at.ctx + at.cnt - (step + u) * ASTEP - 4 * t : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int w = 0; w < NT8 / 4; ++w)
+                if (i >= end) v[i][w] = 0;
           }
           if (KIND == KIND_I8)
 #pragma unroll
-            for (int w = 0; w < NT8 / 4; ++w) v[i][w] ^= 0x80808080u;
-        }
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int w = 0; w < NT8 / 4; ++w)
+              for (int w = 0; w < NT8 / 4; ++w) v[i][w] ^= 0x80808080u;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma16816(o[4 * w + j], pf, pair_across<KIND>(v[0][w], v[1][w], j), pair_across<KIND>(v[2][w], v[3][w], j));
-        copy_step();
-        ++at.step;
-      }
-      // a lane holds columns [t D / 4, (t + 1) D / 4) of rows g and g + 8
+          for (int w = 0; w < NT8 / 4; ++w) {
+            uint32_t b[2][4];
+            pairs_across<KIND, 0>(v[0][w], v[1][w], b[0][0], b[0][1]);
+            pairs_across<KIND, 2>(v[0][w], v[1][w], b[0][2], b[0][3]);
+            pairs_across<KIND, 0>(v[2][w], v[3][w], b[1][0], b[1][1]);
+            pairs_across<KIND, 2>(v[2][w], v[3][w], b[1][2], b[1][3]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (__any_sync(0xffffffffu, l0[half] > 0.f)) {  // joined so that neither sum overflows
-          const float nm = fmaxf(m[half], m0[half] - 60.f), nb = nm == __uint_as_float(0xff800000u) ? 0.f : nm;
-          const float a = ex2(m[half] - nb);
-          l[half] = l[half] * a + l0[half] * ex2(m0[half] - nb);
-          m[half] = nm;
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < NT8; ++j) o[j][2 * half] *= a, o[j][2 * half + 1] *= a;
-        }
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-      }
-      if (seg.s0 == 0 && seg.s1 == seg.steps) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int rr = g + 8 * half;
-          if (rr < rows) {
-            const float inv = l[half] == 0.f ? 0.f : VFIX / l[half];
-#pragma unroll
-            for (int q = 0; q < NT8 / 2; ++q) {
-              const int j = (4 * q) % NT8, e = 2 * half + (4 * q) / NT8;
-              put4<DT>(p, seg, D, at.tile * 16 + rr, t * (D / 4) + 4 * q,
-                       make_float4(o[j][e] * inv, o[j + 1][e] * inv, o[j + 2][e] * inv, o[j + 3][e] * inv));
-            }
-            if (t == 0) put_lse(p, seg, at.tile * 16 + rr, m[half], l[half]);
+              for (int rt = 0; rt < RT; ++rt) mma16816(o[rt][4 * w + j], pf[u][rt], b[0][j], b[1][j]);
           }
         }
-      } else {
-        // the first piece has its own place, the last one takes the ring's
-        const int which = first_piece ? 0 : 1;
-        float4 *to = reinterpret_cast<float4 *>(which ? ring_ptr : smem + L::RING + warp * L::PIECE);
-        if (which) {  // every lane's copies have landed and been read
-          cp_async_wait<0>();
-          __syncwarp();
-        }
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int u = 0; u < SUB; ++u)
+          if (u < nsub) copy_step();
+        step += nsub, now += nsub, at.step += nsub;
+      }
+      // a lane holds columns [t D / 4, (t + 1) D / 4) of rows g and g + 8 of each tile
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float &lr = l[rt][half], &mr = m[rt][half];
+          if (__any_sync(0xffffffffu, l0[rt][half] > 0.f)) {  // joined so that neither sum overflows
+            const float nm = fmaxf(mr, m0[rt][half] - 60.f), nb = nm == NINF ? 0.f : nm;
+            const float a = ex2(mr - nb);
+            lr = lr * a + l0[rt][half] * ex2(m0[rt][half] - nb);
+            mr = nm;
+#pragma unroll
+            for (int j = 0; j < NT8; ++j) o[rt][j][2 * half] *= a, o[rt][j][2 * half + 1] *= a;
+          }
+          lr += __shfl_xor_sync(0xffffffffu, lr, 1);
+          lr += __shfl_xor_sync(0xffffffffu, lr, 2);
+        }
+      const bool whole = seg.s0 == 0 && seg.s1 == seg.steps;
+      // the first piece has its own place, the last one takes the ring's
+      const int which = first_piece ? 0 : 1;
+      float *const to = which ? reinterpret_cast<float *>(ring_ptr) : first_slot;
+      if (!whole && which) {  // every lane's copies have landed and been read
+        cp_async_wait<0>();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = 16 * rt + 8 * half + g;
+          const float inv = l[rt][half] == 0.f ? 0.f : 1.f / l[rt][half];
 #pragma unroll
           for (int q = 0; q < NT8 / 2; ++q) {
             const int j = (4 * q) % NT8, e = 2 * half + (4 * q) / NT8;
-            to[(half * (NT8 / 2) + q) * 32 + lane] = make_float4(o[j][e], o[j + 1][e], o[j + 2][e], o[j + 3][e]);
+            const float4 z = make_float4(o[rt][j][e], o[rt][j + 1][e], o[rt][j + 2][e], o[rt][j + 3][e]);
+            if (!whole) reinterpret_cast<float4 *>(to)[((rt * 2 + half) * (NT8 / 2) + q) * 32 + lane] = z;
+            else if (r < rows) put4<DT>(p, seg, D, r, t * (D / 4) + 4 * q, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
           }
-        if (t == 0) {
-          float *ml = reinterpret_cast<float *>(to) + 16 * D;
-          ml[g] = m[0], ml[g + 8] = m[1], ml[16 + g] = l[0], ml[24 + g] = l[1];
+          if (t == 0) {
+            if (!whole) to[L::ROWS * D + r] = m[rt][half], to[L::ROWS * D + L::ROWS + r] = l[rt][half];
+            else if (r < rows) put_lse(p, seg, r, m[rt][half], l[rt][half]);
+          }
         }
-        if (lane == 0) s_seg[2 * warp + which] = seg, s_has[2 * warp + which] = 1;
-      }
+      if (!whole && lane == 0) s_seg[2 * warp + which] = seg, s_has[2 * warp + which] = 1;
       first_piece = false;
     }
     cp_async_wait<0>();
@@ -548,12 +691,11 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
 
   // ---- the CTA's pieces: neighbours of one segment are merged
   const auto piece_at = [&](int i) -> const float * {
-    return reinterpret_cast<const float *>((i & 1) ? smem + (i >> 1) * ASTAGES * L::STAGE : smem + L::RING + (i >> 1) * L::PIECE);
+    if (i & 1) return reinterpret_cast<const float *>(smem + (i >> 1) * ASTAGES * L::STAGE);
+    return RT == 1 ? reinterpret_cast<const float *>(smem + L::RING) + (i >> 1) * L::PIECE : work + L::SHARED + (i >> 1) * L::PIECE;
   };
-  constexpr int QUADS = 16 * D / 4;  // float4 of a piece
-  constexpr int PF = 16 * D + 32;    // floats of a piece
+  constexpr int QUADS = L::ROWS * D / 4;  // float4 of a piece
   const auto cta_start = [&](long long i) { return total * i / nc; };
-  float *const mine = p.pieces + static_cast<long long>(blockIdx.x) * 2 * PF;
   Segment open[2];
   bool is_open[2] = {false, false};
   for (int i = 0; i < 2 * AW;) {
@@ -570,33 +712,32 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       s1 = s_seg[n].s1;
     }
     const bool whole = seg.s0 == 0 && s1 == seg.steps;
-    const int rows = min(16, seg.cnt * p.G - seg.tile * 16);
-    const int which = seg.s0 > 0 ? 0 : 1;
+    const int rows = seg.cnt * p.G, which = seg.s0 > 0 ? 0 : 1;
     if (!whole) open[which] = seg, is_open[which] = true;
     for (int k = threadIdx.x; k < QUADS; k += ANT) {
       const int ln = k & 31, q = (k >> 5) % (NT8 / 2), row = (k >> 5) / (NT8 / 2) * 8 + (ln >> 2);
       if (row >= rows) continue;
-      float M = __uint_as_float(0xff800000u);
-      for (int e = 0; e < cnt; ++e) M = fmaxf(M, piece_at(idx[e])[16 * D + row]);
-      const float bm = M == __uint_as_float(0xff800000u) ? 0.f : M;
+      float M = NINF;
+      for (int e = 0; e < cnt; ++e) M = fmaxf(M, piece_at(idx[e])[L::ROWS * D + row]);
+      const float bm = M == NINF ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
       for (int e = 0; e < cnt; ++e) {
         const float *pc = piece_at(idx[e]);
-        const float a = ex2(pc[16 * D + row] - bm);
+        const float a = ex2(pc[L::ROWS * D + row] - bm);
         const float4 x = reinterpret_cast<const float4 *>(pc)[k];
         acc.x = fmaf(a, x.x, acc.x), acc.y = fmaf(a, x.y, acc.y), acc.z = fmaf(a, x.z, acc.z), acc.w = fmaf(a, x.w, acc.w);
-        sum = fmaf(a, pc[16 * D + 16 + row], sum);
+        sum = fmaf(a, pc[L::ROWS * D + L::ROWS + row], sum);
       }
       const bool head = q == 0 && (ln & 3) == 0;
       if (whole) {
-        const float inv = sum == 0.f ? 0.f : VFIX / sum;
-        put4<DT>(p, seg, D, seg.tile * 16 + row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (head) put_lse(p, seg, seg.tile * 16 + row, M, sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        put4<DT>(p, seg, D, row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (head) put_lse(p, seg, row, M, sum);
       } else {
-        float *to = mine + which * PF;
+        float *to = work + which * L::PIECE;
         reinterpret_cast<float4 *>(to)[k] = acc;
-        if (head) to[16 * D + row] = M, to[16 * D + 16 + row] = sum;
+        if (head) to[L::ROWS * D + row] = M, to[L::ROWS * D + L::ROWS + row] = sum;
       }
     }
     i = n;
@@ -620,28 +761,28 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     __syncthreads();
     if (!s_last[which]) continue;
     __threadfence();
-    const int rows = min(16, seg.cnt * p.G - seg.tile * 16);
-    const auto shared_piece = [&](int e) { return p.pieces + (static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * PF; };
+    const int rows = seg.cnt * p.G;
+    const auto shared_piece = [&](int e) { return p.pieces + static_cast<long long>(c0 + e) * L::WORK + (e == 0 ? L::PIECE : 0); };
     for (int k = threadIdx.x; k < QUADS; k += ANT) {
       const int ln = k & 31, q = (k >> 5) % (NT8 / 2), row = (k >> 5) / (NT8 / 2) * 8 + (ln >> 2);
       if (row >= rows) continue;
-      float M = __uint_as_float(0xff800000u);
-#pragma unroll 4
-      for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(shared_piece(e) + 16 * D + row));
-      const float bm = M == __uint_as_float(0xff800000u) ? 0.f : M;
+      float M = NINF;
+#pragma unroll 8
+      for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(shared_piece(e) + L::ROWS * D + row));
+      const float bm = M == NINF ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int e = 0; e < n; ++e) {
         const float *pc = shared_piece(e);
-        const float a = ex2(__ldcg(pc + 16 * D + row) - bm);
+        const float a = ex2(__ldcg(pc + L::ROWS * D + row) - bm);
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(pc) + k);
         acc.x = fmaf(a, x.x, acc.x), acc.y = fmaf(a, x.y, acc.y), acc.z = fmaf(a, x.z, acc.z), acc.w = fmaf(a, x.w, acc.w);
-        sum = fmaf(a, __ldcg(pc + 16 * D + 16 + row), sum);
+        sum = fmaf(a, __ldcg(pc + L::ROWS * D + L::ROWS + row), sum);
       }
-      const float inv = sum == 0.f ? 0.f : VFIX / sum;
-      put4<DT>(p, seg, D, seg.tile * 16 + row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (q == 0 && (ln & 3) == 0) put_lse(p, seg, seg.tile * 16 + row, M, sum);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      put4<DT>(p, seg, D, row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (q == 0 && (ln & 3) == 0) put_lse(p, seg, row, M, sum);
     }
     if (threadIdx.x == 0) p.done[c0] = 0;  // zero again for the next call
   }

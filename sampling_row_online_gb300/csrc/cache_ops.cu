@@ -89,23 +89,35 @@ const void *pick_norm_rope(bool vec, bool pairs) {
                : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16>);
 }
 
-// The attention's kernel, its block and shared memory, and the floats of a piece.
+// The attention's kernel, its block and shared memory, and the floats of its
+// workspace per CTA.
 struct AttnChoice {
   const void *fn;
   int threads, smem;
-  size_t piece;
+  size_t work;
 };
+// By the rows per kv head: up to 16, and up to 32, a warp's own matrix
+// instructions keep pace with the memory; from 33 on the tensor cores with
+// accumulators in tensor memory take 128 rows at a time.
 template <int D, int KIND, int DT>
-AttnChoice choose_attn(bool tile) {
-  if (tile) return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, TileLayout<D>::SMEM, TileLayout<D>::PIECE};
-  return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT>), ANT, StreamLayout<D>::SMEM, StreamLayout<D>::PIECE / 4};
+AttnChoice choose_attn(long long rows) {
+  if (rows <= 16) {
+    using L = StreamLayout<D, 1>;
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), ANT, L::SMEM, L::WORK};
+  }
+  if (rows <= 32) {
+    using L = StreamLayout<D, 2>;
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), ANT, L::SMEM, L::WORK};
+  }
+  using L = TileLayout<D>;
+  return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 2 * L::PIECE};
 }
-AttnChoice choose_attn(int D, int kind, int dtype, bool tile) {
+AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   const bool bf = dtype == SPEC_BF16;
-  if (D == 128 && kind == SPEC_E4M3) return bf ? choose_attn<128, KIND_E4M3, DT_BF16>(tile) : choose_attn<128, KIND_E4M3, DT_F16>(tile);
-  if (D == 128) return bf ? choose_attn<128, KIND_I8, DT_BF16>(tile) : choose_attn<128, KIND_I8, DT_F16>(tile);
-  if (kind == SPEC_E4M3) return bf ? choose_attn<64, KIND_E4M3, DT_BF16>(tile) : choose_attn<64, KIND_E4M3, DT_F16>(tile);
-  return bf ? choose_attn<64, KIND_I8, DT_BF16>(tile) : choose_attn<64, KIND_I8, DT_F16>(tile);
+  if (D == 128 && kind == SPEC_E4M3) return bf ? choose_attn<128, KIND_E4M3, DT_BF16>(rows) : choose_attn<128, KIND_E4M3, DT_F16>(rows);
+  if (D == 128) return bf ? choose_attn<128, KIND_I8, DT_BF16>(rows) : choose_attn<128, KIND_I8, DT_F16>(rows);
+  if (kind == SPEC_E4M3) return bf ? choose_attn<64, KIND_E4M3, DT_BF16>(rows) : choose_attn<64, KIND_E4M3, DT_F16>(rows);
+  return bf ? choose_attn<64, KIND_I8, DT_BF16>(rows) : choose_attn<64, KIND_I8, DT_F16>(rows);
 }
 
 }  // namespace
@@ -260,13 +272,13 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   p.B = B, p.N = N, p.W = (N + 31) / 32, p.G = Hq / p.c.Hk;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.q_vec = vectors(*q, 2);
-  const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G > 16);
+  const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G);
   const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   const int grid = num_sms();
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if ((st = get_ws(stream, (2 * grid * k.piece + 3) / 4, &w, static_cast<size_t>(grid)))) return st;
+  if ((st = get_ws(stream, (grid * k.work + 3) / 4, &w, static_cast<size_t>(grid)))) return st;
   p.pieces = reinterpret_cast<float *>(w->partials);
   p.done = w->attn_done;
   p.status = w->status;
