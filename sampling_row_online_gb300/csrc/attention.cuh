@@ -132,6 +132,40 @@ __device__ __forceinline__ Seq sequence(const AttnParams &p, int b) {
   return s;
 }
 
+// Equal stretches of `total` work items for `n` workers: the first `rem` have
+// one more.  (32-bit arithmetic, one division: at a call's start and end every
+// instruction is fetched for the first time, and 64-bit divisions took
+// microseconds.)
+struct Share {
+  unsigned total, n, each, rem;
+  __device__ __forceinline__ Share(unsigned total_, unsigned n_) : total(total_), n(n_), each(total_ / n_), rem(total_ - total_ / n_ * n_) {}
+  __device__ __forceinline__ unsigned start(unsigned i) const { return i * each + min(i, rem); }
+  __device__ __forceinline__ unsigned holder(unsigned item) const {  // each > 0
+    const unsigned big = rem * (each + 1);
+    return item < big ? item / (each + 1) : rem + (item - big) / each;
+  }
+};
+// Inclusive sum over the CTA's threads; `sum` is the CTA's.
+template <int WARPS>
+__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned *s, unsigned &sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the previous use of s is over
+  if (lane == 31) s[warp] = x;
+  __syncthreads();
+  sum = 0;
+#pragma unroll 1
+  for (int i = 0; i < WARPS; ++i) {
+    if (i == warp) x += sum;
+    sum += s[i];
+  }
+  return x;
+}
+
 // Fills the rows that no work item writes: those past a sequence's count
 // (zero, lse -inf) and those of a sequence that does not fit (NaN).
 template <int DT, int NTH>
@@ -192,7 +226,7 @@ struct StreamLayout {
 };
 
 struct Segment {  // the rows of a kv head, and the part of their steps that a piece covers
-  long long at;   // first step in the list of all work
+  unsigned at;    // first step in the list of all work
   int b, h, steps, s0, s1, ctx, cnt;
 };
 
@@ -219,10 +253,9 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Segment s_seg[2 * AW];
   __shared__ int s_has[2 * AW];
-  __shared__ long long s_start[AW + 1];  // first step of each warp's stretch
-  __shared__ long long s_base[AW];       // first step of the sequence that holds it
+  __shared__ unsigned s_base[AW];  // first step of the sequence that holds each warp's first
   __shared__ int s_seq[AW];
-  __shared__ long long s_scan[AW];
+  __shared__ unsigned s_scan[AW];
   __shared__ int s_last[2];
   const CacheView &c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -230,49 +263,40 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   pdl_launch_dependents();
 
   // ---- the list of all work: total, and where this CTA's warps start
-  long long total = 0, nc = 0;
   int rest = 0;  // some sequence has rows that no step writes
-  for (int pass = 0; pass < 2; ++pass) {
-    long long run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += ANT) {
-      const int b = b0 + threadIdx.x;
-      long long w = 0;
-      if (b < p.B) {
-        const Seq s = sequence(p, b);
-        if (s.cnt > 0) w = static_cast<long long>(c.Hk) * ((s.ctx + s.cnt + ASTEP - 1) / ASTEP);
-        rest |= s.cnt != p.N;
-      }
-      long long x = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = x;
-      __syncthreads();
-      long long before = run;
-      for (int i = 0; i < AW; ++i) {
-        if (i < warp) before += s_scan[i];
-        run += s_scan[i];
-      }
-      if (pass == 1) {
-        const long long first = before + x - w;
-        for (int i = 0; i < AW; ++i)
-          if (w > 0 && s_start[i] >= first && s_start[i] < first + w) s_seq[i] = b, s_base[i] = first;
-      }
+  const auto work_of = [&](int b) -> unsigned {
+    if (b >= p.B) return 0;
+    const Seq s = sequence(p, b);
+    rest |= s.cnt != p.N;
+    return s.cnt > 0 ? static_cast<unsigned>(c.Hk) * ((s.ctx + s.cnt + ASTEP - 1) / ASTEP) : 0;
+  };
+  unsigned total = 0, w = 0, upto = 0;  // upto: of all sequences up to this thread's (of the last block of them)
+  for (int b0 = 0; b0 < p.B; b0 += ANT) {
+    unsigned sum;
+    w = work_of(b0 + threadIdx.x);
+    upto = total + block_scan<AW>(w, s_scan, sum);
+    total += sum;
+  }
+  // fewer CTAs where a warp's stretch would be a step or two
+  const unsigned nc = min(gridDim.x, (total + AW * ALEAST - 1) / (AW * ALEAST));
+  if (__syncthreads_or(rest)) fill_rest<DT, ANT>(p, D);
+  if (blockIdx.x >= nc) return;
+  const Share share(total, nc * AW);
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += ANT) {
+    if (p.B > ANT) {
+      unsigned sum;
+      w = work_of(b0 + threadIdx.x);
+      upto = before + block_scan<AW>(w, s_scan, sum);
+      before += sum;
     }
-    if (pass == 0) {
-      total = run;
-      nc = min(static_cast<long long>(gridDim.x), (total + AW * ALEAST - 1) / (AW * ALEAST));
-      if (static_cast<long long>(blockIdx.x) < nc && threadIdx.x <= AW)
-        s_start[threadIdx.x] = total * (static_cast<long long>(blockIdx.x) * AW + threadIdx.x) / (nc * AW);
-      rest = __syncthreads_or(rest);
-      if (static_cast<long long>(blockIdx.x) >= nc) break;
+#pragma unroll 1
+    for (int i = 0; i < AW; ++i) {
+      const unsigned first = share.start(blockIdx.x * AW + i);
+      if (first < upto && first >= upto - w) s_seq[i] = b0 + threadIdx.x, s_base[i] = upto - w;
     }
   }
-  if (rest) fill_rest<DT, ANT>(p, D);
-  if (static_cast<long long>(blockIdx.x) >= nc) return;
   __syncthreads();
 
   unsigned char *const ring_ptr = smem + warp * ASTAGES * L::STAGE;
@@ -280,8 +304,8 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   float *const work = p.pieces + static_cast<long long>(blockIdx.x) * L::WORK;
   float *const first_slot = RT == 1 ? reinterpret_cast<float *>(smem + L::RING) + warp * L::PIECE : work + L::SHARED + warp * L::PIECE;
   uint4 *const q_slot = reinterpret_cast<uint4 *>(smem + L::RING + warp * L::QBYTES);
-  const long long my0 = s_start[warp];
-  const int mine = static_cast<int>(s_start[warp + 1] - my0);
+  const unsigned my0 = share.start(blockIdx.x * AW + warp);
+  const int mine = static_cast<int>(share.start(blockIdx.x * AW + warp + 1) - my0);
   if (lane < 2) s_has[2 * warp + lane] = 0;
 
   // a place in the list of all work
@@ -309,9 +333,9 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     at.b = s_seq[warp];
     enter(at);
     {
-      const long long r = my0 - s_base[warp];
-      at.step = static_cast<int>(r % at.steps);
+      const unsigned r = my0 - s_base[warp];
       at.h = static_cast<int>(r / at.steps);
+      at.step = static_cast<int>(r) - at.h * at.steps;
     }
     Cursor is = at;  // what is copied ahead
     int copied = 0;
@@ -362,7 +386,15 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       ++copied;
       cp_async_commit();
     };
+    // the first segment's queries come closer while the copies are set up
 #pragma unroll
+    for (int rt = 0; rt < 2 * RT; ++rt) {
+      const int r = 8 * rt + g;
+      if (r < at.cnt * p.G)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t *>(p.q) + at.b * p.q_sb + (r / p.G) * p.q_sn +
+                                                      (at.h * p.G + r % p.G) * p.q_sh + t * (D / 4)));
+    }
+#pragma unroll 1
     for (int i = 0; i < ASTAGES; ++i) copy_step();
 
     int now = 0;
@@ -634,9 +666,8 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
               for (int rt = 0; rt < RT; ++rt) mma16816(o[rt][4 * w + j], pf[u][rt], b[0][j], b[1][j]);
           }
         }
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-          if (u < nsub) copy_step();
+#pragma unroll 1
+        for (int u = 0; u < nsub; ++u) copy_step();
         step += nsub, now += nsub, at.step += nsub;
       }
       // a lane holds columns [t D / 4, (t + 1) D / 4) of rows g and g + 8 of each tile
@@ -695,7 +726,6 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     return RT == 1 ? reinterpret_cast<const float *>(smem + L::RING) + (i >> 1) * L::PIECE : work + L::SHARED + (i >> 1) * L::PIECE;
   };
   constexpr int QUADS = L::ROWS * D / 4;  // float4 of a piece
-  const auto cta_start = [&](long long i) { return total * i / nc; };
   Segment open[2];
   bool is_open[2] = {false, false};
   for (int i = 0; i < 2 * AW;) {
@@ -750,13 +780,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   for (int which = 0; which < 2; ++which) {
     if (!is_open[which]) continue;
     const Segment seg = open[which];
-    const auto holder = [&](long long f) {  // the CTA whose stretch holds step f
-      long long i = f * nc / total;
-      while (cta_start(i) > f) --i;
-      while (cta_start(i + 1) <= f) ++i;
-      return static_cast<int>(i);
-    };
-    const int c0 = holder(seg.at), c1 = holder(seg.at + seg.steps - 1), n = c1 - c0 + 1;
+    const int c0 = share.holder(seg.at) / AW, c1 = share.holder(seg.at + seg.steps - 1) / AW, n = c1 - c0 + 1;
     if (threadIdx.x == 0) s_last[which] = atomicAdd(p.done + c0, 1) == n - 1;
     __syncthreads();
     if (!s_last[which]) continue;

@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::MISC);
   volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::MISC + 4);
   int *s_seq = reinterpret_cast<int *>(smem + L::MISC + 8);
-  long long *s_base = reinterpret_cast<long long *>(smem + L::MISC + 16);
-  long long *s_scan = reinterpret_cast<long long *>(smem + L::ML);
+  unsigned *s_base = reinterpret_cast<unsigned *>(smem + L::MISC + 16);
+  unsigned *s_scan = reinterpret_cast<unsigned *>(smem + L::ML);
   const CacheView &c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = T_NT / 32;
@@ -272,48 +272,45 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   pdl_launch_dependents();
 
   // ---- the list of all work, and this CTA's stretch of it
-  const auto work_of = [&](int b) -> long long {
-    const Seq s = sequence(p, b);
-    if (s.cnt <= 0) return 0;
-    const int tiles = (s.cnt * p.G + TQ - 1) / TQ;
-    long long w = 0;
-    if (p.mask) w = static_cast<long long>(tiles) * token_tiles(p, s.ctx, s.cnt, 0);
-    else
-      for (int t = 0; t < tiles; ++t) w += token_tiles(p, s.ctx, s.cnt, t);
-    return w * c.Hk;
+  int rest = 0;  // some sequence has rows that no tile writes
+  const auto head_work = [&](int ctx, int cnt) -> unsigned {  // tiles of one kv head
+    const int tiles = (cnt * p.G + TQ - 1) / TQ;
+    if (p.mask) return static_cast<unsigned>(tiles) * token_tiles(p, ctx, cnt, 0);
+    unsigned w = 0;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) w += token_tiles(p, ctx, cnt, t);
+    return w;
   };
-  long long total = 0, nc = 0, my0 = 0, my1 = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += T_NT) {
-      const int b = b0 + tid;
-      const long long w = b < p.B ? work_of(b) : 0;
-      long long x = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = x;
-      __syncthreads();
-      long long before = run;
-      for (int i = 0; i < NW; ++i) {
-        if (i < warp) before += s_scan[i];
-        run += s_scan[i];
-      }
-      const long long first = before + x - w;
-      if (pass == 1 && w > 0 && my0 >= first && my0 < first + w) *s_seq = b, *s_base = first;
-    }
-    if (pass == 0) {
-      total = run;
-      nc = min(static_cast<long long>(gridDim.x), total);
-      if (static_cast<long long>(blockIdx.x) >= nc) break;
-      my0 = total * blockIdx.x / nc, my1 = total * (blockIdx.x + 1) / nc;
-    }
+  const auto work_of = [&](int b) -> unsigned {
+    if (b >= p.B) return 0;
+    const Seq s = sequence(p, b);
+    rest |= s.cnt != p.N;
+    return s.cnt > 0 ? head_work(s.ctx, s.cnt) * c.Hk : 0;
+  };
+  unsigned total = 0, w = 0, upto = 0;  // upto: of all sequences up to this thread's (of the last block of them)
+  for (int b0 = 0; b0 < p.B; b0 += T_NT) {
+    unsigned sum;
+    w = work_of(b0 + tid);
+    upto = total + block_scan<NW>(w, s_scan, sum);
+    total += sum;
   }
-  fill_rest<DT, T_NT>(p, D);
-  if (my1 <= my0) return;
+  const unsigned nc = min(gridDim.x, total);
+  if (__syncthreads_or(rest)) fill_rest<DT, T_NT>(p, D);
+  if (blockIdx.x >= nc) return;
+  const Share share(total, nc);
+  const unsigned my0 = share.start(blockIdx.x);
+  const int count = static_cast<int>(share.start(blockIdx.x + 1) - my0);
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += T_NT) {
+    if (p.B > T_NT) {
+      unsigned sum;
+      w = work_of(b0 + tid);
+      upto = before + block_scan<NW>(w, s_scan, sum);
+      before += sum;
+    }
+    if (my0 < upto && my0 >= upto - w) *s_seq = b0 + tid, *s_base = upto - w;
+  }
   if (tid == 0) {
     for (int i = 0; i < T_RAW; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], T_CONV / 64);
     for (int i = 0; i < 2; ++i) {
@@ -335,23 +332,19 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   at.b = *s_seq;
   tile_enter(p, at);
   {
-    long long r = my0 - *s_base;
-    at.rt = at.h = 0;
-    long long head = 0;  // tiles of one kv head
-    if (p.mask) head = static_cast<long long>(at.tiles) * token_tiles(p, at.ctx, at.cnt, 0);
-    else
-      for (int t = 0; t < at.tiles; ++t) head += token_tiles(p, at.ctx, at.cnt, t);
+    unsigned r = my0 - *s_base;
+    const unsigned head = head_work(at.ctx, at.cnt);
+    at.rt = 0;
     at.h = static_cast<int>(r / head);
-    r %= head;
+    r -= at.h * head;
     for (;;) {
       at.n = token_tiles(p, at.ctx, at.cnt, at.rt);
-      if (r < at.n) break;
+      if (r < static_cast<unsigned>(at.n)) break;
       r -= at.n;
       ++at.rt;
     }
     at.j = static_cast<int>(r);
   }
-  const int count = static_cast<int>(my1 - my0);
   // a wait that ran out: the role goes on without waiting, its loops end, and
   // the call reports a timeout
   bool lost = false;
@@ -623,14 +616,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       meet();  // the accumulators are free
       if (!whole) {
         // a segment that several CTAs share: the last to arrive merges, in order
-        const long long f0 = my0 + i - s0, f1 = f0 + at.n - 1;
-        const auto holder = [&](long long f) {
-          long long k = f * nc / total;
-          while (total * k / nc > f) --k;
-          while (total * (k + 1) / nc <= f) ++k;
-          return static_cast<int>(k);
-        };
-        const int c0 = holder(f0), n = holder(f1) - c0 + 1;
+        const unsigned f0 = my0 + i - s0;
+        const int c0 = share.holder(f0), n = static_cast<int>(share.holder(f0 + at.n - 1)) - c0 + 1;
         if (tid == 0) {
           *s_last = atomicAdd(p.done + c0, 1) == n - 1;
           __threadfence();

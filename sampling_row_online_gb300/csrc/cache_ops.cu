@@ -272,6 +272,10 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   p.B = B, p.N = N, p.W = (N + 31) / 32, p.G = Hq / p.c.Hk;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.q_vec = vectors(*q, 2);
+  // the kernels count their work (steps of 16 tokens; tiles of 128 rows by 128 tokens) in 31 bits
+  const double row_tiles = std::ceil(static_cast<double>(N) * p.G / TQ);
+  if (static_cast<double>(B) * p.c.Hk * row_tiles * pages_per_seq * p.c.page / 16 >= 2147483648.0)
+    return fail(SPEC_ERR_ARG, "B * Hq * N * pages_per_seq is too large");
   const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G);
   const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
