@@ -20,5 +20,6 @@ __all__ = ["spec_verify", "spec_verify_ex", "spec_verify_host", "spec_verify_noa
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found at once from now on
+        return value
     raise AttributeError(name)

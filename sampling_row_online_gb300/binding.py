@@ -509,25 +509,26 @@ class SpecCache:
     and scales k_scale, v_scale [pages, kv_heads] float32, all contiguous on one GPU; a value is code * scale.
     ``SpecCache.empty`` makes one.  The tensors stay the caller's: the cache only holds references."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "struct", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "struct", "ref", "kv_heads", "head_dim")
 
     def __init__(self, k, v, k_scale, v_scale):
-        if k.dim() != 4 or k.dtype not in _KINDS:
+        shape, kind = k.shape, _KINDS.get(k.dtype)
+        if len(shape) != 4 or kind is None:
             raise ValueError("k must be [pages, kv_heads, page_size, head_dim] float8_e4m3fn or int8")
-        pages, heads, page, dim = k.shape
-        if v.shape != k.shape or v.dtype != k.dtype:
+        if v.shape != shape or v.dtype != k.dtype:
             raise ValueError("v must have the shape and dtype of k")
-        if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
+        if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError("k_scale and v_scale must be [pages, kv_heads]")
         if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
             raise TypeError("k_scale and v_scale must be float32")
-        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
-            if not (t.is_cuda and t.is_contiguous() and t.device == k.device):
-                raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of k")
-        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
-        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
-                                  page, dim, _KINDS[k.dtype])
+        device = k.device
+        if not (k.is_cuda and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and v.device == device and k_scale.device == device and v_scale.device == device):
+            raise ValueError("k, v, k_scale and v_scale must be contiguous CUDA tensors on one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, device
+        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape, kind)
         self.ref = ctypes.byref(self.struct)
+        _, self.kv_heads, _, self.head_dim = shape
 
     @classmethod
     def empty(cls, pages, kv_heads, page_size, head_dim, dtype=torch.float8_e4m3fn, device="cuda"):
@@ -541,12 +542,12 @@ def _heads(t, name, dtype, B, N, H, D):
     """A [B, N, H, D] tensor with a contiguous head as HeadsStruct."""
     if not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != (B, N, H, D):
+    if t.shape != (B, N, H, D):
         raise ValueError(f"{name} must be [{B}, {N}, {H}, {D}], got {list(t.shape)}")
-    s = t.stride()
-    if s[3] != 1 and D > 1:
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 and D > 1:
         raise ValueError(f"{name}: a head's elements must be contiguous")
-    return HeadsStruct(t.data_ptr(), s[0], s[1], s[2])
+    return HeadsStruct(t.data_ptr(), sb, sn, sh)
 
 
 def _index(t, name, shape, device):
@@ -555,7 +556,7 @@ def _index(t, name, shape, device):
         return None
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -576,13 +577,14 @@ def _code(t, name):
 
 
 def _call(fn, where, device, stream, *args):
-    """One library call on `device` and the stream."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+    """One library call on `device` and the stream (None: torch's current one there)."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
-    _check(st, where)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, where)
 
 
 def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True, q_weight=None, k_weight=None,
@@ -637,7 +639,7 @@ def spec_cache_write(cache, page_table, ctx_len, k, v, *, counts=None, stream=No
         raise ValueError("k must be [B, N, kv_heads, head_dim]")
     B, N = k.shape[:2]
     table, per = _table(cache, page_table, B)
-    c = cache.struct
+    c = cache
     code = _code(k, "k")
     ks, vs = (_heads(t, name, k.dtype, B, N, c.kv_heads, c.head_dim) for t, name in ((k, "k"), (v, "v")))
     if k.device != cache.device or v.device != cache.device:
@@ -657,7 +659,7 @@ def spec_cache_read(cache, page_table, start, counts, N, *, dtype=torch.bfloat16
     table, per = _table(cache, page_table, B)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    c = cache.struct
+    c = cache
     outs = []
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
         if t is None:
@@ -684,7 +686,7 @@ def spec_cache_attention(q, cache, page_table, ctx_len, *, counts=None, mask=Non
     B, N, Hq, D = q.shape
     table, per = _table(cache, page_table, B)
     device = cache.device
-    if D != cache.struct.head_dim or q.device != device:
+    if D != cache.head_dim or q.device != device:
         raise ValueError("q must have the cache's head_dim and be on its device")
     code = _code(q, "q")
     qs = _heads(q, "q", q.dtype, B, N, Hq, D)

@@ -191,6 +191,41 @@ __device__ __forceinline__ uint32_t encode4(int kind, float a, float b, float c,
     w |= static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x[j]))) & 0xff) << (8 * j);
   return w;
 }
+// As encode4 for finite values: a_j * inv with inv a power of two.  int8:
+// adding 1.5 * 2^23 rounds to a whole number in the sum's low bits.
+__device__ __forceinline__ uint32_t encode4_finite(int kind, float a, float b, float c, float d, float inv) {
+  if (kind == KIND_E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+    return lo | static_cast<uint32_t>(hi) << 16;
+  }
+  const uint32_t x = __float_as_uint(fmaf(a, inv, 12582912.f)), y = __float_as_uint(fmaf(b, inv, 12582912.f));
+  const uint32_t z = __float_as_uint(fmaf(c, inv, 12582912.f)), w = __float_as_uint(fmaf(d, inv, 12582912.f));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+// Largest magnitude of eight elements, as fp32 bits (inf and NaN: 0x7f800000
+// and above); 16-bit types are compared as bits, two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t magnitude8(const Raw8<DT> &r, uint32_t sofar) {
+  if constexpr (DT == DT_F32) {
+    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sofar = max(sofar, w[j] & 0x7fffffffu);
+  } else {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(sofar) : "r"(w[j] & 0x7fff7fffu));
+  }
+  return sofar;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t x) {  // of what magnitude8 gathered
+  if constexpr (DT == DT_F32) return x;
+  const uint32_t h = max(x & 0xffffu, x >> 16);
+  return DT == DT_BF16 ? h << 16 : __float_as_uint(f16x2_to_f32(h).x);
+}
+
 // The least power of two with amax <= qmax * scale, at least 2^-100, from the
 // bits of amax: 448 = 1.75 * 2^8, 127 = 1.984375 * 2^6.
 __device__ __forceinline__ float scale_for(int kind, uint32_t amax_bits) {
@@ -209,11 +244,11 @@ __device__ __forceinline__ int page_of(const CacheView &c, int b, int blk, int32
 }
 
 // Rounds the rows of a block outside [lo, hi) to a larger scale (ratio =
-// old / new < 1), 16 codes at a time.
+// old / new < 1), 16 codes at a time; thread `tid` of NTH.
 template <int NTH>
-__device__ __forceinline__ void rescale_block(unsigned char *blk, int kind, int page, int D, int lo, int hi, float ratio) {
+__device__ __forceinline__ void rescale_block(unsigned char *blk, int kind, int page, int D, int lo, int hi, float ratio, int tid) {
   const int per_row = D / 16;
-  for (int c = threadIdx.x; c < page * per_row; c += NTH) {
+  for (int c = tid; c < page * per_row; c += NTH) {
     const int row = c / per_row;
     if (row >= lo && row < hi) continue;
     uint4 *at = reinterpret_cast<uint4 *>(blk) + c;
@@ -293,41 +328,51 @@ __global__ void __launch_bounds__(NTH) cache_write_kernel(const __grid_constant_
       raw[i] = load8<DT, VEC>(p.src[t], base + (lo - start + k / per_row) * p.sn[t] + (k % per_row) * 8);
   }
   uint32_t amax = 0;
-  bool bad = false;
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    if (threadIdx.x + i * NTH < chunks) {
+  for (int i = 0; i < MOST; ++i)
+    if (threadIdx.x + i * NTH < chunks) amax = magnitude8<DT>(raw[i], amax);
+  amax = block_max<NTH>(magnitude_bits<DT>(amax), s_max);
+  const bool finite = amax < 0x7f800000u;
+  if (!finite) {  // the largest finite magnitude, and a report
+    amax = 0;
+#pragma unroll 1
+    for (int i = 0; i < MOST; ++i) {
+      const int k = threadIdx.x + i * NTH;
+      if (k >= chunks) break;
       float x[8];
-      unpack8<DT>(raw[i], x);
+      unpack8<DT>(load8<DT, VEC>(p.src[t], base + (lo - start + k / per_row) * p.sn[t] + (k % per_row) * 8), x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t a = __float_as_uint(x[j]) & 0x7fffffffu;
-        if (a < 0x7f800000u) amax = max(amax, a);
-        else bad = true;
+        const uint32_t y = __float_as_uint(x[j]) & 0x7fffffffu;
+        if (y < 0x7f800000u) amax = max(amax, y);
       }
     }
+    amax = block_max<NTH>(amax, s_max);
+    if (threadIdx.x == 0) atomicOr(p.status, ST_NONFINITE);
   }
-  if (bad) atomicOr(p.status, ST_NONFINITE);
-  amax = block_max<NTH>(amax, s_max);
   const float scale = fmaxf(scale_for(c.kind, amax), old);
   if (threadIdx.x == 0) *scale_at = scale;  // every thread has read the old one before the maximum's barrier
   const float inv = 1.f / scale;            // exact for powers of two
-  const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+  const bool simple = finite && (__float_as_uint(scale) & 0x7fffffu) == 0;
+  unsigned char *to = codes + static_cast<long long>(lo - first) * c.D;
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
     const int k = threadIdx.x + i * NTH;
     if (k < chunks) {
       float x[8];
       unpack8<DT>(raw[i], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = pow2 ? x[j] * inv : x[j] / scale;
       uint2 w;
-      w.x = encode4(c.kind, x[0], x[1], x[2], x[3]);
-      w.y = encode4(c.kind, x[4], x[5], x[6], x[7]);
-      *reinterpret_cast<uint2 *>(codes + static_cast<long long>(lo - first + k / per_row) * c.D + (k % per_row) * 8) = w;
+      if (simple) {
+        w.x = encode4_finite(c.kind, x[0], x[1], x[2], x[3], inv);
+        w.y = encode4_finite(c.kind, x[4], x[5], x[6], x[7], inv);
+      } else {
+        w.x = encode4(c.kind, x[0] / scale, x[1] / scale, x[2] / scale, x[3] / scale);
+        w.y = encode4(c.kind, x[4] / scale, x[5] / scale, x[6] / scale, x[7] / scale);
+      }
+      *reinterpret_cast<uint2 *>(to + k * 8) = w;  // the block's rows are contiguous
     }
   }
-  if (!empty && scale > old) rescale_block<NTH>(codes, c.kind, c.page, c.D, lo - first, hi - first, old / scale);
+  if (!empty && scale > old) rescale_block<NTH>(codes, c.kind, c.page, c.D, lo - first, hi - first, old / scale, threadIdx.x);
 }
 
 // ------------------------------------------------------------- read-back
@@ -405,19 +450,21 @@ struct CacheCommitParams {
 };
 constexpr int COMMIT_MAX_NODES = 1024;
 
-// One CTA per (kv head, tensor, sequence).  The nodes of the accepted path:
+// A few CTAs per sequence share its kv heads and tensors, so that the path is
+// found a few times only.  The nodes of the accepted path:
 // every thread walks from its nodes towards the root comparing tokens (the
 // token of depth d is path[d - 1]) and the lowest index that arrives wins;
 // equal token paths hold equal rows, so which of several is taken does not
 // matter.  Node i of the path moves from slot ctx + index[i] to ctx + i.
-// index[i] >= i, so the destination blocks are taken in ascending order and
-// no block is overwritten before its rows have been read.
+// index[i] >= i, so with the rows taken in ascending order none is overwritten
+// before it has been read.  A warp takes a kv head and tensor by itself: it
+// reads a block's new rows once for their maximum and once (from the cache)
+// to write them.
 __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
   __shared__ int s_par[COMMIT_MAX_NODES], s_tok[COMMIT_MAX_NODES], s_path[COMMIT_MAX_NODES], s_index[COMMIT_MAX_NODES];
-  __shared__ uint32_t s_max[8];
   __shared__ int s_node, s_bad, s_first;
   const CacheView &c = p.c;
-  const int h = blockIdx.x >> 1, t = blockIdx.x & 1, b = blockIdx.y;
+  const int b = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
   const int len = p.length[b], ctx = p.ctx[b];
@@ -461,68 +508,78 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant
   }
   if (!ok || s_first >= len) return;
 
-  constexpr int MOST = MAX_PAGE * 128 / 16 / 256;  // vectors of 16 codes per thread
-  unsigned char *base = t ? c.v : c.k;
-  float *scales = t ? c.v_scale : c.k_scale;
-  const int per_row = c.D / 16;
-  for (int row = s_first; row < len;) {
-    const int blk = (ctx + row) >> c.log_page, in = (ctx + row) & (c.page - 1);
-    const int n = min(len - row, c.page - in);
-    const int page = page_of(c, b, blk, p.status);
-    const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
-    const float old = scales[id];
-    uint4 raw[MOST];
-    float from[MOST];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < MOST; ++i) {
-      const int k = threadIdx.x + i * 256;
-      from[i] = -1.f;  // nothing to move
-      if (k >= n * per_row) continue;
-      const int slot = ctx + s_index[row + k / per_row];
-      const int src = page_of(c, b, slot >> c.log_page, p.status);
-      if (src < 0) continue;
-      const long long sid = static_cast<long long>(src) * c.Hk + h;
-      from[i] = scales[sid];
-      raw[i] = *reinterpret_cast<const uint4 *>(base + (sid * c.page + (slot & (c.page - 1))) * c.D + (k % per_row) * 16);
-      const uint32_t *u = &raw[i].x;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[4];
-        decode4(c.kind, u[j], x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a = __float_as_uint(x[e] * from[i]) & 0x7fffffffu;
-          if (a < 0x7f800000u) amax = max(amax, a);
-        }
-      }
-    }
-    amax = block_max<256>(amax, s_max);
-    // a block's scale never shrinks here: the rows of other nodes still stand in it
-    const float scale = fmaxf(scale_for(c.kind, amax), old);
-    __syncthreads();  // every thread has read the block's old scale and rows
-    if (page >= 0) {
-      unsigned char *codes = base + id * c.page * c.D;
-      if (threadIdx.x == 0) scales[id] = scale;
-#pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-        const int k = threadIdx.x + i * 256;
-        if (k >= n * per_row || from[i] < 0.f) continue;
-        uint32_t *u = &raw[i].x;
+  constexpr int BATCH = 4;  // vectors of 16 codes per lane that are read before any is written
+  const int lane = threadIdx.x & 31, log_row = c.D == 128 ? 3 : 2;  // vectors of a row: 8 or 4
+  for (int ht = blockIdx.x * 8 + (threadIdx.x >> 5); ht < 2 * c.Hk; ht += gridDim.x * 8) {
+    const int h = ht >> 1;
+    unsigned char *base = ht & 1 ? c.v : c.k;
+    float *scales = ht & 1 ? c.v_scale : c.k_scale;
+    // vector k of the rows from `row` on, and its scale (-1: a bad page)
+    const auto source = [&](int row, int k, float &scale) -> const uint4 * {
+      const int slot = ctx + s_index[row + (k >> log_row)];
+      const int page = page_of(c, b, slot >> c.log_page, p.status);
+      const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
+      scale = page < 0 ? -1.f : scales[id];
+      return reinterpret_cast<const uint4 *>(base + (id * c.page + (slot & (c.page - 1))) * c.D) + (k & ((1 << log_row) - 1));
+    };
+    for (int row = s_first; row < len;) {
+      const int in = (ctx + row) & (c.page - 1), n = min(len - row, c.page - in), vectors = n << log_row;
+      const int page = page_of(c, b, (ctx + row) >> c.log_page, p.status);
+      const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
+      const float old = scales[id];
+      uint32_t amax = 0;
+      for (int k = lane; k < vectors; k += 32) {
+        float from;
+        const uint4 w = *source(row, k, from);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x[4];
           decode4(c.kind, u[j], x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = x[e] * from[i] / scale;
-          u[j] = encode4(c.kind, x[0], x[1], x[2], x[3]);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a = __float_as_uint(x[e] * from) & 0x7fffffffu;
+            if (a < 0x7f800000u && from >= 0.f) amax = max(amax, a);
+          }
         }
-        *reinterpret_cast<uint4 *>(codes + static_cast<long long>(in + k / per_row) * c.D + (k % per_row) * 16) = raw[i];
       }
-      if (scale > old) rescale_block<256>(codes, c.kind, c.page, c.D, in, in + n, old / scale);
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      // a block's scale never shrinks here: the rows of other nodes still stand in it
+      const float scale = fmaxf(scale_for(c.kind, amax), old);
+      unsigned char *codes = base + id * c.page * c.D;
+      for (int k0 = lane; page >= 0 && k0 - lane < vectors; k0 += 32 * BATCH) {
+        uint4 raw[BATCH];
+        float from[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int k = k0 + 32 * i;
+          from[i] = -1.f;
+          if (k < vectors) raw[i] = *source(row, k, from[i]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          if (from[i] < 0.f) continue;
+          uint32_t *u = &raw[i].x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x[4];
+            decode4(c.kind, u[j], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = x[e] * from[i] / scale;
+            u[j] = encode4(c.kind, x[0], x[1], x[2], x[3]);
+          }
+          reinterpret_cast<uint4 *>(codes + static_cast<long long>(in) * c.D)[k0 + 32 * i] = raw[i];
+        }
+        __syncwarp();
+      }
+      if (page >= 0 && scale > old) {
+        if (lane == 0) scales[id] = scale;
+        rescale_block<32>(codes, c.kind, c.page, c.D, in, in + n, old / scale, lane);
+      }
+      __syncwarp();
+      row += n;
     }
-    __syncthreads();  // the next block's rows may come from this one's scale (its own page)
-    row += n;
   }
 }
 
@@ -543,24 +600,29 @@ struct NormRopeParams {
 // Several tokens to a CTA, `lanes` threads to a row (one head of one token).
 // A thread takes units of the row: eight elements of the first half with the
 // eight that they are rotated with (halves), or eight elements by themselves
-// (neighbouring pairs, and what is not rotated).  The rotation's angle is
-// exact: pos * freq modulo 2^64 is the fraction of a turn in 64 bits, from
-// which 24 go into sincospi; a table of the CTA's tokens holds cos and sin, so
-// that all heads share them.
-template <int DT, int VE, int MAXU>
+// (neighbouring pairs, and what is not rotated).  It loads ROWS rows before it
+// works on the first, so that enough bytes are in flight.  The rotation's
+// angle is exact: pos * freq modulo 2^64 is the fraction of a turn in 64 bits,
+// from which 24 go into sincospi; a table of the CTA's tokens holds cos and
+// sin, so that all heads share them.
+constexpr int ROPE_TOKENS = 16;  // most tokens of a CTA
+template <int DT, int VE, int MAXU, int ROWS>
 __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
+  __shared__ long long s_from[ROPE_TOKENS][2], s_to[ROPE_TOKENS][2];
   const int half = p.rot / 2;
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  const long long first = static_cast<long long>(blockIdx.x) * p.per_cta;
-  const int here = static_cast<int>(min(static_cast<long long>(p.per_cta), tokens - first));
+  const int tokens = p.B * p.N, first = blockIdx.x * p.per_cta, here = min(p.per_cta, tokens - first);
   pdl_wait();
   pdl_launch_dependents();
+  if (threadIdx.x < 2 * here) {
+    const int tk = threadIdx.x >> 1, w = threadIdx.x & 1, b = (first + tk) / p.N, n = (first + tk) - b * p.N;
+    s_from[tk][w] = b * p.ssb[w] + n * p.ssn[w];
+    s_to[tk][w] = b * p.dsb[w] + n * p.dsn[w];
+  }
   for (int i = threadIdx.x; i < here * half; i += 256) {
-    const long long tok = first + i / half;
-    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
-    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : n);
-    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[i % half];
+    const int tk = i / half, tok = first + tk, b = tok / p.N;
+    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : tok - b * p.N);
+    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[i - tk * half];
     // signed fraction of a turn times two, in units of pi
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
     float s, c;
@@ -574,102 +636,120 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   const int units = npair + (p.D - 2 * npair * VE) / VE;
   const int nrot = p.pairs ? p.rot / VE : npair;     // units that are rotated
   const int rows = here * heads, step = 256 / p.lanes;
+  const float over_d = 1.f / static_cast<float>(p.D);
+  const auto place = [&](int u) { return u < npair ? u * VE : (npair + u) * VE; };  // a unit's first element
   // every thread runs the same number of turns: the row sums are shuffles
-  for (int row0 = 0; row0 < rows; row0 += step) {
-    const int row = row0 + threadIdx.x / p.lanes;
-    const bool live = row < rows;
-    const int tk = live ? row / heads : 0, hh = live ? row % heads : 0;
-    const int w = hh >= p.heads[0], h = hh - (w ? p.heads[0] : 0);
-    const long long tok = first + tk;
-    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
-    const long long from = b * p.ssb[w] + n * p.ssn[w] + h * p.ssh[w];
-    const long long to = b * p.dsb[w] + n * p.dsn[w] + h * p.dsh[w];
-    float x[MAXU][2][VE];
-    float sum = 0.f;
+  for (int row0 = threadIdx.x / p.lanes; row0 - static_cast<int>(threadIdx.x) / p.lanes < rows; row0 += step * ROWS) {
+    Raw8<DT> raw[VE == 8 ? ROWS : 1][VE == 8 ? MAXU : 1][2];
+    float single[VE == 8 ? 1 : ROWS][VE == 8 ? 1 : MAXU][2][VE];
+    int tk[ROWS], w[ROWS], h[ROWS];
 #pragma unroll
-    for (int i = 0; i < MAXU; ++i) {
-      const int u = lane + i * p.lanes;
-      if (live && u < units) {
-        const int at = u < npair ? u * VE : 2 * npair * VE + (u - npair) * VE;
+    for (int e = 0; e < ROWS; ++e) {
+      const int row = row0 + e * step;
+      tk[e] = row < rows ? row / heads : -1;
+      const int hh = row - tk[e] * heads;
+      w[e] = hh >= p.heads[0], h[e] = hh - (w[e] ? p.heads[0] : 0);
+      if (tk[e] < 0) continue;
+      const long long from = s_from[tk[e]][w[e]] + h[e] * p.ssh[w[e]];
+#pragma unroll
+      for (int i = 0; i < MAXU; ++i) {
+        const int u = lane + i * p.lanes;
+        if (u >= units) continue;
         if constexpr (VE == 8) {
-          unpack8<DT>(load8<DT, true>(p.src[w], from + at), x[i][0]);
-          if (u < npair) unpack8<DT>(load8<DT, true>(p.src[w], from + at + half), x[i][1]);
+          raw[e][i][0] = load8<DT, true>(p.src[w[e]], from + place(u));
+          if (u < npair) raw[e][i][1] = load8<DT, true>(p.src[w[e]], from + place(u) + half);
         } else {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
-            x[i][0][j] = one_element<DT>(p.src[w], from + at + j);
-            if (u < npair) x[i][1][j] = one_element<DT>(p.src[w], from + at + half + j);
+            single[e][i][0][j] = one_element<DT>(p.src[w[e]], from + place(u) + j);
+            if (u < npair) single[e][i][1][j] = one_element<DT>(p.src[w[e]], from + place(u) + half + j);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          sum = fmaf(x[i][0][j], x[i][0][j], sum);
-          if (u < npair) sum = fmaf(x[i][1][j], x[i][1][j], sum);
         }
       }
     }
-    float r = 1.f;
-    if (p.norm) {
-      for (int o = p.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-    }
-    if (!live) continue;
-    const void *weight = p.weight[w];
-    const float2 *trig = s_trig + tk * half;
 #pragma unroll
-    for (int i = 0; i < MAXU; ++i) {
-      const int u = lane + i * p.lanes;
-      if (u >= units) continue;
-      const int at = u < npair ? u * VE : 2 * npair * VE + (u - npair) * VE;
-      const bool two = u < npair;
+    for (int e = 0; e < ROWS; ++e) {
+      float r = 1.f;
+      if (p.norm) {
+        float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < VE; ++j) x[i][0][j] *= r, x[i][1][j] *= r;
-      if (weight) {
-        if constexpr (VE == 8) {
-          float g[8];
-          unpack8<DT>(load8<DT, true>(weight, at), g);
+        for (int i = 0; i < MAXU; ++i) {
+          const int u = lane + i * p.lanes;
+          if (tk[e] < 0 || u >= units) continue;
+          float x[VE];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[i][0][j] *= g[j];
-          if (two) {
-            unpack8<DT>(load8<DT, true>(weight, at + half), g);
+          for (int side = 0; side < 2; ++side) {
+            if (side == 1 && u >= npair) continue;
+            if constexpr (VE == 8) unpack8<DT>(raw[e][i][side], x);
+            else
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][1][j] *= g[j];
+              for (int j = 0; j < VE; ++j) x[j] = single[e][i][side][j];
+#pragma unroll
+            for (int j = 0; j < VE; ++j) sum = fmaf(x[j], x[j], sum);
           }
+        }
+        for (int o = p.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        r = rsqrtf(fmaf(sum, over_d, p.eps));
+      }
+      if (tk[e] < 0) continue;
+      const void *weight = p.weight[w[e]];
+      const float2 *trig = s_trig + tk[e] * half;
+      const long long to = s_to[tk[e]][w[e]] + h[e] * p.dsh[w[e]];
+#pragma unroll
+      for (int i = 0; i < MAXU; ++i) {
+        const int u = lane + i * p.lanes;
+        if (u >= units) continue;
+        const int at = place(u);
+        const bool two = u < npair;
+        float x[2][VE];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          if (side == 1 && !two) continue;
+          if constexpr (VE == 8) unpack8<DT>(raw[e][i][side], x[side]);
+          else
+#pragma unroll
+            for (int j = 0; j < VE; ++j) x[side][j] = single[e][i][side][j];
+          if (weight) {
+            float g[VE];
+            if constexpr (VE == 8) unpack8<DT>(load8<DT, true>(weight, at + side * half), g);
+            else
+#pragma unroll
+              for (int j = 0; j < VE; ++j) g[j] = one_element<DT>(weight, at + side * half + j);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) x[side][j] *= r * g[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) x[side][j] *= r;
+          }
+        }
+        if (two) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float2 cs = trig[at + j];
+            const float a = x[0][j], c = x[1][j];
+            x[0][j] = a * cs.x - c * cs.y;
+            x[1][j] = c * cs.x + a * cs.y;
+          }
+        } else if (u < nrot) {
+          if constexpr (VE > 1) {
+#pragma unroll
+            for (int j = 0; j < VE; j += 2) {
+              const float2 cs = trig[(at + j) / 2];
+              const float a = x[0][j], c = x[0][j + 1];
+              x[0][j] = a * cs.x - c * cs.y;
+              x[0][j + 1] = c * cs.x + a * cs.y;
+            }
+          }
+        }
+        if constexpr (VE == 8) {
+          store8<DT, true>(p.dst[w[e]], to + at, pack8<DT>(x[0]));
+          if (two) store8<DT, true>(p.dst[w[e]], to + at + half, pack8<DT>(x[1]));
         } else {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
-            x[i][0][j] *= one_element<DT>(weight, at + j);
-            if (two) x[i][1][j] *= one_element<DT>(weight, at + half + j);
+            put_element<DT>(p.dst[w[e]], to + at + j, x[0][j]);
+            if (two) put_element<DT>(p.dst[w[e]], to + at + half + j, x[1][j]);
           }
-        }
-      }
-      if (two) {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float2 cs = trig[at + j];
-          const float a = x[i][0][j], c = x[i][1][j];
-          x[i][0][j] = a * cs.x - c * cs.y;
-          x[i][1][j] = c * cs.x + a * cs.y;
-        }
-      } else if (u < nrot) {
-        if constexpr (VE > 1) {
-#pragma unroll
-          for (int j = 0; j < VE; j += 2) {
-            const float2 cs = trig[(at + j) / 2];
-            const float a = x[i][0][j], c = x[i][0][j + 1];
-            x[i][0][j] = a * cs.x - c * cs.y;
-            x[i][0][j + 1] = c * cs.x + a * cs.y;
-          }
-        }
-      }
-      if constexpr (VE == 8) {
-        store8<DT, true>(p.dst[w], to + at, pack8<DT>(x[i][0]));
-        if (two) store8<DT, true>(p.dst[w], to + at + half, pack8<DT>(x[i][1]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          put_element<DT>(p.dst[w], to + at + j, x[i][0][j]);
-          if (two) put_element<DT>(p.dst[w], to + at + half + j, x[i][1][j]);
         }
       }
     }

@@ -80,13 +80,15 @@ const void *pick_write(bool small, bool vec) {
              : reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, false>);
 }
 
-// vec: units of eight elements (lanes * 2 of them in a row at most 64);
-// otherwise single elements, or two for neighbouring pairs.
+// vec: units of eight elements, at most two to a thread; `one`: one to a
+// thread, then two rows are in flight.  Otherwise single elements, or two for
+// neighbouring pairs.
 template <int DT>
-const void *pick_norm_rope(bool vec, bool pairs) {
-  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2>);
-  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8>)
-               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16>);
+const void *pick_norm_rope(bool vec, bool one, bool pairs) {
+  if (vec) return one ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 1, 2>)
+                      : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2, 1>);
+  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8, 1>)
+               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16, 1>);
 }
 
 // The attention's kernel, its block and shared memory, and the floats of its
@@ -176,13 +178,13 @@ int spec_qk_norm_rope(const spec_heads_t *q, const spec_heads_t *k, const spec_h
   const int npair = pairs ? 0 : rot / 2 / ve, units = npair + (D - 2 * npair * ve) / ve;
   p.lanes = 1;
   while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
-  // four tokens to a CTA share a few turns of its row loop, unless that leaves
-  // SMs without a CTA
+  // several tokens to a CTA, so that its set-up is a small part, as long as
+  // every SM still has several CTAs
   const long long tokens = static_cast<long long>(B) * N;
-  p.per_cta = tokens >= 16LL * num_sms() ? 4 : 1;
-  const void *fn = dtype == SPEC_F32    ? pick_norm_rope<DT_F32>(vec, pairs)
-                   : dtype == SPEC_BF16 ? pick_norm_rope<DT_BF16>(vec, pairs)
-                                        : pick_norm_rope<DT_F16>(vec, pairs);
+  p.per_cta = static_cast<int>(std::max(1LL, std::min<long long>(ROPE_TOKENS, tokens / (8LL * num_sms()))));
+  const void *fn = dtype == SPEC_F32    ? pick_norm_rope<DT_F32>(vec, units <= p.lanes, pairs)
+                   : dtype == SPEC_BF16 ? pick_norm_rope<DT_BF16>(vec, units <= p.lanes, pairs)
+                                        : pick_norm_rope<DT_F16>(vec, units <= p.lanes, pairs);
   return launch(fn, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta)), 256,
                 p.per_cta * (rot / 2) * static_cast<int>(sizeof(float2)), static_cast<cudaStream_t>(stream_ptr), &p,
                 "norm_rope_kernel launch");
@@ -316,7 +318,8 @@ int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int 
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if ((st = get_ws(stream, 1, &w))) return st;
   p.status = w->status;
-  return launch(reinterpret_cast<const void *>(&cache_commit_kernel), dim3(static_cast<unsigned>(2 * p.c.Hk), static_cast<unsigned>(B)), 256, 0,
+  const int share = (2 * p.c.Hk + 7) / 8;  // a warp for each kv head and tensor
+  return launch(reinterpret_cast<const void *>(&cache_commit_kernel), dim3(static_cast<unsigned>(share), static_cast<unsigned>(B)), 256, 0,
                 stream, &p, "cache_commit_kernel launch");
 }
 
