@@ -756,4 +756,117 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   }
 }
 
+// The same for rows of whole vectors with one unit to a thread, which is every
+// usual head: two rows in flight, the weights in registers, a CTA for the
+// queries or the keys of its tokens (blockIdx.y).  What a row costs is instructions (about
+// 100 a vector), so nothing is divided or looked up per row.
+template <int DT, bool PAIRS>
+__global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ NormRopeParams p) {
+  extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
+  __shared__ long long s_from[ROPE_TOKENS], s_to[ROPE_TOKENS];
+  const int w = p.heads[0] == 0 || blockIdx.y == 1;  // queries or keys
+  const int half = p.rot / 2;
+  const int tokens = p.B * p.N, first = blockIdx.x * p.per_cta, here = min(p.per_cta, tokens - first);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x < here) {
+    const int tk = threadIdx.x, b = (first + tk) / p.N, n = (first + tk) - b * p.N;
+    s_from[tk] = b * p.ssb[w] + n * p.ssn[w];
+    s_to[tk] = b * p.dsb[w] + n * p.dsn[w];
+  }
+  const int u = threadIdx.x & (p.lanes - 1), npair = PAIRS ? 0 : half / 8;
+  const bool live = u < npair + (p.D - 16 * npair) / 8, two = u < npair;
+  const int at = two || PAIRS ? u * 8 : (npair + u) * 8;  // the unit's first element
+  const bool turned = PAIRS ? at < p.rot : two;
+  float g[2][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[0][j] = g[1][j] = 1.f;
+  if (p.weight[w] && live) {
+    unpack8<DT>(load8<DT, true>(p.weight[w], at), g[0]);
+    if (two) unpack8<DT>(load8<DT, true>(p.weight[w], at + half), g[1]);
+  }
+  for (int i = threadIdx.x; i < here * half; i += 256) {
+    const int tk = i / half, tok = first + tk, b = tok / p.N;
+    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : tok - b * p.N);
+    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[i - tk * half];
+    // signed fraction of a turn times two, in units of pi
+    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+    float s, c;
+    sincospif(x, &s, &c);
+    s_trig[i] = make_float2(c, s);
+  }
+  __syncthreads();
+  const float over_d = 1.f / static_cast<float>(p.D);
+  const int step = 256 / p.lanes, row0 = threadIdx.x / p.lanes;
+  const int heads = p.heads[w];
+  {
+    const void *const src = p.src[w];
+    void *const dst = p.dst[w];
+    const long long ssh = p.ssh[w], dsh = p.dsh[w];
+    const int step_tk = step / heads, step_h = step - step_tk * heads;
+    int tk = row0 / heads, h = row0 - tk * heads;
+    // every thread runs the same number of turns: the row sums are shuffles
+    for (int left = here * heads; left > 0; left -= 2 * step) {
+      float x[2][2][8];
+      int tks[2], hs[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        tks[e] = tk, hs[e] = h;
+        tk += step_tk, h += step_h;
+        if (h >= heads) h -= heads, ++tk;
+        Raw8<DT> r[2];
+#pragma unroll
+        for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) r[0].v[i] = r[1].v[i] = make_uint4(0, 0, 0, 0);
+        if (live && tks[e] < here) {
+          const long long from = s_from[tks[e]] + hs[e] * ssh + at;
+          r[0] = load8<DT, true>(src, from);
+          if (two) r[1] = load8<DT, true>(src, from + half);
+        }
+        unpack8<DT>(r[0], x[e][0]);
+        if (!PAIRS) unpack8<DT>(r[1], x[e][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (p.norm) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sum = fmaf(x[e][0][j], x[e][0][j], sum);
+            if (!PAIRS) sum = fmaf(x[e][1][j], x[e][1][j], sum);
+          }
+          for (int o = p.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float r = rsqrtf(fmaf(sum, over_d, p.eps));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[e][0][j] *= r * g[0][j];
+            if (!PAIRS) x[e][1][j] *= r * g[1][j];
+          }
+        }
+        if (!live || tks[e] >= here) continue;
+        const float4 *trig = reinterpret_cast<const float4 *>(s_trig + tks[e] * half + (PAIRS ? at / 2 : at));
+        if (turned) {
+#pragma unroll
+          for (int j = 0; j < (PAIRS ? 2 : 4); ++j) {  // two angles at a time
+            const float4 cs = trig[j];
+            if (PAIRS) {
+              float *y = x[e][0] + 4 * j;
+              const float a = y[0], b = y[1], c = y[2], d = y[3];
+              y[0] = a * cs.x - b * cs.y, y[1] = b * cs.x + a * cs.y;
+              y[2] = c * cs.z - d * cs.w, y[3] = d * cs.z + c * cs.w;
+            } else {
+              float *y = x[e][0] + 2 * j, *z = x[e][1] + 2 * j;
+              const float a = y[0], b = z[0], c = y[1], d = z[1];
+              y[0] = a * cs.x - b * cs.y, z[0] = b * cs.x + a * cs.y;
+              y[1] = c * cs.z - d * cs.w, z[1] = d * cs.z + c * cs.w;
+            }
+          }
+        }
+        const long long to = s_to[tks[e]] + hs[e] * dsh + at;
+        store8<DT, true>(dst, to, pack8<DT>(x[e][0]));
+        if (two) store8<DT, true>(dst, to + half, pack8<DT>(x[e][1]));
+      }
+    }
+  }
+}
+
 }  // namespace spec

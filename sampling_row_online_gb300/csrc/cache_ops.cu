@@ -81,12 +81,13 @@ const void *pick_write(bool small, bool vec) {
 }
 
 // vec: units of eight elements, at most two to a thread; `one`: one to a
-// thread, then two rows are in flight.  Otherwise single elements, or two for
-// neighbouring pairs.
+// thread.  Otherwise single elements, or two for neighbouring pairs.
 template <int DT>
 const void *pick_norm_rope(bool vec, bool one, bool pairs) {
-  if (vec) return one ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 1, 2>)
-                      : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2, 1>);
+  if (vec && one)
+    return pairs ? reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, true>)
+                 : reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, false>);
+  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2, 1>);
   return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8, 1>)
                : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16, 1>);
 }
@@ -178,14 +179,16 @@ int spec_qk_norm_rope(const spec_heads_t *q, const spec_heads_t *k, const spec_h
   const int npair = pairs ? 0 : rot / 2 / ve, units = npair + (D - 2 * npair * ve) / ve;
   p.lanes = 1;
   while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
-  // several tokens to a CTA, so that its set-up is a small part, as long as
-  // every SM still has several CTAs
-  const long long tokens = static_cast<long long>(B) * N;
-  p.per_cta = static_cast<int>(std::max(1LL, std::min<long long>(ROPE_TOKENS, tokens / (8LL * num_sms()))));
+  // norm_rope_rows_kernel has a CTA each for a token's queries and keys
+  const unsigned tensors = vec && units <= p.lanes && Hq > 0 && Hk > 0 ? 2 : 1;
+  // one wave of four CTAs per SM where that is at most ROPE_TOKENS tokens to a
+  // CTA: its set-up is a small part then
+  const long long tokens = static_cast<long long>(B) * N, wave = 4LL * num_sms();
+  p.per_cta = static_cast<int>(std::min<long long>(ROPE_TOKENS, (tokens * tensors + wave - 1) / wave));
   const void *fn = dtype == SPEC_F32    ? pick_norm_rope<DT_F32>(vec, units <= p.lanes, pairs)
                    : dtype == SPEC_BF16 ? pick_norm_rope<DT_BF16>(vec, units <= p.lanes, pairs)
                                         : pick_norm_rope<DT_F16>(vec, units <= p.lanes, pairs);
-  return launch(fn, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta)), 256,
+  return launch(fn, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta), tensors), 256,
                 p.per_cta * (rot / 2) * static_cast<int>(sizeof(float2)), static_cast<cudaStream_t>(stream_ptr), &p,
                 "norm_rope_kernel launch");
 }
