@@ -290,11 +290,11 @@ struct CacheWriteParams {
 
 // One CTA per (block that the new rows may touch, kv head and tensor,
 // sequence).  The new rows of the block are read once and kept in registers
-// (at most 64 elements a thread), their maximum gives the scale, and the
+// (MOST chunks of eight a thread), their maximum gives the scale, and the
 // codes follow: 3 bytes of traffic per 16-bit element, the floor.  The block
 // is re-read only where its scale grows under rows that it already holds.
-template <int DT, int NTH, bool VEC>
-__global__ void __launch_bounds__(NTH) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
+template <int DT, int NTH, int MOST, bool VEC>
+__global__ void __launch_bounds__(NTH, NTH == 256 && DT != DT_F32 ? (MOST == 4 ? 5 : 4) : 1) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
   __shared__ uint32_t s_max[NTH / 32];
   const CacheView &c = p.c;
   const int b = blockIdx.z, h = blockIdx.y >> 1, t = blockIdx.y & 1;
@@ -317,15 +317,14 @@ __global__ void __launch_bounds__(NTH) cache_write_kernel(const __grid_constant_
   const bool empty = first >= start;  // the block holds nothing before the new rows
   const float old = empty ? 0.f : *scale_at;
 
-  constexpr int MOST = 8;  // chunks of eight elements per thread
-  const int per_row = c.D / 8, chunks = (hi - lo) * per_row;
-  const long long base = b * p.sb[t] + h * p.sh[t];
+  const int log_row = c.D == 128 ? 4 : 3, chunks = (hi - lo) << log_row;  // 16 or 8 chunks to a row
+  const int row0 = threadIdx.x >> log_row, col = (threadIdx.x & ((1 << log_row) - 1)) * 8;
+  // a thread's chunks are NTH / 16 or NTH / 8 rows apart
+  const long long base = b * p.sb[t] + h * p.sh[t] + (lo - start + row0) * p.sn[t] + col, apart = (NTH >> log_row) * p.sn[t];
   Raw8<DT> raw[MOST];
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
-    const int k = threadIdx.x + i * NTH;
-    if (k < chunks)
-      raw[i] = load8<DT, VEC>(p.src[t], base + (lo - start + k / per_row) * p.sn[t] + (k % per_row) * 8);
+    if (threadIdx.x + i * NTH < chunks) raw[i] = load8<DT, VEC>(p.src[t], base + i * apart);
   }
   uint32_t amax = 0;
 #pragma unroll
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(NTH) cache_write_kernel(const __grid_constant_
       const int k = threadIdx.x + i * NTH;
       if (k >= chunks) break;
       float x[8];
-      unpack8<DT>(load8<DT, VEC>(p.src[t], base + (lo - start + k / per_row) * p.sn[t] + (k % per_row) * 8), x);
+      unpack8<DT>(load8<DT, VEC>(p.src[t], base + i * apart), x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t y = __float_as_uint(x[j]) & 0x7fffffffu;

@@ -72,12 +72,15 @@ int check_cache(const spec_cache_t *c, const int32_t *table, int per, int B, Cac
 // Blocks that n rows from any slot on can touch.
 unsigned blocks_of(int n, int page) { return static_cast<unsigned>((static_cast<long long>(n) + page - 2) / page + 1); }
 
+// rows * D elements of a block: one warp up to 2048, a CTA up to 8192 or 16384.
 template <int DT>
-const void *pick_write(bool small, bool vec) {
-  if (small) return vec ? reinterpret_cast<const void *>(&cache_write_kernel<DT, 32, true>)
-                        : reinterpret_cast<const void *>(&cache_write_kernel<DT, 32, false>);
-  return vec ? reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, true>)
-             : reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, false>);
+const void *pick_write(int elements, bool vec) {
+  if (elements <= 2048) return vec ? reinterpret_cast<const void *>(&cache_write_kernel<DT, 32, 8, true>)
+                                   : reinterpret_cast<const void *>(&cache_write_kernel<DT, 32, 8, false>);
+  if (elements <= 8192) return vec ? reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, 4, true>)
+                                   : reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, 4, false>);
+  return vec ? reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, 8, true>)
+             : reinterpret_cast<const void *>(&cache_write_kernel<DT, 256, 8, false>);
 }
 
 // vec: units of eight elements, at most two to a thread; `one`: one to a
@@ -218,12 +221,11 @@ int spec_cache_write(const spec_cache_t *cache, const int32_t *page_table, int p
   if ((st = get_ws(stream, 1, &w))) return st;
   p.status = w->status;
   const bool vec = vectors(*k, esz) && vectors(*v, esz);
-  // a thread keeps at most 64 elements: one warp where a block's rows fit it
-  const bool small = std::min(N, p.c.page) * p.c.D <= 32 * 64;
-  const void *fn = dtype == SPEC_F32    ? pick_write<DT_F32>(small, vec)
-                   : dtype == SPEC_BF16 ? pick_write<DT_BF16>(small, vec)
-                                        : pick_write<DT_F16>(small, vec);
-  return launch(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(2 * p.c.Hk), static_cast<unsigned>(B)), small ? 32 : 256, 0,
+  const int elements = std::min(N, p.c.page) * p.c.D;  // of a block at most
+  const void *fn = dtype == SPEC_F32    ? pick_write<DT_F32>(elements, vec)
+                   : dtype == SPEC_BF16 ? pick_write<DT_BF16>(elements, vec)
+                                        : pick_write<DT_F16>(elements, vec);
+  return launch(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(2 * p.c.Hk), static_cast<unsigned>(B)), elements <= 2048 ? 32 : 256, 0,
                 stream, &p, "cache_write_kernel launch");
 }
 
