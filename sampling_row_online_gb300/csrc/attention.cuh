@@ -99,6 +99,14 @@ __device__ __forceinline__ void pairs_across(uint32_t a, uint32_t b, uint32_t &l
   }
 }
 
+// An 8 x 8 tile of 16-bit elements, transposed: lane 4 g + t gives row g,
+// columns 2 t and 2 t + 1, and gets those of the transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -192,36 +200,34 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // order, and every warp of the grid takes an equal stretch of it, so ragged
 // lengths need no schedule.  A warp copies the steps ahead into a ring with
 // cp.async; every lane reads back only what it copied itself, so the loop has
-// no barrier at all.  The m16n8k16 fragments allow any order of the contracted
-// index: a lane's 16 bytes of a key row serve four k-steps, and its 16 bytes
-// of each of four value rows serve 16 column tiles, so nothing is exchanged
-// and nothing is transposed; the weights go from the accumulators of the first
-// product to the operand of the second in registers.  RT tiles of 16 rows
-// share the converted codes.
+// no barrier at all.
+//
+// Tokens are the 16 rows of the m16n8k16 products and query rows their 8
+// columns (RT tiles of them): S^T = K Q^T, O^T += V^T P^T.  So the codes are
+// operand A, converted once for all rows, and one token's 8 or fewer rows
+// waste nothing.  The fragments allow any order of the contracted index and of
+// the rows: a lane's 16 bytes of a key row serve four k-steps, its 16 bytes of
+// each of four value rows serve 8 tiles of 16 columns, and only the weights are
+// exchanged between the lanes, by a transpose of 8 x 8 tiles.
 //
 // A stretch that ends inside a segment (the rows of a kv head) leaves a piece
 // (out, offset, sum); the CTA merges the pieces of its warps, and the last CTA
 // to arrive at a segment merges those of its CTAs in index order.
-constexpr int AW = 8;            // warps
-constexpr int ANT = 32 * AW;
-constexpr int ASTAGES = 4;       // steps in flight per warp
+constexpr int ASTAGES = 2;       // steps in flight per warp
 constexpr int ASTEP = 16;        // tokens per step
-constexpr int ALEAST = 4;        // steps per warp at least, before more CTAs take part
+constexpr int ALEAST = 2;        // steps per warp at least, before more CTAs take part
 
 template <int D, int RT>
 struct StreamLayout {
-  static constexpr int SUB = RT == 1 ? 2 : 1;                    // steps per turn of the loop
+  // as many warps as the registers allow (128 and 168 a thread): what a step
+  // costs is the latency of its dependent instructions
+  static constexpr int WARPS = RT == 1 ? 16 : 12, THREADS = 32 * WARPS;
   static constexpr int KB = ASTEP * D, STAGE = 2 * KB + 256;     // codes of keys and values, scales
-  static constexpr int ROWS = 16 * RT;
+  static constexpr int ROWS = 8 * RT;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;              // floats: out, offset, sum
-  static constexpr int RING = AW * ASTAGES * STAGE;
-  // one tile of rows: its queries stay in registers, and the first pieces of
-  // the warps in shared memory; with two the queries take that room, and the
-  // first pieces go through the workspace
-  static constexpr int QBYTES = RT == 1 ? 0 : RT * (D / 16) * 512;  // fragments per warp
-  static constexpr int SMEM = RING + AW * (RT == 1 ? PIECE * 4 : QBYTES);
-  static constexpr int SHARED = 2 * PIECE;                       // floats per CTA that other CTAs read
-  static constexpr int WORK = SHARED + (RT == 1 ? 0 : AW * PIECE);
+  static constexpr int RING = WARPS * ASTAGES * STAGE;
+  static constexpr int SMEM = RING + WARPS * PIECE * 4;          // and the warps' first pieces
+  static constexpr int WORK = 2 * PIECE;                         // floats per CTA that other CTAs read
   static_assert(PIECE * 4 <= ASTAGES * STAGE, "a warp's last piece lies in its own ring");
 };
 
@@ -246,9 +252,10 @@ __device__ __forceinline__ void put_lse(const AttnParams &p, const Segment &g, i
 }
 
 template <int D, int KIND, int DT, int RT>
-__global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, 1) attn_stream_kernel(const __grid_constant__ AttnParams p) {
   using L = StreamLayout<D, RT>;
-  constexpr int CH = D / 64, NT8 = D / 8, SUB = L::SUB;  // 16-byte chunks of a key row per lane; column tiles
+  constexpr int AW = L::WARPS, ANT = L::THREADS;
+  constexpr int CH = D / 64, VB = D / 8, MT = D / 16;  // 16-byte chunks of a key row, bytes of a value row per lane; column tiles
   const float NINF = __uint_as_float(0xff800000u);
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Segment s_seg[2 * AW];
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     upto = total + block_scan<AW>(w, s_scan, sum);
     total += sum;
   }
-  // fewer CTAs where a warp's stretch would be a step or two
+  // fewer CTAs where a warp's stretch would be a step
   const unsigned nc = min(gridDim.x, (total + AW * ALEAST - 1) / (AW * ALEAST));
   if (__syncthreads_or(rest)) fill_rest<DT, ANT>(p, D);
   if (blockIdx.x >= nc) return;
@@ -302,8 +309,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   unsigned char *const ring_ptr = smem + warp * ASTAGES * L::STAGE;
   const uint32_t ring = smem_u32(ring_ptr);
   float *const work = p.pieces + static_cast<long long>(blockIdx.x) * L::WORK;
-  float *const first_slot = RT == 1 ? reinterpret_cast<float *>(smem + L::RING) + warp * L::PIECE : work + L::SHARED + warp * L::PIECE;
-  uint4 *const q_slot = reinterpret_cast<uint4 *>(smem + L::RING + warp * L::QBYTES);
+  float *const first_slot = reinterpret_cast<float *>(smem + L::RING) + warp * L::PIECE;
   const unsigned my0 = share.start(blockIdx.x * AW + warp);
   const int mine = static_cast<int>(share.start(blockIdx.x * AW + warp + 1) - my0);
   if (lane < 2) s_has[2 * warp + lane] = 0;
@@ -337,11 +343,20 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       at.h = static_cast<int>(r / at.steps);
       at.step = static_cast<int>(r) - at.h * at.steps;
     }
+    // the first segment's queries come closer while the copies are set up
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = 8 * rt + g;
+      if (r < at.cnt * p.G)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t *>(p.q) + at.b * p.q_sb + (r / p.G) * p.q_sn +
+                                                      (at.h * p.G + r % p.G) * p.q_sh + t * (D / 4)));
+    }
     Cursor is = at;  // what is copied ahead
     int copied = 0;
     int held_b = -1, held_p = 0, held = 0;  // page ids held_p + lane of sequence held_b
     const unsigned char *kp = nullptr, *vp = nullptr;
-    const float *ksp = nullptr, *vsp = nullptr;
+    const float *scales = nullptr;
+    long long vs_off = c.v_scale - c.k_scale;
     bool bad = false, fresh = true;  // fresh: another page, or its first step
 
     const auto copy_step = [&]() {
@@ -360,22 +375,23 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
           if (bad) page = 0;
           const long long id = static_cast<long long>(page) * c.Hk + is.h;
           const long long off = (id * c.page + in) * D;
-          kp = c.k + off + (4 * (g >> 1) + (g & 1)) * D + 16 * t;
-          vp = c.v + off + 4 * t * D + g * NT8;
-          ksp = c.k_scale + id, vsp = c.v_scale + id;
+          kp = c.k + off + g * D + 16 * t;
+          vp = c.v + off + 2 * t * D + g * VB;
+          scales = c.k_scale + id;
           fresh = false;
         }
         const uint32_t dst = ring + copied % ASTAGES * L::STAGE;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)  // tokens g and g + 8
 #pragma unroll
-          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, kp + 2 * i * D + 64 * j);
+          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, kp + 8 * i * D + 64 * j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async<NT8>(dst + L::KB + (i * 32 + lane) * NT8, vp + i * D);
+        for (int i = 0; i < 4; ++i)  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          cp_async<VB>(dst + L::KB + (i * 32 + lane) * VB, vp + ((i & 1) + 8 * (i >> 1)) * D);
         const uint32_t sc = dst + 2 * L::KB + lane * 8;
         if (!bad) {
-          cp_async<4>(sc, ksp);
-          cp_async<4>(sc + 4, vsp);
+          cp_async<4>(sc, scales);
+          cp_async<4>(sc + 4, scales + vs_off);
         } else {  // a NaN scale makes the rows NaN
           if (lane == 0) atomicOr(p.status, ST_PAGE);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sc), "r"(0x7fc00000u), "r"(0x3f800000u) : "memory");
@@ -386,14 +402,6 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       ++copied;
       cp_async_commit();
     };
-    // the first segment's queries come closer while the copies are set up
-#pragma unroll
-    for (int rt = 0; rt < 2 * RT; ++rt) {
-      const int r = 8 * rt + g;
-      if (r < at.cnt * p.G)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint16_t *>(p.q) + at.b * p.q_sb + (r / p.G) * p.q_sn +
-                                                      (at.h * p.G + r % p.G) * p.q_sh + t * (D / 4)));
-    }
 #pragma unroll 1
     for (int i = 0; i < ASTAGES; ++i) copy_step();
 
@@ -407,285 +415,214 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
       seg.s1 = min(at.steps, at.step + mine - now);
       const int rows = at.cnt * p.G;
 
-      // queries as fp16 fragments with a power of two per row
-      uint32_t qf[RT == 1 ? CH * 4 : 1][4];
+      // queries as fp16 fragments with a power of two per row: a lane loads of
+      // row g, and looks after the scores of rows 2 t and 2 t + 1
+      uint32_t qf[RT][CH * 4][2];
       float fac[RT][2];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        uint32_t f[CH * 4][4];
+        const int r = 8 * rt + g;
+        const bool live = r < rows;
+        const long long base = live ? at.b * p.q_sb + (r / p.G) * p.q_sn + (at.h * p.G + r % p.G) * p.q_sh + 16 * t : 0;
+        Raw8<DT> raw[CH][2];
+        float amax = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = 16 * rt + g + 8 * half;
-          const bool live = r < rows;
-          const long long base = live ? at.b * p.q_sb + (r / p.G) * p.q_sn + (at.h * p.G + r % p.G) * p.q_sh + 16 * t : 0;
-          float x[CH][16];
-          float amax = 0.f;
+        for (int i = 0; i < CH; ++i)
 #pragma unroll
-          for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              Raw8<DT> raw;
-              raw.v[0] = make_uint4(0, 0, 0, 0);
-              if (live) raw = p.q_vec ? load8<DT, true>(p.q, base + 64 * i + 8 * w) : load8<DT, false>(p.q, base + 64 * i + 8 * w);
-              float y[8];
-              unpack8<DT>(raw, y);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                x[i][8 * w + j] = y[j];
-                amax = fmaxf(amax, fabsf(y[j]));
-              }
-            }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          // amax * 2^-e lies in [1, 2)
-          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          fac[rt][half] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
-#pragma unroll
-          for (int i = 0; i < CH; ++i)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              f[i * 4 + w][half] = f32_to_f16x2(x[i][4 * w] * down, x[i][4 * w + 1] * down);
-              f[i * 4 + w][2 + half] = f32_to_f16x2(x[i][4 * w + 2] * down, x[i][4 * w + 3] * down);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < CH * 4; ++k) {
-          if constexpr (RT == 1) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) qf[k][j] = f[k][j];
-          } else {  // a lane reads back only its own
-            q_slot[(rt * CH * 4 + k) * 32 + lane] = make_uint4(f[k][0], f[k][1], f[k][2], f[k][3]);
+          for (int e = 0; e < 2; ++e) {
+            raw[i][e].v[0] = make_uint4(0, 0, 0, 0);
+            if (live) raw[i][e] = p.q_vec ? load8<DT, true>(p.q, base + 64 * i + 8 * e) : load8<DT, false>(p.q, base + 64 * i + 8 * e);
           }
-        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y[8];
+            unpack8<DT>(raw[i][e], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // amax * 2^-e lies in [1, 2)
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+        fac[rt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+        fac[rt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            float y[8];
+            unpack8<DT>(raw[i][w >> 1], y);
+            const float *z = y + 4 * (w & 1);
+            qf[rt][4 * i + w][0] = f32_to_f16x2(z[0] * down, z[1] * down);
+            qf[rt][4 * i + w][1] = f32_to_f16x2(z[2] * down, z[3] * down);
+          }
       }
-      float o[RT][NT8][4];
+      float o[RT][MT][4];
       // exponents' offset (as subtracted: 0 for -inf), sum; the same over blocks without values
       float m[RT][2], base_m[RT][2], l[RT][2], m0[RT][2], l0[RT][2];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-        for (int j = 0; j < NT8; ++j) o[rt][j][0] = o[rt][j][1] = o[rt][j][2] = o[rt][j][3] = 0.f;
+        for (int j = 0; j < MT; ++j) o[rt][j][0] = o[rt][j][1] = o[rt][j][2] = o[rt][j][3] = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) m[rt][half] = m0[rt][half] = NINF, base_m[rt][half] = l[rt][half] = l0[rt][half] = 0.f;
+        for (int e = 0; e < 2; ++e) m[rt][e] = m0[rt][e] = NINF, base_m[rt][e] = l[rt][e] = l0[rt][e] = 0.f;
       }
 
-      for (int step = seg.s0; step < seg.s1;) {
-        const int nsub = min(SUB, seg.s1 - step);
-        cp_async_wait<ASTAGES - SUB>();
-        const unsigned char *st[SUB];
-        float2 sc[SUB];
-        // scores: two tiles of 8 tokens a step; column n of tile i is token
-        // 4 (n / 2) + n % 2 + 2 i, so a lane holds tokens 4 t .. 4 t + 3
-        float s[SUB][RT][2][4];
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          st[u] = ring_ptr + (now + u) % ASTAGES * L::STAGE;
-          sc[u] = *reinterpret_cast<const float2 *>(st[u] + 2 * L::KB + lane * 8);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) s[u][rt][i][0] = s[u][rt][i][1] = s[u][rt][i][2] = s[u][rt][i][3] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          uint32_t aw[SUB][2][4];
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 a = lds128(st[u] + ((i * CH + j) * 32 + lane) * 16);
-              aw[u][i][0] = a.x, aw[u][i][1] = a.y, aw[u][i][2] = a.z, aw[u][i][3] = a.w;
-            }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t q[RT][4];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              if constexpr (RT == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) q[rt][e] = qf[4 * j + w][e];
-              } else {
-                const uint4 a = lds128(q_slot + (rt * CH * 4 + 4 * j + w) * 32 + lane);
-                q[rt][0] = a.x, q[rt][1] = a.y, q[rt][2] = a.z, q[rt][3] = a.w;
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t b0, b1;
-                pairs_of<KIND>(KIND == KIND_I8 ? aw[u][i][w] ^ 0x80808080u : aw[u][i][w], b0, b1);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) mma16816(s[u][rt][i], q[rt], b0, b1);
-              }
-          }
-        }
-        // new tokens, slots past the last one, or a step that is not there
-        const bool edge = (step + SUB) * ASTEP > at.ctx || nsub < SUB;
-        bool zero[SUB];
-        float lv[SUB], rv[SUB];
-        float x[SUB][RT][2][4];  // row g or g + 8, token 4 t + j
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          zero[u] = sc[u].y <= LEAST_V_SCALE;  // no values in this block: it counts in a sum of its own
-          lv[u] = zero[u] ? 0.f : lg2(sc[u].y), rv[u] = u < nsub ? 1.f / sc[u].y : 0.f;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float f = fac[rt][half] * sc[u].x;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x[u][rt][half][j] = fmaf(s[u][rt][j >> 1][2 * half + (j & 1)], f, lv[u]);
-            }
-        }
-        if (edge) {
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int node = min((16 * rt + g + 8 * half) / p.G, p.N - 1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int n = (step + u) * ASTEP + 4 * t + j - at.ctx;
-                  bool seen = n < 0;
-                  if (n >= 0 && n < at.cnt)
-                    seen = p.mask ? (p.mask[(static_cast<long long>(at.b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
-                  if (!seen || u >= nsub) x[u][rt][half][j] = NINF;
-                }
-              }
-        }
-        bool any_zero = false;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) any_zero |= u < nsub && zero[u];
-        if (any_zero) {
-#pragma unroll
-          for (int u = 0; u < SUB; ++u) {
-            if (u >= nsub || !zero[u]) continue;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                float(&y)[4] = x[u][rt][half];
-                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float nm = fmaxf(m0[rt][half], top), nb = nm == NINF ? 0.f : nm;
-                l0[rt][half] *= ex2(m0[rt][half] - nb);
-                m0[rt][half] = nm;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) l0[rt][half] += ex2(y[j] - nb), y[j] = NINF;
-              }
-            rv[u] = 0.f;
-          }
-        }
-        // the offset moves only when a weight would pass 2^15.9
-        bool up = false;
-        float top[RT][2];
+      for (int step = seg.s0; step < seg.s1; ++step, ++now, ++at.step) {
+        cp_async_wait<ASTAGES - 1>();
+        const unsigned char *st = ring_ptr + now % ASTAGES * L::STAGE;
+        const float2 sc = *reinterpret_cast<const float2 *>(st + 2 * L::KB + lane * 8);
+        // scores of tokens g (0, 1) and g + 8 (2, 3) and rows 2 t, 2 t + 1; two chains of products
+        float s[RT][CH][4];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float v = NINF;
+          for (int j = 0; j < CH; ++j) s[rt][j][0] = s[rt][j][1] = s[rt][j][2] = s[rt][j][3] = 0.f;
+        uint32_t kw[CH][2][4];
 #pragma unroll
-            for (int u = 0; u < SUB; ++u)
+        for (int j = 0; j < CH; ++j)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v = fmaxf(v, x[u][rt][half][j]);
-            top[rt][half] = v;
-            up |= v > m[rt][half] + (WEIGHT_UP + WEIGHT_SLACK);
+          for (int i = 0; i < 2; ++i) {
+            const uint4 a = lds128(st + ((i * CH + j) * 32 + lane) * 16);
+            kw[j][i][0] = a.x, kw[j][i][1] = a.y, kw[j][i][2] = a.z, kw[j][i][3] = a.w;
           }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            uint32_t a[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pairs_of<KIND>(KIND == KIND_I8 ? kw[j][i][w] ^ 0x80808080u : kw[j][i][w], a[i], a[2 + i]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) mma16816(s[rt][j], a, qf[rt][4 * j + w][0], qf[rt][4 * j + w][1]);
+          }
+        const bool edge = (step + 1) * ASTEP > at.ctx;  // new tokens, or slots past the last one
+        const bool zero = sc.y <= LEAST_V_SCALE;        // no values in this block: it counts in a sum of its own
+        const float lv = zero ? 0.f : lg2(sc.y), rv = 1.f / sc.y;
+        float x[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = fac[rt][j & 1] * sc.x;
+            x[rt][j] = fmaf(CH == 2 ? s[rt][0][j] + s[rt][CH - 1][j] : s[rt][0][j], f, lv);
+          }
+        if (edge) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int node = min((8 * rt + 2 * t + (j & 1)) / p.G, p.N - 1), n = step * ASTEP + g + 8 * (j >> 1) - at.ctx;
+              bool seen = n < 0;
+              if (n >= 0 && n < at.cnt)
+                seen = p.mask ? (p.mask[(static_cast<long long>(at.b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
+              if (!seen) x[rt][j] = NINF;
+            }
+        }
+        const auto over_tokens = [](float v) {  // maximum over a row's tokens
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        };
+        if (zero) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float nm = fmaxf(m0[rt][e], over_tokens(fmaxf(x[rt][e], x[rt][2 + e]))), nb = nm == NINF ? 0.f : nm;
+              l0[rt][e] = l0[rt][e] * ex2(m0[rt][e] - nb) + ex2(x[rt][e] - nb) + ex2(x[rt][2 + e] - nb);
+              m0[rt][e] = nm;
+            }
+          copy_step();
+          continue;
+        }
+        // the offset moves only when a weight would pass 2^15.9
+        bool up = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) up |= fmaxf(x[rt][e], x[rt][2 + e]) > m[rt][e] + (WEIGHT_UP + WEIGHT_SLACK);
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float v = top[rt][half];
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-              const float nm = fmaxf(m[rt][half], v - WEIGHT_UP);
+            for (int e = 0; e < 2; ++e) {
+              const float nm = fmaxf(m[rt][e], over_tokens(fmaxf(x[rt][e], x[rt][2 + e])) - WEIGHT_UP);
               const float nb = nm == NINF ? 0.f : nm;
-              const float a = ex2(m[rt][half] - nb);  // 0 from -inf
-              m[rt][half] = nm, base_m[rt][half] = nb, l[rt][half] *= a;
+              const float a = ex2(m[rt][e] - nb);  // 0 from -inf
+              m[rt][e] = nm, base_m[rt][e] = nb, l[rt][e] *= a;
 #pragma unroll
-              for (int j = 0; j < NT8; ++j) o[rt][j][2 * half] *= a, o[rt][j][2 * half + 1] *= a;
+              for (int j = 0; j < MT; ++j) o[rt][j][e] *= a, o[rt][j][2 + e] *= a;
             }
         }
-        uint32_t pf[SUB][RT][4];
+        uint32_t pf[RT][2];
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+        for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
+          for (int j = 0; j < 4; ++j) x[rt][j] = ex2(x[rt][j] - base_m[rt][j & 1]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float(&y)[4] = x[u][rt][half];
+          for (int e = 0; e < 2; ++e) l[rt][e] = fmaf(x[rt][e] + x[rt][2 + e], rv, l[rt][e]);
+          pf[rt][0] = transpose8(f32_to_f16x2(x[rt][0], x[rt][1]));
+          pf[rt][1] = transpose8(f32_to_f16x2(x[rt][2], x[rt][3]));
+        }
+        uint32_t v[4][VB / 4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = ex2(y[j] - base_m[rt][half]);
-              l[rt][half] = fmaf((y[0] + y[1]) + (y[2] + y[3]), rv[u], l[rt][half]);
-              pf[u][rt][half] = f32_to_f16x2(y[0], y[1]);
-              pf[u][rt][2 + half] = f32_to_f16x2(y[2], y[3]);
-            }
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint4 a = lds128(st + L::KB + (i * 32 + lane) * 16);
+            v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+          } else {
+            const uint2 a = *reinterpret_cast<const uint2 *>(st + L::KB + (i * 32 + lane) * 8);
+            v[i][0] = a.x, v[i][1] = a.y;
           }
+        }
+        if (edge) {  // rows that are not there may hold anything, NaN codes too
+          const int end = at.ctx + at.cnt - step * ASTEP - 2 * t;
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          uint32_t v[4][NT8 / 4];
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (D == 128) {
-              const uint4 a = lds128(st[u] + L::KB + (i * 32 + lane) * 16);
-              v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
-            } else {
-              const uint2 a = *reinterpret_cast<const uint2 *>(st[u] + L::KB + (i * 32 + lane) * 8);
-              v[i][0] = a.x, v[i][1] = a.y;
-            }
-          }
-          if (edge) {  // rows that are not there may hold anything, NaN codes too
-            const int end = u < nsub ? at.ctx + at.cnt - (step + u) * ASTEP - 4 * t : 0;
+            for (int w = 0; w < VB / 4; ++w)
+              if ((i & 1) + 8 * (i >> 1) >= end) v[i][w] = 0;
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int w = 0; w < NT8 / 4; ++w)
-                if (i >= end) v[i][w] = 0;
-          }
+        for (int w = 0; w < VB / 4; ++w) {
           if (KIND == KIND_I8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) v[i][w] ^= 0x80808080u;
+          // rows g and g + 8 of a column tile are bytes j and j + 1
+          uint32_t a[2][4];
+          pairs_across<KIND, 0>(v[0][w], v[1][w], a[0][0], a[0][1]);
+          pairs_across<KIND, 0>(v[2][w], v[3][w], a[0][2], a[0][3]);
+          pairs_across<KIND, 2>(v[0][w], v[1][w], a[1][0], a[1][1]);
+          pairs_across<KIND, 2>(v[2][w], v[3][w], a[1][2], a[1][3]);
 #pragma unroll
-              for (int w = 0; w < NT8 / 4; ++w) v[i][w] ^= 0x80808080u;
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int w = 0; w < NT8 / 4; ++w) {
-            uint32_t b[2][4];
-            pairs_across<KIND, 0>(v[0][w], v[1][w], b[0][0], b[0][1]);
-            pairs_across<KIND, 2>(v[0][w], v[1][w], b[0][2], b[0][3]);
-            pairs_across<KIND, 0>(v[2][w], v[3][w], b[1][0], b[1][1]);
-            pairs_across<KIND, 2>(v[2][w], v[3][w], b[1][2], b[1][3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) mma16816(o[rt][4 * w + j], pf[u][rt], b[0][j], b[1][j]);
-          }
+            for (int rt = 0; rt < RT; ++rt) mma16816(o[rt][2 * w + j], a[j], pf[rt][0], pf[rt][1]);
         }
-#pragma unroll 1
-        for (int u = 0; u < nsub; ++u) copy_step();
-        step += nsub, now += nsub, at.step += nsub;
+        copy_step();
       }
-      // a lane holds columns [t D / 4, (t + 1) D / 4) of rows g and g + 8 of each tile
+      // a lane holds columns [g D / 8, (g + 1) D / 8) of rows 2 t and 2 t + 1 of each tile
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float &lr = l[rt][half], &mr = m[rt][half];
-          if (__any_sync(0xffffffffu, l0[rt][half] > 0.f)) {  // joined so that neither sum overflows
-            const float nm = fmaxf(mr, m0[rt][half] - 60.f), nb = nm == NINF ? 0.f : nm;
+        for (int e = 0; e < 2; ++e) {
+          float &lr = l[rt][e], &mr = m[rt][e];
+          if (__any_sync(0xffffffffu, l0[rt][e] > 0.f)) {  // joined so that neither sum overflows
+            const float nm = fmaxf(mr, m0[rt][e] - 60.f), nb = nm == NINF ? 0.f : nm;
             const float a = ex2(mr - nb);
-            lr = lr * a + l0[rt][half] * ex2(m0[rt][half] - nb);
+            lr = lr * a + l0[rt][e] * ex2(m0[rt][e] - nb);
             mr = nm;
 #pragma unroll
-            for (int j = 0; j < NT8; ++j) o[rt][j][2 * half] *= a, o[rt][j][2 * half + 1] *= a;
+            for (int j = 0; j < MT; ++j) o[rt][j][e] *= a, o[rt][j][2 + e] *= a;
           }
-          lr += __shfl_xor_sync(0xffffffffu, lr, 1);
-          lr += __shfl_xor_sync(0xffffffffu, lr, 2);
+          lr += __shfl_xor_sync(0xffffffffu, lr, 4);
+          lr += __shfl_xor_sync(0xffffffffu, lr, 8);
+          lr += __shfl_xor_sync(0xffffffffu, lr, 16);
         }
       const bool whole = seg.s0 == 0 && seg.s1 == seg.steps;
       // the first piece has its own place, the last one takes the ring's
@@ -698,19 +635,18 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = 16 * rt + 8 * half + g;
-          const float inv = l[rt][half] == 0.f ? 0.f : 1.f / l[rt][half];
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * rt + 2 * t + e;
+          const float inv = l[rt][e] == 0.f ? 0.f : 1.f / l[rt][e];
 #pragma unroll
-          for (int q = 0; q < NT8 / 2; ++q) {
-            const int j = (4 * q) % NT8, e = 2 * half + (4 * q) / NT8;
-            const float4 z = make_float4(o[rt][j][e], o[rt][j + 1][e], o[rt][j + 2][e], o[rt][j + 3][e]);
-            if (!whole) reinterpret_cast<float4 *>(to)[((rt * 2 + half) * (NT8 / 2) + q) * 32 + lane] = z;
-            else if (r < rows) put4<DT>(p, seg, D, r, t * (D / 4) + 4 * q, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
+          for (int q = 0; q < MT / 2; ++q) {
+            const float4 z = make_float4(o[rt][2 * q][e], o[rt][2 * q][2 + e], o[rt][2 * q + 1][e], o[rt][2 * q + 1][2 + e]);
+            if (!whole) reinterpret_cast<float4 *>(to)[((rt * 2 + e) * (MT / 2) + q) * 32 + lane] = z;
+            else if (r < rows) put4<DT>(p, seg, D, r, g * VB + 4 * q, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
           }
-          if (t == 0) {
-            if (!whole) to[L::ROWS * D + r] = m[rt][half], to[L::ROWS * D + L::ROWS + r] = l[rt][half];
-            else if (r < rows) put_lse(p, seg, r, m[rt][half], l[rt][half]);
+          if (g == 0) {
+            if (!whole) to[L::ROWS * D + r] = m[rt][e], to[L::ROWS * D + L::ROWS + r] = l[rt][e];
+            else if (r < rows) put_lse(p, seg, r, m[rt][e], l[rt][e]);
           }
         }
       if (!whole && lane == 0) s_seg[2 * warp + which] = seg, s_has[2 * warp + which] = 1;
@@ -722,47 +658,53 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
 
   // ---- the CTA's pieces: neighbours of one segment are merged
   const auto piece_at = [&](int i) -> const float * {
-    if (i & 1) return reinterpret_cast<const float *>(smem + (i >> 1) * ASTAGES * L::STAGE);
-    return RT == 1 ? reinterpret_cast<const float *>(smem + L::RING) + (i >> 1) * L::PIECE : work + L::SHARED + (i >> 1) * L::PIECE;
+    return reinterpret_cast<const float *>(i & 1 ? smem + (i >> 1) * ASTAGES * L::STAGE : smem + L::RING + (i >> 1) * L::PIECE * 4);
   };
   constexpr int QUADS = L::ROWS * D / 4;  // float4 of a piece
+  // row and first column of float4 k of a piece
+  const auto row_of = [](int k) { return (k >> 5) / MT * 8 + 2 * (k & 3) + (k >> 5) / (MT / 2) % 2; };
+  const auto col_of = [](int k) { return ((k & 31) >> 2) * VB + (k >> 5) % (MT / 2) * 4; };
   Segment open[2];
   bool is_open[2] = {false, false};
+#pragma unroll 1
   for (int i = 0; i < 2 * AW;) {
     if (!s_has[i]) {
       ++i;
       continue;
     }
     const Segment seg = s_seg[i];
-    int n = i, s1 = seg.s1, idx[AW + 1], cnt = 0;  // a segment has at most one piece per warp
+    int n = i, last = i;  // the segment's pieces are among slots i .. last
+#pragma unroll 1
     for (; n < 2 * AW; ++n) {
       if (!s_has[n]) continue;
       if (s_seg[n].at != seg.at) break;
-      idx[cnt++] = n;
-      s1 = s_seg[n].s1;
+      last = n;
     }
-    const bool whole = seg.s0 == 0 && s1 == seg.steps;
+    const bool whole = seg.s0 == 0 && s_seg[last].s1 == seg.steps;
     const int rows = seg.cnt * p.G, which = seg.s0 > 0 ? 0 : 1;
     if (!whole) open[which] = seg, is_open[which] = true;
+#pragma unroll 1
     for (int k = threadIdx.x; k < QUADS; k += ANT) {
-      const int ln = k & 31, q = (k >> 5) % (NT8 / 2), row = (k >> 5) / (NT8 / 2) * 8 + (ln >> 2);
+      const int row = row_of(k);
       if (row >= rows) continue;
       float M = NINF;
-      for (int e = 0; e < cnt; ++e) M = fmaxf(M, piece_at(idx[e])[L::ROWS * D + row]);
+      for (int e = i; e <= last; ++e)
+        if (s_has[e]) M = fmaxf(M, piece_at(e)[L::ROWS * D + row]);
       const float bm = M == NINF ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
-      for (int e = 0; e < cnt; ++e) {
-        const float *pc = piece_at(idx[e]);
+      for (int e = i; e <= last; ++e) {
+        if (!s_has[e]) continue;
+        const float *pc = piece_at(e);
         const float a = ex2(pc[L::ROWS * D + row] - bm);
         const float4 x = reinterpret_cast<const float4 *>(pc)[k];
         acc.x = fmaf(a, x.x, acc.x), acc.y = fmaf(a, x.y, acc.y), acc.z = fmaf(a, x.z, acc.z), acc.w = fmaf(a, x.w, acc.w);
         sum = fmaf(a, pc[L::ROWS * D + L::ROWS + row], sum);
       }
-      const bool head = q == 0 && (ln & 3) == 0;
+      const bool head = col_of(k) == 0;
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        put4<DT>(p, seg, D, row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        put4<DT>(p, seg, D, row, col_of(k), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         if (head) put_lse(p, seg, row, M, sum);
       } else {
         float *to = work + which * L::PIECE;
@@ -777,6 +719,7 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
   // ---- segments that several CTAs share: the last to arrive merges
   __threadfence();
   __syncthreads();
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     if (!is_open[which]) continue;
     const Segment seg = open[which];
@@ -787,8 +730,9 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
     __threadfence();
     const int rows = seg.cnt * p.G;
     const auto shared_piece = [&](int e) { return p.pieces + static_cast<long long>(c0 + e) * L::WORK + (e == 0 ? L::PIECE : 0); };
+#pragma unroll 1
     for (int k = threadIdx.x; k < QUADS; k += ANT) {
-      const int ln = k & 31, q = (k >> 5) % (NT8 / 2), row = (k >> 5) / (NT8 / 2) * 8 + (ln >> 2);
+      const int row = row_of(k);
       if (row >= rows) continue;
       float M = NINF;
 #pragma unroll 8
@@ -805,8 +749,8 @@ __global__ void __launch_bounds__(ANT, 1) attn_stream_kernel(const __grid_consta
         sum = fmaf(a, __ldcg(pc + L::ROWS * D + L::ROWS + row), sum);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      put4<DT>(p, seg, D, row, (ln & 3) * (D / 4) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (q == 0 && (ln & 3) == 0) put_lse(p, seg, row, M, sum);
+      put4<DT>(p, seg, D, row, col_of(k), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (col_of(k) == 0) put_lse(p, seg, row, M, sum);
     }
     if (threadIdx.x == 0) p.done[c0] = 0;  // zero again for the next call
   }

@@ -102,18 +102,18 @@ struct AttnChoice {
   int threads, smem;
   size_t work;
 };
-// By the rows per kv head: up to 16, and up to 32, a warp's own matrix
-// instructions keep pace with the memory; from 33 on the tensor cores with
+// By the rows per kv head: up to 8, and up to 16, a warp's own matrix
+// instructions keep pace with the memory; from 17 on the tensor cores with
 // accumulators in tensor memory take 128 rows at a time.
 template <int D, int KIND, int DT>
 AttnChoice choose_attn(long long rows) {
-  if (rows <= 16) {
+  if (rows <= 8) {
     using L = StreamLayout<D, 1>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), ANT, L::SMEM, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), L::THREADS, L::SMEM, L::WORK};
   }
-  if (rows <= 32) {
+  if (rows <= 16) {
     using L = StreamLayout<D, 2>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), ANT, L::SMEM, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::WORK};
   }
   using L = TileLayout<D>;
   return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 2 * L::PIECE};
