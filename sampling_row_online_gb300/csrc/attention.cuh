@@ -115,12 +115,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Asynchronous copy to shared memory under the L2 policy `pol`.
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, uint64_t pol) {
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(pol) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "l"(pol) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -213,15 +214,20 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // A stretch that ends inside a segment (the rows of a kv head) leaves a piece
 // (out, offset, sum); the CTA merges the pieces of its warps, and the last CTA
 // to arrive at a segment merges those of its CTAs in index order.
+//
+// SMs are not served alike (of equal stretches the slowest ends 12 % after the
+// median), but shorter stretches on more CTAs lost more at their ends than
+// they levelled: 615 us with one stretch per resident CTA, 616 with two, 634
+// with eight (one token, 64 sequences of up to 32768 tokens, 8 rows per head).
 constexpr int ASTAGES = 2;       // steps in flight per warp
 constexpr int ASTEP = 16;        // tokens per step
 constexpr int ALEAST = 2;        // steps per warp at least, before more CTAs take part
 
 template <int D, int RT>
 struct StreamLayout {
-  // as many warps as the registers allow (128 and 168 a thread): what a step
-  // costs is the latency of its dependent instructions
-  static constexpr int WARPS = RT == 1 ? 16 : 12, THREADS = 32 * WARPS;
+  // 128 registers a thread and two CTAs per SM, or 255 and one (12 warps of
+  // 168 spilled: 16 rows at 8192 tokens 211 us, 8 warps 185 us)
+  static constexpr int WARPS = 8, THREADS = 32 * WARPS, RESIDENT = RT == 1 ? 2 : 1;
   static constexpr int KB = ASTEP * D, STAGE = 2 * KB + 256;     // codes of keys and values, scales
   static constexpr int ROWS = 8 * RT;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;              // floats: out, offset, sum
@@ -252,7 +258,7 @@ __device__ __forceinline__ void put_lse(const AttnParams &p, const Segment &g, i
 }
 
 template <int D, int KIND, int DT, int RT>
-__global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, 1) attn_stream_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, RT>::RESIDENT) attn_stream_kernel(const __grid_constant__ AttnParams p) {
   using L = StreamLayout<D, RT>;
   constexpr int AW = L::WARPS, ANT = L::THREADS;
   constexpr int CH = D / 64, VB = D / 8, MT = D / 16;  // 16-byte chunks of a key row, bytes of a value row per lane; column tiles
@@ -356,7 +362,8 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, 1) attn_stream_k
     int held_b = -1, held_p = 0, held = 0;  // page ids held_p + lane of sequence held_b
     const unsigned char *kp = nullptr, *vp = nullptr;
     const float *scales = nullptr;
-    long long vs_off = c.v_scale - c.k_scale;
+    const long long vs_off = c.v_scale - c.k_scale;
+    const uint64_t pol = policy_evict_first();  // what is read once does not push the kernel's code out of L2
     bool bad = false, fresh = true;  // fresh: another page, or its first step
 
     const auto copy_step = [&]() {
@@ -384,14 +391,14 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, 1) attn_stream_k
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // tokens g and g + 8
 #pragma unroll
-          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, kp + 8 * i * D + 64 * j);
+          for (int j = 0; j < CH; ++j) cp_async<16>(dst + ((i * CH + j) * 32 + lane) * 16, kp + 8 * i * D + 64 * j, pol);
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-          cp_async<VB>(dst + L::KB + (i * 32 + lane) * VB, vp + ((i & 1) + 8 * (i >> 1)) * D);
+          cp_async<VB>(dst + L::KB + (i * 32 + lane) * VB, vp + ((i & 1) + 8 * (i >> 1)) * D, pol);
         const uint32_t sc = dst + 2 * L::KB + lane * 8;
         if (!bad) {
-          cp_async<4>(sc, scales);
-          cp_async<4>(sc + 4, scales + vs_off);
+          cp_async<4>(sc, scales, pol);
+          cp_async<4>(sc + 4, scales + vs_off, pol);
         } else {  // a NaN scale makes the rows NaN
           if (lane == 0) atomicOr(p.status, ST_PAGE);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sc), "r"(0x7fc00000u), "r"(0x3f800000u) : "memory");
@@ -734,19 +741,32 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, 1) attn_stream_k
     for (int k = threadIdx.x; k < QUADS; k += ANT) {
       const int row = row_of(k);
       if (row >= rows) continue;
-      float M = NINF;
-#pragma unroll 8
-      for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(shared_piece(e) + L::ROWS * D + row));
-      const float bm = M == NINF ? 0.f : M;
+      float M = NINF, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-#pragma unroll 8
-      for (int e = 0; e < n; ++e) {
-        const float *pc = shared_piece(e);
-        const float a = ex2(__ldcg(pc + L::ROWS * D + row) - bm);
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(pc) + k);
-        acc.x = fmaf(a, x.x, acc.x), acc.y = fmaf(a, x.y, acc.y), acc.z = fmaf(a, x.z, acc.z), acc.w = fmaf(a, x.w, acc.w);
-        sum = fmaf(a, __ldcg(pc + L::ROWS * D + L::ROWS + row), sum);
+#pragma unroll 1
+      for (int e0 = 0; e0 < n; e0 += 8) {  // eight pieces a round trip
+        float mm[8], ll[8], top = M;
+        float4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float *pc = shared_piece(min(e0 + e, n - 1));
+          mm[e] = e0 + e < n ? __ldcg(pc + L::ROWS * D + row) : NINF;
+          ll[e] = __ldcg(pc + L::ROWS * D + L::ROWS + row);
+          x[e] = __ldcg(reinterpret_cast<const float4 *>(pc) + k);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, mm[e]);
+        const float base = top == NINF ? 0.f : top;
+        float a = ex2(M - base);
+        M = top;
+        acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a, sum *= a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e0 + e >= n) continue;
+          a = ex2(mm[e] - base);
+          acc.x = fmaf(a, x[e].x, acc.x), acc.y = fmaf(a, x[e].y, acc.y), acc.z = fmaf(a, x[e].z, acc.z), acc.w = fmaf(a, x[e].w, acc.w);
+          sum = fmaf(a, ll[e], sum);
+        }
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       put4<DT>(p, seg, D, row, col_of(k), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));

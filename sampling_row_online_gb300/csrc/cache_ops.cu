@@ -99,7 +99,7 @@ const void *pick_norm_rope(bool vec, bool one, bool pairs) {
 // workspace per CTA.
 struct AttnChoice {
   const void *fn;
-  int threads, smem;
+  int threads, smem, ctas;  // ctas: per SM
   size_t work;
 };
 // By the rows per kv head: up to 8, and up to 16, a warp's own matrix
@@ -109,14 +109,14 @@ template <int D, int KIND, int DT>
 AttnChoice choose_attn(long long rows) {
   if (rows <= 8) {
     using L = StreamLayout<D, 1>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), L::THREADS, L::SMEM, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
   }
   if (rows <= 16) {
     using L = StreamLayout<D, 2>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
   }
   using L = TileLayout<D>;
-  return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 2 * L::PIECE};
+  return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 1, 2 * L::PIECE};
 }
 AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   const bool bf = dtype == SPEC_BF16;
@@ -286,7 +286,7 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G);
   const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
-  const int grid = num_sms();
+  const int grid = num_sms() * k.ctas;
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if ((st = get_ws(stream, (grid * k.work + 3) / 4, &w, static_cast<size_t>(grid)))) return st;
