@@ -221,7 +221,7 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // with eight (one token, 64 sequences of up to 32768 tokens, 8 rows per head).
 constexpr int ASTAGES = 2;       // steps in flight per warp
 constexpr int ASTEP = 16;        // tokens per step
-constexpr int ALEAST = 2;        // steps per warp at least, before more CTAs take part
+constexpr int ALEAST = 4;        // steps per warp at least, before more CTAs take part
 
 template <int D, int RT>
 struct StreamLayout {
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
   __shared__ int s_seq[AW];
   __shared__ unsigned s_scan[AW];
   __shared__ int s_last[2];
+  __shared__ int2 s_range[2];  // the CTAs of a segment: first, number
   const CacheView &c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -726,15 +727,19 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
   // ---- segments that several CTAs share: the last to arrive merges
   __threadfence();
   __syncthreads();
+  if (threadIdx.x < 2 && is_open[threadIdx.x]) {  // a thread for each
+    const Segment &seg = open[threadIdx.x];
+    const int c0 = share.holder(seg.at) / AW, c1 = share.holder(seg.at + seg.steps - 1) / AW;
+    s_range[threadIdx.x] = make_int2(c0, c1 - c0 + 1);
+    s_last[threadIdx.x] = atomicAdd(p.done + c0, 1) == c1 - c0;
+    __threadfence();
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
-    if (!is_open[which]) continue;
+    if (!is_open[which] || !s_last[which]) continue;
     const Segment seg = open[which];
-    const int c0 = share.holder(seg.at) / AW, c1 = share.holder(seg.at + seg.steps - 1) / AW, n = c1 - c0 + 1;
-    if (threadIdx.x == 0) s_last[which] = atomicAdd(p.done + c0, 1) == n - 1;
-    __syncthreads();
-    if (!s_last[which]) continue;
-    __threadfence();
+    const int c0 = s_range[which].x, n = s_range[which].y;
     const int rows = seg.cnt * p.G;
     const auto shared_piece = [&](int e) { return p.pieces + static_cast<long long>(c0 + e) * L::WORK + (e == 0 ? L::PIECE : 0); };
 #pragma unroll 1
