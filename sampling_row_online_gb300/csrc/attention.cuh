@@ -219,7 +219,6 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // median), but shorter stretches on more CTAs lost more at their ends than
 // they levelled: 615 us with one stretch per resident CTA, 616 with two, 634
 // with eight (one token, 64 sequences of up to 32768 tokens, 8 rows per head).
-constexpr int ASTAGES = 2;       // steps in flight per warp
 constexpr int ASTEP = 16;        // tokens per step
 constexpr int ALEAST = 4;        // steps per warp at least, before more CTAs take part
 
@@ -228,13 +227,14 @@ struct StreamLayout {
   // 128 registers a thread and two CTAs per SM, or 255 and one (12 warps of
   // 168 spilled: 16 rows at 8192 tokens 211 us, 8 warps 185 us)
   static constexpr int WARPS = 8, THREADS = 32 * WARPS, RESIDENT = RT == 1 ? 2 : 1;
+  static constexpr int STAGES = RT <= 2 ? 2 : 3;                 // steps in flight per warp
   static constexpr int KB = ASTEP * D, STAGE = 2 * KB + 256;     // codes of keys and values, scales
   static constexpr int ROWS = 8 * RT;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;              // floats: out, offset, sum
-  static constexpr int RING = WARPS * ASTAGES * STAGE;
+  static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int SMEM = RING + WARPS * PIECE * 4;          // and the warps' first pieces
   static constexpr int WORK = 2 * PIECE;                         // floats per CTA that other CTAs read
-  static_assert(PIECE * 4 <= ASTAGES * STAGE, "a warp's last piece lies in its own ring");
+  static_assert(PIECE * 4 <= STAGES * STAGE, "a warp's last piece lies in its own ring");
 };
 
 struct Segment {  // the rows of a kv head, and the part of their steps that a piece covers
@@ -260,7 +260,7 @@ __device__ __forceinline__ void put_lse(const AttnParams &p, const Segment &g, i
 template <int D, int KIND, int DT, int RT>
 __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, RT>::RESIDENT) attn_stream_kernel(const __grid_constant__ AttnParams p) {
   using L = StreamLayout<D, RT>;
-  constexpr int AW = L::WARPS, ANT = L::THREADS;
+  constexpr int AW = L::WARPS, ANT = L::THREADS, ASTAGES = L::STAGES;
   constexpr int CH = D / 64, VB = D / 8, MT = D / 16;  // 16-byte chunks of a key row, bytes of a value row per lane; column tiles
   const float NINF = __uint_as_float(0xff800000u);
   extern __shared__ __align__(1024) unsigned char smem[];

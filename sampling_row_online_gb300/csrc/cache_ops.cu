@@ -102,9 +102,11 @@ struct AttnChoice {
   int threads, smem, ctas;  // ctas: per SM
   size_t work;
 };
-// By the rows per kv head: up to 8, and up to 16, a warp's own matrix
-// instructions keep pace with the memory; from 17 on the tensor cores with
-// accumulators in tensor memory take 128 rows at a time.
+// By the rows per kv head.  Up to 24 a warp's own matrix instructions, 8 rows at
+// a time, are faster; beyond, the tensor cores with accumulators in tensor
+// memory, 128 rows at a time.  (64 sequences of up to 8192 tokens, 8 kv heads,
+// e4m3 / int8: 4 rows 171 / 172 us, 16 rows 185 / 203, 24 rows 227 / 245; the
+// tile kernel takes 274 / 279 for 24 and 32 rows and 294 / 307 for 48.)
 template <int D, int KIND, int DT>
 AttnChoice choose_attn(long long rows) {
   if (rows <= 8) {
@@ -114,6 +116,10 @@ AttnChoice choose_attn(long long rows) {
   if (rows <= 16) {
     using L = StreamLayout<D, 2>;
     return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
+  }
+  if (rows <= 24) {
+    using L = StreamLayout<D, 3>;
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 3>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
   }
   using L = TileLayout<D>;
   return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 1, 2 * L::PIECE};
