@@ -610,3 +610,62 @@ def test_empty_calls():
     assert binding.spec_cache_attention(q, cache, one, ints(0))[0].shape == q.shape
     assert binding.spec_qk_norm_rope(q, None)[0].shape == q.shape
     assert binding.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("kind,D", [("e4m3", 128), ("int8", 128), ("e4m3", 64), ("int8", 64)])
+@pytest.mark.parametrize("N,G", [(2, 4), (3, 3), (2, 8), (17, 1), (23, 1), (3, 8), (6, 4), (25, 1), (4, 8), (43, 3), (16, 8), (37, 7)])
+def test_attention_by_rows_per_kv_head(kind, D, N, G):
+    """Each size class of rows (8, 16, 24, and tiles of 128), at its borders, over lengths on both sides of a tile and
+    with blocks without values."""
+    ctx = [0, 127 - N, 128, 1000, 2300]
+    ctx[1] = max(ctx[1], 0)
+    state = make_cache(len(ctx), 2300 + N, 2, 64, D, kind, N + G)
+    state[3][::6] = 0
+    g = torch.Generator().manual_seed(N + G)
+    q = torch.randn((len(ctx), N, 2 * G, D), generator=g).to(BF16)
+    check_attention(state, kind, ctx, None, q, None)
+    parent = random_trees(g, len(ctx), N)
+    check_attention(state, kind, ctx, [N, N, 1, N - 1, N], q, binding.spec_tree_mask(parent.cuda())[0].cpu())
+
+
+@pytest.mark.parametrize("N", [1, 8])
+def test_attention_of_many_sequences(N):
+    """More sequences than a CTA has threads, many of them empty."""
+    B, page, D = 2000, 16, 64
+    state = make_cache(B, 48 + N, 1, page, D, "e4m3", 3)
+    g = torch.Generator().manual_seed(5)
+    ctx = torch.randint(0, 49, (B,), generator=g).tolist()
+    counts = [N if i % 3 else 0 for i in range(B)]
+    q = torch.randn((B, N, 4, D), generator=g).to(BF16)
+    cache, table = on_gpu(state)
+    out, lse = binding.spec_cache_attention(q.cuda(), cache, table, ints(*ctx), counts=ints(*counts), want_lse=True)
+    assert binding.spec_get_status() == 0
+    out, lse = out.cpu().double(), lse.cpu().double()
+    empty = torch.tensor(counts) == 0
+    assert torch.all(out[empty] == 0) and torch.all(lse[empty] == -math.inf)
+    want = ref.Cache(*state, "e4m3")
+    for b in range(1, B, 31):
+        o, l, to, tl = ref.attention(want, b, ctx[b], counts[b], q[b].double(), None, D ** -0.5)
+        if counts[b]:
+            assert torch.all((out[b] - o).abs() <= to + 2.0 ** -8 * o.abs()) and torch.all((lse[b] - l).abs() <= tl)
+
+
+def test_two_streams_share_a_cache():
+    """Calls on two streams at once read one cache, each with its own workspace."""
+    state = make_cache(4, 5000, 2, 64, 128, "e4m3", 5)
+    cache, table = on_gpu(state)
+    g = torch.Generator().manual_seed(3)
+    qs = [torch.randn((4, n, 8, 128), generator=g).to(BF16).cuda() for n in (1, 20)]
+    ctx = ints(4900, 3000, 17, 0)
+    want = [binding.spec_cache_attention(q, cache, table, ctx)[0] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for q, s in zip(qs, streams):
+            with torch.cuda.stream(s):
+                got.append(binding.spec_cache_attention(q, cache, table, ctx, stream=s)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
+    assert all(binding.spec_get_status(s) == 0 for s in streams)
