@@ -220,7 +220,7 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // they levelled: 615 us with one stretch per resident CTA, 616 with two, 634
 // with eight (one token, 64 sequences of up to 32768 tokens, 8 rows per head).
 constexpr int ASTEP = 16;        // tokens per step
-constexpr int ALEAST = 4;        // steps per warp at least, before more CTAs take part
+constexpr int ALEAST = 2;        // steps per warp at least, before more CTAs take part
 
 template <int D, int RT>
 struct StreamLayout {
@@ -291,8 +291,12 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
     upto = total + block_scan<AW>(w, s_scan, sum);
     total += sum;
   }
-  // fewer CTAs where a warp's stretch would be a step
-  const unsigned nc = min(gridDim.x, (total + AW * ALEAST - 1) / (AW * ALEAST));
+  // fewer CTAs where a warp's stretch would be a step, but a warp for each
+  // segment; and about sqrt(steps) CTAs to a segment at most: a step costs a
+  // warp what a piece costs the last CTA
+  const unsigned segments = static_cast<unsigned>(p.B) * c.Hk;
+  const unsigned most = static_cast<unsigned>(sqrtf(static_cast<float>(total) * static_cast<float>(segments))) + 1;
+  const unsigned nc = min(min(gridDim.x, total), max(min(most, (total + AW * ALEAST - 1) / (AW * ALEAST)), (segments + AW - 1) / AW));
   if (__syncthreads_or(rest)) fill_rest<DT, ANT>(p, D);
   if (blockIdx.x >= nc) return;
   const Share share(total, nc * AW);
