@@ -554,9 +554,9 @@ def _index(t, name, shape, device):
     """A contiguous int32 tensor of this shape on this device, or None, as a pointer."""
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
+    if t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -611,10 +611,13 @@ def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True,
         if t.device != x.device:
             raise ValueError("q and k must be on one device")
         src = _heads(t, name, x.dtype, B, N, H, D)
-        out = torch.empty((B, N, H, D), dtype=t.dtype, device=t.device) if out is None else out
-        if out.device != x.device:
-            raise ValueError(f"out_{name} must be on the device of {name}")
-        dst = _heads(out, "out_" + name, x.dtype, B, N, H, D)
+        if out is None:
+            out = torch.empty((B, N, H, D), dtype=t.dtype, device=t.device)
+            dst = HeadsStruct(out.data_ptr(), N * H * D, H * D, D)
+        else:
+            if out.device != x.device:
+                raise ValueError(f"out_{name} must be on the device of {name}")
+            dst = _heads(out, "out_" + name, x.dtype, B, N, H, D)
         if w is not None:
             if w.dtype != x.dtype or tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != x.device:
                 raise ValueError(f"{name}_weight must be a contiguous [{D}] tensor of {x.dtype} on {x.device}")
@@ -659,14 +662,15 @@ def spec_cache_read(cache, page_table, start, counts, N, *, dtype=torch.bfloat16
     table, per = _table(cache, page_table, B)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    c = cache
+    shape, device = (B, N, cache.kv_heads, cache.head_dim), cache.device
     outs = []
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
         if t is None:
-            t = torch.empty((B, N, c.kv_heads, c.head_dim), dtype=dtype, device=cache.device)
-        _heads(t, name, dtype, B, N, c.kv_heads, c.head_dim)
-        if not t.is_contiguous() or t.device != cache.device:
-            raise ValueError(f"{name} must be contiguous and on the cache's device")
+            t = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            _heads(t, name, dtype, *shape)
+            if not t.is_contiguous() or t.device != device:
+                raise ValueError(f"{name} must be contiguous and on the cache's device")
         outs.append(t)
     _call(lib.spec_cache_read, "spec_cache_read", cache.device, stream, cache.ref, table, per,
           _index(start, "start", (B,), cache.device), _index(counts, "counts", (B,), cache.device), outs[0].data_ptr(),
