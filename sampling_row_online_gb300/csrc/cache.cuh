@@ -293,6 +293,9 @@ struct CacheWriteParams {
 // (MOST chunks of eight a thread), their maximum gives the scale, and the
 // codes follow: 3 bytes of traffic per 16-bit element, the floor.  The block
 // is re-read only where its scale grows under rows that it already holds.
+// 8 sequences of up to 8000 rows, bf16 to int8: 49 us, 6.0 TB/s (the floor is
+// 43.5); one row each of 64 sequences: 2.7 us, the latency of length, page and
+// row.
 template <int DT, int NTH, int MOST, bool VEC>
 __global__ void __launch_bounds__(NTH, NTH == 256 && DT != DT_F32 ? (MOST == 4 ? 5 : 4) : 1) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
   __shared__ uint32_t s_max[NTH / 32];
@@ -385,7 +388,8 @@ struct CacheReadParams {
 
 // One CTA per (block, kv head, sequence): the block's rows of both tensors,
 // 16 codes to a thread; rows past the count are zero, a sequence that does
-// not fit its pages and the rows of a bad page are NaN.
+// not fit its pages and the rows of a bad page are NaN.  Bound by HBM: 8
+// sequences of up to 32768 rows, e4m3 to bf16, 234 us, 6.3 TB/s with the zeros.
 template <int DT>
 __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p) {
   const CacheView &c = p.c;
@@ -458,7 +462,9 @@ constexpr int COMMIT_MAX_NODES = 1024;
 // index[i] >= i, so with the rows taken in ascending order none is overwritten
 // before it has been read.  A warp takes a kv head and tensor by itself: it
 // reads a block's new rows once for their maximum and once (from the cache)
-// to write them.
+// to write them.  The bytes are few, the latency of walk and reads counts: 32
+// trees of 63 nodes 4.7 us, 256 of 255 nodes 18 us (a CTA per head and tensor
+// took 32, one with a barrier per block 46).
 __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
   __shared__ int s_par[COMMIT_MAX_NODES], s_tok[COMMIT_MAX_NODES], s_path[COMMIT_MAX_NODES], s_index[COMMIT_MAX_NODES];
   __shared__ int s_node, s_bad, s_first;
@@ -599,13 +605,14 @@ struct NormRopeParams {
 // Several tokens to a CTA, `lanes` threads to a row (one head of one token).
 // A thread takes units of the row: eight elements of the first half with the
 // eight that they are rotated with (halves), or eight elements by themselves
-// (neighbouring pairs, and what is not rotated).  It loads ROWS rows before it
-// works on the first, so that enough bytes are in flight.  The rotation's
-// angle is exact: pos * freq modulo 2^64 is the fraction of a turn in 64 bits,
-// from which 24 go into sincospi; a table of the CTA's tokens holds cos and
-// sin, so that all heads share them.
+// (neighbouring pairs, and what is not rotated).  The rotation's angle is
+// exact: pos * freq modulo 2^64 is the fraction of a turn in 64 bits, from
+// which 24 go into sincospi; a table of the CTA's tokens holds cos and sin, so
+// that all heads share them.  This form takes any even head size, stride and
+// alignment: single elements, or two for neighbouring pairs, where vectors do
+// not fit.
 constexpr int ROPE_TOKENS = 16;  // most tokens of a CTA
-template <int DT, int VE, int MAXU, int ROWS>
+template <int DT, int VE, int MAXU>
 __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
   __shared__ long long s_from[ROPE_TOKENS][2], s_to[ROPE_TOKENS][2];
@@ -638,51 +645,46 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   const float over_d = 1.f / static_cast<float>(p.D);
   const auto place = [&](int u) { return u < npair ? u * VE : (npair + u) * VE; };  // a unit's first element
   // every thread runs the same number of turns: the row sums are shuffles
-  for (int row0 = threadIdx.x / p.lanes; row0 - static_cast<int>(threadIdx.x) / p.lanes < rows; row0 += step * ROWS) {
-    Raw8<DT> raw[VE == 8 ? ROWS : 1][VE == 8 ? MAXU : 1][2];
-    float single[VE == 8 ? 1 : ROWS][VE == 8 ? 1 : MAXU][2][VE];
-    int tk[ROWS], w[ROWS], h[ROWS];
-#pragma unroll
-    for (int e = 0; e < ROWS; ++e) {
-      const int row = row0 + e * step;
-      tk[e] = row < rows ? row / heads : -1;
-      const int hh = row - tk[e] * heads;
-      w[e] = hh >= p.heads[0], h[e] = hh - (w[e] ? p.heads[0] : 0);
-      if (tk[e] < 0) continue;
-      const long long from = s_from[tk[e]][w[e]] + h[e] * p.ssh[w[e]];
+  for (int row0 = threadIdx.x / p.lanes; row0 - static_cast<int>(threadIdx.x) / p.lanes < rows; row0 += step) {
+    Raw8<DT> raw[VE == 8 ? MAXU : 1][2];
+    float single[VE == 8 ? 1 : MAXU][2][VE];
+    const bool live = row0 < rows;
+    const int tk = live ? row0 / heads : 0, hh = row0 - tk * heads;
+    const int w = hh >= p.heads[0], h = hh - (w ? p.heads[0] : 0);
+    if (live) {
+      const long long from = s_from[tk][w] + h * p.ssh[w];
 #pragma unroll
       for (int i = 0; i < MAXU; ++i) {
         const int u = lane + i * p.lanes;
         if (u >= units) continue;
         if constexpr (VE == 8) {
-          raw[e][i][0] = load8<DT, true>(p.src[w[e]], from + place(u));
-          if (u < npair) raw[e][i][1] = load8<DT, true>(p.src[w[e]], from + place(u) + half);
+          raw[i][0] = load8<DT, true>(p.src[w], from + place(u));
+          if (u < npair) raw[i][1] = load8<DT, true>(p.src[w], from + place(u) + half);
         } else {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
-            single[e][i][0][j] = one_element<DT>(p.src[w[e]], from + place(u) + j);
-            if (u < npair) single[e][i][1][j] = one_element<DT>(p.src[w[e]], from + place(u) + half + j);
+            single[i][0][j] = one_element<DT>(p.src[w], from + place(u) + j);
+            if (u < npair) single[i][1][j] = one_element<DT>(p.src[w], from + place(u) + half + j);
           }
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < ROWS; ++e) {
+    {
       float r = 1.f;
       if (p.norm) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < MAXU; ++i) {
           const int u = lane + i * p.lanes;
-          if (tk[e] < 0 || u >= units) continue;
+          if (!live || u >= units) continue;
           float x[VE];
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             if (side == 1 && u >= npair) continue;
-            if constexpr (VE == 8) unpack8<DT>(raw[e][i][side], x);
+            if constexpr (VE == 8) unpack8<DT>(raw[i][side], x);
             else
 #pragma unroll
-              for (int j = 0; j < VE; ++j) x[j] = single[e][i][side][j];
+              for (int j = 0; j < VE; ++j) x[j] = single[i][side][j];
 #pragma unroll
             for (int j = 0; j < VE; ++j) sum = fmaf(x[j], x[j], sum);
           }
@@ -690,10 +692,10 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
         for (int o = p.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         r = rsqrtf(fmaf(sum, over_d, p.eps));
       }
-      if (tk[e] < 0) continue;
-      const void *weight = p.weight[w[e]];
-      const float2 *trig = s_trig + tk[e] * half;
-      const long long to = s_to[tk[e]][w[e]] + h[e] * p.dsh[w[e]];
+      if (!live) continue;
+      const void *weight = p.weight[w];
+      const float2 *trig = s_trig + tk * half;
+      const long long to = s_to[tk][w] + h * p.dsh[w];
 #pragma unroll
       for (int i = 0; i < MAXU; ++i) {
         const int u = lane + i * p.lanes;
@@ -704,10 +706,10 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           if (side == 1 && !two) continue;
-          if constexpr (VE == 8) unpack8<DT>(raw[e][i][side], x[side]);
+          if constexpr (VE == 8) unpack8<DT>(raw[i][side], x[side]);
           else
 #pragma unroll
-            for (int j = 0; j < VE; ++j) x[side][j] = single[e][i][side][j];
+            for (int j = 0; j < VE; ++j) x[side][j] = single[i][side][j];
           if (weight) {
             float g[VE];
             if constexpr (VE == 8) unpack8<DT>(load8<DT, true>(weight, at + side * half), g);
@@ -741,13 +743,13 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
           }
         }
         if constexpr (VE == 8) {
-          store8<DT, true>(p.dst[w[e]], to + at, pack8<DT>(x[0]));
-          if (two) store8<DT, true>(p.dst[w[e]], to + at + half, pack8<DT>(x[1]));
+          store8<DT, true>(p.dst[w], to + at, pack8<DT>(x[0]));
+          if (two) store8<DT, true>(p.dst[w], to + at + half, pack8<DT>(x[1]));
         } else {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
-            put_element<DT>(p.dst[w[e]], to + at + j, x[0][j]);
-            if (two) put_element<DT>(p.dst[w[e]], to + at + half + j, x[1][j]);
+            put_element<DT>(p.dst[w], to + at + j, x[0][j]);
+            if (two) put_element<DT>(p.dst[w], to + at + half + j, x[1][j]);
           }
         }
       }
@@ -757,8 +759,10 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 
 // The same for rows of whole vectors with one unit to a thread, which is every
 // usual head: two rows in flight, the weights in registers, a CTA for the
-// queries or the keys of its tokens (blockIdx.y).  What a row costs is instructions (about
-// 100 a vector), so nothing is divided or looked up per row.
+// queries or the keys of its tokens (blockIdx.y).  What a row costs is
+// instructions (about 85 a vector), so nothing is divided or looked up per
+// row.  16380 tokens, 40 heads of 128, bf16: 68 us, 4.9 TB/s, bound by issue
+// (the kernel above took 112).
 template <int DT, bool PAIRS>
 __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ NormRopeParams p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]

@@ -90,9 +90,9 @@ const void *pick_norm_rope(bool vec, bool one, bool pairs) {
   if (vec && one)
     return pairs ? reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, true>)
                  : reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, false>);
-  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2, 1>);
-  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8, 1>)
-               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16, 1>);
+  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2>);
+  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8>)
+               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16>);
 }
 
 // The attention's kernel, its block and shared memory, and the floats of its
