@@ -169,9 +169,10 @@ __device__ __forceinline__ void decode4(int kind, uint32_t w, float (&x)[4]) {
         : "r"(w));
     const float2 f = f16x2_to_f32(lo), g = f16x2_to_f32(hi);
     x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
-  } else {
+  } else {  // the code + 128 as the low bits of 2^23 + code + 128; conversion instructions run at a quarter of the rate
+    w ^= 0x80808080u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j)));
+    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | j)) - 8388736.f;
   }
 }
 // Four fp32 values (already divided by the scale) as codes: nearest, ties to
@@ -185,11 +186,11 @@ __device__ __forceinline__ uint32_t encode4(int kind, float a, float b, float c,
     return lo | static_cast<uint32_t>(hi) << 16;
   }
   const float x[4] = {a, b, c, d};
-  uint32_t w = 0;
+  uint32_t u[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)  // __float2int_rn saturates and gives 0 for NaN
-    w |= static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x[j]))) & 0xff) << (8 * j);
-  return w;
+  for (int j = 0; j < 4; ++j)  // adding 1.5 * 2^23 rounds to a whole number in the sum's low bits
+    u[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(x[j] == x[j] ? x[j] : 0.f, -127.f), 127.f), 12582912.f));
+  return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
 }
 // As encode4 for finite values: a_j * inv with inv a power of two.  int8:
 // adding 1.5 * 2^23 rounds to a whole number in the sum's low bits.
@@ -244,23 +245,34 @@ __device__ __forceinline__ int page_of(const CacheView &c, int b, int blk, int32
 }
 
 // Rounds the rows of a block outside [lo, hi) to a larger scale (ratio =
-// old / new < 1), 16 codes at a time; thread `tid` of NTH.
+// old / new < 1), 16 codes at a time; thread `tid` of NTH.  A single warp reads
+// four times before it writes.
 template <int NTH>
 __device__ __forceinline__ void rescale_block(unsigned char *blk, int kind, int page, int D, int lo, int hi, float ratio, int tid) {
-  const int per_row = D / 16;
-  for (int c = tid; c < page * per_row; c += NTH) {
-    const int row = c / per_row;
-    if (row >= lo && row < hi) continue;
-    uint4 *at = reinterpret_cast<uint4 *>(blk) + c;
-    uint4 w = *at;
-    uint32_t *u = &w.x;
+  constexpr int FLY = NTH == 32 ? 4 : 1;
+  const int log_row = D == 128 ? 3 : 2, chunks = page << log_row;
+  uint4 *at = reinterpret_cast<uint4 *>(blk);
+  for (int c0 = tid; c0 < chunks; c0 += NTH * FLY) {
+    uint4 w[FLY];
+    bool mine[FLY];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x[4];
-      decode4(kind, u[j], x);
-      u[j] = encode4(kind, x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
+    for (int i = 0; i < FLY; ++i) {
+      const int c = c0 + i * NTH, row = c >> log_row;
+      mine[i] = c < chunks && (row < lo || row >= hi);
+      if (mine[i]) w[i] = at[c];
     }
-    *at = w;
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) {
+      if (!mine[i]) continue;
+      uint32_t *u = &w[i].x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x[4];
+        decode4(kind, u[j], x);
+        u[j] = encode4(kind, x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
+      }
+      at[c0 + i * NTH] = w[i];
+    }
   }
 }
 
@@ -461,11 +473,13 @@ constexpr int COMMIT_MAX_NODES = 1024;
 // matter.  Node i of the path moves from slot ctx + index[i] to ctx + i.
 // index[i] >= i, so with the rows taken in ascending order none is overwritten
 // before it has been read.  A warp takes a kv head and tensor by itself: it
-// reads a block's new rows once for their maximum and once (from the cache)
-// to write them.  The bytes are few, the latency of walk and reads counts: 32
-// trees of 63 nodes 4.7 us, 256 of 255 nodes 18 us (a CTA per head and tensor
-// took 32, one with a barrier per block 46).
-__global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
+// reads a block's new rows once for their maximum and once more (from L2) to
+// write them, unless they fit its registers.  The bytes are few; the latency of
+// walk and reads counts, and with four CTAs per SM the issue slots: 32 trees of
+// 63 nodes 4.3 us, 256 of 255 nodes 10.3 us (four vectors in flight 11.0, with
+// spills; a division and conversion instructions for each element 18; a CTA per
+// head and tensor 32; one with a barrier per block 46).
+__global__ void __launch_bounds__(256, 4) cache_commit_kernel(const __grid_constant__ CacheCommitParams p) {
   __shared__ int s_par[COMMIT_MAX_NODES], s_tok[COMMIT_MAX_NODES], s_path[COMMIT_MAX_NODES], s_index[COMMIT_MAX_NODES];
   __shared__ int s_node, s_bad, s_first;
   const CacheView &c = p.c;
@@ -513,38 +527,64 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant
   }
   if (!ok || s_first >= len) return;
 
-  constexpr int BATCH = 4;  // vectors of 16 codes per lane that are read before any is written
+  // the pages of the path's rows, over the tokens of the path (done with)
+  int *s_page = s_path;
+  for (int i = s_first + threadIdx.x; i < len; i += 256) s_page[i] = page_of(c, b, (ctx + s_index[i]) >> c.log_page, p.status);
+  __syncthreads();
+
+  constexpr int BATCH = 2;  // vectors of 16 codes per lane in flight
   const int lane = threadIdx.x & 31, log_row = c.D == 128 ? 3 : 2;  // vectors of a row: 8 or 4
   for (int ht = blockIdx.x * 8 + (threadIdx.x >> 5); ht < 2 * c.Hk; ht += gridDim.x * 8) {
     const int h = ht >> 1;
     unsigned char *base = ht & 1 ? c.v : c.k;
     float *scales = ht & 1 ? c.v_scale : c.k_scale;
-    // vector k of the rows from `row` on, and its scale (-1: a bad page)
-    const auto source = [&](int row, int k, float &scale) -> const uint4 * {
-      const int slot = ctx + s_index[row + (k >> log_row)];
-      const int page = page_of(c, b, slot >> c.log_page, p.status);
-      const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
-      scale = page < 0 ? -1.f : scales[id];
-      return reinterpret_cast<const uint4 *>(base + (id * c.page + (slot & (c.page - 1))) * c.D) + (k & ((1 << log_row) - 1));
-    };
     for (int row = s_first; row < len;) {
       const int in = (ctx + row) & (c.page - 1), n = min(len - row, c.page - in), vectors = n << log_row;
       const int page = page_of(c, b, (ctx + row) >> c.log_page, p.status);
       const long long id = static_cast<long long>(max(page, 0)) * c.Hk + h;
       const float old = scales[id];
+      uint4 raw[BATCH];
+      float from[BATCH];  // scales of the vectors; -1: a bad page, or past the last row
+      const auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int k = k0 + 32 * i, r = row + (k >> log_row);
+          raw[i] = make_uint4(0, 0, 0, 0);
+          from[i] = -1.f;
+          if (k >= vectors || s_page[r] < 0) continue;
+          const long long at = static_cast<long long>(s_page[r]) * c.Hk + h;
+          const int slot = (ctx + s_index[r]) & (c.page - 1);
+          from[i] = scales[at];
+          raw[i] = reinterpret_cast<const uint4 *>(base + (at * c.page + slot) * c.D)[k & ((1 << log_row) - 1)];
+        }
+      };
       uint32_t amax = 0;
-      for (int k = lane; k < vectors; k += 32) {
-        float from;
-        const uint4 w = *source(row, k, from);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int k0 = lane; k0 - lane < vectors; k0 += 32 * BATCH) {
+        load(k0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x[4];
-          decode4(c.kind, u[j], x);
+        for (int i = 0; i < BATCH; ++i) {
+          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          float x[4], most = 0.f;  // fmaxf passes over NaN
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a = __float_as_uint(x[e] * from) & 0x7fffffffu;
-            if (a < 0x7f800000u && from >= 0.f) amax = max(amax, a);
+          for (int j = 0; j < 4; ++j) {
+            decode4(c.kind, u[j], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(x[e]));
+          }
+          if (!(from[i] >= 0.f)) continue;
+          most *= from[i];
+          if (most < INFINITY) {  // false for NaN
+            amax = max(amax, __float_as_uint(fabsf(most)));  // not a negative zero
+          } else {  // a huge scale: the largest of the finite products
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              decode4(c.kind, j < 2 ? (j ? raw[i].y : raw[i].x) : (j == 2 ? raw[i].z : raw[i].w), x);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float a = fabsf(x[e] * from[i]);
+                if (a < INFINITY) amax = max(amax, __float_as_uint(a));
+              }
+            }
           }
         }
       }
@@ -552,15 +592,12 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant
       // a block's scale never shrinks here: the rows of other nodes still stand in it
       const float scale = fmaxf(scale_for(c.kind, amax), old);
       unsigned char *codes = base + id * c.page * c.D;
+      // powers of two (every scale of this library's own): the product with
+      // the inverse is the quotient
+      const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
+      const float inv = 1.f / scale;
       for (int k0 = lane; page >= 0 && k0 - lane < vectors; k0 += 32 * BATCH) {
-        uint4 raw[BATCH];
-        float from[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int k = k0 + 32 * i;
-          from[i] = -1.f;
-          if (k < vectors) raw[i] = *source(row, k, from[i]);
-        }
+        if (vectors > 32 * BATCH) load(k0);  // else they are in registers
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
@@ -571,7 +608,14 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const __grid_constant
             float x[4];
             decode4(c.kind, u[j], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = x[e] * from[i] / scale;
+            for (int e = 0; e < 4; ++e) x[e] *= from[i];
+            if (exact) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] *= inv;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] /= scale;
+            }
             u[j] = encode4(c.kind, x[0], x[1], x[2], x[3]);
           }
           reinterpret_cast<uint4 *>(codes + static_cast<long long>(in) * c.D)[k0 + 32 * i] = raw[i];

@@ -63,6 +63,29 @@ class Cache:
         part = lambda y: y.permute(0, 2, 1, 3).reshape(-1, H, y.shape[-1])[off:off + last - first]  # noqa: E731
         return part(x * scale) if scaled else (part(x), part(scale.expand(-1, -1, self.page, 1))[..., 0])
 
+    def row_f32(self, t, b, slot):
+        """As row, the product rounded to 32 bits."""
+        p = int(self.table[b, slot // self.page])
+        return values(self.codes[t][p, :, slot % self.page], self.kind).float() * self.scales[t][p][:, None]
+
+    def put_f32(self, t, b, start, rows):
+        """As put of a commit, for any scales and rows: quotients and products rounded to 32 bits, NaN as 0."""
+        code = lambda x: nearest(x.nan_to_num(0.0, math.inf, -math.inf).double(), self.kind).view(torch.uint8)  # noqa: E731
+        at = 0
+        while at < len(rows):
+            blk, r = divmod(start + at, self.page)
+            n = min(self.page - r, len(rows) - at)
+            p = int(self.table[b, blk])
+            for h in range(rows.shape[1]):
+                x, old, codes = rows[at:at + n, h], self.scales[t][p, h].clone(), self.codes[t][p, h].view(torch.uint8)
+                fine = x[torch.isfinite(x)]
+                new = torch.tensor(max(scale_for(fine.abs().max().item() if fine.numel() else 0.0, self.kind), old.item()))
+                if new > old:
+                    codes.copy_(code(values(self.codes[t][p, h], self.kind).float() * (old / new)))
+                    self.scales[t][p, h] = new
+                codes[r:r + n] = code(x / new)
+            at += n
+
     def put(self, t, b, start, rows, may_start_anew):
         at = 0
         while at < len(rows):

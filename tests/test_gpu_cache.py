@@ -487,6 +487,43 @@ def test_commit(kind, page, D, N, shared):
     same_state(cache, want)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,D", [(16, 128), (32, 64)])
+def test_commit_of_any_scales_and_codes(kind, page, D):
+    """Scales that are no powers of two, zero, minus zero and so large that products overflow; codes that the write
+    never makes (NaN, -128): every step in 32 bits, bit for bit."""
+    B, N, Hk, ctx = 4, 90, 2, [5, 0, 20, 31]
+    g = torch.Generator().manual_seed(page)
+    state = list(make_cache(B, 31 + N, Hk, page, D, kind, 3))
+    odd = 0x7f if kind == "e4m3" else 0x80
+    for t in (0, 1):
+        raw = state[t].view(torch.uint8)
+        raw[torch.rand(raw.shape, generator=g) < 0.01] = odd
+        scale = state[2 + t]
+        scale *= 1 + torch.rand(scale.shape, generator=g)
+        pick = torch.rand(scale.shape, generator=g)
+        scale[pick < 0.3] = 1.37 * 2.0 ** 122
+        scale[pick < 0.15] = 0.0
+        scale[pick < 0.07] = -0.0
+    parent = torch.arange(-3, N - 3, dtype=torch.int32).clamp(min=0)       # three chains from the root
+    parent[0] = -1
+    tokens = torch.arange(100, 100 + N, dtype=torch.int32).repeat(B, 1)
+    ids = [[0] + list(range(s, N, 3))[:n] for s, n in ((2, 29), (3, 17), (2, 5), (3, 29))]
+    path, length = torch.full((B, 31), -1, dtype=torch.int32), torch.tensor([len(i) for i in ids], dtype=torch.int32)
+    want = ref.Cache(*state, kind)
+    for b in range(B):
+        path[b, :len(ids[b]) - 1] = 100 + torch.tensor(ids[b][1:], dtype=torch.int32)
+        for t in (0, 1):
+            rows = [want.row_f32(t, b, ctx[b] + n) for n in ids[b][1:]]
+            want.put_f32(t, b, ctx[b] + 1, torch.stack(rows))
+    cache, table = on_gpu(state)
+    index, _ = binding.spec_cache_commit(cache, table, ints(*ctx), parent.cuda(), tokens.cuda(), path.cuda(), length.cuda())
+    assert binding.spec_get_status() == 0
+    for b in range(B):
+        assert index[b, :len(ids[b])].tolist() == ids[b]
+    same_state(cache, want)
+
+
 def test_commit_leaves_failed_sequences_alone():
     N, D = 4, 64
     parent = ints(-1, 0, 0, 1).repeat(4, 1)
