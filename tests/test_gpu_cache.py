@@ -232,6 +232,12 @@ def test_norm_rope(dtype, D, rot, pairs, norm, B, N, Hq, Hk):
         assert torch.all((y.cpu().double() - exp).abs() <= tol)
 
 
+@pytest.mark.parametrize("D,rot,pairs", [(80, 80, False), (128, 48, True), (128, 128, False), (64, 48, False)])
+def test_norm_rope_of_many_tokens(D, rot, pairs):
+    """Several angles to a thread, whether or not their number divides the threads."""
+    test_norm_rope(BF16, D, rot, pairs, True, 3, 5000, 2, 1)
+
+
 def test_norm_rope_in_place_strided_and_single():
     g = torch.Generator().manual_seed(1)
     both = torch.randn((2, 9, 6, 128), generator=g).to(BF16).cuda()       # q and k heads in one tensor
