@@ -162,7 +162,7 @@ struct TileLayout {
 
 struct TileBars {
   uint64_t raw_full[T_RAW], raw_empty[T_RAW], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
-  uint64_t sc_full[T_SCALES], q_full;
+  uint64_t sc_full[T_SCALES], q_full[2];  // q_full: for each group's product warp, segments with a tile of the group
 };
 static_assert(sizeof(TileBars) <= 40 * 8, "barriers");
 
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 8), mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < T_SCALES; ++i) mbar_init(&bar.sc_full[i], 1);
-    mbar_init(&bar.q_full, T_SOFT / 32);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.q_full[i], T_SOFT / 32);
     fence_mbar_init();
   }
   if (warp == (T_SOFT + T_CONV) / 32) tmem_alloc(s_tmem, 512);
@@ -414,9 +414,17 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           *reinterpret_cast<uint4 *>(smem + L::Q + (chunk >> 3) * 16384 + r * 128 + ((chunk & 7) ^ (r & 7)) * 16) = w;
         }
         fence_async_smem();
-        arrive(&bar.q_full);
       }
       const int s0 = at.j, end = min(at.n - at.j, count - i) + i;
+      const bool has[2] = {end - i >= 2 || !(i & 1), end - i >= 2 || (i & 1)};  // the group has a tile
+      // A product warp waits for the segments of its group's tiles alone.  The
+      // softmax ends such a segment after that group's last product, so the
+      // barrier is never a phase ahead of the warp; a warp that also waited for
+      // the other group's segments could fall two phases behind, where parities
+      // are equal again.
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (has[e]) arrive(&bar.q_full[e]);
       // A tile is weighed again, and the accumulator scaled, when the offset
       // moves.  Over a long axis the largest weight starts at 2^8: fp16 then
       // keeps its full precision down to 2^-22 of it, and the offset moves once
@@ -552,7 +560,6 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         if (lane == 0) mbar_arrive_many(&bar.p_full[grp], (warp & 3) == 0 ? 4 - (rows - 1) / 32 : 1);
       }
       // ---- the end of the segment: both groups' parts meet
-      const bool has[2] = {end - i >= 2 || !(i & 1), end - i >= 2 || (i & 1)};  // the group had a tile
       if (live && has[grp]) {
         wait(&bar.o_done[grp], (uses - 1) & 1);
         tc_after_sync();
@@ -712,9 +719,9 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       };
       TileCursor u = at;
       int i = g;  // this group's next tile
-      uint32_t ph = 0;
-      for (int seg0 = 0, seg1 = at.n - at.j, segs = 0;; tile_next(p, u), seg0 = seg1, seg1 += u.n, ++segs) {
-        one(&bar.q_full, segs & 1);
+      uint32_t ph = 0, ph_q = 0;
+      for (int seg1 = at.n - at.j;; tile_next(p, u), seg1 += u.n) {
+        if (i < min(seg1, count)) one(&bar.q_full[g], ph_q), ph_q ^= 1;
         for (const int end = min(seg1, count), first = i; i < end; i += 2, ph ^= 1) {
           one(&bar.k_full[g], ph);
           tc_after_sync();
