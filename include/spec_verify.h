@@ -35,10 +35,17 @@
  *     that work drains, and they wait for it to complete before reading
  *     anything, so stream order is unchanged.
  *   - The library keeps one grow-only device workspace per (device, stream)
- *     pair (a few ints per sequence).  Growing it calls cudaMalloc, so the
- *     first call of a new size on a stream should not be inside a CUDA graph
- *     capture.  Two calls that overlap on the GPU must use different streams.
- *     spec_shutdown() frees every workspace.
+ *     pair: 16 bytes per row, 16 KB of the row and consumer warp in a
+ *     verification, up to 21 MB for spec_cache_attention (it depends on Hq * N /
+ *     kv_heads, head_dim and the number of SMs, not on the lengths), a few ints
+ *     per sequence otherwise.  Growing it (to twice its size at least) calls
+ *     cudaMalloc, so the first call of a new size on a stream should not be
+ *     inside a CUDA graph capture.
+ *     What a call has outgrown stays allocated, so a graph captured earlier can
+ *     be replayed after any later call; a replay uses the workspace of the
+ *     stream that was captured.  Two calls or replays that overlap on the GPU
+ *     must use the workspaces of different streams.  spec_shutdown() frees
+ *     every workspace; graphs captured before it must not be replayed.
  *   - Identical inputs and seed give identical outputs, bit for bit.
  */
 #ifndef SPEC_VERIFY_H

@@ -25,9 +25,10 @@ int cuda_fail(cudaError_t e, const char *what);
 // cudaLaunchKernelExC, or the injected failure of spec_debug_fail_launch.
 cudaError_t launch_kernel(const cudaLaunchConfig_t *cfg, const void *fn, void **args);
 
-// Per (device, stream): the status word (never reallocated), the row
-// partials of the current call (float4 per job and slice, grow-only), and a
-// staging area for the host-buffer entry point.
+// Per (device, stream): the status word (never reallocated), the partials of
+// the current call (rows of the verification: float4 per job and slice; pieces
+// of the attention; grow-only), counters, and a staging area for the
+// host-buffer entry point.
 struct Workspace {
   int device = -1;
   cudaStream_t stream = nullptr;
@@ -40,6 +41,11 @@ struct Workspace {
   size_t ngram_cap = 0;
   int *attn_done = nullptr;   // cache attention: arrived-CTA counters, zero between calls
   size_t attn_cap = 0;
+  // What partials and counters have outgrown, until spec_shutdown: a CUDA graph
+  // captured before still points there.  A buffer grows to twice its size at
+  // least, so all that it has outgrown is smaller than it, and in 2^40 bytes.
+  void *outgrown[128] = {};
+  int n_outgrown = 0;
 };
 
 // The stream's workspace with room for nparts partials and, where asked for,

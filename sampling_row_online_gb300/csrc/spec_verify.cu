@@ -74,6 +74,33 @@ Workspace *find_ws(int device, cudaStream_t stream, bool create) {
   return w;
 }
 
+// Makes *buf hold `need` elements.  The outgrown buffer is not freed: a CUDA
+// graph captured on the stream before may be replayed later.
+template <typename T>
+int grow(Workspace *w, T **buf, size_t *cap, size_t need, const char *what) {
+  if (*cap >= need) return SPEC_OK;
+  if (*buf && w->n_outgrown == static_cast<int>(sizeof w->outgrown / sizeof *w->outgrown))
+    return fail(SPEC_ERR_CUDA, "a workspace has grown too often");
+  const size_t n = std::max(need, 2 * *cap);
+  T *fresh = nullptr;
+  const cudaError_t e = cudaMalloc(&fresh, sizeof(T) * n);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  if (*buf) w->outgrown[w->n_outgrown++] = *buf;
+  *buf = fresh;
+  *cap = n;
+  return SPEC_OK;
+}
+// The same for counters, which start at zero.
+int grow_counters(Workspace *w, int **buf, size_t *cap, size_t need, cudaStream_t stream) {
+  if (*cap >= need) return SPEC_OK;
+  const int st = grow(w, buf, cap, need, "cudaMalloc(counters)");
+  if (st) return st;
+  const cudaError_t e = cudaMemsetAsync(*buf, 0, sizeof(int) * *cap, stream);
+  if (e == cudaSuccess) return SPEC_OK;
+  *cap = 0;  // not zeroed: the next call tries again
+  return cuda_fail(e, "cudaMemsetAsync(counters)");
+}
+
 }  // namespace
 
 int get_ws(cudaStream_t stream, size_t nparts, Workspace **out, size_t nattn) {
@@ -88,30 +115,9 @@ int get_ws(cudaStream_t stream, size_t nparts, Workspace **out, size_t nattn) {
     e = cudaMemsetAsync(w->status, 0, CONTROL_BYTES, stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
   }
-  if (w->cap_parts < nparts) {
-    if (w->partials) {
-      e = cudaFree(w->partials);  // synchronises the device: no call still uses it
-      w->partials = nullptr;
-      w->cap_parts = 0;
-      if (e != cudaSuccess) return cuda_fail(e, "cudaFree(partials)");
-    }
-    e = cudaMalloc(&w->partials, sizeof(float4) * nparts);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(partials)");
-    w->cap_parts = nparts;
-  }
-  if (w->attn_cap < nattn) {
-    if (w->attn_done) {
-      e = cudaFree(w->attn_done);  // synchronises the device: no call still uses it
-      w->attn_done = nullptr;
-      w->attn_cap = 0;
-      if (e != cudaSuccess) return cuda_fail(e, "cudaFree(attention counters)");
-    }
-    if ((e = cudaMalloc(&w->attn_done, sizeof(int) * nattn)) != cudaSuccess)
-      return cuda_fail(e, "cudaMalloc(attention counters)");
-    if ((e = cudaMemsetAsync(w->attn_done, 0, sizeof(int) * nattn, stream)) != cudaSuccess)
-      return cuda_fail(e, "cudaMemsetAsync(attention counters)");
-    w->attn_cap = nattn;
-  }
+  int st = grow(w, &w->partials, &w->cap_parts, nparts, "cudaMalloc(partials)");
+  if (st) return st;
+  if ((st = grow_counters(w, &w->attn_done, &w->attn_cap, nattn, stream))) return st;
   *out = w;
   return SPEC_OK;
 }
@@ -793,20 +799,9 @@ int spec_ngram_propose(const int32_t *tokens, const int32_t *lengths, int B, int
   Workspace *w = nullptr;
   int st = get_ws(stream, (part_bytes + 15) / 16, &w);
   if (st) return st;
-  if (w->ngram_cap < static_cast<size_t>(B)) {
+  {
     std::lock_guard<std::mutex> lock(g_mu);
-    cudaError_t e;
-    if (w->ngram_done) {
-      e = cudaFree(w->ngram_done);  // synchronises the device: no call still uses it
-      w->ngram_done = nullptr;
-      w->ngram_cap = 0;
-      if (e != cudaSuccess) return cuda_fail(e, "cudaFree(ngram counters)");
-    }
-    if ((e = cudaMalloc(&w->ngram_done, sizeof(int) * B)) != cudaSuccess)
-      return cuda_fail(e, "cudaMalloc(ngram counters)");
-    if ((e = cudaMemsetAsync(w->ngram_done, 0, sizeof(int) * B, stream)) != cudaSuccess)
-      return cuda_fail(e, "cudaMemsetAsync(ngram counters)");
-    w->ngram_cap = B;
+    if ((st = grow_counters(w, &w->ngram_done, &w->ngram_cap, static_cast<size_t>(B), stream))) return st;
   }
   // G <= 8: the sequence's CTAs form a cluster and combine on chip
   const bool cl = G <= NGRAM_MAX_CLUSTER;
@@ -1109,6 +1104,7 @@ void spec_shutdown(void) {
     if (w->stage) cudaFree(w->stage);
     if (w->ngram_done) cudaFree(w->ngram_done);
     if (w->attn_done) cudaFree(w->attn_done);
+    for (int i = 0; i < w->n_outgrown; ++i) cudaFree(w->outgrown[i]);
     delete w;
   }
   g_ws.clear();
