@@ -478,8 +478,10 @@ int spec_eagle2_rerank(const float *node_values, const int32_t *node_parents,
  * hold anything.  The scales that spec_cache_write and spec_cache_commit give
  * are powers of two: the least with amax <= qmax * scale (qmax: 448 for e4m3,
  * 127 for int8) over the block's new rows, at least 2^-100.  A caller's own
- * codes may come with any non-negative finite scales (value scales below 2^-100
- * count as 0 in the attention).
+ * codes may come with any non-negative finite scales under which the values are
+ * finite (value scales up to 2^-100 count as 0 in the attention; the others that
+ * one token sees should lie within a factor of 2^80 of one another: beyond it,
+ * slots with the smallest can be left out of the softmax's sum).
  *
  * Errors on the device (spec_get_status): a sequence whose slots do not fit
  * its pages (SPEC_ERR_ARG) or a page id outside [0, pages) (SPEC_ERR_PAGE) has

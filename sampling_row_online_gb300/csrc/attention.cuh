@@ -52,7 +52,10 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 constexpr float WEIGHT_UP = 13.f, WEIGHT_SLACK = 2.9f;  // the largest weight is 2^13 to 2^15.9
-constexpr float LEAST_V_SCALE = 7.888609052210118e-31f;  // 2^-100: below it a block counts as zero
+constexpr float LEAST_V_SCALE = 7.888609052210118e-31f;  // 2^-100: up to it a block counts as zero
+// A slot adds up to 2^15.9 / sv, below 2^115.9, to the sum: held as 2^-18 of
+// it, under an offset that is 18 higher, 2^30 slots stay below 2^128.
+constexpr float SUM_UP = 18.f, SUM_DOWN = 3.814697265625e-06f;
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -260,6 +263,21 @@ __device__ __forceinline__ void put_lse(const AttnParams &p, const Segment &g, i
   const long long row = (static_cast<long long>(g.b) * p.N + r / p.G) * (p.c.Hk * p.G) + g.h * p.G + r % p.G;
   p.lse[row] = l == 0.f ? __uint_as_float(0xff800000u) : (m + log2f(l)) * 0.6931471805599453f;
 }
+
+// What a row's products take: `down`, then `inv`, 2^-18 / sum together (0 where
+// nothing is seen); neither leaves fp32's range where the sum does not.
+struct Inverse {
+  float down, inv;
+  __device__ __forceinline__ explicit Inverse(float sum) {
+    const bool big = sum > 1.f;
+    down = big ? SUM_DOWN : 1.f;
+    inv = sum == 0.f ? 0.f : 1.f / (big ? sum : sum * (1.f / SUM_DOWN));
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * down * inv; }
+  __device__ __forceinline__ float4 operator()(float4 x) const {
+    return make_float4((*this)(x.x), (*this)(x.y), (*this)(x.z), (*this)(x.w));
+  }
+};
 
 template <int D, int KIND, int DT, int RT>
 __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, RT>::RESIDENT) attn_stream_kernel(const __grid_constant__ AttnParams p) {
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
           }
         const bool edge = (step + 1) * ASTEP > at.ctx;  // new tokens, or slots past the last one
         const bool zero = sc.y <= LEAST_V_SCALE;        // no values in this block: it counts in a sum of its own
-        const float lv = zero ? 0.f : lg2(sc.y), rv = 1.f / sc.y;
+        const float lv = zero ? 0.f : lg2(sc.y), rv = 1.f / sc.y * SUM_DOWN;
         float x[RT][4];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -628,6 +646,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float &lr = l[rt][e], &mr = m[rt][e];
+          mr += SUM_UP;
           if (__any_sync(0xffffffffu, l0[rt][e] > 0.f)) {  // joined so that neither sum overflows
             const float nm = fmaxf(mr, m0[rt][e] - 60.f), nb = nm == NINF ? 0.f : nm;
             const float a = ex2(mr - nb);
@@ -653,12 +672,12 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 8 * rt + 2 * t + e;
-          const float inv = l[rt][e] == 0.f ? 0.f : 1.f / l[rt][e];
+          const Inverse over(l[rt][e]);
 #pragma unroll
           for (int q = 0; q < MT / 2; ++q) {
             const float4 z = make_float4(o[rt][2 * q][e], o[rt][2 * q][2 + e], o[rt][2 * q + 1][e], o[rt][2 * q + 1][2 + e]);
             if (!whole) reinterpret_cast<float4 *>(to)[((rt * 2 + e) * (MT / 2) + q) * 32 + lane] = z;
-            else if (r < rows) put4<DT>(p, seg, D, r, g * VB + 4 * q, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
+            else if (r < rows) put4<DT>(p, seg, D, r, g * VB + 4 * q, over(z));
           }
           if (g == 0) {
             if (!whole) to[L::ROWS * D + r] = m[rt][e], to[L::ROWS * D + L::ROWS + r] = l[rt][e];
@@ -719,8 +738,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
       }
       const bool head = col_of(k) == 0;
       if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        put4<DT>(p, seg, D, row, col_of(k), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        put4<DT>(p, seg, D, row, col_of(k), Inverse(sum)(acc));
         if (head) put_lse(p, seg, row, M, sum);
       } else {
         float *to = work + which * L::PIECE;
@@ -781,8 +799,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
           sum = fmaf(a, ll[e], sum);
         }
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      put4<DT>(p, seg, D, row, col_of(k), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      put4<DT>(p, seg, D, row, col_of(k), Inverse(sum)(acc));
       if (col_of(k) == 0) put_lse(p, seg, row, M, sum);
     }
     if (threadIdx.x == 0) p.done[c0] = 0;  // zero again for the next call

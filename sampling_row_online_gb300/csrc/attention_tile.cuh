@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
                   pk[16 * q + 8 * hf + e / 2] = f32_to_f16x2(x.x, x.y);
                 }
                 const float2 both = add2(part[0], part[1]);
-                if (!zero) sum = fmaf(both.x + both.y, ex2(-sc.y), sum);
+                if (!zero) sum = fmaf((both.x + both.y) * SUM_DOWN, ex2(-sc.y), sum);
               }
             }
           };
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       tc_after_sync();
       // all products with the queries are done: their place takes the sums
       float4 *sums = reinterpret_cast<float4 *>(smem + L::Q);
-      sums[quarter * 128 + r] = make_float4(m, l, m0, l0);
+      sums[quarter * 128 + r] = make_float4(m + SUM_UP, l, m0, l0);
       meet();
       float M = NINF, mg[2];
       float4 each[4];
@@ -585,8 +585,8 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       for (int e = 0; e < 4; ++e) sum += each[e].y * ex2(each[e].x - bm) + each[e].w * ex2(each[e].z - bm);
       const bool whole = s0 == 0 && s0 + end - i == at.n;
       const int which = s0 > 0 ? 0 : 1;
-      const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-      const float aw = ex2(mg[0] - bm) * inv, bw = ex2(mg[1] - bm) * inv;
+      const Inverse over(sum);
+      const float aw = ex2(mg[0] - bm) * (whole ? over.inv : 1.f), bw = ex2(mg[1] - bm) * (whole ? over.inv : 1.f);
       float *piece = mine + which * L::PIECE;
       const long long orow = (static_cast<long long>(at.b) * p.N + node) * (c.Hk * p.G) + at.h * p.G + row % p.G;
 #pragma unroll
@@ -607,7 +607,9 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 16; e += 8) {
-              const float w[8] = {z[e], z[e + 1], z[e + 2], z[e + 3], z[e + 4], z[e + 5], z[e + 6], z[e + 7]};
+              float w[8];
+#pragma unroll
+              for (int g = 0; g < 8; ++g) w[g] = z[e + g] * over.down;
               store8<DT, true>(p.out, orow * D + col + e, pack8<DT>(w));
             }
           } else {
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
             const float b2 = M2 == NINF ? 0.f : M2;
             float sum2 = 0.f;
             for (int e = 0; e < n; ++e) sum2 = fmaf(ex2(__ldcg(part(e) + 128 * D + r) - b2), __ldcg(part(e) + 128 * D + 128 + r), sum2);
-            const float inv2 = sum2 == 0.f ? 0.f : 1.f / sum2;
+            const Inverse over2(sum2);
 #pragma unroll 1
             for (int q = 0; q < D / 64; ++q) {
               const int col = quarter * (D / 4) + 16 * q;
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
               for (int e = 0; e < 16; e += 8) {
                 float w[8];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) w[g] = z[e + g] * inv2;
+                for (int g = 0; g < 8; ++g) w[g] = over2(z[e + g]);
                 store8<DT, true>(p.out, orow * D + col + e, pack8<DT>(w));
               }
             }
