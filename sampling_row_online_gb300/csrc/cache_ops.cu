@@ -101,6 +101,7 @@ struct AttnChoice {
   const void *fn;
   int threads, smem, ctas;  // ctas: per SM
   size_t work;
+  int rows, tokens;         // of a work item
 };
 // By the rows per kv head.  Up to 24 a warp's own matrix instructions, 8 rows at
 // a time, are faster; beyond, the tensor cores with accumulators in tensor
@@ -111,18 +112,18 @@ template <int D, int KIND, int DT>
 AttnChoice choose_attn(long long rows) {
   if (rows <= 8) {
     using L = StreamLayout<D, 1>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 1>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK, L::ROWS, ASTEP};
   }
   if (rows <= 16) {
     using L = StreamLayout<D, 2>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 2>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK, L::ROWS, ASTEP};
   }
   if (rows <= 24) {
     using L = StreamLayout<D, 3>;
-    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 3>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK};
+    return {reinterpret_cast<const void *>(&attn_stream_kernel<D, KIND, DT, 3>), L::THREADS, L::SMEM, L::RESIDENT, L::WORK, L::ROWS, ASTEP};
   }
   using L = TileLayout<D>;
-  return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 1, 2 * L::PIECE};
+  return {reinterpret_cast<const void *>(&attn_tile_kernel<D, KIND, DT>), T_NT, L::SMEM, 1, 2 * L::PIECE, TQ, TK};
 }
 AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   const bool bf = dtype == SPEC_BF16;
@@ -285,11 +286,13 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   p.B = B, p.N = N, p.W = (N + 31) / 32, p.G = Hq / p.c.Hk;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.q_vec = vectors(*q, 2);
-  // the kernels count their work (steps of 16 tokens; tiles of 128 rows by 128 tokens) in 31 bits
-  const double row_tiles = std::ceil(static_cast<double>(N) * p.G / TQ);
-  if (static_cast<double>(B) * p.c.Hk * row_tiles * pages_per_seq * p.c.page / 16 >= 2147483648.0)
-    return fail(SPEC_ERR_ARG, "B * Hq * N * pages_per_seq is too large");
   const AttnChoice k = choose_attn(p.c.D, p.c.kind, dtype, static_cast<long long>(N) * p.G);
+  // the kernels count their work items in 31 bits; a kv head's rows fit 31 bits
+  // with them (fewer than 2^16 per token, no more tokens than slots)
+  const double row_tiles = std::ceil(static_cast<double>(N) * p.G / k.rows);
+  const double steps = std::ceil(static_cast<double>(pages_per_seq) * p.c.page / k.tokens);
+  if (static_cast<double>(B) * p.c.Hk * row_tiles * steps >= 2147483648.0)
+    return fail(SPEC_ERR_ARG, "B * Hq * N * pages_per_seq is too large");
   const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   const int grid = num_sms() * k.ctas;
