@@ -484,10 +484,12 @@ int spec_eagle2_rerank(const float *node_values, const int32_t *node_parents,
  * slots with the smallest can be left out of the softmax's sum).
  *
  * Errors on the device (spec_get_status): a sequence whose slots do not fit
- * its pages (SPEC_ERR_ARG) or a page id outside [0, pages) (SPEC_ERR_PAGE) has
- * NaN outputs, or is not written (only the bad page's rows, where its others
- * are good).  Where a bounded wait of the attention ran out
- * (SPEC_ERR_TIMEOUT), the outputs of that call are not to be used.
+ * its pages (SPEC_ERR_ARG) has NaN outputs, or is not written.  A page id
+ * outside [0, pages) (SPEC_ERR_PAGE) makes NaN what needs the page (the rows
+ * read of it; every token whose attention sees one of its slots), and its rows
+ * are not written; the sequence's others are as they would be.  Where a bounded
+ * wait of the attention ran out (SPEC_ERR_TIMEOUT), the outputs of that call are
+ * not to be used.
  */
 typedef struct {
   void *k, *v;              /* codes [pages, kv_heads, page_size, head_dim], 16-byte aligned */

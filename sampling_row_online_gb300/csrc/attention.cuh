@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
         if (!bad) {
           cp_async<4>(sc, scales, pol);
           cp_async<4>(sc + 4, scales + vs_off, pol);
-        } else {  // a NaN scale makes the rows NaN
+        } else {  // a NaN scale makes the rows NaN that see the page
           if (lane == 0) atomicOr(p.status, ST_PAGE);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sc), "r"(0x7fc00000u), "r"(0x3f800000u) : "memory");
         }
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(StreamLayout<D, RT>::THREADS, StreamLayout<D, 
             v[i][0] = a.x, v[i][1] = a.y;
           }
         }
-        if (edge) {  // rows that are not there may hold anything, NaN codes too
-          const int end = at.ctx + at.cnt - step * ASTEP - 2 * t;
+        if (edge) {  // rows that are not there, or another page's for a bad one, may hold anything, NaN codes too
+          const int end = sc.x == sc.x ? at.ctx + at.cnt - step * ASTEP - 2 * t : 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::MISC);
   volatile int *s_last = reinterpret_cast<volatile int *>(smem + L::MISC + 4);
   int *s_seq = reinterpret_cast<int *>(smem + L::MISC + 8);
+  volatile int *s_bad = reinterpret_cast<volatile int *>(smem + L::MISC + 32);  // [T_RAW]: a slot holds another page's rows
   unsigned *s_base = reinterpret_cast<unsigned *>(smem + L::MISC + 16);
   unsigned *s_scan = reinterpret_cast<unsigned *>(smem + L::ML);
   const CacheView &c = p.c;
@@ -469,23 +470,22 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
               tmem_ld16(tS + 32 * q + 16, s[1]);
               tc_wait_ld(s[0]);
               tc_wait_ld(s[1]);
-              if constexpr (decltype(at_edge)::value) {
-                const uint32_t bits = seen32(q);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((bits >> e) & 1)) s[e >> 4][e & 15] = 0xff800000u;
-              }
+              uint32_t bits = ~0u;
+              if constexpr (decltype(at_edge)::value) bits = seen32(q);
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {  // 16 tokens that share their scales
                 const float2 sc = sc_at[2 * q + hf];
                 const bool zero = sc.y == NINF;  // a block without values: every exponent becomes -inf
                 any_zero |= zero;
-                // a factor of 0 (no keys, no scale) must leave what is not seen at -inf
-                const float f = fmaxf(fac * sc.x, 1e-37f), off = sc.y - base;
+                const float f = fac * sc.x, off = sc.y - base;  // NaN for a bad page
                 float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                   float2 x = fma2(make_float2(__uint_as_float(s[hf][e]), __uint_as_float(s[hf][e + 1])), make_float2(f, f), make_float2(off, off));
+                  if constexpr (decltype(at_edge)::value) {  // after the scale: a bad page is NaN only where it is seen
+                    if (!((bits >> (16 * hf + e)) & 1)) x.x = NINF;
+                    if (!((bits >> (16 * hf + e + 1)) & 1)) x.y = NINF;
+                  }
                   hi = fmaxf(fmaxf(hi, x.x), x.y);
                   x.x = ex2(x.x), x.y = ex2(x.y);
                   part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
@@ -690,14 +690,14 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       if (left == 0) tile_next(p, u), left = u.n;
       const int j = u.n - left;
       --left;
-      const bool safe = (j + 1) * TK <= u.ctx + u.cnt;  // every row of the tile has been written
+      const bool written = (j + 1) * TK <= u.ctx + u.cnt;  // every row of the tile
       const uint32_t buf = i & 1, ph = (i >> 1) & 1;
       const int slot = (2 * i + t) % T_RAW;
       lazy_wait(&bar.raw_full[slot], ((2 * i + t) / T_RAW) & 1);
       lazy_wait(t ? &bar.v_empty[buf] : &bar.k_empty[buf], ph ^ 1);
       const unsigned char *raw = smem + L::RAW + slot * L::RAWB;
       unsigned char *to = smem + (t ? L::V : L::K) + buf * L::OP;
-      if (safe) convert_tile<D, KIND, false>(raw, to, ct);
+      if (written && !s_bad[slot]) convert_tile<D, KIND, false>(raw, to, ct);
       else convert_tile<D, KIND, true>(raw, to, ct);
       fence_async_smem();
       arrive(t ? &bar.v_full[buf] : &bar.k_full[buf]);
@@ -760,6 +760,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
       const int j = u.n - left, tok = j * TK + 16 * (lane & 7), len = u.ctx + u.cnt;
       const bool there = lane < 8 && tok < len, bad = there && static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages);
       const long long id = static_cast<long long>(bad ? 0 : page) * c.Hk + u.h;
+      const bool any_bad = __any_sync(0xffffffffu, bad);
       if (bad) atomicOr(p.status, ST_PAGE);
       float ks = 0.f, vs = 1.f;
       if (there) ks = c.k_scale[id], vs = c.v_scale[id];
@@ -777,7 +778,10 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         const int slot = (2 * i + t) % T_RAW;
         lazy_wait(&bar.raw_empty[slot], (((2 * i + t) / T_RAW) & 1) ^ 1);
         if (lost) break;  // no copy into a slot that may be in use
-        if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], bytes * pages);
+        if (lane == 0) {
+          s_bad[slot] = any_bad;
+          mbar_arrive_expect_tx(&bar.raw_full[slot], bytes * pages);
+        }
         __syncwarp();
         if (lead)
           asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(T_NT, 1) attn_tile_kernel(const __grid_constan
         issued = 2 * i + t + 1;
       }
       if (lane < 8) {
-        const float lv = bad ? __uint_as_float(0x7fc00000u) : vs <= LEAST_V_SCALE ? __uint_as_float(0xff800000u) : lg2(vs);
+        const float lv = bad ? 0.f : vs <= LEAST_V_SCALE ? __uint_as_float(0xff800000u) : lg2(vs);
         reinterpret_cast<float2 *>(smem + L::SCALES)[(i % T_SCALES) * 8 + lane] = make_float2(bad ? __uint_as_float(0x7fc00000u) : ks, lv);
       }
       arrive(&bar.sc_full[i % T_SCALES]);
