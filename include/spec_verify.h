@@ -576,7 +576,10 @@ int spec_cache_read(const spec_cache_t *cache, const int32_t *page_table, int pa
  *   lse           [B, N, Hq] float or NULL: the natural logarithm of the sum of
  *                 exp(scale * q . k_j); -inf where nothing is seen
  * 0 <= N <= SPEC_MAX_NEW_TOKENS; N = 1 is a decoding step.  Scores, sums and
- * the output are held in fp32.
+ * the output are held in fp32.  Queries are rounded to fp16 under a power of two
+ * per row (exact down to 2^-14 of the row's largest element), softmax weights to
+ * fp16 (2^-11 of the weight) where they meet the value codes; the sum takes the
+ * unrounded weights.
  */
 int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
                          const int32_t *ctx_len, const int32_t *counts, const spec_heads_t *q,

@@ -11,14 +11,20 @@
 //   out = sum_j w_j cv_j / sum_j w_j / sv_j:
 //
 // the value's scale rides in the exponent, so the largest weight that meets
-// the codes lies in [2^13, 2^15.9] whatever the scales are (fp16 keeps its full
-// precision down to 2^-27 of it), and both scales cost nothing more than the
-// multiply-add that every score needs anyway.  Codes of both kinds
-// are exact in fp16 (e4m3 as code * 2^-8, by moving bits; int8 by an offset),
-// queries are fp16 with a power of two per row, and the products accumulate in
-// fp32; the one rounding inside is that of the weights to fp16 (half a step
-// 2^-12 relative).  Sums, maxima and the output stay in fp32 until the output
-// is rounded once.
+// the codes lies in [2^13, 2^15.9] whatever the scales are, and both scales cost
+// nothing more than the multiply-add that every score needs anyway.  (The tile
+// kernel starts at 2^8 over eight or more tiles of tokens.)  What is rounded:
+// * weights to fp16 before they meet the codes, by half a step, 2^-11 relative,
+//   or by fp16's least half step 2^-25 below 2^-14: 2^-38 of the largest weight
+//   (2^-33 where that is 2^8).  The sum takes them in fp32, before that.
+// * queries to fp16 under a power of two per row that puts the largest element
+//   in [1, 2): bf16 and fp16 elements stay exact down to 2^-14 of it, below that
+//   they are off by 2^-25 of it at most.
+// * the output, once.
+// Codes are exact in fp16 (e4m3 by the conversion instruction, int8 by an
+// offset); products accumulate, and maxima, sums and the output are held, in
+// fp32.  exp2 flushes weights below 2^-126, which is why value scales of one row
+// should lie within 2^80 of one another: a slot's part of the sum is w / sv.
 //
 // Rows: row r of kv head h is node r / G, query head h G + r % G, with G the
 // query heads per kv head.
@@ -62,9 +68,10 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
-// Two codes, each in the upper byte of a half, as fp16: e4m3 as value * 2^-8
+// Two e4m3 codes, each in the upper byte of a half, as fp16 of value * 2^-8
 // (sign to the sign, the seven other bits to the top of exponent and mantissa;
-// subnormals stay exact), the lower bytes do not matter.
+// subnormals stay exact, and any bits give a finite number); the lower bytes do
+// not matter.
 __device__ __forceinline__ uint32_t e4m3_halves(uint32_t x) { return ((x >> 1) & 0x3f803f80u) | (x & 0x80008000u); }
 // int8 codes plus 128 in halves 0x6400 | u, which are 1024 + u, as fp16.
 __device__ __forceinline__ uint32_t i8_halves(uint32_t u) {
@@ -214,9 +221,11 @@ __device__ __forceinline__ void fill_rest(const AttnParams &p, int D) {
 // each of four value rows serve 8 tiles of 16 columns, and only the weights are
 // exchanged between the lanes, by a transpose of 8 x 8 tiles.
 //
-// One token, 8 rows per head, 64 sequences of up to 32768 tokens: 609 to 628 us,
+// One token, 8 rows per head, 64 sequences of up to 32768 tokens: 594 to 628 us,
 // 5.2 TB/s, bound by how evenly the SMs are served; 24 rows at up to 8192
-// tokens: 227 us (e4m3), 245 us (int8), bound by a step's instructions.
+// tokens: 227 to 232 us (e4m3), 244 to 251 us (int8), bound by a step's
+// instructions.  At head size 128 the forms for 8 and for 24 rows spill 20 to
+// 32 bytes a thread; what that costs has not been measured.
 //
 // A stretch that ends inside a segment (the rows of a kv head) leaves a piece
 // (out, offset, sum); the CTA merges the pieces of its warps, and the last CTA

@@ -113,9 +113,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 //
 // What bounds it is the dependent chain of a group's tile: scores, weights,
 // products and the signals between them take about 5000 clocks for two tiles
-// (1024 each of products, 1792 of shared-memory traffic).  32 trees of 63 nodes
-// over up to 16384 tokens, 32 heads on 8: 533 us, 765 TFLOP/s; 48 rows per head
-// at up to 8192 tokens: 294 us, 2.8 TB/s.
+// (1024 each of products, 1792 of shared-memory traffic), and the two groups run
+// in phase, so that their weights slow each other down.  Every token tile is
+// copied and converted once for each 128 rows of its kv head.  At these
+// register counts it spills (382 bytes of stores and 520 of loads a thread at head
+// size 128, 362 and 496 at 64).  32 trees of 63 nodes over up to 16384 tokens, 32
+// heads on 8: 528 to 559 us over several GPUs, 730 to 772 TFLOP/s; 48 rows per
+// head at up to 8192 tokens: 294 us, 2.8 TB/s; 1024 new tokens of 4 sequences
+// behind 8192: 747 us, 782 TFLOP/s of what a chain sees.
 constexpr int TQ = 128, TK = 128;    // rows, tokens of a tile
 constexpr int T_SOFT = 512;          // softmax threads: two groups, two threads per row
 constexpr int T_CONV = 256;          // conversion threads: half for keys, half for values, so that neither waits for the other's buffer

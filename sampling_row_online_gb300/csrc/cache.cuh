@@ -22,7 +22,6 @@ namespace spec {
 
 constexpr int DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2;  // SPEC_F32, SPEC_BF16, SPEC_F16
 constexpr int KIND_E4M3 = 0, KIND_I8 = 1;           // SPEC_E4M3, SPEC_I8
-constexpr int MAX_PAGE = 128;                       // page_size <= 128
 constexpr int MAX_ROPE = 256;                       // rotated pairs per head
 
 struct CacheView {  // spec_cache_t and the call's page table
@@ -805,8 +804,10 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 // usual head: two rows in flight, the weights in registers, a CTA for the
 // queries or the keys of its tokens (blockIdx.y).  What a row costs is
 // instructions (about 85 a vector), so nothing is divided or looked up per
-// row.  16380 tokens, 40 heads of 128, bf16: 66.5 us, 5.0 TB/s, bound by issue
-// (the kernel above took 112).
+// row.  16380 tokens, 40 heads of 128, bf16: half of the head rotated in
+// neighbouring pairs 66.5 us, 5.0 TB/s, bound by issue (the kernel above took
+// 112); the whole head in two halves 72.7 us, 4.6 TB/s, with two units of a row to a
+// thread and 52 bytes of spills each way (fp32: 12).
 template <int DT, bool PAIRS>
 __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ NormRopeParams p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
