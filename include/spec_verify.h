@@ -89,6 +89,7 @@ enum { SPEC_E4M3 = 0, SPEC_I8 = 1 };
 #define SPEC_EAGLE_MAX_CANDIDATES 4096 /* F * k of one expansion step */
 #define SPEC_EAGLE_MAX_NODES 8192      /* M of spec_eagle2_rerank */
 #define SPEC_MAX_NEW_TOKENS 65536      /* N of spec_cache_attention */
+#define SPEC_MAX_AXES 8                /* axes of spec_qk_norm_rope_axes */
 
 /* Counters a caller may ask spec_verify_ex to accumulate (device memory,
  * zeroed by the caller, added to atomically by every call that receives it).
@@ -468,6 +469,10 @@ int spec_eagle2_rerank(const float *node_values, const int32_t *node_parents,
  *                         move together, the context grows
  *   spec_cache_read       reads cached rows back
  *
+ * and for prompts
+ *
+ *   spec_qk_norm_rope_axes  the rotation for tokens of images and videos
+ *
  * A chain needs no commit: its accepted tokens already stand behind the
  * context, which grows by n_accepted + 1.
  *
@@ -533,6 +538,23 @@ int spec_qk_norm_rope(const spec_heads_t *q, const spec_heads_t *k, const spec_h
                       const int32_t *base, const int32_t *offset, int B, int N, int Hq, int Hk, int D,
                       int dtype, int norm, float eps, const double *inv_freq, int rot, int pairs,
                       void *stream);
+
+/*
+ * spec_qk_norm_rope_axes — spec_qk_norm_rope for positions with several axes,
+ * as the tokens of images and videos have them (time, height, width): pair i
+ * turns by the position on its own axis,
+ *   f = (base[b] + positions[b, n, axis[i]]) * inv_freq[i].
+ *   positions     [B, N, axes] int32 (may be NULL iff rot == 0)
+ *   axis          HOST array [rot / 2] of int32, each in [0, axes)
+ *   1 <= axes <= SPEC_MAX_AXES; everything else as spec_qk_norm_rope
+ * A text token has the same position on every axis: where all do, the result
+ * is that of spec_qk_norm_rope with this position, bit for bit.
+ */
+int spec_qk_norm_rope_axes(const spec_heads_t *q, const spec_heads_t *k, const spec_heads_t *out_q,
+                           const spec_heads_t *out_k, const void *q_weight, const void *k_weight,
+                           const int32_t *base, const int32_t *positions, int axes, int B, int N, int Hq,
+                           int Hk, int D, int dtype, int norm, float eps, const double *inv_freq,
+                           const int32_t *axis, int rot, int pairs, void *stream);
 
 /*
  * spec_cache_write — quantises the first counts[b] of N new rows of each

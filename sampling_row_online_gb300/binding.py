@@ -80,6 +80,7 @@ def library():
     lib.spec_eagle2_expand.argtypes = [vp, vp, i32, i32, i32, i32, f32, i32, vp, vp, vp, i32, i32, i32, vp, vp]
     lib.spec_eagle2_rerank.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     lib.spec_qk_norm_rope.argtypes = [vp] * 8 + [i32] * 7 + [f32, vp, i32, i32, vp]
+    lib.spec_qk_norm_rope_axes.argtypes = [vp] * 8 + [i32] * 8 + [f32, vp, vp, i32, i32, vp]
     lib.spec_cache_write.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.spec_cache_read.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.spec_cache_attention.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp]
@@ -98,7 +99,7 @@ def library():
                  "spec_tree_max_depth", "spec_tree_mask", "spec_ngram_propose", "spec_topk",
                  "spec_eagle2_expand", "spec_eagle2_rerank", "spec_get_status", "spec_verify_noalloc",
                  "spec_noalloc_get_status", "spec_debug_noalloc_status", "spec_qk_norm_rope", "spec_cache_write",
-                 "spec_cache_read", "spec_cache_attention", "spec_cache_commit"):
+                 "spec_cache_read", "spec_cache_attention", "spec_cache_commit", "spec_qk_norm_rope_axes"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -587,20 +588,13 @@ def _call(fn, where, device, stream, *args):
         _check(st, where)
 
 
-def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True, q_weight=None, k_weight=None,
-                      eps=1e-6, pairs=False, out_q=None, out_k=None, stream=None):
-    """Norms of queries and keys for each head and the position rotation, in one pass.
-
-    q [B, N, Hq, D], k [B, N, Hk, D] (either may be None) in float32, bfloat16 or float16, any strides with a
-    contiguous head; weights [D] of the same dtype or None.  inv_freq: float64 host tensor [rot / 2] or None (no
-    rotation); the position of token (b, n) is base[b] + offset[b, n] (int32; None: 0 and n).  pairs: neighbouring
-    elements are rotated together, not the two halves.  Returns (out_q, out_k); out_q may be q, out_k may be k."""
-    lib = library()
+def _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k):
+    """What spec_qk_norm_rope and spec_qk_norm_rope_axes share: (tensors, weights, head counts, outputs, inv_freq, rot)."""
     x = q if q is not None else k
     if x is None or x.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, head_dim]")
     B, N, _, D = x.shape
-    code = _code(x, "q" if q is not None else "k")
+    _code(x, "q" if q is not None else "k")
     heads, srcs, dsts, outs, weights = [0, 0], [None, None], [None, None], [None, None], [None, None]
     for i, (t, out, w, name) in enumerate(((q, out_q, q_weight, "q"), (k, out_k, k_weight, "k"))):
         if t is None:
@@ -628,9 +622,41 @@ def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True,
         if inv_freq.device.type != "cpu" or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-d float64 tensor on the host")
         freq, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    ref = [None if s is None else ctypes.byref(s) for s in srcs + dsts]
-    _call(lib.spec_qk_norm_rope, "spec_qk_norm_rope", x.device, stream, *ref, *weights, _index(base, "base", (B,), x.device),
-          _index(offset, "offset", (B, N), x.device), B, N, heads[0], heads[1], D, code, int(norm), eps, freq, rot, int(pairs))
+    return [None if s is None else ctypes.byref(s) for s in srcs + dsts], weights, heads, outs, freq, rot
+
+
+def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True, q_weight=None, k_weight=None,
+                      eps=1e-6, pairs=False, out_q=None, out_k=None, stream=None):
+    """Norms of queries and keys for each head and the position rotation, in one pass.
+
+    q [B, N, Hq, D], k [B, N, Hk, D] (either may be None) in float32, bfloat16 or float16, any strides with a
+    contiguous head; weights [D] of the same dtype or None.  inv_freq: float64 host tensor [rot / 2] or None (no
+    rotation); the position of token (b, n) is base[b] + offset[b, n] (int32; None: 0 and n).  pairs: neighbouring
+    elements are rotated together, not the two halves.  Returns (out_q, out_k); out_q may be q, out_k may be k."""
+    ref, weights, heads, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
+    x = outs[0] if outs[0] is not None else outs[1]
+    B, N, _, D = x.shape
+    _call(library().spec_qk_norm_rope, "spec_qk_norm_rope", x.device, stream, *ref, *weights, _index(base, "base", (B,), x.device),
+          _index(offset, "offset", (B, N), x.device), B, N, heads[0], heads[1], D, _DTYPES[x.dtype], int(norm), eps, freq, rot, int(pairs))
+    return tuple(outs)
+
+
+def spec_qk_norm_rope_axes(q, k, inv_freq, axis, positions, *, base=None, norm=True, q_weight=None, k_weight=None, eps=1e-6,
+                           pairs=False, out_q=None, out_k=None, stream=None):
+    """As spec_qk_norm_rope for positions with several axes (time, height and width of an image's or a video's tokens):
+    positions [B, N, axes] int32; pair i turns by (base[b] + positions[b, n, axis[i]]) * inv_freq[i].  inv_freq: float64,
+    axis: int32, both host tensors [rot / 2].  Returns (out_q, out_k)."""
+    ref, weights, heads, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
+    x = outs[0] if outs[0] is not None else outs[1]
+    B, N, _, D = x.shape
+    if positions is None or positions.dim() != 3:
+        raise ValueError("positions must be [B, N, axes]")
+    if axis is None or axis.device.type != "cpu" or axis.dtype != torch.int32 or not axis.is_contiguous() or axis.shape != (rot // 2,):
+        raise ValueError("axis must be a contiguous int32 tensor of the length of inv_freq, on the host")
+    axes = positions.shape[2]
+    _call(library().spec_qk_norm_rope_axes, "spec_qk_norm_rope_axes", x.device, stream, *ref, *weights,
+          _index(base, "base", (B,), x.device), _index(positions, "positions", (B, N, axes), x.device), axes, B, N, heads[0], heads[1],
+          D, _DTYPES[x.dtype], int(norm), eps, freq, axis.data_ptr(), rot, int(pairs))
     return tuple(outs)
 
 

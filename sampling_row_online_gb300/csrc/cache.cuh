@@ -14,13 +14,14 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device.cuh"
+#include "elements.cuh"
 #include "ptx.cuh"
 
 namespace spec {
 
-constexpr int DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2;  // SPEC_F32, SPEC_BF16, SPEC_F16
 constexpr int KIND_E4M3 = 0, KIND_I8 = 1;           // SPEC_E4M3, SPEC_I8
 constexpr int MAX_ROPE = 256;                       // rotated pairs per head
 
@@ -30,133 +31,6 @@ struct CacheView {  // spec_cache_t and the call's page table
   const int32_t *table;       // [B, per]
   int pages, Hk, page, log_page, D, kind, per;
 };
-
-// ------------------------------------------------------------- elements
-// Eight elements of a row as loaded: one 16-byte vector, or two for fp32.
-template <int DT>
-struct Raw8 {
-  uint4 v[DT == DT_F32 ? 2 : 1];
-};
-
-__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
-  float2 r;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <int DT>
-__device__ __forceinline__ float one_element(const void *base, long long i) {
-  if (DT == DT_F32) return static_cast<const float *>(base)[i];
-  const uint16_t h = static_cast<const uint16_t *>(base)[i];
-  if (DT == DT_BF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
-  return f16x2_to_f32(h).x;
-}
-template <int DT>
-__device__ __forceinline__ void put_element(void *base, long long i, float x) {
-  if (DT == DT_F32) static_cast<float *>(base)[i] = x;
-  else if (DT == DT_BF16) static_cast<uint16_t *>(base)[i] = static_cast<uint16_t>(f32_to_bf16x2(x, 0.f));
-  else static_cast<uint16_t *>(base)[i] = static_cast<uint16_t>(f32_to_f16x2(x, 0.f));
-}
-
-// The eight elements from element offset i; VEC: 16-byte aligned there.
-template <int DT, bool VEC>
-__device__ __forceinline__ Raw8<DT> load8(const void *base, long long i) {
-  Raw8<DT> r;
-  if constexpr (VEC) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + i * (DT == DT_F32 ? 4 : 2));
-    r.v[0] = p[0];
-    if constexpr (DT == DT_F32) r.v[1] = p[1];
-  } else if constexpr (DT == DT_F32) {
-    const uint32_t *p = static_cast<const uint32_t *>(base) + i;
-    r.v[0] = make_uint4(p[0], p[1], p[2], p[3]);
-    r.v[1] = make_uint4(p[4], p[5], p[6], p[7]);
-  } else {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + i;
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = p[2 * j] | static_cast<uint32_t>(p[2 * j + 1]) << 16;
-    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return r;
-}
-template <int DT>
-__device__ __forceinline__ void unpack8(const Raw8<DT> &r, float (&x)[8]) {
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-  if constexpr (DT == DT_F32) {
-    const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = __uint_as_float(w[j]);
-      x[4 + j] = __uint_as_float(u[j]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (DT == DT_BF16) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      } else {
-        const float2 f = f16x2_to_f32(w[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-      }
-    }
-  }
-}
-// One rounding, from fp32 to the output's type.
-template <int DT>
-__device__ __forceinline__ Raw8<DT> pack8(const float (&x)[8]) {
-  Raw8<DT> r;
-  if constexpr (DT == DT_F32) {
-    r.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    r.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = DT == DT_BF16 ? f32_to_bf16x2(x[2 * j], x[2 * j + 1]) : f32_to_f16x2(x[2 * j], x[2 * j + 1]);
-    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return r;
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void store8(void *base, long long i, const Raw8<DT> &r) {
-  if constexpr (VEC) {
-    uint4 *p = reinterpret_cast<uint4 *>(static_cast<char *>(base) + i * (DT == DT_F32 ? 4 : 2));
-    p[0] = r.v[0];
-    if constexpr (DT == DT_F32) p[1] = r.v[1];
-  } else {
-    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-    if constexpr (DT == DT_F32) {
-      const uint32_t u[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-      uint32_t *p = static_cast<uint32_t *>(base) + i;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = w[j];
-        p[4 + j] = u[j];
-      }
-    } else {
-      uint16_t *p = static_cast<uint16_t *>(base) + i;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[2 * j] = static_cast<uint16_t>(w[j]);
-        p[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
-      }
-    }
-  }
-}
 
 // ---------------------------------------------------------------- codes
 // Four codes of a word as fp32.
@@ -644,6 +518,25 @@ struct NormRopeParams {
   float eps;
   unsigned long long freq[MAX_ROPE];  // 2^64 turns per position, modulo 2^64
 };
+// The same for positions with several axes: offset is [B, N, axes], and pair i
+// turns by the position on axis[i].
+struct NormRopeAxesParams : NormRopeParams {
+  int axes;
+  uint8_t axis[MAX_ROPE];
+};
+// The position of token `tok` (token n of sequence b) that pair i turns by;
+// `axis`: what axis_of gave for it.
+template <class P>
+__device__ __forceinline__ int axis_of(const P &p, int i) {
+  if constexpr (std::is_same_v<P, NormRopeAxesParams>) return p.axis[i];
+  return 0;
+}
+template <class P>
+__device__ __forceinline__ long long position_of(const P &p, int tok, int b, int axis) {
+  const long long base = p.base ? p.base[b] : 0;
+  if constexpr (std::is_same_v<P, NormRopeAxesParams>) return base + p.offset[static_cast<long long>(tok) * p.axes + axis];
+  return base + (p.offset ? p.offset[tok] : tok - b * p.N);
+}
 
 // Several tokens to a CTA, `lanes` threads to a row (one head of one token).
 // A thread takes units of the row: eight elements of the first half with the
@@ -655,8 +548,8 @@ struct NormRopeParams {
 // alignment: single elements, or two for neighbouring pairs, where vectors do
 // not fit.
 constexpr int ROPE_TOKENS = 16;  // most tokens of a CTA
-template <int DT, int VE, int MAXU>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+template <int DT, int VE, int MAXU, class P = NormRopeParams>
+__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ P p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
   __shared__ long long s_from[ROPE_TOKENS][2], s_to[ROPE_TOKENS][2];
   const int half = p.rot / 2;
@@ -670,7 +563,7 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   }
   for (int i = threadIdx.x; i < here * half; i += 256) {
     const int tk = i / half, tok = first + tk, b = tok / p.N;
-    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : tok - b * p.N);
+    const long long pos = position_of(p, tok, b, axis_of(p, i - tk * half));
     const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[i - tk * half];
     // signed fraction of a turn times two, in units of pi
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
@@ -808,8 +701,8 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 // neighbouring pairs 66.5 us, 5.0 TB/s, bound by issue (the kernel above took
 // 112); the whole head in two halves 72.7 us, 4.6 TB/s, with two units of a row to a
 // thread and 52 bytes of spills each way (fp32: 12).
-template <int DT, bool PAIRS>
-__global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ NormRopeParams p) {
+template <int DT, bool PAIRS, class P = NormRopeParams>
+__global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ P p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
   __shared__ long long s_from[ROPE_TOKENS], s_to[ROPE_TOKENS];
   const int w = p.heads[0] == 0 || blockIdx.y == 1;  // queries or keys
@@ -826,7 +719,8 @@ __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_con
   // 16380 tokens 66.5 and 68.3)
   const bool same = half == 0 || 256 % half == 0;
   unsigned long long freq = half ? p.freq[threadIdx.x % half] : 0;
-  asm volatile("" : "+l"(freq));  // read here
+  int axis = half ? axis_of(p, threadIdx.x % half) : 0;
+  asm volatile("" : "+l"(freq), "+r"(axis));  // read here
   pdl_wait();
   pdl_launch_dependents();
   const int u = threadIdx.x & (p.lanes - 1), npair = PAIRS ? 0 : half / 8;
@@ -842,8 +736,8 @@ __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_con
   }
   for (int i = threadIdx.x; i < here * half; i += 256) {
     const int tk = i / half, tok = first + tk, b = tok / p.N;
-    const long long pos = static_cast<long long>(p.base ? p.base[b] : 0) + (p.offset ? p.offset[tok] : tok - b * p.N);
-    if (!same) freq = p.freq[i - tk * half];
+    if (!same) freq = p.freq[i - tk * half], axis = axis_of(p, i - tk * half);
+    const long long pos = position_of(p, tok, b, axis);
     const unsigned long long turn = static_cast<unsigned long long>(pos) * freq;
     // signed fraction of a turn times two, in units of pi
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;

@@ -12,19 +12,9 @@
 #include "spec_verify.h"
 
 namespace spec {
-namespace {
-
-bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-int size_of(int dtype) { return dtype == SPEC_F32 ? 4 : 2; }
-bool known_dtype(int dtype) { return dtype == SPEC_F32 || dtype == SPEC_BF16 || dtype == SPEC_F16; }
-
-// 16-byte vectors may be used at every row of h.
-bool vectors(const spec_heads_t &h, int esz) {
-  return aligned16(h.data) && h.stride_b * esz % 16 == 0 && h.stride_n * esz % 16 == 0 && h.stride_h * esz % 16 == 0;
-}
 
 // Launches as a programmatic dependent of what precedes it on the stream.
-int launch(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what) {
+int launch_dependent(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what) {
   cudaLaunchAttribute pdl;
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
@@ -38,6 +28,17 @@ int launch(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream
   void *args[] = {params};
   const cudaError_t e = launch_kernel(&cfg, fn, args);
   return e == cudaSuccess ? static_cast<int>(SPEC_OK) : cuda_fail(e, what);
+}
+
+namespace {
+
+bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+int size_of(int dtype) { return dtype == SPEC_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype == SPEC_F32 || dtype == SPEC_BF16 || dtype == SPEC_F16; }
+
+// 16-byte vectors may be used at every row of h.
+bool vectors(const spec_heads_t &h, int esz) {
+  return aligned16(h.data) && h.stride_b * esz % 16 == 0 && h.stride_n * esz % 16 == 0 && h.stride_h * esz % 16 == 0;
 }
 
 int check_cache(const spec_cache_t *c, const int32_t *table, int per, int B, CacheView *view) {
@@ -85,14 +86,82 @@ const void *pick_write(int elements, bool vec) {
 
 // vec: units of eight elements, at most two to a thread; `one`: one to a
 // thread.  Otherwise single elements, or two for neighbouring pairs.
-template <int DT>
+template <int DT, class P>
 const void *pick_norm_rope(bool vec, bool one, bool pairs) {
   if (vec && one)
-    return pairs ? reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, true>)
-                 : reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, false>);
-  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2>);
-  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8>)
-               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16>);
+    return pairs ? reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, true, P>)
+                 : reinterpret_cast<const void *>(&norm_rope_rows_kernel<DT, false, P>);
+  if (vec) return reinterpret_cast<const void *>(&norm_rope_kernel<DT, 8, 2, P>);
+  return pairs ? reinterpret_cast<const void *>(&norm_rope_kernel<DT, 2, 8, P>)
+               : reinterpret_cast<const void *>(&norm_rope_kernel<DT, 1, 16, P>);
+}
+// A call's tensors and sizes into p, and its launch: spec_qk_norm_rope, and with
+// P = NormRopeAxesParams (p.axes set) spec_qk_norm_rope_axes.
+template <class P>
+int norm_rope(P &p, const spec_heads_t *q, const spec_heads_t *k, const spec_heads_t *out_q, const spec_heads_t *out_k,
+              const void *q_weight, const void *k_weight, const int32_t *base, const int32_t *offset, int B, int N, int Hq, int Hk,
+              int D, int dtype, int norm, float eps, const double *inv_freq, const int32_t *axis, int rot, int pairs, void *stream_ptr) {
+  constexpr bool AXES = std::is_same_v<P, NormRopeAxesParams>;
+  if (!known_dtype(dtype)) return fail(SPEC_ERR_DTYPE, "dtype must be SPEC_F32, SPEC_BF16 or SPEC_F16");
+  if (B < 0 || N < 0 || static_cast<long long>(B) * N > INT_MAX / 2) return fail(SPEC_ERR_ARG, "B and N must be >= 0 and B * N < 2^30");
+  if (Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535) return fail(SPEC_ERR_ARG, "head counts out of range [0, 65535]");
+  if (D < 2 || D > 512 || D % 2) return fail(SPEC_ERR_ARG, "head_dim must be even and in [2, 512]");
+  if (rot < 0 || rot > D || rot % 2) return fail(SPEC_ERR_ARG, "rot must be even and in [0, head_dim]");
+  if (norm != 0 && norm != 1) return fail(SPEC_ERR_ARG, "norm must be 0 or 1");
+  if (pairs != 0 && pairs != 1) return fail(SPEC_ERR_ARG, "pairs must be 0 or 1");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPEC_ERR_ARG, "eps must be finite and >= 0");
+  if (rot > 0 && !inv_freq) return fail(SPEC_ERR_ARG, "inv_freq is NULL");
+  if (AXES && rot > 0 && !axis) return fail(SPEC_ERR_ARG, "axis is NULL");
+  if (!norm && (q_weight || k_weight)) return fail(SPEC_ERR_ARG, "weights are given without the norm");
+  if (B == 0 || N == 0 || Hq + Hk == 0) return SPEC_OK;
+  if ((Hq > 0 && (!q || !out_q || !q->data || !out_q->data)) || (Hk > 0 && (!k || !out_k || !k->data || !out_k->data)))
+    return fail(SPEC_ERR_ARG, "a tensor is NULL");
+  if (AXES && rot > 0 && !offset) return fail(SPEC_ERR_ARG, "positions is NULL");
+  const int esz = size_of(dtype);
+  const spec_heads_t *src[2] = {q, k}, *dst[2] = {out_q, out_k};
+  const void *weight[2] = {q_weight, k_weight};
+  const int heads[2] = {Hq, Hk};
+  bool vec = D % 8 == 0 && (pairs ? rot % 8 == 0 : rot % 16 == 0);
+  for (int i = 0; i < 2; ++i) {
+    p.heads[i] = heads[i];
+    if (heads[i] == 0) continue;
+    p.src[i] = src[i]->data;
+    p.dst[i] = dst[i]->data;
+    p.weight[i] = weight[i];
+    p.ssb[i] = src[i]->stride_b, p.ssn[i] = src[i]->stride_n, p.ssh[i] = src[i]->stride_h;
+    p.dsb[i] = dst[i]->stride_b, p.dsn[i] = dst[i]->stride_n, p.dsh[i] = dst[i]->stride_h;
+    vec = vec && vectors(*src[i], esz) && vectors(*dst[i], esz) && aligned16(weight[i]);
+  }
+  p.base = base;
+  p.offset = offset;
+  p.B = B, p.N = N, p.D = D, p.rot = rot;
+  p.norm = norm, p.pairs = pairs, p.eps = eps;
+  for (int i = 0; i < rot / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return fail(SPEC_ERR_ARG, "inv_freq must be finite");
+    if constexpr (AXES) {
+      if (axis[i] < 0 || axis[i] >= p.axes) return fail(SPEC_ERR_ARG, "axis out of range [0, axes)");
+      p.axis[i] = static_cast<uint8_t>(axis[i]);
+    }
+    // turns per position; whole turns drop out, since positions are whole
+    const double turns = inv_freq[i] * 0.15915494309189533577, frac = turns - std::floor(turns);
+    p.freq[i] = frac >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(frac, 64));
+  }
+  const int ve = vec ? 8 : pairs ? 2 : 1;
+  const int npair = pairs ? 0 : rot / 2 / ve, units = npair + (D - 2 * npair * ve) / ve;
+  p.lanes = 1;
+  while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
+  // norm_rope_rows_kernel has a CTA each for a token's queries and keys
+  const unsigned tensors = vec && units <= p.lanes && Hq > 0 && Hk > 0 ? 2 : 1;
+  // one wave of four CTAs per SM where that is at most ROPE_TOKENS tokens to a
+  // CTA: its set-up is a small part then
+  const long long tokens = static_cast<long long>(B) * N, wave = 4LL * num_sms();
+  p.per_cta = static_cast<int>(std::min<long long>(ROPE_TOKENS, (tokens * tensors + wave - 1) / wave));
+  const void *fn = dtype == SPEC_F32    ? pick_norm_rope<DT_F32, P>(vec, units <= p.lanes, pairs)
+                   : dtype == SPEC_BF16 ? pick_norm_rope<DT_BF16, P>(vec, units <= p.lanes, pairs)
+                                        : pick_norm_rope<DT_F16, P>(vec, units <= p.lanes, pairs);
+  return launch_dependent(fn, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta), tensors), 256,
+                p.per_cta * (rot / 2) * static_cast<int>(sizeof(float2)), static_cast<cudaStream_t>(stream_ptr), &p,
+                "norm_rope_kernel launch");
 }
 
 // The attention's kernel, its block and shared memory, and the floats of its
@@ -145,62 +214,23 @@ int spec_qk_norm_rope(const spec_heads_t *q, const spec_heads_t *k, const spec_h
                       int Hq, int Hk, int D, int dtype, int norm, float eps, const double *inv_freq, int rot, int pairs,
                       void *stream_ptr) {
   NvtxRange nvtx_range("spec_qk_norm_rope");
-  if (!known_dtype(dtype)) return fail(SPEC_ERR_DTYPE, "dtype must be SPEC_F32, SPEC_BF16 or SPEC_F16");
-  if (B < 0 || N < 0 || static_cast<long long>(B) * N > INT_MAX / 2) return fail(SPEC_ERR_ARG, "B and N must be >= 0 and B * N < 2^30");
-  if (Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535) return fail(SPEC_ERR_ARG, "head counts out of range [0, 65535]");
-  if (D < 2 || D > 512 || D % 2) return fail(SPEC_ERR_ARG, "head_dim must be even and in [2, 512]");
-  if (rot < 0 || rot > D || rot % 2) return fail(SPEC_ERR_ARG, "rot must be even and in [0, head_dim]");
-  if (norm != 0 && norm != 1) return fail(SPEC_ERR_ARG, "norm must be 0 or 1");
-  if (pairs != 0 && pairs != 1) return fail(SPEC_ERR_ARG, "pairs must be 0 or 1");
-  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPEC_ERR_ARG, "eps must be finite and >= 0");
-  if (rot > 0 && !inv_freq) return fail(SPEC_ERR_ARG, "inv_freq is NULL");
-  if (!norm && (q_weight || k_weight)) return fail(SPEC_ERR_ARG, "weights are given without the norm");
-  if (B == 0 || N == 0 || Hq + Hk == 0) return SPEC_OK;
-  if ((Hq > 0 && (!q || !out_q || !q->data || !out_q->data)) || (Hk > 0 && (!k || !out_k || !k->data || !out_k->data)))
-    return fail(SPEC_ERR_ARG, "a tensor is NULL");
-  const int esz = size_of(dtype);
   NormRopeParams p;
   std::memset(&p, 0, sizeof p);
-  const spec_heads_t *src[2] = {q, k}, *dst[2] = {out_q, out_k};
-  const void *weight[2] = {q_weight, k_weight};
-  const int heads[2] = {Hq, Hk};
-  bool vec = D % 8 == 0 && (pairs ? rot % 8 == 0 : rot % 16 == 0);
-  for (int i = 0; i < 2; ++i) {
-    p.heads[i] = heads[i];
-    if (heads[i] == 0) continue;
-    p.src[i] = src[i]->data;
-    p.dst[i] = dst[i]->data;
-    p.weight[i] = weight[i];
-    p.ssb[i] = src[i]->stride_b, p.ssn[i] = src[i]->stride_n, p.ssh[i] = src[i]->stride_h;
-    p.dsb[i] = dst[i]->stride_b, p.dsn[i] = dst[i]->stride_n, p.dsh[i] = dst[i]->stride_h;
-    vec = vec && vectors(*src[i], esz) && vectors(*dst[i], esz) && aligned16(weight[i]);
-  }
-  p.base = base;
-  p.offset = offset;
-  p.B = B, p.N = N, p.D = D, p.rot = rot;
-  p.norm = norm, p.pairs = pairs, p.eps = eps;
-  for (int i = 0; i < rot / 2; ++i) {
-    if (!std::isfinite(inv_freq[i])) return fail(SPEC_ERR_ARG, "inv_freq must be finite");
-    // turns per position; whole turns drop out, since positions are whole
-    const double turns = inv_freq[i] * 0.15915494309189533577, frac = turns - std::floor(turns);
-    p.freq[i] = frac >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(frac, 64));
-  }
-  const int ve = vec ? 8 : pairs ? 2 : 1;
-  const int npair = pairs ? 0 : rot / 2 / ve, units = npair + (D - 2 * npair * ve) / ve;
-  p.lanes = 1;
-  while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
-  // norm_rope_rows_kernel has a CTA each for a token's queries and keys
-  const unsigned tensors = vec && units <= p.lanes && Hq > 0 && Hk > 0 ? 2 : 1;
-  // one wave of four CTAs per SM where that is at most ROPE_TOKENS tokens to a
-  // CTA: its set-up is a small part then
-  const long long tokens = static_cast<long long>(B) * N, wave = 4LL * num_sms();
-  p.per_cta = static_cast<int>(std::min<long long>(ROPE_TOKENS, (tokens * tensors + wave - 1) / wave));
-  const void *fn = dtype == SPEC_F32    ? pick_norm_rope<DT_F32>(vec, units <= p.lanes, pairs)
-                   : dtype == SPEC_BF16 ? pick_norm_rope<DT_BF16>(vec, units <= p.lanes, pairs)
-                                        : pick_norm_rope<DT_F16>(vec, units <= p.lanes, pairs);
-  return launch(fn, dim3(static_cast<unsigned>((tokens + p.per_cta - 1) / p.per_cta), tensors), 256,
-                p.per_cta * (rot / 2) * static_cast<int>(sizeof(float2)), static_cast<cudaStream_t>(stream_ptr), &p,
-                "norm_rope_kernel launch");
+  return norm_rope(p, q, k, out_q, out_k, q_weight, k_weight, base, offset, B, N, Hq, Hk, D, dtype, norm, eps, inv_freq, nullptr, rot, pairs,
+                   stream_ptr);
+}
+
+int spec_qk_norm_rope_axes(const spec_heads_t *q, const spec_heads_t *k, const spec_heads_t *out_q, const spec_heads_t *out_k,
+                           const void *q_weight, const void *k_weight, const int32_t *base, const int32_t *positions, int axes,
+                           int B, int N, int Hq, int Hk, int D, int dtype, int norm, float eps, const double *inv_freq,
+                           const int32_t *axis, int rot, int pairs, void *stream_ptr) {
+  NvtxRange nvtx_range("spec_qk_norm_rope_axes");
+  if (axes < 1 || axes > SPEC_MAX_AXES) return fail(SPEC_ERR_ARG, "axes out of range [1, SPEC_MAX_AXES]");
+  NormRopeAxesParams p;
+  std::memset(&p, 0, sizeof p);
+  p.axes = axes;
+  return norm_rope(p, q, k, out_q, out_k, q_weight, k_weight, base, positions, B, N, Hq, Hk, D, dtype, norm, eps, inv_freq, axis, rot, pairs,
+                   stream_ptr);
 }
 
 int spec_cache_write(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len,
@@ -232,7 +262,7 @@ int spec_cache_write(const spec_cache_t *cache, const int32_t *page_table, int p
   const void *fn = dtype == SPEC_F32    ? pick_write<DT_F32>(elements, vec)
                    : dtype == SPEC_BF16 ? pick_write<DT_BF16>(elements, vec)
                                         : pick_write<DT_F16>(elements, vec);
-  return launch(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(2 * p.c.Hk), static_cast<unsigned>(B)), elements <= 2048 ? 32 : 256, 0,
+  return launch_dependent(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(2 * p.c.Hk), static_cast<unsigned>(B)), elements <= 2048 ? 32 : 256, 0,
                 stream, &p, "cache_write_kernel launch");
 }
 
@@ -258,7 +288,7 @@ int spec_cache_read(const spec_cache_t *cache, const int32_t *page_table, int pa
   const void *fn = dtype == SPEC_F32    ? reinterpret_cast<const void *>(&cache_read_kernel<DT_F32>)
                    : dtype == SPEC_BF16 ? reinterpret_cast<const void *>(&cache_read_kernel<DT_BF16>)
                                         : reinterpret_cast<const void *>(&cache_read_kernel<DT_F16>);
-  return launch(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(p.c.Hk), static_cast<unsigned>(B)), 256, 0, stream, &p,
+  return launch_dependent(fn, dim3(blocks_of(N, p.c.page), static_cast<unsigned>(p.c.Hk), static_cast<unsigned>(B)), 256, 0, stream, &p,
                 "cache_read_kernel launch");
 }
 
@@ -302,7 +332,7 @@ int spec_cache_attention(const spec_cache_t *cache, const int32_t *page_table, i
   p.pieces = reinterpret_cast<float *>(w->partials);
   p.done = w->attn_done;
   p.status = w->status;
-  return launch(k.fn, dim3(static_cast<unsigned>(grid)), k.threads, k.smem, stream, &p, "attention kernel launch");
+  return launch_dependent(k.fn, dim3(static_cast<unsigned>(grid)), k.threads, k.smem, stream, &p, "attention kernel launch");
 }
 
 int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len,
@@ -333,7 +363,7 @@ int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int 
   if ((st = get_ws(stream, 1, &w))) return st;
   p.status = w->status;
   const int share = (2 * p.c.Hk + 7) / 8;  // a warp for each kv head and tensor
-  return launch(reinterpret_cast<const void *>(&cache_commit_kernel), dim3(static_cast<unsigned>(share), static_cast<unsigned>(B)), 256, 0,
+  return launch_dependent(reinterpret_cast<const void *>(&cache_commit_kernel), dim3(static_cast<unsigned>(share), static_cast<unsigned>(B)), 256, 0,
                 stream, &p, "cache_commit_kernel launch");
 }
 
