@@ -88,7 +88,7 @@ enum { SPEC_E4M3 = 0, SPEC_I8 = 1 };
 #define SPEC_MAX_TOPK 32         /* k of spec_topk / spec_eagle2_expand */
 #define SPEC_EAGLE_MAX_CANDIDATES 4096 /* F * k of one expansion step */
 #define SPEC_EAGLE_MAX_NODES 8192      /* M of spec_eagle2_rerank */
-#define SPEC_MAX_NEW_TOKENS 65536      /* N of spec_cache_attention */
+#define SPEC_MAX_NEW_TOKENS 65536      /* N of spec_cache_attention and spec_cache_weights */
 #define SPEC_MAX_AXES 8                /* axes of spec_qk_norm_rope_axes */
 
 /* Counters a caller may ask spec_verify_ex to accumulate (device memory,
@@ -469,9 +469,12 @@ int spec_eagle2_rerank(const float *node_values, const int32_t *node_parents,
  *                         move together, the context grows
  *   spec_cache_read       reads cached rows back
  *
- * and for prompts
+ * and for prompts and contexts that outgrow their memory
  *
  *   spec_qk_norm_rope_axes  the rotation for tokens of images and videos
+ *   spec_prompt_attention   attention among a prompt's tokens, not quantised
+ *   spec_cache_weights      how much attention each slot has received
+ *   spec_cache_evict        gives up the slots that received least
  *
  * A chain needs no commit: its accepted tokens already stand behind the
  * context, which grows by n_accepted + 1.
@@ -557,6 +560,30 @@ int spec_qk_norm_rope_axes(const spec_heads_t *q, const spec_heads_t *k, const s
                            const int32_t *axis, int rot, int pairs, void *stream);
 
 /*
+ * spec_prompt_attention — causal softmax attention among the tokens of whole
+ * prompts, before their keys and values are quantised.  B sequences stand
+ * packed one behind the other: sequence b has the rows starts[b] ...
+ * starts[b + 1] - 1 of T (none where the two are equal), and
+ *   out_i = sum_j p_j v_j, p = softmax(scale * q_i . k_j)
+ * over the rows j <= i of i's own sequence.  Query head h uses kv head
+ * h / (Hq / Hk).
+ *   q             [T, Hq, D], k and v [T, Hk, D] as spec_heads_t (stride_b is
+ *                 not used), SPEC_BF16 or SPEC_F16, D 64 or 128
+ *   starts        [B + 1] int32, ascending, in [0, T]
+ *   out           [T, Hq, D] contiguous, 16-byte aligned, dtype
+ *   lse           [T, Hq] float or NULL: the natural logarithm of the sum of
+ *                 exp(scale * q_i . k_j)
+ * Rows of no sequence (before starts[0], from starts[B] on) are not read; out
+ * is 0 and lse -inf there.  A row does not depend on what later rows or other
+ * sequences hold, be it infinities or NaN.  starts that are not ascending, or
+ * leave [0, T], make all of out and lse NaN, and spec_get_status then returns
+ * SPEC_ERR_ARG.
+ */
+int spec_prompt_attention(const spec_heads_t *q, const spec_heads_t *k, const spec_heads_t *v,
+                          const int32_t *starts, int B, int T, int Hq, int Hk, int D, int dtype, float scale,
+                          void *out, float *lse, void *stream);
+
+/*
  * spec_cache_write — quantises the first counts[b] of N new rows of each
  * sequence into slots ctx_len[b] ... of the cache.  A block that holds no slot
  * before ctx_len[b] takes the scale of its new rows; any other block's scale
@@ -631,11 +658,59 @@ int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int 
                       int N, int path_len, int32_t *out_index, int32_t *out_ctx_len, void *stream);
 
 /*
+ * spec_cache_weights — how much attention each slot receives: for every kv
+ * head h and slot s, the sum over the new tokens i < counts[b] that see s and
+ * over the query heads of h of
+ *   exp(scale * q_i . k_s - lse_i)
+ * is added to weights[b, h, s] where s < ctx_len[b]; the new tokens' own slots
+ * start anew (their sums are set).  Other slots' weights stay as they are.
+ *   q, mask, ctx_len, counts, N, scale, dtype   as spec_cache_attention, after
+ *                 it (or after spec_cache_commit: an accepted path is a chain
+ *                 of counts[b] tokens)
+ *   lse           [B, N, Hq] float, as spec_cache_attention gives it; a row of
+ *                 -inf adds nothing
+ *   weights       [B, kv_heads, pages_per_seq * page_size] float, 16-byte
+ *                 aligned, updated in place
+ * Sums are fp32, in a fixed order.  The weights of a bad page's slots, and of
+ * a sequence whose slots do not fit its pages, stay as they are.
+ */
+int spec_cache_weights(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                       const int32_t *ctx_len, const int32_t *counts, const spec_heads_t *q,
+                       const uint32_t *mask, const float *lse, int B, int N, int Hq, int dtype, float scale,
+                       float *weights, void *stream);
+
+/*
+ * spec_cache_evict — brings every context of more than `keep` slots down to
+ * `keep`, each kv head by itself: it keeps its first `first` slots, its last
+ * `last` slots, and of the others those with the largest weights (ties to the
+ * lower slot; NaN counts as less than any number).  The kept slots move
+ * together in their order, into the sequence's first pages, and their weights
+ * with them.  Every block that holds kept rows then has the scale that
+ * spec_cache_write gives these values, and codes rounded to it (exactly the
+ * same values unless a scale of a row has grown).
+ *   weights       [B, kv_heads, pages_per_seq * page_size] float, 16-byte
+ *                 aligned, in place (slots from `keep` on stay as they are)
+ *   keep >= 1, first, last >= 0, first + last <= keep
+ *   out_index     [B, kv_heads, keep] int32: the slots that were kept,
+ *                 ascending (all of them where there are no more than keep),
+ *                 then -1
+ *   out_ctx_len   [B] int32: min(ctx_len[b], keep) (not ctx_len's own memory)
+ * Keys keep the rotation of their own positions: a token that follows stands
+ * at its true position (the base of spec_qk_norm_rope), not at the number of
+ * slots that are left.  Two sequences must not share pages.  A sequence whose
+ * slots do not fit its pages, or that must be moved and has a bad page, is left
+ * as it is (index -1, its length as given).
+ */
+int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq,
+                     const int32_t *ctx_len, float *weights, int B, int keep, int first, int last,
+                     int32_t *out_index, int32_t *out_ctx_len, void *stream);
+
+/*
  * spec_get_status — waits for `stream`, then returns (and clears) the first
  * device-side error recorded by calls on it: SPEC_OK, SPEC_ERR_TOKEN_RANGE,
  * SPEC_ERR_PARENT, SPEC_ERR_TIMEOUT, SPEC_ERR_ARG (a lengths[] entry of
- * spec_ngram_propose out of range, or slots that do not fit a sequence's
- * pages), SPEC_ERR_PAGE, SPEC_ERR_NONFINITE, or SPEC_ERR_CUDA for an
+ * spec_ngram_propose out of range, slots that do not fit a sequence's pages,
+ * or starts of spec_prompt_attention that do not ascend within [0, T]), SPEC_ERR_PAGE, SPEC_ERR_NONFINITE, or SPEC_ERR_CUDA for an
  * asynchronous CUDA error.  While a SPEC_ERR_TIMEOUT is recorded and not yet read, every
  * verification on the stream (chains, point-mass drafts, trees) writes -1
  * for its outputs (n_accepted or length -1, tokens -1) instead of values

@@ -81,6 +81,9 @@ def library():
     lib.spec_eagle2_rerank.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     lib.spec_qk_norm_rope.argtypes = [vp] * 8 + [i32] * 7 + [f32, vp, i32, i32, vp]
     lib.spec_qk_norm_rope_axes.argtypes = [vp] * 8 + [i32] * 8 + [f32, vp, vp, i32, i32, vp]
+    lib.spec_prompt_attention.argtypes = [vp] * 4 + [i32] * 6 + [f32, vp, vp, vp]
+    lib.spec_cache_weights.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp]
+    lib.spec_cache_evict.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
     lib.spec_cache_write.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.spec_cache_read.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
     lib.spec_cache_attention.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp]
@@ -99,7 +102,8 @@ def library():
                  "spec_tree_max_depth", "spec_tree_mask", "spec_ngram_propose", "spec_topk",
                  "spec_eagle2_expand", "spec_eagle2_rerank", "spec_get_status", "spec_verify_noalloc",
                  "spec_noalloc_get_status", "spec_debug_noalloc_status", "spec_qk_norm_rope", "spec_cache_write",
-                 "spec_cache_read", "spec_cache_attention", "spec_cache_commit", "spec_qk_norm_rope_axes"):
+                 "spec_cache_read", "spec_cache_attention", "spec_cache_commit", "spec_qk_norm_rope_axes", "spec_prompt_attention",
+                 "spec_cache_weights", "spec_cache_evict"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -660,6 +664,35 @@ def spec_qk_norm_rope_axes(q, k, inv_freq, axis, positions, *, base=None, norm=T
     return tuple(outs)
 
 
+def spec_prompt_attention(q, k, v, starts, *, scale=None, out=None, want_lse=False, stream=None):
+    """Causal attention among the tokens of whole prompts that stand packed one behind the other: q [T, Hq, head_dim],
+    k and v [T, Hk, head_dim] (bfloat16 or float16, any strides with a contiguous head), sequence b in the rows starts[b]
+    ... starts[b + 1] - 1 (int32 [B + 1], ascending).  scale: head_dim ** -0.5 by default.  Returns (out [T, Hq, head_dim],
+    lse [T, Hq] float32 or None); rows of no sequence are 0 and -inf."""
+    lib = library()
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [T, Hq, head_dim], k and v [T, Hk, head_dim]")
+    T, Hq, D = q.shape
+    Hk, device = k.shape[1], q.device
+    code = _code(q, "q")
+    qs = _heads(q[None], "q", q.dtype, 1, T, Hq, D)
+    ks, vs = (_heads(t[None], name, q.dtype, 1, T, Hk, D) for t, name in ((k, "k"), (v, "v")))
+    if k.device != device or v.device != device:
+        raise ValueError("q, k and v must be on one device")
+    if starts is None or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be [B + 1]")
+    B = starts.shape[0] - 1
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != device:
+        raise ValueError("out must be contiguous, on the device of q, and of the shape and dtype of q")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=device) if want_lse else None
+    _call(lib.spec_prompt_attention, "spec_prompt_attention", device, stream, ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs),
+          _index(starts, "starts", (B + 1,), device), B, T, Hq, Hk, D, code, D ** -0.5 if scale is None else scale, out.data_ptr(),
+          None if lse is None else lse.data_ptr())
+    return out, lse
+
+
 def spec_cache_write(cache, page_table, ctx_len, k, v, *, counts=None, stream=None):
     """Quantises the first counts[b] rows (None: all N) of k, v [B, N, kv_heads, head_dim] into the cache's slots
     from ctx_len[b] on.  page_table [B, pages_per_seq], ctx_len and counts [B], all int32."""
@@ -754,6 +787,59 @@ def spec_cache_commit(cache, page_table, ctx_len, parent, node_tokens, path, len
           _index(ctx_len, "ctx_len", (B,), device), _index(parent, "parent", (B, N) if each else (N,), device), int(each),
           _index(node_tokens, "node_tokens", (B, N), device), _index(path, "path", (B, P), device),
           _index(length, "length", (B,), device), B, N, P, index.data_ptr(), new_len.data_ptr())
+    return index, new_len
+
+
+def _slot_weights(weights, cache, per, B):
+    """weights [B, kv_heads, pages_per_seq * page_size] as a pointer."""
+    shape = (B, cache.kv_heads, per * cache.struct.page_size)
+    if weights.dtype != torch.float32:
+        raise TypeError(f"weights must be torch.float32, got {weights.dtype}")
+    if weights.shape != shape or weights.device != cache.device or not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous CUDA tensor {list(shape)} on {cache.device}")
+    return weights.data_ptr()
+
+
+def spec_cache_weights(q, cache, page_table, ctx_len, lse, weights, *, counts=None, mask=None, scale=None, stream=None):
+    """Adds to weights [B, kv_heads, slots] (float32, slots = pages_per_seq * page_size) the attention that each slot
+    receives from the new tokens: the sum of exp(scale * q . k - lse) over those that see it and over the query heads of
+    its kv head.  The new tokens' own slots start anew.  q, ctx_len, counts, mask and scale as spec_cache_attention, lse
+    [B, N, Hq] as it gives it."""
+    lib = library()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, head_dim]")
+    B, N, Hq, D = q.shape
+    table, per = _table(cache, page_table, B)
+    device = cache.device
+    if D != cache.head_dim or q.device != device:
+        raise ValueError("q must have the cache's head_dim and be on its device")
+    code = _code(q, "q")
+    qs = _heads(q, "q", q.dtype, B, N, Hq, D)
+    if ctx_len is None:
+        raise ValueError("ctx_len is missing")
+    if lse.dtype != torch.float32 or lse.shape != (B, N, Hq) or lse.device != device or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor {[B, N, Hq]} on the cache's device")
+    _call(lib.spec_cache_weights, "spec_cache_weights", device, stream, cache.ref, table, per,
+          _index(ctx_len, "ctx_len", (B,), device), _index(counts, "counts", (B,), device), ctypes.byref(qs),
+          _index(mask, "mask", (B, N, (N + 31) // 32), device), lse.data_ptr(), B, N, Hq, code, D ** -0.5 if scale is None else scale,
+          _slot_weights(weights, cache, per, B))
+
+
+def spec_cache_evict(cache, page_table, ctx_len, weights, keep, *, first=0, last=0, stream=None):
+    """Brings every context of more than `keep` slots down to `keep`, each kv head by itself: its first `first`, its last
+    `last`, and of the others those with the largest weights [B, kv_heads, slots] (ties to the lower slot).  The kept rows
+    move together in the cache, and their weights too.  Returns (the kept slots [B, kv_heads, keep], then -1; the new
+    context lengths [B])."""
+    lib = library()
+    B = page_table.shape[0]
+    table, per = _table(cache, page_table, B)
+    if ctx_len is None:
+        raise ValueError("ctx_len is missing")
+    index = torch.empty((B, cache.kv_heads, max(int(keep), 0)), dtype=torch.int32, device=cache.device)
+    new_len = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    _call(lib.spec_cache_evict, "spec_cache_evict", cache.device, stream, cache.ref, table, per,
+          _index(ctx_len, "ctx_len", (B,), cache.device), _slot_weights(weights, cache, per, B), B, int(keep), int(first), int(last),
+          index.data_ptr(), new_len.data_ptr())
     return index, new_len
 
 

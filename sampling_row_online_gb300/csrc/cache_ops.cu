@@ -8,6 +8,7 @@
 #include "attention.cuh"
 #include "attention_tile.cuh"
 #include "cache.cuh"
+#include "evict.cuh"
 #include "host.h"
 #include "spec_verify.h"
 
@@ -202,6 +203,16 @@ AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   return bf ? choose_attn<64, KIND_I8, DT_BF16>(rows) : choose_attn<64, KIND_I8, DT_F16>(rows);
 }
 
+template <int D>
+const void *pick_weights(int kind, int dtype) {
+  const bool bf = dtype == SPEC_BF16;
+  if (kind == SPEC_E4M3) return bf ? reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_E4M3, DT_BF16>)
+                                   : reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_E4M3, DT_F16>);
+  return bf ? reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_I8, DT_BF16>)
+            : reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_I8, DT_F16>);
+}
+const void *pick_weights(int D, int kind, int dtype) { return D == 128 ? pick_weights<128>(kind, dtype) : pick_weights<64>(kind, dtype); }
+
 }  // namespace
 }  // namespace spec
 
@@ -365,6 +376,76 @@ int spec_cache_commit(const spec_cache_t *cache, const int32_t *page_table, int 
   const int share = (2 * p.c.Hk + 7) / 8;  // a warp for each kv head and tensor
   return launch_dependent(reinterpret_cast<const void *>(&cache_commit_kernel), dim3(static_cast<unsigned>(share), static_cast<unsigned>(B)), 256, 0,
                 stream, &p, "cache_commit_kernel launch");
+}
+
+int spec_cache_weights(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len,
+                       const int32_t *counts, const spec_heads_t *q, const uint32_t *mask, const float *lse, int B, int N, int Hq,
+                       int dtype, float scale, float *weights, void *stream_ptr) {
+  NvtxRange nvtx_range("spec_cache_weights");
+  WeightsParams p = {};
+  int st = check_cache(cache, page_table, pages_per_seq, B, &p.c);
+  if (st) return st;
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return fail(SPEC_ERR_DTYPE, "dtype must be SPEC_BF16 or SPEC_F16");
+  if (N < 0 || N > SPEC_MAX_NEW_TOKENS) return fail(SPEC_ERR_ARG, "N out of range [0, 65536]");
+  if (Hq < 1 || Hq > 65535 || Hq % p.c.Hk) return fail(SPEC_ERR_ARG, "Hq must be a multiple of kv_heads, at most 65535");
+  if (!std::isfinite(scale)) return fail(SPEC_ERR_ARG, "scale must be finite");
+  if (B == 0 || N == 0) return SPEC_OK;
+  if (!ctx_len || !q || !q->data || !lse || !weights) return fail(SPEC_ERR_ARG, "NULL pointer");
+  if (!aligned16(weights)) return fail(SPEC_ERR_ALIGN, "weights must be 16-byte aligned");
+  p.q = q->data;
+  p.q_sb = q->stride_b, p.q_sn = q->stride_n, p.q_sh = q->stride_h;
+  p.lse = const_cast<float *>(lse);
+  p.weights = weights;
+  p.ctx = ctx_len;
+  p.counts = counts;
+  p.mask = mask;
+  p.B = B, p.N = N, p.W = (N + 31) / 32, p.G = Hq / p.c.Hk;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.q_vec = vectors(*q, 2);
+  const long long rows = static_cast<long long>(N) * p.G;
+  if (rows > INT_MAX / 2) return fail(SPEC_ERR_ARG, "N * Hq / kv_heads is too large");
+  p.chunk = static_cast<int>(std::min<long long>((rows + 7) / 8 * 8, WMAX));
+  const double tiles = std::ceil(static_cast<double>(pages_per_seq) * p.c.page / WTOK);
+  if (static_cast<double>(B) * p.c.Hk * tiles >= 2147483648.0) return fail(SPEC_ERR_ARG, "B * kv_heads * pages_per_seq is too large");
+  const void *fn = pick_weights(p.c.D, p.c.kind, dtype);
+  const int smem = p.chunk * (p.c.D * 2 + 8);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, WMAX * (p.c.D * 2 + 8));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
+  Workspace *w = nullptr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if ((st = get_ws(stream, 1, &w))) return st;
+  p.status = w->status;
+  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * num_sms())), WT, smem, stream, &p, "cache_weights_kernel launch");
+}
+
+int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len, float *weights,
+                     int B, int keep, int first, int last, int32_t *out_index, int32_t *out_ctx_len, void *stream_ptr) {
+  NvtxRange nvtx_range("spec_cache_evict");
+  EvictParams p = {};
+  int st = check_cache(cache, page_table, pages_per_seq, B, &p.c);
+  if (st) return st;
+  if (keep < 1 || keep > (1 << 30)) return fail(SPEC_ERR_ARG, "keep out of range [1, 2^30]");
+  if (first < 0 || last < 0 || first > keep || last > keep - first) return fail(SPEC_ERR_ARG, "first and last must be >= 0 and at most keep together");
+  if (B == 0) return SPEC_OK;
+  if (!ctx_len || !weights || !out_index || !out_ctx_len) return fail(SPEC_ERR_ARG, "NULL pointer");
+  if (out_ctx_len == ctx_len) return fail(SPEC_ERR_ARG, "out_ctx_len must not be ctx_len");
+  if (!aligned16(weights)) return fail(SPEC_ERR_ALIGN, "weights must be 16-byte aligned");
+  p.ctx = ctx_len;
+  p.weights = weights;
+  p.keep = keep, p.first = first, p.last = last;
+  p.out_index = out_index;
+  p.out_ctx = out_ctx_len;
+  const void *select = reinterpret_cast<const void *>(&evict_select_kernel), *move = reinterpret_cast<const void *>(&evict_move_kernel);
+  const int smem = EM_BYTES + EM_ROWS * static_cast<int>(sizeof(float));
+  const cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
+  Workspace *w = nullptr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if ((st = get_ws(stream, 1, &w))) return st;
+  p.status = w->status;
+  const unsigned Hk = static_cast<unsigned>(p.c.Hk), batch = static_cast<unsigned>(B);
+  if ((st = launch_dependent(select, dim3(Hk, batch), EV_NT, 0, stream, &p, "evict_select_kernel launch"))) return st;
+  return launch_dependent(move, dim3(2 * Hk, batch), EM_NT, smem, stream, &p, "evict_move_kernel launch");
 }
 
 }  // extern "C"
