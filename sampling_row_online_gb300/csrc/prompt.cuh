@@ -1,69 +1,651 @@
 // Causal attention among the tokens of whole prompts, packed one behind the
-// other.
+// other: tensor cores with the accumulators in tensor memory.
+//
+//   out_i = sum_{j <= i} softmax(scale q_i . k_j) v_j   in i's own sequence.
+//
+// In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m), with
+// m 8 below a running maximum of x that is at most 7.9 behind, so the largest
+// weight of a row lies in [2^8, 2^15.9]: m moves in the first tile of a row and
+// rarely after it, and fp16 keeps full precision down to 2^-22 of the largest.
+// What is rounded: weights to the inputs' type before they meet the values (one
+// instruction takes one type; half a step, 2^-8 relative for bf16 and 2^-11 for
+// fp16), and the output, once.  Sums (of the unrounded weights), maxima,
+// products and lse are fp32.
 #pragma once
+
+#include <cuda.h>
 
 #include <cstdint>
 
 #include "device.cuh"
 #include "elements.cuh"
+#include "share.cuh"
+#include "tcgen05.cuh"
 
 namespace spec {
 
+// The rows of a tile are G query heads (that share a kv head) of `tile` tokens,
+// token by token; two tiles, A and B, go through the token tiles together.
+constexpr int PT = 128;              // rows of a tile, tokens of a token tile
+constexpr int P_SOFT = 256;          // softmax threads: a thread per row of A and of B
+constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products, B's products, a look at the values
+// Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
+constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
+static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
+constexpr float P_UP = 8.f, P_SLACK = 7.9f;
+constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
+
 struct PromptParams {
-  const void *q, *k, *v;  // [T, Hq, D], [T, Hk, D], strides in elements
-  long long q_sn, q_sh, k_sn, k_sh, v_sn, v_sh;
+  CUtensorMap q, k, v;    // [T, Hq / G, G, D] and [T, Hk, D]
   void *out;              // [T, Hq, D]
   float *lse;             // [T, Hq] or NULL
   const int32_t *starts;  // [B + 1]
-  int B, T, Hq, G, D;
-  float scale_log2;
+  int B, T, Hq;
+  int G, heads, per_kv;   // query heads of a tile, groups of them, groups of a kv head
+  int tile;               // tokens of a row tile: 128 / G
+  int period, gain;       // after `period` pairs of row tiles their ends are `gain` token tiles further
+  int ends[P_STEPS + 1];  // token tiles of the first i pairs together
+  float scale_log2;       // scale * log2(e)
+  float *pieces;          // [CTA][2][2 groups] unfinished pieces
+  int *done;              // [CTA][2 groups] arrivals per segment, by its first CTA; zero between calls
   int32_t *status;
 };
 
-// One warp per token and query head.
+template <int D>
+struct PromptLayout {
+  static constexpr int OP = PT * D * 2;  // an operand tile
+  static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, MARKS = 6 * OP;  // two tiles each
+  static constexpr int BARS = MARKS + 3 * D * 4;  // MARKS: first tokens with NaN, +inf, -inf in each column
+  static constexpr int SMEM = BARS + 256;
+  static constexpr int PIECE = PT * D + 2 * PT;  // floats: out, offset, sum
+};
+
+struct PromptBars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_seen[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
+  uint32_t tmem;
+  int marked;                  // 1 + the segment that the marks are of
+  int ended[P_SOFT / 32];      // segments that each softmax warp is done with
+};
+static_assert(sizeof(PromptBars) <= 256, "barriers");
+
+// A segment: a pair of row tiles of one group of heads of a sequence.
+struct PromptPlace {
+  int b, h, r, j, n;  // r: pair, j: token tile, n: token tiles of the pair
+  int start, len;
+};
+__device__ __forceinline__ int prompt_pair_tiles(const PromptParams &p, int len, int r) {
+  return (min((r + 1) * 2 * p.tile, len) + PT - 1) / PT;
+}
+// Token tiles of the first k pairs, none of them cut short.
+__device__ __forceinline__ unsigned prompt_tiles_before(const PromptParams &p, unsigned k) {
+  const unsigned m = k / p.period, e = k - m * p.period;
+  return m * p.ends[p.period] + p.gain * p.period * (m * (m - 1) / 2) + p.ends[e] + e * m * p.gain;
+}
+__device__ __forceinline__ unsigned prompt_head_tiles(const PromptParams &p, int len) {
+  if (len <= 0) return 0;
+  const unsigned pairs = (len + 2 * p.tile - 1) / (2 * p.tile);
+  return prompt_tiles_before(p, pairs - 1) + (len + PT - 1) / PT;
+}
+__device__ __forceinline__ void prompt_enter(const PromptParams &p, PromptPlace &u) {  // sequence u.b, or the next with tokens
+  for (;; ++u.b) {
+    u.start = p.starts[u.b];
+    u.len = p.starts[u.b + 1] - u.start;
+    if (u.len > 0) return;
+  }
+}
+__device__ __forceinline__ void prompt_next(const PromptParams &p, PromptPlace &u) {  // the next segment
+  u.j = 0;
+  if (++u.r * 2 * p.tile >= u.len) {
+    u.r = 0;
+    if (++u.h == p.heads) {
+      u.h = 0;
+      ++u.b;
+      prompt_enter(p, u);
+    }
+  }
+  u.n = prompt_pair_tiles(p, u.len, u.r);
+}
+// Token tiles that group g of the pair sees.
+__device__ __forceinline__ int prompt_group_tiles(const PromptParams &p, const PromptPlace &u, int g) {
+  const int from = (2 * u.r + g) * p.tile;
+  return from >= u.len ? 0 : (min(from + p.tile, u.len) + PT - 1) / PT;
+}
+// Whether some row of the pair does not see all of token tile j.
+__device__ __forceinline__ bool prompt_edge(const PromptParams &p, const PromptPlace &u, int j) { return (j + 1) * PT > 2 * u.r * p.tile + 1; }
+
 template <int DT>
-__global__ void __launch_bounds__(256) prompt_plain_kernel(const __grid_constant__ PromptParams p) {
-  __shared__ int s_bad;
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return DT == DT_BF16 ? f32_to_bf16x2(lo, hi) : f32_to_f16x2(lo, hi);
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+               "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+               "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A persistent CTA per SM takes an equal stretch of the list of all (sequence,
+// group of heads, pair of row tiles, token tile).  Segments that several CTAs
+// share leave pieces (out, offset, sum), which the last CTA to arrive joins in
+// index order, so results do not depend on timing.
+//
+//   copies    Q of both row tiles, K and V tiles, as swizzled operands (TMA)
+//   products  a warp per row tile: S = Q K^T, O += P V (P in tensor memory, over S)
+//   softmax   a thread per row: S -> P under the running offset, the output
+//   values    looks for values that are not finite where some row does not see
+//             all of the tile: 0 * inf is not 0.  They are taken out, and marked
+//             with their token, and rows that see them get them at the end.
+template <int D, int DT>
+__global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  using L = PromptLayout<D>;
+  extern __shared__ __align__(1024) unsigned char psm[];
+  __shared__ unsigned s_scan[P_NT / 32];
+  __shared__ int s_seq, s_last[2];
+  __shared__ unsigned s_base;
+  PromptBars &bar = *reinterpret_cast<PromptBars *>(psm + L::BARS);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float NINF = __uint_as_float(0xff800000u), QNAN = __uint_as_float(0x7fc00000u);
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i <= p.B; i += 256) {
-    const int s = p.starts[i];
-    if (s < 0 || s > p.T || (i > 0 && s < p.starts[i - 1])) s_bad = 1;
+
+  // ---- the list of all work, and this CTA's stretch of it
+  int wrong = 0;
+  const auto work_of = [&](int b) -> unsigned {
+    if (b >= p.B) return 0;
+    const int s = p.starts[b], e = p.starts[b + 1];
+    if (s < 0 || e < s || e > p.T) {
+      wrong = 1;
+      return 0;
+    }
+    return prompt_head_tiles(p, e - s) * p.heads;
+  };
+  unsigned total = 0, w = 0, upto = 0;  // upto: of all sequences up to this thread's (of the last block of them)
+  for (int b0 = 0; b0 < p.B; b0 += P_NT) {
+    unsigned sum;
+    w = work_of(b0 + tid);
+    upto = total + block_scan<P_NT / 32>(w, s_scan, sum);
+    total += sum;
   }
+  if (p.B == 0 && (p.starts[0] < 0 || p.starts[0] > p.T)) wrong = 1;
+  wrong = __syncthreads_or(wrong);
+  {  // rows of no sequence
+    const long long row = static_cast<long long>(p.Hq) * D / 8, lo = wrong ? 0 : p.starts[0], hi = wrong ? 0 : p.starts[p.B];
+    const float v = wrong ? QNAN : 0.f, x[8] = {v, v, v, v, v, v, v, v};
+    const Raw8<DT> raw = pack8<DT>(x);
+    const long long step = static_cast<long long>(gridDim.x) * P_NT, me = static_cast<long long>(blockIdx.x) * P_NT + tid;
+    for (long long i = me; i < lo * row; i += step) store8<DT, true>(p.out, i * 8, raw);
+    for (long long i = hi * row + me; i < p.T * row; i += step) store8<DT, true>(p.out, i * 8, raw);
+    if (p.lse) {
+      for (long long i = me; i < lo * p.Hq; i += step) p.lse[i] = wrong ? v : NINF;
+      for (long long i = hi * p.Hq + me; i < static_cast<long long>(p.T) * p.Hq; i += step) p.lse[i] = wrong ? v : NINF;
+    }
+  }
+  if (wrong && blockIdx.x == 0 && tid == 0) atomicOr(p.status, ST_LENGTH);
+  const unsigned nc = wrong ? 0 : min(gridDim.x, total);
+  if (blockIdx.x >= nc) return;
+  const Share share(total, nc);
+  const unsigned my0 = share.start(blockIdx.x);
+  const int count = static_cast<int>(share.start(blockIdx.x + 1) - my0);
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += P_NT) {
+    if (p.B > P_NT) {
+      unsigned sum;
+      w = work_of(b0 + tid);
+      upto = before + block_scan<P_NT / 32>(w, s_scan, sum);
+      before += sum;
+    }
+    if (my0 < upto && my0 >= upto - w) s_seq = b0 + tid, s_base = upto - w;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2);
+      mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 3), mbar_init(&bar.v_seen[i], 1);
+      mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1);
+    }
+    fence_mbar_init();
+    bar.marked = 0;
+    for (int i = 0; i < P_SOFT / 32; ++i) bar.ended[i] = 0;
+  }
+  if (warp == P_SOFT / 32) tmem_alloc(&bar.tmem, 512);
+  tc_before_sync();
   __syncthreads();
-  const bool bad = s_bad;
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, ST_LENGTH);
-  const long long item = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (item >= static_cast<long long>(p.T) * p.Hq) return;
-  const int lane = threadIdx.x & 31, tok = static_cast<int>(item / p.Hq), h = static_cast<int>(item % p.Hq), per = p.D / 32;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
-  float out_lse = -INFINITY;
-  if (bad) {
-    out_lse = o[0] = o[1] = o[2] = o[3] = __uint_as_float(0x7fc00000u);
-  } else if (tok >= p.starts[0] && tok < p.starts[p.B]) {
-    int lo = 0, hi = p.B;  // the last sequence that starts at or before the token
+  tc_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&bar.tmem);
+
+  PromptPlace at;
+  at.b = s_seq;
+  prompt_enter(p, at);
+  {
+    unsigned r = my0 - s_base;
+    const unsigned head = prompt_head_tiles(p, at.len);
+    at.h = static_cast<int>(r / head);
+    r -= at.h * head;
+    int lo = 0, hi = (at.len + 2 * p.tile - 1) / (2 * p.tile);  // the last pair that starts at or before tile r
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (p.starts[mid] <= tok) lo = mid;
+      const int mid = (lo + hi) >> 1;
+      if (prompt_tiles_before(p, mid) <= r) lo = mid;
       else hi = mid;
     }
-    for (int e = 0; e < per; ++e) q[e] = one_element<DT>(p.q, tok * p.q_sn + h * p.q_sh + lane * per + e);
-    for (int j = p.starts[lo]; j <= tok; ++j) {
-      float s = 0.f;
-      for (int e = 0; e < per; ++e) s = fmaf(q[e], one_element<DT>(p.k, j * p.k_sn + h / p.G * p.k_sh + lane * per + e), s);
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= p.scale_log2;
-      const float nm = fmaxf(m, s), a = exp2f(m - nm), w = exp2f(s - nm);
-      m = nm, l = l * a + w;
-      for (int e = 0; e < per; ++e) o[e] = fmaf(w, one_element<DT>(p.v, j * p.v_sn + h / p.G * p.v_sh + lane * per + e), o[e] * a);
-    }
-    for (int e = 0; e < per; ++e) o[e] /= l;
-    out_lse = (m + log2f(l)) * 0.6931471805599453f;
+    at.r = lo;
+    at.n = prompt_pair_tiles(p, at.len, lo);
+    at.j = static_cast<int>(r - prompt_tiles_before(p, lo));
   }
-  for (int e = 0; e < per; ++e) put_element<DT>(p.out, item * p.D + lane * per + e, o[e]);
-  if (p.lse && lane == 0) p.lse[item] = out_lse;
+  // a wait that ran out: the role goes on without waiting, its loops end, and
+  // the call reports a timeout
+  bool lost = false;
+  const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
+    if (!lost && !__all_sync(0xffffffffu, tile_wait<0>(b, parity))) lost = true;
+  };
+  const auto one = [&](uint64_t *b, uint32_t parity) {  // a single thread
+    if (!lost && !tile_wait<0>(b, parity)) lost = true;
+  };
+
+  if (warp < P_SOFT / 32) {
+    // ------------------------------------------------------------ softmax
+    more_registers<P_REG_SOFT>();
+    const int g = warp >> 2, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
+    const uint32_t tS = tmem + lanes + g * PT, tO = tmem + lanes + 256 + g * PT;
+    const int tok_in = r / p.G, head_in = r - tok_in * p.G, first_in = 32 * (warp & 3) / p.G;  // first_in: of the warp's first row
+    const float f = p.scale_log2;
+    uint32_t uses = 0;  // tiles of this group
+    int seg = 0;
+    for (int i = 0; i < count; ++seg) {
+      const int s0 = at.j, end = min(at.n, s0 + count - i), mine = min(end, prompt_group_tiles(p, at, g));  // tiles s0 .. mine - 1
+      const int from = (2 * at.r + g) * p.tile, tok = from + tok_in;
+      const bool live = tok_in < p.tile && tok < at.len;
+      float m = NINF, base = 0.f, l = 0.f;
+      const uint32_t uses0 = uses;
+      for (int j = s0; j < mine; ++j, ++uses) {
+        wait(&bar.s_full[g], uses & 1);
+        tc_after_sync();
+        const int lim = tok - j * PT;  // the last column that the row sees
+        const bool edge = from + first_in < j * PT + PT - 1;
+        const auto bits_of = [&](int q) -> uint32_t {  // the columns that it sees, of 32
+          const int n = lim + 1 - 32 * q;
+          return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+        };
+        float top = NINF;
+        if (j == s0) {  // the largest exponent first
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            tmem_ld32(tS + 32 * q, s);
+            tc_wait_ld32(s);
+            const uint32_t bits = edge ? bits_of(q) : ~0u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = __uint_as_float(s[e]) * f;
+              top = fmaxf(top, bits >> e & 1 ? x : NINF);
+            }
+          }
+          m = top - P_UP;
+          base = m == NINF ? 0.f : m;
+        }
+        uint32_t pk[64];
+        float sum, hi;
+        const auto weights = [&](auto at_edge) {
+          hi = NINF;
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t s[2][32];
+          tmem_ld32(tS, s[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tc_wait_ld32(s[q & 1]);
+            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
+            uint32_t bits = ~0u;
+            if constexpr (decltype(at_edge)::value) bits = bits_of(q);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 x = fma2(make_float2(__uint_as_float(s[q & 1][e]), __uint_as_float(s[q & 1][e + 1])), make_float2(f, f), make_float2(-base, -base));
+              if constexpr (decltype(at_edge)::value) {
+                if (!(bits >> e & 1)) x.x = NINF;
+                if (!(bits >> e & 2)) x.y = NINF;
+              }
+              hi = fmaxf(fmaxf(hi, x.x), x.y);
+              x.x = ex2(x.x), x.y = ex2(x.y);
+              part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
+              pk[16 * q + e / 2] = pack2<DT>(x.x, x.y);
+            }
+          }
+          const float2 both = add2(part[0], part[1]);
+          sum = both.x + both.y;
+        };
+#pragma unroll 1
+        for (;;) {
+          if (edge) weights(Flag<true>{});
+          else weights(Flag<false>{});
+          // the offset moves only when a weight would pass 2^15.9
+          if (!__any_sync(0xffffffffu, live && hi + base > m + (P_UP + P_SLACK))) break;
+          const float nm = fmaxf(m, hi + base - P_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
+          l *= a;
+          m = nm, base = nb;
+          if (uses != uses0) {  // O holds the products of this segment's earlier tiles
+            wait(&bar.o_done[g], (uses - 1) & 1);
+            tc_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * q, o);
+              tc_wait_ld32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st16(tO + 32 * q, o);
+              tmem_st16(tO + 32 * q + 16, o + 16);
+            }
+          }
+        }
+        l += sum;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(tS + 16 * q, pk + 16 * q);  // weights over scores that have been read
+        tc_wait_st();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[g]);
+      }
+      // ---- the end of the segment
+      const bool any = mine > s0, whole = s0 == 0 && end == at.n, active = from < at.len;
+      if (any) {
+        wait(&bar.o_done[g], (uses - 1) & 1);
+        tc_after_sync();
+      }
+      const int *mark = reinterpret_cast<const int *>(psm + L::MARKS);
+      const bool marked = any && *reinterpret_cast<const volatile int *>(&bar.marked) == seg + 1;
+      const long long orow = static_cast<long long>(at.start + tok) * p.Hq + at.h * p.G + head_in;
+      const int which = s0 > 0 ? 0 : 1;
+      float *const piece = p.pieces + ((static_cast<long long>(blockIdx.x) * 2 + which) * 2 + g) * L::PIECE;
+      if (active) {
+        const float inv = whole ? 1.f / l : 1.f;
+#pragma unroll 1
+        for (int q = 0; q < D / 32 && any; ++q) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(tO + 32 * q, o);
+          tc_wait_ld32(o);
+          float z[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(o[e]) * inv;
+          if (marked) {  // values that are not finite, for the rows that see them
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int d = 32 * q + e;
+              if (tok >= mark[D + d]) z[e] += INFINITY;
+              if (tok >= mark[2 * D + d]) z[e] -= INFINITY;
+              if (tok >= mark[d]) z[e] = QNAN;
+            }
+          }
+          if (live) {
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = z[e + k];
+                store8<DT, true>(p.out, orow * D + 32 * q + e, pack8<DT>(x));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                reinterpret_cast<float4 *>(piece)[(8 * q + e / 4) * PT + r] = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+            }
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (live) {
+          if (!whole) piece[PT * D + r] = m, piece[PT * D + PT + r] = l;
+          else if (p.lse) p.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+        }
+        if (!whole) {
+          // a segment that several CTAs share: the last to arrive joins, in order
+          __threadfence();
+          named_sync(1 + g, 128);
+          const unsigned f0 = my0 + i - s0;
+          const int c0 = share.holder(f0), n = static_cast<int>(share.holder(f0 + at.n - 1)) - c0 + 1;
+          if (r == 0) {
+            s_last[g] = atomicAdd(p.done + 2 * c0 + g, 1) == n - 1;
+            __threadfence();
+          }
+          named_sync(1 + g, 128);
+          if (*reinterpret_cast<volatile int *>(&s_last[g])) {
+            __threadfence();
+            if (live) {
+              const auto part = [&](int e) { return p.pieces + ((static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * 2 + g) * L::PIECE; };
+              float M = NINF, sum = 0.f;
+              for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(part(e) + PT * D + r));
+              const float bm = M == NINF ? 0.f : M;
+              for (int e = 0; e < n; ++e) sum = fmaf(ex2(__ldcg(part(e) + PT * D + r) - bm), __ldcg(part(e) + PT * D + PT + r), sum);
+              const float over = 1.f / sum;
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                float z[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = 0.f;
+                for (int e = 0; e < n; ++e) {
+                  const float me = __ldcg(part(e) + PT * D + r);
+                  if (me == NINF) continue;  // a piece without tiles that this row sees holds nothing
+                  const float a = ex2(me - bm);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(e)) + (4 * q + k) * PT + r);
+                    z[4 * k] = fmaf(a, x.x, z[4 * k]), z[4 * k + 1] = fmaf(a, x.y, z[4 * k + 1]);
+                    z[4 * k + 2] = fmaf(a, x.z, z[4 * k + 2]), z[4 * k + 3] = fmaf(a, x.w, z[4 * k + 3]);
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                  float x[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) x[k] = z[e + k] * over;
+                  store8<DT, true>(p.out, orow * D + 16 * q + e, pack8<DT>(x));
+                }
+              }
+              if (p.lse) p.lse[orow] = (M + log2f(sum)) * 0.6931471805599453f;
+            }
+            if (r == 0) p.done[2 * c0 + g] = 0;  // zero again for the next call
+          }
+        }
+      }
+      if (lane == 0) *reinterpret_cast<volatile int *>(&bar.ended[warp]) = seg + 1;
+      i += end - s0;
+      if (i < count) prompt_next(p, at);
+    }
+  } else {
+    fewer_registers<P_REG_REST>();
+    const int role = warp - P_SOFT / 32;
+    if (role == 0) {
+      // ------------------------------------------------------------ copies
+      if (lane == 0) {
+        const uint32_t sm = smem_u32(psm);
+        const int kv_bytes = L::OP, q_bytes = p.tile * p.G * D * 2;
+        uint32_t q_uses[2] = {0, 0};
+        PromptPlace u = at;
+        int s0 = u.j, issued = 0;
+        for (int i = 0; i < count; ++i) {
+          const uint32_t s = i & 1, ph = (i >> 1) & 1;
+          const int row = u.start + u.j * PT, kv = u.h / p.per_kv;
+          one(&bar.k_empty[s], ph ^ 1);
+          if (lost) break;
+          mbar_arrive_expect_tx(&bar.k_full[s], kv_bytes);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) tma_load(sm + L::K + s * L::OP + x * 16384, &p.k, 64 * x, kv, row, &bar.k_full[s]);
+          if (u.j == s0)
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+              if (s0 >= prompt_group_tiles(p, u, g)) continue;
+              one(&bar.q_empty[g], (q_uses[g] & 1) ^ 1);
+              if (lost) break;
+              ++q_uses[g];
+              mbar_arrive_expect_tx(&bar.q_full[g], q_bytes);
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+                tma_load(sm + L::Q + g * L::OP + x * 16384, &p.q, 64 * x, 0, u.h, u.start + (2 * u.r + g) * p.tile, &bar.q_full[g]);
+            }
+          if (!lost) one(&bar.v_empty[s], ph ^ 1);
+          if (lost) {
+            issued = 2 * i + 1;
+            break;
+          }
+          mbar_arrive_expect_tx(&bar.v_full[s], kv_bytes);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) tma_load(sm + L::V + s * L::OP + x * 16384, &p.v, 64 * x, kv, row, &bar.v_full[s]);
+          issued = 2 * i + 2;
+          if (++u.j == u.n && i + 1 < count) prompt_next(p, u), s0 = 0;
+        }
+        // no copy outlives the CTA, even after a wait that ran out
+        const bool was = lost;
+        lost = false;
+        for (int k = max(0, issued - 4); k < issued; ++k) one(k & 1 ? &bar.v_full[(k >> 1) & 1] : &bar.k_full[(k >> 1) & 1], (k >> 2) & 1);
+        for (int g = 0; g < 2; ++g)
+          if (q_uses[g]) one(&bar.q_full[g], (q_uses[g] - 1) & 1);
+        lost |= was;
+      }
+    } else if (role <= 2) {
+      // ---------------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
+        constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
+        constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
+        const int g = role - 1;
+        const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * PT;
+        const uint64_t dQ = tc_desc(sm + L::Q + g * L::OP, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
+        uint32_t uses = 0, q_uses = 0, seen[2] = {0, 0};
+        PromptPlace u = at;
+        for (int i = 0; i < count;) {
+          const int s0 = u.j, end = min(u.n, s0 + count - i), n = prompt_group_tiles(p, u, g), mine = min(end, n);
+          if (s0 < mine) one(&bar.q_full[g], q_uses & 1), ++q_uses;
+          for (int j = s0; j < end; ++j, ++i) {
+            const uint32_t s = i & 1, ph = (i >> 1) & 1;
+            const uint64_t dK = dK0 + (s * L::OP >> 4), dV = dV0 + (s * L::OP >> 4);
+            const bool edge = prompt_edge(p, u, j);
+            one(&bar.k_full[s], ph);
+            if (j >= mine) {  // the other row tile's alone
+              mbar_arrive(&bar.k_empty[s]);
+              one(&bar.v_full[s], ph);
+              if (edge) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
+              mbar_arrive(&bar.v_empty[s]);
+              continue;
+            }
+            tc_after_sync();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
+              const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+              tc_mma_ss(tS, dQ + off, dK + off, ID_S, k > 0);
+            }
+            tc_commit(&bar.s_full[g]);
+            tc_commit(&bar.k_empty[s]);
+            if (j + 1 == mine) tc_commit(&bar.q_empty[g]);
+            one(&bar.v_full[s], ph);
+            if (edge) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
+            one(&bar.p_full[g], uses & 1);
+            ++uses;
+            tc_after_sync();
+#pragma unroll
+            for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
+              tc_mma_ts(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || j != s0);
+            tc_commit(&bar.o_done[g]);
+            tc_commit(&bar.v_empty[s]);
+          }
+          u.j = end;
+          if (i < count) prompt_next(p, u);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ values
+      constexpr uint32_t EXP = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+      PromptPlace u = at;
+      int *const mark = reinterpret_cast<int *>(psm + L::MARKS);
+      int seg = 0;
+      for (int i = 0; i < count; ++i) {
+        const uint32_t s = i & 1, ph = (i >> 1) & 1;
+        wait(&bar.v_full[s], ph);
+        if (prompt_edge(p, u, u.j)) {
+          unsigned char *const tile = psm + L::V + s * L::OP;
+          uint32_t most = 0;
+#pragma unroll 8
+          for (int k = 0; k < L::OP / 512; ++k) {
+            const uint4 x = lds128(tile + (k * 32 + lane) * 16);
+            asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.x & 0x7fff7fffu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.y & 0x7fff7fffu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.z & 0x7fff7fffu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.w & 0x7fff7fffu));
+          }
+          if (__any_sync(0xffffffffu, (most & 0xffffu) >= EXP || (most >> 16) >= EXP)) {
+            volatile int *const marked = &bar.marked, *const ended = bar.ended;
+            if (*marked != seg + 1) {  // the marks of an earlier segment may still be read
+              for (int polls = 0; !lost && !__all_sync(0xffffffffu, ended[lane % (P_SOFT / 32)] >= seg); ++polls) {
+                __nanosleep(100);
+                lost = polls > 1 << 18;
+              }
+              for (int d = lane; d < 3 * D; d += 32) mark[d] = INT32_MAX;
+              __syncwarp();
+              if (lane == 0) *marked = seg + 1;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < L::OP / 64; ++k) {  // two elements at a time: panel, row, swizzled chunk of eight
+              uint32_t *const word = reinterpret_cast<uint32_t *>(tile) + k * 16 + (lane & 15);
+              const int byte = (k * 16 + (lane & 15)) * 4, panel = byte >> 14, row = (byte >> 7) & 127;
+              const int d0 = panel * 64 + ((((byte >> 4) & 7) ^ (row & 7)) << 3) + ((byte & 15) >> 1);
+              const uint32_t x = *word;
+              uint32_t y = x;
+              if (lane < 16) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t half = (x >> (16 * e)) & 0xffffu, size = half & 0x7fffu;
+                  if (size < EXP) continue;
+                  y &= e ? 0x0000ffffu : 0xffff0000u;
+                  const int kind = size > EXP ? 0 : half & 0x8000u ? 2 : 1;
+                  atomicMin(&mark[kind * D + d0 + e], u.j * PT + row);
+                }
+                if (y != x) *word = y;
+              }
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.v_seen[s]);
+        }
+        // also where there was nothing to look at: a warp that let phases pass
+        // could take one for another
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_empty[s]);
+        if (++u.j == u.n && i + 1 < count) prompt_next(p, u), ++seg;
+      }
+    }
+  }
+  if (lost) atomicOr(p.status, ST_TIMEOUT);
+  tc_before_sync();
+  __syncthreads();
+  if (warp == P_SOFT / 32) {
+    tc_after_sync();
+    tmem_free(tmem, 512);
+  }
+}
+
+// Rows that the copies cannot take as they lie (not 16-byte aligned, or their
+// strides are not), to [T, H, D].
+struct PackParams {
+  const uint16_t *src;
+  long long sn, sh;  // strides in elements
+  uint16_t *dst;
+  int T, H, D;
+};
+__global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant__ PackParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long n = static_cast<long long>(p.T) * p.H * p.D;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const long long row = i / p.D;
+    p.dst[i] = p.src[row / p.H * p.sn + row % p.H * p.sh + i % p.D];
+  }
 }
 
 }  // namespace spec
