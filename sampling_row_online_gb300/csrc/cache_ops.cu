@@ -15,17 +15,20 @@
 namespace spec {
 
 // Launches as a programmatic dependent of what precedes it on the stream.
-int launch_dependent(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what) {
-  cudaLaunchAttribute pdl;
-  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl.val.programmaticStreamSerializationAllowed = 1;
+int launch_dependent(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what, unsigned cluster) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cfg.attrs = &pdl;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   void *args[] = {params};
   const cudaError_t e = launch_kernel(&cfg, fn, args);
   return e == cudaSuccess ? static_cast<int>(SPEC_OK) : cuda_fail(e, what);
@@ -436,16 +439,28 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   p.out_index = out_index;
   p.out_ctx = out_ctx_len;
   const void *select = reinterpret_cast<const void *>(&evict_select_kernel), *move = reinterpret_cast<const void *>(&evict_move_kernel);
-  const int smem = EM_BYTES + EM_ROWS * static_cast<int>(sizeof(float));
-  const cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, EM_SMEM);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if ((st = get_ws(stream, 1, &w))) return st;
   p.status = w->status;
+  // CTAs of a cluster: up to 8, as far as there is work for them and all of them
+  // run together
+  const auto cluster = [](long long work, long long groups, int per_sm) {
+    unsigned n = 1;
+    while (n < 8 && n < work && 2 * n * groups <= static_cast<long long>(per_sm) * num_sms()) n *= 2;
+    return n;
+  };
   const unsigned Hk = static_cast<unsigned>(p.c.Hk), batch = static_cast<unsigned>(B);
-  if ((st = launch_dependent(select, dim3(Hk, batch), EV_NT, 0, stream, &p, "evict_select_kernel launch"))) return st;
-  return launch_dependent(move, dim3(2 * Hk, batch), EM_NT, smem, stream, &p, "evict_move_kernel launch");
+  const long long heads = static_cast<long long>(Hk) * batch, slots = static_cast<long long>(p.c.per) * p.c.page;
+  // a slice of the slots in registers wherever 8 CTAs can hold them
+  unsigned n = cluster((slots + EV_NT * 4 - 1) / (EV_NT * 4), heads, 3);
+  while (n < 8 && n * EV_SLICE < slots) n *= 2;
+  if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, 0, stream, &p, "evict_select_kernel launch", n))) return st;
+  const int rows = EM_BYTES / p.c.D;
+  n = cluster((keep + rows - 1) / rows, 2 * heads, 5);
+  return launch_dependent(move, dim3(2 * Hk * n, batch), EM_NT, EM_SMEM, stream, &p, "evict_move_kernel launch", n);
 }
 
 }  // extern "C"

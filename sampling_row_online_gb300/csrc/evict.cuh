@@ -226,7 +226,8 @@ struct EvictParams {
   int32_t *out_index, *out_ctx;
   int32_t *status;
 };
-constexpr int EV_NT = 512, EV_BINS = 2048;
+constexpr int EV_NT = 512, EV_BINS = 2048, EV_EACH = 16;  // threads, bins, slots of a thread at a time
+constexpr int EV_SLICE = EV_NT * EV_EACH;                  // slots of a CTA at a time
 
 // Weights as whole numbers of the same order: NaN below everything, both zeros
 // equal.
@@ -236,42 +237,65 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A CTA per kv head and sequence finds the k-th largest weight by its digits,
-// 11, 11 and 10 bits from the top (a histogram each), and then goes over the
-// slots in order: what is above it, and of its equals the first ones, is
-// listed, and its weight moves along.  A slot never moves up, so a stretch of
-// slots that has been read may be overwritten.
+// A cluster per kv head and sequence finds the k-th largest weight by its
+// digits, 11, 11 and 10 bits from the top (a histogram each, added up through
+// distributed shared memory), and then goes over the slots in order: what is
+// above it, and of its equals the first ones, is listed, and its weight moves
+// along.  Every CTA has a slice of the slots in registers, so the weights are
+// read once and may be overwritten.  Slots that do not fit are left to one CTA,
+// which reads them once for each digit and once more: a slot never moves up, so
+// it too overwrites only what it has read.
 __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ unsigned s_hist[EV_BINS], s_scan[EV_NT / 32];
-  __shared__ unsigned s_digit, s_rem;
-  __shared__ int s_bad;
+  __shared__ __align__(16) unsigned s_hist[2][EV_BINS];
+  __shared__ unsigned s_scan[EV_NT / 32], s_digit, s_rem, s_total;
   const CacheView &c = p.c;
-  const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int b = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   const int ctx = p.ctx[b];
   const long long S = static_cast<long long>(c.per) * c.page;
   int32_t *const index = p.out_index + (static_cast<long long>(b) * c.Hk + h) * p.keep;
-  bool ok = ctx >= 0 && ctx <= S;
-  if (!ok && tid == 0) atomicOr(p.status, ST_SLOTS);
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  if (ok && ctx > p.keep) {
+  const bool fits = ctx >= 0 && ctx <= S;
+  int bad = 0;
+  if (fits && ctx > p.keep) {
     const int blocks = (ctx + c.page - 1) >> c.log_page;
+#pragma unroll 4
     for (int i = tid; i < blocks; i += EV_NT)
-      if (static_cast<unsigned>(c.table[static_cast<long long>(b) * c.per + i]) >= static_cast<unsigned>(c.pages)) s_bad = 1;
-    __syncthreads();
-    if (s_bad) {
-      ok = false;
-      if (tid == 0) atomicOr(p.status, ST_PAGE);
-    }
+      bad |= static_cast<unsigned>(c.table[static_cast<long long>(b) * c.per + i]) >= static_cast<unsigned>(c.pages);
   }
-  if (h == 0 && tid == 0) p.out_ctx[b] = ok ? min(ctx, p.keep) : ctx;
+  // this CTA's slots: [s0, s1), EV_SLICE of them at a time
+  int slice = ((ctx + C - 1) / C + 3) & ~3;
+  const bool joint = C > 1 && slice <= EV_SLICE;
+  if (!joint) slice = ctx;
+  const int s0 = joint ? min(rank * slice, ctx) : 0, s1 = joint ? min(s0 + slice, ctx) : ctx;
+  float *const wts = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
+  float v[EV_EACH];
+  const auto load = [&](int from) {  // a thread's slots are neighbours
+    const int at = from + tid * EV_EACH;
+#pragma unroll
+    for (int i = 0; i < EV_EACH; i += 4) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at + i < s1) x = *reinterpret_cast<const float4 *>(wts + at + i);
+      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
+  };
+  const bool one = s1 - s0 <= EV_SLICE;
+  if (fits && ctx > p.keep && one) load(s0);
+  for (int i = tid; i < 2 * EV_BINS; i += EV_NT) s_hist[0][i] = 0;
+  bad = __syncthreads_or(bad);
+  const bool ok = fits && !bad;
+  if (rank == 0 && tid == 0) {
+    if (!fits) atomicOr(p.status, ST_SLOTS);
+    if (bad) atomicOr(p.status, ST_PAGE);
+    if (h == 0) p.out_ctx[b] = ok ? min(ctx, p.keep) : ctx;
+  }
   if (!ok || ctx <= p.keep) {
-    for (int i = tid; i < p.keep; i += EV_NT) index[i] = ok && i < ctx ? i : -1;
+    for (int i = rank * EV_NT + tid; i < p.keep; i += C * EV_NT) index[i] = ok && i < ctx ? i : -1;
     return;
   }
-  float *const wts = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
+  if (!joint && rank > 0) return;
+
   const int lo = p.first, hi = ctx - p.last;
   unsigned rem = p.keep - p.first - p.last;  // of hi - lo, which are more
   uint32_t key = 0;                          // the digits found so far, at their place
@@ -281,29 +305,43 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 2 ? 10 : 11, down = up - bits;
-      for (int i = tid; i < EV_BINS; i += EV_NT) s_hist[i] = 0;
-      __syncthreads();
-      for (int i0 = lo + tid; i0 < hi; i0 += 4 * EV_NT) {
-        float w[4];
+      unsigned *const hist = s_hist[pass & 1];
+      if (pass == 2) {  // the other CTAs have read the first digit's counts before the second digit's barrier
+        for (int i = tid; i < EV_BINS; i += EV_NT) hist[i] = 0;
+        __syncthreads();
+      }
+#pragma unroll 1
+      for (int from = s0; from < s1; from += EV_SLICE) {
+        if (!one) load(from);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = i0 + e * EV_NT < hi ? wts[i0 + e * EV_NT] : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = weight_key(w[e]);
-          if (i0 + e * EV_NT < hi && (pass == 0 || u >> up == key >> up)) atomicAdd(&s_hist[u >> down & ((1u << bits) - 1)], 1u);
+        for (int i = 0; i < EV_EACH; ++i) {
+          const int s = from + tid * EV_EACH + i;
+          const uint32_t u = weight_key(v[i]);
+          if (s >= lo && s < hi && s < s1 && (pass == 0 || u >> up == key >> up)) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
         }
       }
-      __syncthreads();
+      if (joint) cluster_sync();
+      else __syncthreads();
       // four bins to a thread, from the top
-      unsigned n[4], four = 0;
+      const unsigned *mine = &hist[EV_BINS - 4 - 4 * tid];
+      uint4 n = make_uint4(0, 0, 0, 0);
+      if (joint) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) n[e] = s_hist[EV_BINS - 1 - 4 * tid - e], four += n[e];
+        for (int i = 0; i < 8; ++i) {
+          if (i >= C) break;
+          const uint4 x = dsmem_ld_v4(dsmem_addr(mine, i));
+          n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
+        }
+      } else {
+        n = *reinterpret_cast<const uint4 *>(mine);
+      }
+      const unsigned four = n.x + n.y + n.z + n.w, each[4] = {n.w, n.z, n.y, n.x};
       unsigned sum;
       unsigned above = block_scan<EV_NT / 32>(four, s_scan, sum) - four;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (above < rem && above + n[e] >= rem) s_digit = EV_BINS - 1 - 4 * tid - e, s_rem = rem - above;
-        above += n[e];
+        if (above < rem && above + each[e] >= rem) s_digit = EV_BINS - 1 - 4 * tid - e, s_rem = rem - above;
+        above += each[e];
       }
       __syncthreads();
       key |= s_digit << down;
@@ -311,57 +349,64 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       up = down;
     }
   }
-  // in order: `rem` of those that equal the key, and all above it
-  unsigned placed = 0, equal = 0;  // so far
+  // in order: all above the key, and the first `rem` of those that equal it
+  unsigned n_more = 0, n_same = 0;  // before this stretch of slots
 #pragma unroll 1
-  for (int s0 = 0; s0 < ctx; s0 += 4 * EV_NT) {
-    const int at = s0 + 4 * tid;
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
-    if (at < ctx) {
-      const float4 x = *reinterpret_cast<const float4 *>(wts + at);
-      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    }
-    unsigned more = 0, same = 0;  // bits of the four slots
+  for (int from = s0; from < max(s1, s0 + 1); from += EV_SLICE) {
+    if (!one) load(from);
+    unsigned more = 0, same = 0;  // bits of a thread's slots
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int s = at + e;
-      if (s >= ctx) continue;
-      const uint32_t u = weight_key(w[e]);
-      if (s < lo || s >= hi || (some && u > key)) more |= 1u << e;
-      else if (some && u == key) same |= 1u << e;
+    for (int i = 0; i < EV_EACH; ++i) {
+      const int s = from + tid * EV_EACH + i;
+      const uint32_t u = weight_key(v[i]);
+      if (s >= s1) continue;
+      if (s < lo || s >= hi || (some && u > key)) more |= 1u << i;
+      else if (some && u == key) same |= 1u << i;
     }
     const unsigned both = __popc(more) | __popc(same) << 16;
     unsigned sum;
-    const unsigned upto = block_scan<EV_NT / 32>(both, s_scan, sum) - both;  // every weight of the stretch has been read
-    unsigned n_more = upto & 0xffffu, n_same = upto >> 16;
-    // of the first n equals of this stretch, those that are kept
-    const auto kept_equals = [&](unsigned n) { return min(equal + n, rem) - min(equal, rem); };
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool is_same = same >> e & 1;
-      if ((more >> e & 1) || (is_same && equal + n_same < rem)) {
-        const unsigned pos = placed + n_more + kept_equals(n_same);
-        index[pos] = at + e;
-        wts[pos] = w[e];
+    const unsigned upto = block_scan<EV_NT / 32>(both, s_scan, sum) - both;  // the stretch's weights have been read
+    if (joint) {
+      if (tid == 0) s_total = sum;
+      cluster_sync();
+      for (int i = 0; i < rank; ++i) {
+        const unsigned x = static_cast<unsigned>(dsmem_ld_s32(dsmem_addr(&s_total, i)));
+        n_more += x & 0xffffu, n_same += x >> 16;
       }
-      n_more += more >> e & 1, n_same += is_same;
     }
-    placed += (sum & 0xffffu) + kept_equals(sum >> 16);
-    equal += sum >> 16;
+    unsigned m = n_more + (upto & 0xffffu), e = n_same + (upto >> 16);
+#pragma unroll
+    for (int i = 0; i < EV_EACH; ++i) {
+      const bool is_more = more >> i & 1, is_same = same >> i & 1;
+      if (is_more || (is_same && e < rem)) {
+        const unsigned pos = m + min(e, rem);
+        index[pos] = from + tid * EV_EACH + i;
+        wts[pos] = v[i];
+      }
+      m += is_more, e += is_same;
+    }
+    n_more += sum & 0xffffu, n_same += sum >> 16;
   }
+  if (joint) cluster_sync();  // no CTA leaves while others read its counts
 }
 
-// A CTA per kv head, tensor and sequence moves the kept rows together, some
-// blocks at a time: their rows are gathered in shared memory, the largest
-// magnitude of each block gives its scale, and the codes are written.  A row
-// never moves to a later block, so whatever later blocks take is still there.
-constexpr int EM_NT = 256, EM_BYTES = 65536, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
+// A cluster per kv head, tensor and sequence moves the kept rows together, some
+// blocks to a CTA at a time: their rows are gathered in shared memory, the
+// largest magnitude of each block gives its scale, and the codes are written
+// once the whole cluster has read.  A row never moves to a later block, so
+// whatever later rounds take is still there.
+constexpr int EM_NT = 256, EM_BYTES = 32768, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
+constexpr int EM_SMEM = EM_BYTES + EM_ROWS * 12;
 __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ __align__(16) unsigned char dyn[];  // rows, then their scales
+  extern __shared__ __align__(16) unsigned char dyn[];  // rows; where they come from; their scales
   __shared__ unsigned s_amax[EM_BLOCKS];
+  __shared__ long long s_to[EM_BLOCKS];
   const CacheView &c = p.c;
-  const int b = blockIdx.y, h = blockIdx.x >> 1, tensor = blockIdx.x & 1, tid = threadIdx.x, lane = tid & 31;
-  float *const s_from = reinterpret_cast<float *>(dyn + EM_BYTES);
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int b = blockIdx.y, h = blockIdx.x / C >> 1, tensor = blockIdx.x / C & 1, tid = threadIdx.x, lane = tid & 31;
+  uint4 *const s_row = reinterpret_cast<uint4 *>(dyn);
+  const uint4 **const s_at = reinterpret_cast<const uint4 **>(dyn + EM_BYTES);
+  float *const s_from = reinterpret_cast<float *>(dyn + EM_BYTES + EM_ROWS * 8);
   pdl_wait();
   pdl_launch_dependents();
   if (p.ctx[b] <= p.keep || p.out_ctx[b] != p.keep) return;  // nothing to move, or an error
@@ -369,20 +414,30 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
   float *const scales = tensor ? c.v_scale : c.k_scale;
   const int32_t *const index = p.out_index + (static_cast<long long>(b) * c.Hk + h) * p.keep;
   const int32_t *const table = c.table + static_cast<long long>(b) * c.per;
-  const int log_row = c.D == 128 ? 3 : 2, most = EM_BYTES / c.D;  // vectors of a row, rows at a time
-  uint4 *const s_row = reinterpret_cast<uint4 *>(dyn);
+  const int log_row = c.D == 128 ? 3 : 2, last = (1 << log_row) - 1, most = EM_BYTES / c.D;  // vectors of a row; rows at a time
 #pragma unroll 1
-  for (int r0 = 0; r0 < p.keep; r0 += most) {
-    const int rows = min(most, p.keep - r0), vectors = rows << log_row, blocks = (rows + c.page - 1) >> c.log_page;
-    for (int i = tid; i < blocks; i += EM_NT) s_amax[i] = 0;
-    for (int k = tid; k < vectors; k += EM_NT) {
-      const int row = k >> log_row, slot = index[r0 + row];
+  for (int round = 0; round < p.keep; round += most * C) {
+    const int r0 = round + rank * most, rows = max(0, min(most, p.keep - r0));
+    const int vectors = rows << log_row, blocks = (rows + c.page - 1) >> c.log_page;
+#pragma unroll
+    for (int i = 0; i < EM_ROWS / EM_NT; ++i) {
+      const int row = tid + i * EM_NT;
+      if (row >= rows) continue;
+      const int slot = index[r0 + row];
       const long long id = static_cast<long long>(table[slot >> c.log_page]) * c.Hk + h;
-      cp_async16(s_row + k, codes + (id * c.page + (slot & (c.page - 1))) * c.D + ((k & ((1 << log_row) - 1)) << 4));
-      if ((k & ((1 << log_row) - 1)) == 0) s_from[row] = scales[id];
+      s_from[row] = scales[id];
+      s_at[row] = reinterpret_cast<const uint4 *>(codes + (id * c.page + (slot & (c.page - 1))) * c.D);
     }
+    if (tid < blocks) {
+      s_amax[tid] = 0;
+      s_to[tid] = static_cast<long long>(table[(r0 >> c.log_page) + tid]) * c.Hk + h;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int k = tid; k < vectors; k += EM_NT) cp_async16(s_row + k, s_at[k >> log_row] + (k & last));
     cp_async_wait_all();
     __syncthreads();
+#pragma unroll 2
     for (int k0 = tid - lane; k0 < vectors; k0 += EM_NT) {  // a warp's vectors belong to one block
       const int k = k0 + lane;
       float m = 0.f;
@@ -401,7 +456,9 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
       const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
       if (lane == 0) atomicMax(&s_amax[k0 >> log_row >> c.log_page], largest);
     }
-    __syncthreads();
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+#pragma unroll 2
     for (int k = tid; k < vectors; k += EM_NT) {
       const int row = k >> log_row, blk = row >> c.log_page;
       const float scale = scale_for(c.kind, s_amax[blk]), inv = 1.f / scale, from = s_from[row];
@@ -413,9 +470,8 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
         decode4(c.kind, u[j], x);
         u[j] = encode4(c.kind, x[0] * from * inv, x[1] * from * inv, x[2] * from * inv, x[3] * from * inv);
       }
-      const int slot = r0 + row;
-      const long long id = static_cast<long long>(table[slot >> c.log_page]) * c.Hk + h;
-      reinterpret_cast<uint4 *>(codes + (id * c.page + (slot & (c.page - 1))) * c.D)[k & ((1 << log_row) - 1)] = make_uint4(u[0], u[1], u[2], u[3]);
+      const long long id = s_to[blk];
+      reinterpret_cast<uint4 *>(codes + (id * c.page + (row & (c.page - 1))) * c.D)[k & last] = make_uint4(u[0], u[1], u[2], u[3]);
       if (k == (blk << c.log_page) << log_row) scales[id] = scale;
     }
     __syncthreads();

@@ -55,7 +55,8 @@ int get_ws(cudaStream_t stream, size_t nparts, Workspace **out, size_t nattn = 0
 int num_sms();
 
 // Launches one kernel, whose parameters are *params, as a programmatic
-// dependent of what precedes it on the stream (cache_ops.cu).
-int launch_dependent(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what);
+// dependent of what precedes it on the stream, in clusters of `cluster` CTAs
+// along x (cache_ops.cu).
+int launch_dependent(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, void *params, const char *what, unsigned cluster = 1);
 
 }  // namespace spec
