@@ -439,7 +439,8 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   p.out_index = out_index;
   p.out_ctx = out_ctx_len;
   const void *select = reinterpret_cast<const void *>(&evict_select_kernel), *move = reinterpret_cast<const void *>(&evict_move_kernel);
-  const cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, EM_SMEM);
+  cudaError_t e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, EM_SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_SMEM);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
@@ -457,7 +458,7 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   // a slice of the slots in registers wherever 8 CTAs can hold them
   unsigned n = cluster((slots + EV_NT * 4 - 1) / (EV_NT * 4), heads, 3);
   while (n < 8 && n * EV_SLICE < slots) n *= 2;
-  if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, 0, stream, &p, "evict_select_kernel launch", n))) return st;
+  if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, EV_SMEM, stream, &p, "evict_select_kernel launch", n))) return st;
   const int rows = EM_BYTES / p.c.D;
   n = cluster((keep + rows - 1) / rows, 2 * heads, 5);
   return launch_dependent(move, dim3(2 * Hk * n, batch), EM_NT, EM_SMEM, stream, &p, "evict_move_kernel launch", n);

@@ -226,8 +226,9 @@ struct EvictParams {
   int32_t *out_index, *out_ctx;
   int32_t *status;
 };
-constexpr int EV_NT = 512, EV_BINS = 2048, EV_EACH = 16;  // threads, bins, slots of a thread at a time
-constexpr int EV_SLICE = EV_NT * EV_EACH;                  // slots of a CTA at a time
+constexpr int EV_NT = 512, EV_BINS = 2048;       // threads, bins
+constexpr int EV_SLICE = 8192;                   // slots of a CTA at a time
+constexpr int EV_SMEM = (EV_SLICE + 2 * EV_BINS) * 4;
 
 // Weights as whole numbers of the same order: NaN below everything, both zeros
 // equal.
@@ -241,48 +242,48 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // digits, 11, 11 and 10 bits from the top (a histogram each, added up through
 // distributed shared memory), and then goes over the slots in order: what is
 // above it, and of its equals the first ones, is listed, and its weight moves
-// along.  Every CTA has a slice of the slots in registers, so the weights are
-// read once and may be overwritten.  Slots that do not fit are left to one CTA,
-// which reads them once for each digit and once more: a slot never moves up, so
-// it too overwrites only what it has read.
+// along.  Every CTA has a slice of the slots in shared memory, so the weights
+// are read once and may be overwritten.  Slots that do not fit are left to one
+// CTA, which reads them once for each digit and once more: a slot never moves
+// up, so it too overwrites only what it has read.  What bounds it is the chain
+// of counts, barriers and scans, and the fetch of code that runs a few times:
+// all loops are short.
 __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ __align__(16) unsigned s_hist[2][EV_BINS];
+  extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ unsigned s_scan[EV_NT / 32], s_digit, s_rem, s_total;
+  float *const s_val = reinterpret_cast<float *>(dyn);
+  unsigned *const s_hist = reinterpret_cast<unsigned *>(dyn) + EV_SLICE;  // two of them
   const CacheView &c = p.c;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int b = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x;
+  const int b = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
+#pragma unroll 1
+  for (int i = tid; i < 2 * EV_BINS; i += EV_NT) s_hist[i] = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int ctx = p.ctx[b];
   const long long S = static_cast<long long>(c.per) * c.page;
   int32_t *const index = p.out_index + (static_cast<long long>(b) * c.Hk + h) * p.keep;
-  const bool fits = ctx >= 0 && ctx <= S;
-  int bad = 0;
-  if (fits && ctx > p.keep) {
-    const int blocks = (ctx + c.page - 1) >> c.log_page;
-#pragma unroll 4
-    for (int i = tid; i < blocks; i += EV_NT)
-      bad |= static_cast<unsigned>(c.table[static_cast<long long>(b) * c.per + i]) >= static_cast<unsigned>(c.pages);
-  }
+  const bool fits = ctx >= 0 && ctx <= S, moves = fits && ctx > p.keep;
   // this CTA's slots: [s0, s1), EV_SLICE of them at a time
   int slice = ((ctx + C - 1) / C + 3) & ~3;
   const bool joint = C > 1 && slice <= EV_SLICE;
   if (!joint) slice = ctx;
   const int s0 = joint ? min(rank * slice, ctx) : 0, s1 = joint ? min(s0 + slice, ctx) : ctx;
   float *const wts = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
-  float v[EV_EACH];
-  const auto load = [&](int from) {  // a thread's slots are neighbours
-    const int at = from + tid * EV_EACH;
-#pragma unroll
-    for (int i = 0; i < EV_EACH; i += 4) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (at + i < s1) x = *reinterpret_cast<const float4 *>(wts + at + i);
-      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    }
+  const auto load = [&](int from) {
+    const int n = min(EV_SLICE, s1 - from);
+#pragma unroll 2
+    for (int i = 4 * tid; i < n; i += 4 * EV_NT) *reinterpret_cast<float4 *>(s_val + i) = *reinterpret_cast<const float4 *>(wts + from + i);
   };
   const bool one = s1 - s0 <= EV_SLICE;
-  if (fits && ctx > p.keep && one) load(s0);
-  for (int i = tid; i < 2 * EV_BINS; i += EV_NT) s_hist[0][i] = 0;
+  int bad = 0;
+  if (moves) {
+    if (one) load(s0);
+    const int blocks = (ctx + c.page - 1) >> c.log_page;
+#pragma unroll 1
+    for (int i = tid; i < blocks; i += EV_NT)
+      bad |= static_cast<unsigned>(c.table[static_cast<long long>(b) * c.per + i]) >= static_cast<unsigned>(c.pages);
+  }
   bad = __syncthreads_or(bad);
   const bool ok = fits && !bad;
   if (rank == 0 && tid == 0) {
@@ -290,7 +291,8 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
     if (bad) atomicOr(p.status, ST_PAGE);
     if (h == 0) p.out_ctx[b] = ok ? min(ctx, p.keep) : ctx;
   }
-  if (!ok || ctx <= p.keep) {
+  if (!ok || !moves) {
+#pragma unroll 1
     for (int i = rank * EV_NT + tid; i < p.keep; i += C * EV_NT) index[i] = ok && i < ctx ? i : -1;
     return;
   }
@@ -305,43 +307,45 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 2 ? 10 : 11, down = up - bits;
-      unsigned *const hist = s_hist[pass & 1];
+      unsigned *const hist = s_hist + (pass & 1) * EV_BINS;
       if (pass == 2) {  // the other CTAs have read the first digit's counts before the second digit's barrier
+#pragma unroll 1
         for (int i = tid; i < EV_BINS; i += EV_NT) hist[i] = 0;
         __syncthreads();
       }
 #pragma unroll 1
       for (int from = s0; from < s1; from += EV_SLICE) {
-        if (!one) load(from);
-#pragma unroll
-        for (int i = 0; i < EV_EACH; ++i) {
-          const int s = from + tid * EV_EACH + i;
-          const uint32_t u = weight_key(v[i]);
-          if (s >= lo && s < hi && s < s1 && (pass == 0 || u >> up == key >> up)) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
+        if (!one) {
+          __syncthreads();
+          load(from);
+          __syncthreads();
+        }
+        const int first = max(lo - from, 0), end = min(min(hi, s1) - from, EV_SLICE);
+#pragma unroll 2
+        for (int i = first + tid; i < end; i += EV_NT) {
+          const uint32_t u = weight_key(s_val[i]);
+          if (pass == 0 || u >> up == key >> up) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
         }
       }
       if (joint) cluster_sync();
       else __syncthreads();
       // four bins to a thread, from the top
       const unsigned *mine = &hist[EV_BINS - 4 - 4 * tid];
-      uint4 n = make_uint4(0, 0, 0, 0);
+      uint4 n = *reinterpret_cast<const uint4 *>(mine);
       if (joint) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= C) break;
-          const uint4 x = dsmem_ld_v4(dsmem_addr(mine, i));
+#pragma unroll 2
+        for (int i = 1; i < C; ++i) {
+          const uint4 x = dsmem_ld_v4(dsmem_addr(mine, (rank + i) & (C - 1)));
           n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
         }
-      } else {
-        n = *reinterpret_cast<const uint4 *>(mine);
       }
       const unsigned four = n.x + n.y + n.z + n.w, each[4] = {n.w, n.z, n.y, n.x};
       unsigned sum;
       unsigned above = block_scan<EV_NT / 32>(four, s_scan, sum) - four;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (above < rem && above + each[e] >= rem) s_digit = EV_BINS - 1 - 4 * tid - e, s_rem = rem - above;
-        above += each[e];
+      if (above < rem && above + four >= rem) {
+        int e = 0;
+        while (above + each[e] < rem) above += each[e++];
+        s_digit = EV_BINS - 1 - 4 * tid - e, s_rem = rem - above;
       }
       __syncthreads();
       key |= s_digit << down;
@@ -349,45 +353,75 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       up = down;
     }
   }
-  // in order: all above the key, and the first `rem` of those that equal it
+  // in order: all above the key, and the first `rem` of those that equal it; a
+  // warp's slots are neighbours
   unsigned n_more = 0, n_same = 0;  // before this stretch of slots
 #pragma unroll 1
   for (int from = s0; from < max(s1, s0 + 1); from += EV_SLICE) {
-    if (!one) load(from);
-    unsigned more = 0, same = 0;  // bits of a thread's slots
-#pragma unroll
-    for (int i = 0; i < EV_EACH; ++i) {
-      const int s = from + tid * EV_EACH + i;
-      const uint32_t u = weight_key(v[i]);
-      if (s >= s1) continue;
-      if (s < lo || s >= hi || (some && u > key)) more |= 1u << i;
-      else if (some && u == key) same |= 1u << i;
+    if (!one) {
+      __syncthreads();
+      load(from);
+      __syncthreads();
     }
-    const unsigned both = __popc(more) | __popc(same) << 16;
+    const int n = min(EV_SLICE, s1 - from), part = (n + EV_NT - 1) / EV_NT * 32, w0 = (tid >> 5) * part, w1 = min(w0 + part, n);
+    const auto look = [&](int i, bool &more, bool &same) {
+      const int s = from + i;
+      const uint32_t u = i < w1 ? weight_key(s_val[i]) : 0;
+      const bool given = s < lo || s >= hi;
+      more = i < w1 && (given || (some && u > key));
+      same = i < w1 && !given && some && u == key;
+    };
+    unsigned both = 0;  // of the warp
+#pragma unroll 1
+    for (int i = w0; i < w1; i += 32) {
+      bool more, same;
+      look(i + lane, more, same);
+      both += __popc(__ballot_sync(0xffffffffu, more)) | __popc(__ballot_sync(0xffffffffu, same)) << 16;
+    }
     unsigned sum;
-    const unsigned upto = block_scan<EV_NT / 32>(both, s_scan, sum) - both;  // the stretch's weights have been read
+    const unsigned upto = block_scan<EV_NT / 32>(lane == 0 ? both : 0, s_scan, sum);  // the stretch's weights have been read
     if (joint) {
       if (tid == 0) s_total = sum;
       cluster_sync();
+#pragma unroll 1
       for (int i = 0; i < rank; ++i) {
         const unsigned x = static_cast<unsigned>(dsmem_ld_s32(dsmem_addr(&s_total, i)));
         n_more += x & 0xffffu, n_same += x >> 16;
       }
     }
-    unsigned m = n_more + (upto & 0xffffu), e = n_same + (upto >> 16);
-#pragma unroll
-    for (int i = 0; i < EV_EACH; ++i) {
-      const bool is_more = more >> i & 1, is_same = same >> i & 1;
-      if (is_more || (is_same && e < rem)) {
-        const unsigned pos = m + min(e, rem);
-        index[pos] = from + tid * EV_EACH + i;
-        wts[pos] = v[i];
+    const unsigned start = __shfl_sync(0xffffffffu, upto, 0) - both;
+    unsigned m = n_more + (start & 0xffffu), e = n_same + (start >> 16);
+#pragma unroll 1
+    for (int i = w0; i < w1; i += 32) {
+      bool more, same;
+      look(i + lane, more, same);
+      const unsigned bm = __ballot_sync(0xffffffffu, more), be = __ballot_sync(0xffffffffu, same), below = (1u << lane) - 1;
+      const unsigned mm = m + __popc(bm & below), ee = e + __popc(be & below);
+      if (more || (same && ee < rem)) {
+        const unsigned pos = mm + min(ee, rem);
+        index[pos] = from + i + lane;
+        wts[pos] = s_val[i + lane];
       }
-      m += is_more, e += is_same;
+      m += __popc(bm), e += __popc(be);
     }
     n_more += sum & 0xffffu, n_same += sum >> 16;
   }
   if (joint) cluster_sync();  // no CTA leaves while others read its counts
+}
+
+// A code's magnitude in the upper byte of each half of the result: e4m3 as its
+// seven bits, which are in order; int8 as the absolute value (128 for -128).
+__device__ __forceinline__ uint32_t magnitudes(int kind, uint32_t w, uint32_t sofar) {
+  const uint32_t a = w & 0xff00ff00u, b = w << 8 & 0xff00ff00u;
+  if (kind == KIND_E4M3) {
+    asm("max.u16x2 %0, %0, %1;" : "+r"(sofar) : "r"(a & 0x7f007f00u));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(sofar) : "r"(b & 0x7f007f00u));
+  } else {
+    const uint32_t x = __vabsdiffs2(a, 0), y = __vabsdiffs2(b, 0);
+    asm("max.u16x2 %0, %0, %1;" : "+r"(sofar) : "r"(x));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(sofar) : "r"(y));
+  }
+  return sofar;
 }
 
 // A cluster per kv head, tensor and sequence moves the kept rows together, some
@@ -443,13 +477,14 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
       float m = 0.f;
       if (k < vectors) {
         const uint4 w = s_row[k];
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x[4];
-          decode4(c.kind, u[j], x);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[e]));
+        uint32_t x = magnitudes(c.kind, w.w, magnitudes(c.kind, w.z, magnitudes(c.kind, w.y, magnitudes(c.kind, w.x, 0))));
+        x = max(x & 0xffffu, x >> 16) >> 8;
+        if (c.kind == KIND_E4M3) {
+          float y[4];
+          decode4(KIND_E4M3, x, y);
+          m = x < 0x7f ? y[0] : 448.f;  // a NaN code, which the cache does not have, is as large as any
+        } else {
+          m = static_cast<float>(x);
         }
         m *= s_from[k >> log_row];
       }
@@ -464,11 +499,31 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
       const float scale = scale_for(c.kind, s_amax[blk]), inv = 1.f / scale, from = s_from[row];
       const uint4 w = s_row[k];
       uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      // The same scale, the same codes (-128 is not among them: its block's scale
+      // is larger).  A power of two: e4m3 in fp16, where codes times 2^-14 to 2^15
+      // are exact as far as their rounding to e4m3 can tell; conversions between
+      // 8 and 32 bits would bound the kernel.
+      const float ratio = from * inv;
+      const bool two = ((__float_as_uint(from) | __float_as_uint(ratio)) & 0x7fffffu) == 0 && from >= 0x1p-126f && ratio >= 0x1p-14f && ratio <= 0x1p15f;
+      if (two && ratio == 1.f) {
+      } else if (two && c.kind == KIND_E4M3) {
+        const uint32_t r2 = f32_to_f16x2(ratio, ratio);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[4];
-        decode4(c.kind, u[j], x);
-        u[j] = encode4(c.kind, x[0] * from * inv, x[1] * from * inv, x[2] * from * inv, x[3] * from * inv);
+        for (int j = 0; j < 4; ++j) {
+          asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 x, y;\n\tmov.b32 {a, b}, %0;\n\tcvt.rn.f16x2.e4m3x2 x, a;\n\tcvt.rn.f16x2.e4m3x2 y, b;\n\t"
+              "mul.rn.f16x2 x, x, %1;\n\tmul.rn.f16x2 y, y, %1;\n\t"
+              "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, y;\n\tmov.b32 %0, {a, b};\n\t}"
+              : "+r"(u[j])
+              : "r"(r2));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x[4];
+          decode4(c.kind, u[j], x);
+          if (two) u[j] = encode4_finite(c.kind, x[0], x[1], x[2], x[3], ratio);
+          else u[j] = encode4(c.kind, x[0] * from * inv, x[1] * from * inv, x[2] * from * inv, x[3] * from * inv);
+        }
       }
       const long long id = s_to[blk];
       reinterpret_cast<uint4 *>(codes + (id * c.page + (row & (c.page - 1))) * c.D)[k & last] = make_uint4(u[0], u[1], u[2], u[3]);
