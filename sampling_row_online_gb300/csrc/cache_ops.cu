@@ -460,7 +460,7 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   while (n < 8 && n * EV_SLICE < slots) n *= 2;
   if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, EV_SMEM, stream, &p, "evict_select_kernel launch", n))) return st;
   const int rows = EM_BYTES / p.c.D;
-  n = cluster((keep + rows - 1) / rows, 2 * heads, 5);
+  n = cluster((keep + rows - 1) / rows, 2 * heads, 8);
   return launch_dependent(move, dim3(2 * Hk * n, batch), EM_NT, EM_SMEM, stream, &p, "evict_move_kernel launch", n);
 }
 

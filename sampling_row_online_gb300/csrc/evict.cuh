@@ -237,6 +237,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float key_weight(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
 // A cluster per kv head and sequence finds the k-th largest weight by its
 // digits, 11, 11 and 10 bits from the top (a histogram each, added up through
@@ -251,7 +252,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ unsigned s_scan[EV_NT / 32], s_digit, s_rem, s_total;
-  float *const s_val = reinterpret_cast<float *>(dyn);
+  uint32_t *const s_key = reinterpret_cast<uint32_t *>(dyn);
   unsigned *const s_hist = reinterpret_cast<unsigned *>(dyn) + EV_SLICE;  // two of them
   const CacheView &c = p.c;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
@@ -273,7 +274,10 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
   const auto load = [&](int from) {
     const int n = min(EV_SLICE, s1 - from);
 #pragma unroll 2
-    for (int i = 4 * tid; i < n; i += 4 * EV_NT) *reinterpret_cast<float4 *>(s_val + i) = *reinterpret_cast<const float4 *>(wts + from + i);
+    for (int i = 4 * tid; i < n; i += 4 * EV_NT) {
+      const float4 x = *reinterpret_cast<const float4 *>(wts + from + i);
+      *reinterpret_cast<uint4 *>(s_key + i) = make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+    }
   };
   const bool one = s1 - s0 <= EV_SLICE;
   int bad = 0;
@@ -321,9 +325,9 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
           __syncthreads();
         }
         const int first = max(lo - from, 0), end = min(min(hi, s1) - from, EV_SLICE);
-#pragma unroll 2
+#pragma unroll 4
         for (int i = first + tid; i < end; i += EV_NT) {
-          const uint32_t u = weight_key(s_val[i]);
+          const uint32_t u = s_key[i];
           if (pass == 0 || u >> up == key >> up) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
         }
       }
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
     const int n = min(EV_SLICE, s1 - from), part = (n + EV_NT - 1) / EV_NT * 32, w0 = (tid >> 5) * part, w1 = min(w0 + part, n);
     const auto look = [&](int i, bool &more, bool &same) {
       const int s = from + i;
-      const uint32_t u = i < w1 ? weight_key(s_val[i]) : 0;
+      const uint32_t u = i < w1 ? s_key[i] : 0;
       const bool given = s < lo || s >= hi;
       more = i < w1 && (given || (some && u > key));
       same = i < w1 && !given && some && u == key;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       if (more || (same && ee < rem)) {
         const unsigned pos = mm + min(ee, rem);
         index[pos] = from + i + lane;
-        wts[pos] = s_val[i + lane];
+        wts[pos] = key_weight(s_key[i + lane]);
       }
       m += __popc(bm), e += __popc(be);
     }
@@ -435,6 +439,7 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
   extern __shared__ __align__(16) unsigned char dyn[];  // rows; where they come from; their scales
   __shared__ unsigned s_amax[EM_BLOCKS];
   __shared__ long long s_to[EM_BLOCKS];
+  __shared__ float2 s_scale[EM_BLOCKS];  // and its inverse
   const CacheView &c = p.c;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int b = blockIdx.y, h = blockIdx.x / C >> 1, tensor = blockIdx.x / C & 1, tid = threadIdx.x, lane = tid & 31;
@@ -491,12 +496,18 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
       const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
       if (lane == 0) atomicMax(&s_amax[k0 >> log_row >> c.log_page], largest);
     }
+    __syncthreads();
+    if (tid < blocks) {
+      const float scale = scale_for(c.kind, s_amax[tid]);
+      s_scale[tid] = make_float2(scale, 1.f / scale);
+    }
     if (C > 1) cluster_sync();
     else __syncthreads();
+    if (tid < blocks) scales[s_to[tid]] = s_scale[tid].x;
 #pragma unroll 2
     for (int k = tid; k < vectors; k += EM_NT) {
       const int row = k >> log_row, blk = row >> c.log_page;
-      const float scale = scale_for(c.kind, s_amax[blk]), inv = 1.f / scale, from = s_from[row];
+      const float inv = s_scale[blk].y, from = s_from[row];
       const uint4 w = s_row[k];
       uint32_t u[4] = {w.x, w.y, w.z, w.w};
       // The same scale, the same codes (-128 is not among them: its block's scale
@@ -527,7 +538,6 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
       }
       const long long id = s_to[blk];
       reinterpret_cast<uint4 *>(codes + (id * c.page + (row & (c.page - 1))) * c.D)[k & last] = make_uint4(u[0], u[1], u[2], u[3]);
-      if (k == (blk << c.log_page) << log_row) scales[id] = scale;
     }
     __syncthreads();
   }
