@@ -3,10 +3,12 @@
 //
 //   out_i = sum_{j <= i} softmax(scale q_i . k_j) v_j   in i's own sequence.
 //
-// In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m), with
-// m 8 below a running maximum of x that is at most 7.9 behind, so the largest
-// weight of a row lies in [2^8, 2^15.9]: m moves in the first tile of a row and
-// rarely after it, and fp16 keeps full precision down to 2^-22 of the largest.
+// In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  m is
+// 8 below the maximum of x over a row's first tile, and moves to 8 below the
+// maximum again where the weights of a later tile come to more than 60000
+// together.  So the largest weight of a row lies in [2^8, 60000], fp16 keeps full
+// precision down to 2^-22 of it, and a tile's maximum is looked for only where m
+// moves: its sum tells.
 // What is rounded: weights to the inputs' type before they meet the values (one
 // instruction takes one type; half a step, 2^-8 relative for bf16 and 2^-11 for
 // fp16), and the output, once.  Sums (of the unrounded weights), maxima,
@@ -32,7 +34,7 @@ constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products
 // Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
-constexpr float P_UP = 8.f, P_SLACK = 7.9f;
+constexpr float P_UP = 8.f, P_MOST = 60000.f;
 constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
 
 struct PromptParams {
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
     const uint32_t tS = tmem + lanes + g * PT, tO = tmem + lanes + 256 + g * PT;
     const int tok_in = r / p.G, head_in = r - tok_in * p.G, first_in = 32 * (warp & 3) / p.G;  // first_in: of the warp's first row
     const float f = p.scale_log2;
+    const uint32_t flip = f < 0.f ? 0x80000000u : 0u;
     uint32_t uses = 0;  // tiles of this group
     int seg = 0;
     for (int i = 0; i < count; ++seg) {
@@ -272,27 +275,32 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           const int n = lim + 1 - 32 * q;
           return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
         };
-        float top = NINF;
-        if (j == s0) {  // the largest exponent first
+        const auto largest = [&]() {  // exponent
+          float top = NINF;
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t s[32];
             tmem_ld32(tS + 32 * q, s);
             tc_wait_ld32(s);
             const uint32_t bits = edge ? bits_of(q) : ~0u;
+            if (edge) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = __uint_as_float(s[e]) * f;
-              top = fmaxf(top, bits >> e & 1 ? x : NINF);
+              for (int e = 0; e < 32; ++e)
+                if (bits >> e & 1) top = fmaxf(top, __uint_as_float(s[e] ^ flip));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[e] ^ flip)), __uint_as_float(s[e + 1] ^ flip));
             }
           }
-          m = top - P_UP;
+          return top == NINF ? NINF : top * fabsf(f);  // not 0 * inf
+        };
+        if (j == s0) {
+          m = largest() - P_UP;
           base = m == NINF ? 0.f : m;
         }
         uint32_t pk[64];
-        float sum, hi;
+        float sum;
         const auto weights = [&](auto at_edge) {
-          hi = NINF;
           float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t s[2][32];
           tmem_ld32(tS, s[0]);
@@ -309,7 +317,6 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
                 if (!(bits >> e & 1)) x.x = NINF;
                 if (!(bits >> e & 2)) x.y = NINF;
               }
-              hi = fmaxf(fmaxf(hi, x.x), x.y);
               x.x = ex2(x.x), x.y = ex2(x.y);
               part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
               pk[16 * q + e / 2] = pack2<DT>(x.x, x.y);
@@ -322,9 +329,9 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
         for (;;) {
           if (edge) weights(Flag<true>{});
           else weights(Flag<false>{});
-          // the offset moves only when a weight would pass 2^15.9
-          if (!__any_sync(0xffffffffu, live && hi + base > m + (P_UP + P_SLACK))) break;
-          const float nm = fmaxf(m, hi + base - P_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
+          if (!__any_sync(0xffffffffu, live && sum > P_MOST)) break;
+          // some weight is above 2^8.8: the offset moves
+          const float nm = fmaxf(m, largest() - P_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
           l *= a;
           m = nm, base = nb;
           if (uses != uses0) {  // O holds the products of this segment's earlier tiles
