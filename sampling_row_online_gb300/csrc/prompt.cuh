@@ -30,7 +30,7 @@ namespace spec {
 // token by token; two tiles, A and B, go through the token tiles together.
 constexpr int PT = 128;              // rows of a tile, tokens of a token tile
 constexpr int P_SOFT = 256;          // softmax threads: a thread per row of A and of B
-constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products, B's products, a look at the values
+constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, products, a look at the values; an idle one
 // Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
@@ -137,7 +137,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // index order, so results do not depend on timing.
 //
 //   copies    Q of both row tiles, K and V tiles, as swizzled operands (TMA)
-//   products  a warp per row tile: S = Q K^T, O += P V (P in tensor memory, over S)
+//   products  S = Q K^T, O += P V (P in tensor memory, over S)
 //   softmax   a thread per row: S -> P under the running offset, the output
 //   values    looks for values that are not finite where some row does not see
 //             all of the tile: 0 * inf is not 0.  They are taken out, and marked
@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2);
-      mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 3), mbar_init(&bar.v_seen[i], 1);
+      mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 2), mbar_init(&bar.v_seen[i], 1);
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1);
     }
@@ -514,56 +514,68 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           if (q_uses[g]) one(&bar.q_full[g], (q_uses[g] - 1) & 1);
         lost |= was;
       }
-    } else if (role <= 2) {
+    } else if (role == 1) {
       // ---------------------------------------------------------- products
+      // One thread issues A's and B's in turn: PV of a tile and S of the next
+      // tile for A, then for B.  So one row tile's softmax runs under the other's
+      // products; issued from a warp each, the products mixed, both row tiles
+      // waited for both, and their softmaxes ran at the same time (4300 clocks a
+      // token tile where this takes @@).
       if (lane == 0) {
         constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
         constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
         constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
-        const int g = role - 1;
-        const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * PT;
-        const uint64_t dQ = tc_desc(sm + L::Q + g * L::OP, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
-        uint32_t uses = 0, q_uses = 0, seen[2] = {0, 0};
-        PromptPlace u = at;
-        for (int i = 0; i < count;) {
-          const int s0 = u.j, end = min(u.n, s0 + count - i), n = prompt_group_tiles(p, u, g), mine = min(end, n);
-          if (s0 < mine) one(&bar.q_full[g], q_uses & 1), ++q_uses;
-          for (int j = s0; j < end; ++j, ++i) {
-            const uint32_t s = i & 1, ph = (i >> 1) & 1;
-            const uint64_t dK = dK0 + (s * L::OP >> 4), dV = dV0 + (s * L::OP >> 4);
-            const bool edge = prompt_edge(p, u, j);
-            one(&bar.k_full[s], ph);
-            if (j >= mine) {  // the other row tile's alone
-              mbar_arrive(&bar.k_empty[s]);
-              one(&bar.v_full[s], ph);
-              if (edge) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
-              mbar_arrive(&bar.v_empty[s]);
-              continue;
-            }
-            tc_after_sync();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
-              const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              tc_mma_ss(tS, dQ + off, dK + off, ID_S, k > 0);
-            }
-            tc_commit(&bar.s_full[g]);
-            tc_commit(&bar.k_empty[s]);
-            if (j + 1 == mine) tc_commit(&bar.q_empty[g]);
-            one(&bar.v_full[s], ph);
-            if (edge) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
-            one(&bar.p_full[g], uses & 1);
-            ++uses;
-            tc_after_sync();
-#pragma unroll
-            for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
-              tc_mma_ts(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || j != s0);
-            tc_commit(&bar.o_done[g]);
-            tc_commit(&bar.v_empty[s]);
+        const uint32_t sm = smem_u32(psm);
+        const uint64_t dQ0 = tc_desc(sm + L::Q, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
+        uint32_t uses[2] = {0, 0}, q_uses[2] = {0, 0}, seen[2] = {0, 0};
+        PromptPlace u = at, next = at;
+        int tiles[2] = {0, 0}, coming[2] = {prompt_group_tiles(p, next, 0), prompt_group_tiles(p, next, 1)};  // of tile i's pair, of the next one's
+        for (int i = -1; i < count; ++i) {
+          const uint32_t s = i & 1, t = (i + 1) & 1;
+          const uint64_t dV = dV0 + (s * L::OP >> 4), dK = dK0 + (t * L::OP >> 4);
+          const bool more = i + 1 < count;
+          if (more) one(&bar.k_full[t], ((i + 1) >> 1) & 1);
+          if (i >= 0) {
+            one(&bar.v_full[s], (i >> 1) & 1);
+            if (prompt_edge(p, u, u.j)) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
           }
-          u.j = end;
-          if (i < count) prompt_next(p, u);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t tS = tmem + g * PT, tO = tmem + 256 + g * PT;
+            if (i >= 0 && u.j < tiles[g]) {
+              one(&bar.p_full[g], uses[g] & 1);
+              ++uses[g];
+              tc_after_sync();
+#pragma unroll
+              for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
+                tc_mma_ts(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && u.j > 0));
+              tc_commit(&bar.o_done[g]);
+            }
+            if (i >= 0 && g == 1) tc_commit(&bar.v_empty[s]);
+            if (more && next.j < coming[g]) {
+              if (i < 0 || next.j == 0) one(&bar.q_full[g], q_uses[g] & 1), ++q_uses[g];
+              tc_after_sync();
+              const uint64_t dQ = dQ0 + (g * L::OP >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
+                const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                tc_mma_ss(tS, dQ + off, dK + off, ID_S, k > 0);
+              }
+              tc_commit(&bar.s_full[g]);
+              if (next.j + 1 == coming[g]) tc_commit(&bar.q_empty[g]);
+            }
+            if (more && g == 1) tc_commit(&bar.k_empty[t]);
+          }
+          u = next;
+          tiles[0] = coming[0], tiles[1] = coming[1];
+          if (++next.j == next.n && i + 2 < count) {
+            prompt_next(p, next);
+            coming[0] = prompt_group_tiles(p, next, 0), coming[1] = prompt_group_tiles(p, next, 1);
+          }
         }
       }
+    } else if (role == 2) {
+      // nothing: registers are split by warpgroups
     } else {
       // ------------------------------------------------------------ values
       constexpr uint32_t EXP = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
