@@ -112,8 +112,8 @@ __device__ __forceinline__ int prompt_group_tiles(const PromptParams &p, const P
   const int from = (2 * u.r + g) * p.tile;
   return from >= u.len ? 0 : (min(from + p.tile, u.len) + PT - 1) / PT;
 }
-// Whether some row of the pair does not see all of token tile j.
-__device__ __forceinline__ bool prompt_edge(const PromptParams &p, const PromptPlace &u, int j) { return (j + 1) * PT > 2 * u.r * p.tile + 1; }
+// The first token tile that some row of the pair does not see all of.
+__device__ __forceinline__ int prompt_first_edge(const PromptParams &p, const PromptPlace &u) { return (2 * u.r * p.tile + 1) / PT; }
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -516,62 +516,61 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       }
     } else if (role == 1) {
       // ---------------------------------------------------------- products
-      // One thread issues A's and B's in turn: PV of a tile and S of the next
-      // tile for A, then for B.  So one row tile's softmax runs under the other's
+      // One warp issues A's and B's in turn: PV of a tile and S of the next tile
+      // for A, then for B.  So one row tile's softmax runs under the other's
       // products; issued from a warp each, the products mixed, both row tiles
-      // waited for both, and their softmaxes ran at the same time (4300 clocks a
-      // token tile where this takes @@).
-      if (lane == 0) {
-        constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
-        constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
-        constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
-        const uint32_t sm = smem_u32(psm);
-        const uint64_t dQ0 = tc_desc(sm + L::Q, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
-        uint32_t uses[2] = {0, 0}, q_uses[2] = {0, 0}, seen[2] = {0, 0};
-        PromptPlace u = at, next = at;
-        int tiles[2] = {0, 0}, coming[2] = {prompt_group_tiles(p, next, 0), prompt_group_tiles(p, next, 1)};  // of tile i's pair, of the next one's
-        for (int i = -1; i < count; ++i) {
-          const uint32_t s = i & 1, t = (i + 1) & 1;
-          const uint64_t dV = dV0 + (s * L::OP >> 4), dK = dK0 + (t * L::OP >> 4);
-          const bool more = i + 1 < count;
-          if (more) one(&bar.k_full[t], ((i + 1) >> 1) & 1);
-          if (i >= 0) {
-            one(&bar.v_full[s], (i >> 1) & 1);
-            if (prompt_edge(p, u, u.j)) one(&bar.v_seen[s], seen[s] & 1), ++seen[s];
+      // waited for both, and their softmaxes ran at the same time.
+      constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
+      constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
+      constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
+      const uint32_t sm = smem_u32(psm);
+      const uint64_t dQ0 = tc_desc(sm + L::Q, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
+      uint32_t uses[2] = {0, 0}, q_uses[2] = {0, 0}, seen[2] = {0, 0};
+      PromptPlace next = at;
+      int j = 0, tiles[2] = {0, 0}, coming[2] = {prompt_group_tiles(p, next, 0), prompt_group_tiles(p, next, 1)};  // of tile i's pair, of the next one's
+      int edge = 0, coming_edge = prompt_first_edge(p, next);
+      for (int i = -1; i < count; ++i) {
+        const uint32_t s = i & 1, t = (i + 1) & 1;
+        const uint64_t dV = dV0 + (s * L::OP >> 4), dK = dK0 + (t * L::OP >> 4);
+        const bool more = i + 1 < count;
+        if (more) wait(&bar.k_full[t], ((i + 1) >> 1) & 1);
+        if (i >= 0) {
+          wait(&bar.v_full[s], (i >> 1) & 1);
+          if (j >= edge) wait(&bar.v_seen[s], seen[s] & 1), ++seen[s];
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t tS = tmem + g * PT, tO = tmem + 256 + g * PT;
+          if (i >= 0 && j < tiles[g]) {
+            wait(&bar.p_full[g], uses[g] & 1);
+            ++uses[g];
+            tc_after_sync();
+#pragma unroll
+            for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
+              tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+            tc_commit_warp(&bar.o_done[g]);
           }
+          if (i >= 0 && g == 1) tc_commit_warp(&bar.v_empty[s]);
+          if (more && next.j < coming[g]) {
+            if (i < 0 || next.j == 0) wait(&bar.q_full[g], q_uses[g] & 1), ++q_uses[g];
+            tc_after_sync();
+            const uint64_t dQ = dQ0 + (g * L::OP >> 4);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint32_t tS = tmem + g * PT, tO = tmem + 256 + g * PT;
-            if (i >= 0 && u.j < tiles[g]) {
-              one(&bar.p_full[g], uses[g] & 1);
-              ++uses[g];
-              tc_after_sync();
-#pragma unroll
-              for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
-                tc_mma_ts(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && u.j > 0));
-              tc_commit(&bar.o_done[g]);
+            for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
+              const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+              tc_mma_ss_warp(tS, dQ + off, dK + off, ID_S, k > 0);
             }
-            if (i >= 0 && g == 1) tc_commit(&bar.v_empty[s]);
-            if (more && next.j < coming[g]) {
-              if (i < 0 || next.j == 0) one(&bar.q_full[g], q_uses[g] & 1), ++q_uses[g];
-              tc_after_sync();
-              const uint64_t dQ = dQ0 + (g * L::OP >> 4);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
-                const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                tc_mma_ss(tS, dQ + off, dK + off, ID_S, k > 0);
-              }
-              tc_commit(&bar.s_full[g]);
-              if (next.j + 1 == coming[g]) tc_commit(&bar.q_empty[g]);
-            }
-            if (more && g == 1) tc_commit(&bar.k_empty[t]);
+            tc_commit_warp(&bar.s_full[g]);
+            if (next.j + 1 == coming[g]) tc_commit_warp(&bar.q_empty[g]);
           }
-          u = next;
-          tiles[0] = coming[0], tiles[1] = coming[1];
-          if (++next.j == next.n && i + 2 < count) {
-            prompt_next(p, next);
-            coming[0] = prompt_group_tiles(p, next, 0), coming[1] = prompt_group_tiles(p, next, 1);
-          }
+          if (more && g == 1) tc_commit_warp(&bar.k_empty[t]);
+        }
+        j = next.j;
+        tiles[0] = coming[0], tiles[1] = coming[1], edge = coming_edge;
+        if (++next.j == next.n && i + 2 < count) {
+          prompt_next(p, next);
+          coming[0] = prompt_group_tiles(p, next, 0), coming[1] = prompt_group_tiles(p, next, 1);
+          coming_edge = prompt_first_edge(p, next);
         }
       }
     } else if (role == 2) {
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       for (int i = 0; i < count; ++i) {
         const uint32_t s = i & 1, ph = (i >> 1) & 1;
         wait(&bar.v_full[s], ph);
-        if (prompt_edge(p, u, u.j)) {
+        if (u.j >= prompt_first_edge(p, u)) {
           unsigned char *const tile = psm + L::V + s * L::OP;
           uint32_t most = 0;
 #pragma unroll 8
