@@ -30,7 +30,7 @@ namespace spec {
 // token by token; two tiles, A and B, go through the token tiles together.
 constexpr int PT = 128;              // rows of a tile, tokens of a token tile
 constexpr int P_SOFT = 256;          // softmax threads: a thread per row of A and of B
-constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, products, a look at the values; an idle one
+constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products, B's products, a look at the values
 // Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
@@ -64,6 +64,7 @@ struct PromptLayout {
 
 struct PromptBars {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_seen[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t turn[2];
   uint32_t tmem;
   int marked;                  // 1 + the segment that the marks are of
   int ended[P_SOFT / 32];      // segments that each softmax warp is done with
@@ -206,11 +207,12 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 2), mbar_init(&bar.v_seen[i], 1);
+      mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2);
+      mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 3), mbar_init(&bar.v_seen[i], 1);
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1), mbar_init(&bar.turn[i], 1);
     }
+    mbar_arrive(&bar.turn[0]);  // A begins
     fence_mbar_init();
     bar.marked = 0;
     for (int i = 0; i < P_SOFT / 32; ++i) bar.ended[i] = 0;
@@ -514,67 +516,70 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           if (q_uses[g]) one(&bar.q_full[g], (q_uses[g] - 1) & 1);
         lost |= was;
       }
-    } else if (role == 1) {
+    } else if (role <= 2) {
       // ---------------------------------------------------------- products
-      // One warp issues A's and B's in turn: PV of a tile and S of the next tile
-      // for A, then for B.  So one row tile's softmax runs under the other's
-      // products; issued from a warp each, the products mixed, both row tiles
-      // waited for both, and their softmaxes ran at the same time.
+      // A warp for each row tile.  They take turns: PV of a tile and S of the
+      // next tile for A, then for B, so that one row tile's softmax runs under
+      // the other's products; without turns the products mix, both row tiles
+      // wait for both, and their softmaxes run at the same time.  What a warp
+      // waits for, and its arrivals, pass under the other's products.
       constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
       constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
       constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
-      const uint32_t sm = smem_u32(psm);
-      const uint64_t dQ0 = tc_desc(sm + L::Q, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
-      uint32_t uses[2] = {0, 0}, q_uses[2] = {0, 0}, seen[2] = {0, 0};
+      const int g = role - 1;
+      const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * PT;
+      const uint64_t dQ = tc_desc(sm + L::Q + g * L::OP, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
+      uint32_t uses = 0, q_uses = 0, seen[2] = {0, 0};
       PromptPlace next = at;
-      int j = 0, tiles[2] = {0, 0}, coming[2] = {prompt_group_tiles(p, next, 0), prompt_group_tiles(p, next, 1)};  // of tile i's pair, of the next one's
+      int j = 0, tiles = 0, coming = prompt_group_tiles(p, next, g);  // of tile i's pair, of the next one's
       int edge = 0, coming_edge = prompt_first_edge(p, next);
       for (int i = -1; i < count; ++i) {
         const uint32_t s = i & 1, t = (i + 1) & 1;
         const uint64_t dV = dV0 + (s * L::OP >> 4), dK = dK0 + (t * L::OP >> 4);
-        const bool more = i + 1 < count;
+        const bool more = i + 1 < count, has_v = i >= 0 && j < tiles, has_k = more && next.j < coming;
         if (more) wait(&bar.k_full[t], ((i + 1) >> 1) & 1);
+        if (has_k && (i < 0 || next.j == 0)) wait(&bar.q_full[g], q_uses & 1), ++q_uses;
         if (i >= 0) {
           wait(&bar.v_full[s], (i >> 1) & 1);
           if (j >= edge) wait(&bar.v_seen[s], seen[s] & 1), ++seen[s];
         }
+        if (has_v) wait(&bar.p_full[g], uses & 1), ++uses;
+        wait(&bar.turn[g], (i + 1) & 1);
+        tc_after_sync();
+        if (has_v) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t tS = tmem + g * PT, tO = tmem + 256 + g * PT;
-          if (i >= 0 && j < tiles[g]) {
-            wait(&bar.p_full[g], uses[g] & 1);
-            ++uses[g];
-            tc_after_sync();
-#pragma unroll
-            for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
-              tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
-            tc_commit_warp(&bar.o_done[g]);
-          }
-          if (i >= 0 && g == 1) tc_commit_warp(&bar.v_empty[s]);
-          if (more && next.j < coming[g]) {
-            if (i < 0 || next.j == 0) wait(&bar.q_full[g], q_uses[g] & 1), ++q_uses[g];
-            tc_after_sync();
-            const uint64_t dQ = dQ0 + (g * L::OP >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
-              const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              tc_mma_ss_warp(tS, dQ + off, dK + off, ID_S, k > 0);
-            }
-            tc_commit_warp(&bar.s_full[g]);
-            if (next.j + 1 == coming[g]) tc_commit_warp(&bar.q_empty[g]);
-          }
-          if (more && g == 1) tc_commit_warp(&bar.k_empty[t]);
+          for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
+            tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+          if (j + 1 == tiles || !has_k) tc_commit_warp(&bar.o_done[g]);
         }
-        j = next.j;
-        tiles[0] = coming[0], tiles[1] = coming[1], edge = coming_edge;
+        if (has_k) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
+            const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            tc_mma_ss_warp(tS, dQ + off, dK + off, ID_S, k > 0);
+          }
+        }
+        mbar_arrive_warp(&bar.turn[g ^ 1]);
+        if (has_k) {
+          tc_commit_warp(&bar.s_full[g]);
+          tc_commit_warp(&bar.k_empty[t]);
+          if (next.j + 1 == coming) tc_commit_warp(&bar.q_empty[g]);
+        } else if (more) {
+          mbar_arrive_warp(&bar.k_empty[t]);
+        }
+        if (has_v) {
+          if (j + 1 != tiles && has_k) tc_commit_warp(&bar.o_done[g]);
+          tc_commit_warp(&bar.v_empty[s]);
+        } else if (i >= 0) {
+          mbar_arrive_warp(&bar.v_empty[s]);
+        }
+        j = next.j, tiles = coming, edge = coming_edge;
         if (++next.j == next.n && i + 2 < count) {
           prompt_next(p, next);
-          coming[0] = prompt_group_tiles(p, next, 0), coming[1] = prompt_group_tiles(p, next, 1);
+          coming = prompt_group_tiles(p, next, g);
           coming_edge = prompt_first_edge(p, next);
         }
       }
-    } else if (role == 2) {
-      // nothing: registers are split by warpgroups
     } else {
       // ------------------------------------------------------------ values
       constexpr uint32_t EXP = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
