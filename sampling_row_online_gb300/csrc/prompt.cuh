@@ -409,6 +409,8 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
         tc_before_sync();
         __syncwarp();
         if (live) {
+          if (!any)  // a piece without tiles that this row tile sees
+            for (int k = 0; k < D / 4; ++k) reinterpret_cast<float4 *>(piece)[k * PT + r] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (!whole) piece[PT * D + r] = m, piece[PT * D + PT + r] = l;
           else if (p.lse) p.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -428,32 +430,33 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
             if (live) {
               const auto part = [&](int e) { return p.pieces + ((static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * 2 + g) * L::PIECE; };
               float M = NINF, sum = 0.f;
+#pragma unroll 4
               for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(part(e) + PT * D + r));
-              const float bm = M == NINF ? 0.f : M;
-              for (int e = 0; e < n; ++e) sum = fmaf(ex2(__ldcg(part(e) + PT * D + r) - bm), __ldcg(part(e) + PT * D + PT + r), sum);
-              const float over = 1.f / sum;
 #pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                float z[16];
+              for (int q = 0; q < D / 64; ++q) {  // 64 columns at a time: 16 loads a piece on their way together
+                float4 z[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z[e] = 0.f;
+                for (int k = 0; k < 16; ++k) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                sum = 0.f;
+#pragma unroll 1
                 for (int e = 0; e < n; ++e) {
-                  const float me = __ldcg(part(e) + PT * D + r);
-                  if (me == NINF) continue;  // a piece without tiles that this row sees holds nothing
-                  const float a = ex2(me - bm);
+                  const float *from = part(e);
+                  const float a = ex2(__ldcg(from + PT * D + r) - M), le = __ldcg(from + PT * D + PT + r);  // M: every row sees a token
+                  float4 x[16];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(e)) + (4 * q + k) * PT + r);
-                    z[4 * k] = fmaf(a, x.x, z[4 * k]), z[4 * k + 1] = fmaf(a, x.y, z[4 * k + 1]);
-                    z[4 * k + 2] = fmaf(a, x.z, z[4 * k + 2]), z[4 * k + 3] = fmaf(a, x.w, z[4 * k + 3]);
+                  for (int k = 0; k < 16; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(from) + (16 * q + k) * PT + r);
+                  sum = fmaf(a, le, sum);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    z[k].x = fmaf(a, x[k].x, z[k].x), z[k].y = fmaf(a, x[k].y, z[k].y);
+                    z[k].z = fmaf(a, x[k].z, z[k].z), z[k].w = fmaf(a, x[k].w, z[k].w);
                   }
                 }
+                const float over = 1.f / sum;
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                  float x[8];
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) x[k] = z[e + k] * over;
-                  store8<DT, true>(p.out, orow * D + 16 * q + e, pack8<DT>(x));
+                for (int k = 0; k < 16; k += 2) {
+                  const float x[8] = {z[k].x * over, z[k].y * over, z[k].z * over, z[k].w * over, z[k + 1].x * over, z[k + 1].y * over, z[k + 1].z * over, z[k + 1].w * over};
+                  store8<DT, true>(p.out, orow * D + 64 * q + 4 * k, pack8<DT>(x));
                 }
               }
               if (p.lse) p.lse[orow] = (M + log2f(sum)) * 0.6931471805599453f;
