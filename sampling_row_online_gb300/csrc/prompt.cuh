@@ -4,12 +4,11 @@
 //   out_i = sum_{j <= i} softmax(scale q_i . k_j) v_j   in i's own sequence.
 //
 // In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  m is
-// 9 below the maximum of x over a row's first tile, and moves up by a whole
-// number, to 8 or 9 below the maximum, where the weights of 64 later tokens come
-// to more than 60000 together.  So the largest weight of a row lies in
-// [2^8, 60000], fp16 keeps full precision down to 2^-22 of it, the maximum is
-// looked for only where m moves (the sum tells), and what has been weighed is
-// then scaled by a power of two.
+// 8 below the maximum of x over a row's first tile, and moves to 8 below the
+// maximum again where the weights of a later tile come to more than 60000
+// together.  So the largest weight of a row lies in [2^8, 60000], fp16 keeps full
+// precision down to 2^-22 of it, and a tile's maximum is looked for only where m
+// moves: its sum tells.
 // What is rounded: weights to the inputs' type before they meet the values (one
 // instruction takes one type; half a step, 2^-8 relative for bf16 and 2^-11 for
 // fp16), and the output, once.  Sums (of the unrounded weights), maxima,
@@ -31,9 +30,11 @@ namespace spec {
 // token by token; two tiles, A and B, go through the token tiles together.
 constexpr int PT = 128;              // rows of a tile, tokens of a token tile
 constexpr int P_SOFT = 256;          // softmax threads: a thread per row of A and of B
-constexpr int P_OUT = 128;           // output threads: a thread per row
-constexpr int P_NT = P_SOFT + P_OUT + 128;  // and a warp each for copies, A's products, B's products, a look at the values
-constexpr float P_UP = 9.f, P_MOST = 60000.f;
+constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products, B's products, a look at the values
+// Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
+constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
+static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
+constexpr float P_UP = 8.f, P_MOST = 60000.f;
 constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
 
 struct PromptParams {
@@ -52,23 +53,28 @@ struct PromptParams {
   int32_t *status;
 };
 
+struct PromptLast {  // of the segment whose output is still to be read
+  long long row;
+  int tok, any, live, whole, seg, first, n, which;  // not whole: first CTA of the segment, number of CTAs, the piece's place
+  float m, l;
+};
+
 template <int D>
 struct PromptLayout {
   static constexpr int OP = PT * D * 2;  // an operand tile
-  static constexpr int Q = 0, K = 2 * OP, V = 4 * OP;  // two tiles each
-  static constexpr int MARKS = 6 * OP;           // first tokens with NaN, +inf, -inf in each column
-  static constexpr int ML = MARKS + 3 * D * 4;    // [2][128] (offset, sum) of the rows
-  static constexpr int BARS = ML + 2 * PT * 8;
+  static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, MARKS = 6 * OP;  // two tiles each
+  static constexpr int LAST = MARKS + 3 * D * 4;  // [P_SOFT] PromptLast
+  static constexpr int BARS = LAST + P_SOFT * sizeof(PromptLast);  // MARKS: first tokens with NaN, +inf, -inf in each column
   static constexpr int SMEM = BARS + 256;
   static constexpr int PIECE = PT * D + 2 * PT;  // floats: out, offset, sum
 };
 
 struct PromptBars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_seen[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free[2], ml_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_seen[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
   uint64_t turn[2];
   uint32_t tmem;
   int marked;                  // 1 + the segment that the marks are of
-  int ended[P_OUT / 32];       // segments that each output warp is done with
+  int ended[P_SOFT / 32];      // segments that each softmax warp is done with
 };
 static_assert(sizeof(PromptBars) <= 256, "barriers");
 
@@ -109,11 +115,21 @@ __device__ __forceinline__ void prompt_next(const PromptParams &p, PromptPlace &
   }
   u.n = prompt_pair_tiles(p, u.len, u.r);
 }
-// Token tiles that group g of the pair sees.
+// The first token of row tile g of the pair (from len on where it has none).  A
+// row tile that is alone in its pair goes to A and to B in turn, so that short
+// sequences keep both busy.
+__device__ __forceinline__ int prompt_from(const PromptParams &p, const PromptPlace &u, int g) {
+  const int from = 2 * u.r * p.tile;
+  if (from + p.tile < u.len) return from + g * p.tile;
+  return ((u.h ^ u.b) & 1) == g ? from : u.len;
+}
+// Token tiles that it sees.
 __device__ __forceinline__ int prompt_group_tiles(const PromptParams &p, const PromptPlace &u, int g) {
-  const int from = (2 * u.r + g) * p.tile;
+  const int from = prompt_from(p, u, g);
   return from >= u.len ? 0 : (min(from + p.tile, u.len) + PT - 1) / PT;
 }
+// Tokens of tile j in sixteens: the products stop there.
+__device__ __forceinline__ int prompt_sixteens(const PromptPlace &u, int j) { return (min(PT, u.len - j * PT) + 15) / 16; }
 // The first token tile that some row of the pair does not see all of.
 __device__ __forceinline__ int prompt_first_edge(const PromptParams &p, const PromptPlace &u) { return (2 * u.r * p.tile + 1) / PT; }
 
@@ -122,13 +138,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return DT == DT_BF16 ? f32_to_bf16x2(lo, hi) : f32_to_f16x2(lo, hi);
 }
 
-template <int DT>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  return DT == DT_BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : f16x2_to_f32(w);
-}
 // 64 bytes of a row.  A store instruction takes a clock for each of its 32 rows,
 // so there are two of 32 bytes where the address allows it, not four.
-__device__ __forceinline__ void store64(void *to, const uint32_t (&y)[16], bool wide) {
+__device__ __forceinline__ void store64(void *to, const uint32_t *y, bool wide) {
 #pragma unroll
   for (int i = 0; i < 16; i += 8) {
     uint32_t *at = static_cast<uint32_t *>(to) + i;
@@ -161,8 +173,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 //
 //   copies    Q of both row tiles, K and V tiles, as swizzled operands (TMA)
 //   products  S = Q K^T, O += P V (P in tensor memory, over S)
-//   softmax   a thread per row: S -> P under the running offset
-//   output    a thread per row of A, then of B: O / sum, or a piece, and the joining
+//   softmax   a thread per row: S -> P under the running offset, the output
 //   values    looks for values that are not finite where some row does not see
 //             all of the tile: 0 * inf is not 0.  They are taken out, and marked
 //             with their token, and rows that see them get them at the end.
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   using L = PromptLayout<D>;
   extern __shared__ __align__(1024) unsigned char psm[];
   __shared__ unsigned s_scan[P_NT / 32];
-  __shared__ int s_seq, s_last;
+  __shared__ int s_seq, s_last[2];
   __shared__ unsigned s_base;
   PromptBars &bar = *reinterpret_cast<PromptBars *>(psm + L::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -234,14 +245,13 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 3), mbar_init(&bar.v_seen[i], 1);
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_done[i], 1), mbar_init(&bar.turn[i], 1);
-      mbar_init(&bar.o_free[i], P_OUT / 32), mbar_init(&bar.ml_full[i], 4);
     }
     mbar_arrive(&bar.turn[0]);  // A begins
     fence_mbar_init();
     bar.marked = 0;
-    for (int i = 0; i < P_OUT / 32; ++i) bar.ended[i] = 0;
+    for (int i = 0; i < P_SOFT / 32; ++i) bar.ended[i] = 0;
   }
-  if (warp == (P_SOFT + P_OUT) / 32) tmem_alloc(&bar.tmem, 512);
+  if (warp == P_SOFT / 32) tmem_alloc(&bar.tmem, 512);
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
@@ -271,281 +281,300 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   const auto wait = [&](uint64_t *b, uint32_t parity) {  // warp-wide
     if (!lost && !__all_sync(0xffffffffu, tile_wait<0>(b, parity))) lost = true;
   };
-  const auto lazy_wait = [&](uint64_t *b, uint32_t parity) {  // where latency hides: polls take issue slots from the softmax
+  const auto wait2 = [&](uint64_t *b, uint32_t parity, uint64_t *c, uint32_t parity_c) {  // both: the polls overlap
+    if (lost) return;
+    bool done = false;
+#pragma unroll 1
+    for (int polls = 0; polls < 1 << 20 && !done; ++polls) {
+      const bool x = mbar_try_wait(b, parity), y = mbar_try_wait(c, parity_c);
+      done = __all_sync(0xffffffffu, x && y);
+    }
+    lost = !done;
+  };
+  const auto lazy_wait = [&](uint64_t *b, uint32_t parity) {  // where latency hides
     if (!lost && !__all_sync(0xffffffffu, tile_wait<100>(b, parity))) lost = true;
   };
   const auto one = [&](uint64_t *b, uint32_t parity) {  // a single thread
-    if (!lost && !tile_wait<100>(b, parity)) lost = true;
+    if (!lost && !tile_wait<0>(b, parity)) lost = true;
   };
 
   if (warp < P_SOFT / 32) {
     // ------------------------------------------------------------ softmax
+    more_registers<P_REG_SOFT>();
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
     const uint32_t tS = tmem + lanes + g * PT, tO = tmem + lanes + 256 + g * PT;
-    const int tok_in = r / p.G, first_in = 32 * (warp & 3) / p.G;  // first_in: of the warp's first row
+    const int tok_in = r / p.G, head_in = r - tok_in * p.G, first_in = 32 * (warp & 3) / p.G;  // first_in: of the warp's first row
     // scores times f; a scale of zero as the least number, so that a hidden
     // column's infinite score stays infinite
     const float f = p.scale_log2 == 0.f ? __uint_as_float(1u) : p.scale_log2;
     const uint32_t flip = f < 0.f ? 0x80000000u : 0u, hidden = 0xff800000u ^ flip;
-    float2 *const ml = reinterpret_cast<float2 *>(psm + L::ML) + g * PT + r;
-    uint32_t uses = 0, parts = 0;  // tiles, and segments' parts, of this group
-    for (int i = 0; i < count;) {
-      const int s0 = at.j, end = min(at.n, s0 + count - i), mine = min(end, prompt_group_tiles(p, at, g));  // tiles s0 .. mine - 1
-      const int from = (2 * at.r + g) * p.tile, tok = from + tok_in;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+    uint32_t uses = 0;  // tiles of this group
+    // The output of a segment waits for its last products, so it is read only
+    // after the next segment's first weights have been made, and written while
+    // the products with them run.
+    // What it takes then lies in shared memory.
+    PromptLast &last = reinterpret_cast<PromptLast *>(psm + L::LAST)[tid];
+    bool there = false;
+    // `between` runs as soon as O has been read.
+    const auto output = [&](auto between) {
+      const bool any = last.any;  // it had tiles
+      const int *mark = reinterpret_cast<const int *>(psm + L::MARKS);
+      if (any) {
+        wait(&bar.o_done[g], (uses - 1) & 1);
+        tc_after_sync();
+      }
+      const bool marked = *reinterpret_cast<const volatile int *>(&bar.marked) == last.seg + 1;
+      const float inv = last.whole ? 1.f / last.l : 1.f;
+      if (any && last.whole && !marked) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t ob[32];  // the output's row in its type
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + c + 32 * q, o);
+            tc_wait_ld32(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ob[16 * q + e] = pack2<DT>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          }
+          tc_before_sync();
+          if (c + 64 == D) between();
+          if (last.live)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) store64(static_cast<uint16_t *>(p.out) + last.row * D + c + 32 * q, ob + 16 * q, wide);
+          __syncwarp();
+        }
+      } else if (any) {
+        float *const piece = p.pieces + ((static_cast<long long>(blockIdx.x) * 2 + last.which) * 2 + g) * L::PIECE;
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t o[16];
+          __syncwarp();
+          tmem_ld16(tO + 16 * q, o);
+          tc_wait_ld(o);
+          float z[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            z[e] = __uint_as_float(o[e]) * inv;
+            if (marked) {  // values that are not finite, for the rows that see them
+              const int d = 16 * q + e;
+              if (last.tok >= mark[D + d]) z[e] += INFINITY;
+              if (last.tok >= mark[2 * D + d]) z[e] -= INFINITY;
+              if (last.tok >= mark[d]) z[e] = QNAN;
+            }
+          }
+          if (!last.live) continue;
+          if (last.whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              const float x[8] = {z[e], z[e + 1], z[e + 2], z[e + 3], z[e + 4], z[e + 5], z[e + 6], z[e + 7]};
+              store8<DT, true>(p.out, last.row * D + 16 * q + e, pack8<DT>(x));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              reinterpret_cast<float4 *>(piece)[(4 * q + e / 4) * PT + r] = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+          }
+        }
+        tc_before_sync();
+        between();
+      } else {
+        between();
+      }
+      float *const piece = p.pieces + ((static_cast<long long>(blockIdx.x) * 2 + last.which) * 2 + g) * L::PIECE;
+      if (last.live) {
+        if (last.whole) {
+          if (p.lse) p.lse[last.row] = (last.m + log2f(last.l)) * 0.6931471805599453f;
+        } else {
+          if (!any)  // nothing that this row tile sees
+            for (int k = 0; k < D / 4; ++k) reinterpret_cast<float4 *>(piece)[k * PT + r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          piece[PT * D + r] = last.m, piece[PT * D + PT + r] = last.l;
+        }
+      }
+      if (!last.whole) {
+        // a segment that several CTAs share: the last to arrive joins, in order
+        const int c0 = last.first, n = last.n;
+        __threadfence();
+        named_sync(1 + g, 128);
+        if (r == 0) {
+          s_last[g] = atomicAdd(p.done + 2 * c0 + g, 1) == n - 1;
+          __threadfence();
+        }
+        named_sync(1 + g, 128);
+        if (*reinterpret_cast<volatile int *>(&s_last[g])) {
+          __threadfence();
+          if (last.live) {
+            const auto part = [&](int e) { return p.pieces + ((static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * 2 + g) * L::PIECE; };
+            float M = NINF, sum = 0.f;
+#pragma unroll 4
+            for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(part(e) + PT * D + r));
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {  // 32 columns at a time: eight loads a piece, of two pieces, on their way together
+              float4 z[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              sum = 0.f;
+#pragma unroll 2
+              for (int e = 0; e < n; ++e) {
+                const float *from = part(e);
+                const float a = ex2(__ldcg(from + PT * D + r) - M), le = __ldcg(from + PT * D + PT + r);  // M: every row sees a token
+                float4 x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(from) + (8 * q + k) * PT + r);
+                sum = fmaf(a, le, sum);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  z[k].x = fmaf(a, x[k].x, z[k].x), z[k].y = fmaf(a, x[k].y, z[k].y);
+                  z[k].z = fmaf(a, x[k].z, z[k].z), z[k].w = fmaf(a, x[k].w, z[k].w);
+                }
+              }
+              const float over = 1.f / sum;
+              uint32_t y[16];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[2 * k] = pack2<DT>(z[k].x * over, z[k].y * over), y[2 * k + 1] = pack2<DT>(z[k].z * over, z[k].w * over);
+              store64(static_cast<uint16_t *>(p.out) + last.row * D + 32 * q, y, wide);
+            }
+            if (p.lse) p.lse[last.row] = (M + log2f(sum)) * 0.6931471805599453f;
+          }
+          if (r == 0) p.done[2 * c0 + g] = 0;  // zero again for the next call
+        }
+        named_sync(1 + g, 128);  // s_last may be written again
+      }
+      there = false;
+    };
+    const auto ended = [&](int seg) {  // segments that are done with
+      __syncwarp();
+      if (lane == 0) *reinterpret_cast<volatile int *>(&bar.ended[warp]) = seg;
+    };
+    for (int i = 0, seg = 0;; ++seg) {
+      // tiles s0 .. mine - 1; after the last segment none, to write the last output
+      const bool over = i >= count;
+      const int s0 = over ? 0 : at.j, end = over ? 0 : min(at.n, s0 + count - i), mine = over ? 0 : min(end, prompt_group_tiles(p, at, g));
+      const int from = prompt_from(p, at, g), tok = from + tok_in;
       const bool live = tok_in < p.tile && tok < at.len;
       float m = NINF, base = 0.f, l = 0.f;
-      for (int j = s0; j < mine; ++j, ++uses) {
+      const uint32_t uses0 = uses;
+      for (int j = s0; j < mine || there; ++j) {
+        const auto weighed = [&]() {
+          __syncwarp();
+          if (j < mine && lane == 0) mbar_arrive(&bar.p_full[g]);
+        };
+        if (j < mine) {
         wait(&bar.s_full[g], uses & 1);
         tc_after_sync();
-        const bool edge = from + first_in < j * PT + PT - 1;  // a row of the warp does not see all columns
-        const int lim = tok - j * PT;                         // the last one that this row sees
-        const auto hide = [&](uint32_t (&s)[16], int q) {
-          if (edge)
+        const int lim = tok - j * PT;  // the last column that the row sees
+        const bool edge = from + first_in < j * PT + PT - 1;
+        const auto hide = [&](uint32_t (&s)[32], int q) {
+          if (__builtin_expect(edge, 0)) {
+            const int n = lim + 1 - 32 * q;
+            const uint32_t bits = n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;  // the columns that the row sees
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e > lim - 16 * q) s[e] = hidden;
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1)) s[e] = hidden;
+          }
         };
-        const auto largest = [&](int from, int to) {  // exponent of these columns (sixteenths)
+        const auto largest = [&]() {  // exponent
           float top = NINF;
-#pragma unroll 2
-          for (int q = from; q < to; ++q) {
-            uint32_t s[16];
-            tmem_ld16(tS + 16 * q, s);
-            tc_wait_ld(s);
+#pragma unroll 1
+          for (int q = 0; 32 * q < at.len - j * PT && q < 4; ++q) {
+            uint32_t s[32];
+            tmem_ld32(tS + 32 * q, s);
+            tc_wait_ld32(s);
             hide(s, q);
+            if (flip) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[e] ^ flip)), __uint_as_float(s[e + 1] ^ flip));
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e] ^ 0x80000000u));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
+            }
           }
           return top * fabsf(f);
         };
         if (j == s0) {
-          m = largest(0, PT / 16) - P_UP;
+          m = largest() - P_UP;
           base = m == NINF ? 0.f : m;
         }
-        uint32_t s[2][16];
-        tmem_ld16(tS, s[0]);
-        // half of the columns at a time: scores -> weights, over scores that have
-        // been read; the next columns are on their way
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-          float sum;
-#pragma unroll 1
-          for (;;) {
-            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[64];
+        float sum;
+        const auto weights = [&]() {
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t s[2][32];
+          tmem_ld32(tS, s[0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int q = 4 * half + i;
-              tc_wait_ld(s[i & 1]);
-              if (i < 3 || half == 0) tmem_ld16(tS + 16 * (q + 1), s[(i + 1) & 1]);
-              hide(s[i & 1], q);
+          for (int q = 0; q < 4; ++q) {
+            tc_wait_ld32(s[q & 1]);
+            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
+            hide(s[q & 1], q);
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float2 x = fma2(make_float2(__uint_as_float(s[i & 1][e]), __uint_as_float(s[i & 1][e + 1])), make_float2(f, f), make_float2(-base, -base));
-                x.x = ex2(x.x), x.y = ex2(x.y);
-                part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
-                pk[8 * i + e / 2] = pack2<DT>(x.x, x.y);
-              }
+            for (int e = 0; e < 32; e += 2) {
+              float2 x = fma2(make_float2(__uint_as_float(s[q & 1][e]), __uint_as_float(s[q & 1][e + 1])), make_float2(f, f), make_float2(-base, -base));
+              x.x = ex2(x.x), x.y = ex2(x.y);
+              part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
+              pk[16 * q + e / 2] = pack2<DT>(x.x, x.y);
             }
-            const float2 both = add2(part[0], part[1]);
-            sum = both.x + both.y;
-            if (!__any_sync(0xffffffffu, live && sum > P_MOST)) break;
-            // some weight is above 2^9.8: the offset moves, and all weights so far are scaled
-            const float up = ceilf(largest(4 * half, 4 * half + 4) - P_UP - m);
-            const float a = !(up > 0.f) ? 1.f : up < 127.f ? __uint_as_float(static_cast<uint32_t>(127.f - up) << 23) : 0.f;
-            if (up > 0.f) m += up, base = m;
-            l *= a;
-            if (j > s0) {  // O holds the products of this segment's earlier tiles
-              wait(&bar.o_done[g], (uses - 1) & 1);
-              tc_after_sync();
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * c, o);
-                tc_wait_ld(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                tmem_st16(tO + 16 * c, o);
-              }
-            }
-            tc_wait_st();
-#pragma unroll 1
-            for (int c = 0; c < 2 * half; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tS + 16 * c, o);
-              tc_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 x = unpack2<DT>(o[e]);
-                o[e] = pack2<DT>(x.x * a, x.y * a);
-              }
-              tmem_st16(tS + 16 * c, o);
-            }
-            tmem_ld16(tS + 64 * half, s[0]);
           }
-          l += sum;
-          tmem_st16(tS + 32 * half, pk);
-          tmem_st16(tS + 32 * half + 16, pk + 16);
+          const float2 both = add2(part[0], part[1]);
+          sum = both.x + both.y;
+        };
+#pragma unroll 1
+        for (;;) {
+          weights();
+          if (__builtin_expect(!__any_sync(0xffffffffu, live && sum > P_MOST), 1)) break;
+          // some weight is above 2^8.8: the offset moves
+          const float nm = fmaxf(m, largest() - P_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
+          l *= a;
+          m = nm, base = nb;
+          if (uses != uses0) {  // O holds the products of this segment's earlier tiles
+            wait(&bar.o_done[g], (uses - 1) & 1);
+            tc_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * q, o);
+              tc_wait_ld32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st16(tO + 32 * q, o);
+              tmem_st16(tO + 32 * q + 16, o + 16);
+            }
+          }
         }
+        l += sum;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(tS + 16 * q, pk + 16 * q);  // weights over scores that have been read
         tc_wait_st();
         tc_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[g]);
+        }
+        if (__builtin_expect(!there, 1)) {
+          weighed();
+        } else {
+          output(weighed);
+          ended(seg);
+        }
+        if (j < mine) ++uses;
       }
-      if (mine > s0) {  // the output's part: offset and sum
-        if (parts) wait(&bar.o_free[g], (parts - 1) & 1);
-        ++parts;
-        *ml = make_float2(m, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ml_full[g]);
+      if (over) break;
+      // ---- the end of the segment
+      last.any = mine > s0, last.live = live, last.whole = s0 == 0 && end == at.n;
+      last.seg = seg, last.tok = tok, last.which = s0 > 0 ? 0 : 1;
+      last.m = m, last.l = l;
+      last.row = static_cast<long long>(at.start + tok) * p.Hq + at.h * p.G + head_in;
+      if (!last.whole) {
+        const unsigned f0 = my0 + i - s0;
+        last.first = share.holder(f0);
+        last.n = static_cast<int>(share.holder(f0 + at.n - 1)) - last.first + 1;
       }
-      i += end - s0;
-      if (i < count) prompt_next(p, at);
-    }
-  } else if (warp < (P_SOFT + P_OUT) / 32) {
-    // ------------------------------------------------------------- output
-    // under the next segment's first tile: O is free as soon as it has been read
-    const int r = tid & 127;
-    const int tok_in = r / p.G, head_in = r - tok_in * p.G;
-    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-    const int *mark = reinterpret_cast<const int *>(psm + L::MARKS);
-    uint32_t uses[2] = {0, 0}, parts[2] = {0, 0};
-    int seg = 0;
-    for (int i = 0; i < count; ++seg) {
-      const int s0 = at.j, end = min(at.n, s0 + count - i);
-      const bool whole = s0 == 0 && end == at.n;
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t tO = tmem + (static_cast<uint32_t>(warp & 3) << 21) + 256 + g * PT;
-        const int from = (2 * at.r + g) * p.tile, tok = from + tok_in, mine = min(end, prompt_group_tiles(p, at, g));
-        if (from >= at.len) continue;
-        const bool any = mine > s0, live = tok_in < p.tile && tok < at.len;
-        float m = NINF, l = 0.f;
-        bool marked = false;
-        if (any) {
-          if (g) uses[1] += mine - s0;
-          else uses[0] += mine - s0;
-          lazy_wait(&bar.ml_full[g], (g ? parts[1] : parts[0]) & 1);
-          if (g) ++parts[1];
-          else ++parts[0];
-          const float2 x = reinterpret_cast<const float2 *>(psm + L::ML)[g * PT + r];
-          m = x.x, l = x.y;
-          lazy_wait(&bar.o_done[g], ((g ? uses[1] : uses[0]) - 1) & 1);
-          tc_after_sync();
-          marked = *reinterpret_cast<const volatile int *>(&bar.marked) == seg + 1;
-        }
-        const long long orow = static_cast<long long>(at.start + tok) * p.Hq + at.h * p.G + head_in;
-        const int which = s0 > 0 ? 0 : 1;
-        float *const piece = p.pieces + ((static_cast<long long>(blockIdx.x) * 2 + which) * 2 + g) * L::PIECE;
-        const float inv = whole ? 1.f / l : 1.f;
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          __syncwarp();
-          if (any) {
-            tmem_ld32(tO + 32 * q, o);
-            tc_wait_ld32(o);
-            if (q == D / 32 - 1) {
-              tc_before_sync();
-              __syncwarp();
-              if ((tid & 31) == 0) mbar_arrive(&bar.o_free[g]);
-            }
-          } else {  // a piece without tiles that this row tile sees
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
-          float z[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(o[e]) * inv;
-          if (marked) {  // values that are not finite, for the rows that see them
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
-              const int d = 32 * q + e;
-              float x = 0.f;
-              if (tok >= mark[D + d]) x += INFINITY;
-              if (tok >= mark[2 * D + d]) x -= INFINITY;
-              if (tok >= mark[d]) x = QNAN;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k == e) z[k] += x;
-            }
-          }
-          if (live) {
-            if (whole) {
-              uint32_t y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = pack2<DT>(z[2 * e], z[2 * e + 1]);
-              store64(static_cast<uint16_t *>(p.out) + orow * D + 32 * q, y, wide);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                reinterpret_cast<float4 *>(piece)[(8 * q + e / 4) * PT + r] = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
-            }
-          }
-        }
-        if (live) {
-          if (!whole) piece[PT * D + r] = m, piece[PT * D + PT + r] = l;
-          else if (p.lse) p.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
-        }
-        if (!whole) {
-          // a segment that several CTAs share: the last to arrive joins, in order
-          __threadfence();
-          named_sync(1, P_OUT);
-          const unsigned f0 = my0 + i - s0;
-          const int c0 = share.holder(f0), n = static_cast<int>(share.holder(f0 + at.n - 1)) - c0 + 1;
-          if (r == 0) {
-            s_last = atomicAdd(p.done + 2 * c0 + g, 1) == n - 1;
-            __threadfence();
-          }
-          named_sync(1, P_OUT);
-          if (*reinterpret_cast<volatile int *>(&s_last)) {
-            __threadfence();
-            if (live) {
-              const auto part = [&](int e) { return p.pieces + ((static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * 2 + g) * L::PIECE; };
-              float M = NINF, sum = 0.f;
-#pragma unroll 4
-              for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(part(e) + PT * D + r));
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {  // 32 columns at a time: eight loads a piece, two pieces, on their way together
-                float4 z[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                sum = 0.f;
-#pragma unroll 2
-                for (int e = 0; e < n; ++e) {
-                  const float *at = part(e);
-                  const float a = ex2(__ldcg(at + PT * D + r) - M), le = __ldcg(at + PT * D + PT + r);  // M: every row sees a token
-                  float4 x[8];
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(at) + (8 * q + k) * PT + r);
-                  sum = fmaf(a, le, sum);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    z[k].x = fmaf(a, x[k].x, z[k].x), z[k].y = fmaf(a, x[k].y, z[k].y);
-                    z[k].z = fmaf(a, x[k].z, z[k].z), z[k].w = fmaf(a, x[k].w, z[k].w);
-                  }
-                }
-                const float over = 1.f / sum;
-                uint32_t y[16];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[2 * k] = pack2<DT>(z[k].x * over, z[k].y * over), y[2 * k + 1] = pack2<DT>(z[k].z * over, z[k].w * over);
-                store64(static_cast<uint16_t *>(p.out) + orow * D + 32 * q, y, wide);
-              }
-              if (p.lse) p.lse[orow] = (M + log2f(sum)) * 0.6931471805599453f;
-            }
-            if (r == 0) p.done[2 * c0 + g] = 0;  // zero again for the next call
-          }
-          named_sync(1, P_OUT);  // s_last may be written again
-        }
-      }
-      __syncwarp();
-      if (lane == 0) *reinterpret_cast<volatile int *>(&bar.ended[warp & 3]) = seg + 1;
+      there = last.any || (from < at.len && !last.whole);
+      if (!there) ended(seg + 1);
       i += end - s0;
       if (i < count) prompt_next(p, at);
     }
   } else {
-    const int role = warp - (P_SOFT + P_OUT) / 32;
+    fewer_registers<P_REG_REST>();
+    const int role = warp - P_SOFT / 32;
     if (role == 0) {
       // ------------------------------------------------------------ copies
       if (lane == 0) {
@@ -572,7 +601,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
               mbar_arrive_expect_tx(&bar.q_full[g], q_bytes);
 #pragma unroll
               for (int x = 0; x < D / 64; ++x)
-                tma_load(sm + L::Q + g * L::OP + x * 16384, &p.q, 64 * x, 0, u.h, u.start + (2 * u.r + g) * p.tile, &bar.q_full[g]);
+                tma_load(sm + L::Q + g * L::OP + x * 16384, &p.q, 64 * x, 0, u.h, u.start + prompt_from(p, u, g), &bar.q_full[g]);
             }
           if (!lost) one(&bar.v_empty[s], ph ^ 1);
           if (lost) {
@@ -601,14 +630,14 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       // wait for both, and their softmaxes run at the same time.  What a warp
       // waits for, and its arrivals, pass under the other's products.
       constexpr uint32_t TYPE = DT == DT_BF16 ? 1u << 7 | 1u << 10 : 0u;
-      constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 8) << 17 | (PT / 16) << 24;
+      constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 16) << 24;  // without the columns
       constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
       const int g = role - 1;
       const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * PT;
       const uint64_t dQ = tc_desc(sm + L::Q + g * L::OP, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
-      uint32_t uses = 0, q_uses = 0, parts = 0, seen[2] = {0, 0};
+      uint32_t uses = 0, q_uses = 0, seen[2] = {0, 0};
       PromptPlace next = at;
-      int j = 0, tiles = 0, coming = prompt_group_tiles(p, next, g);  // of tile i's pair, of the next one's
+      int j = 0, sixteens = 0, tiles = 0, coming = prompt_group_tiles(p, next, g);  // of tile i's pair, of the next one's
       int edge = 0, coming_edge = prompt_first_edge(p, next);
       for (int i = -1; i < count; ++i) {
         const uint32_t s = i & 1, t = (i + 1) & 1;
@@ -620,27 +649,29 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           wait(&bar.v_full[s], (i >> 1) & 1);
           if (j >= edge) wait(&bar.v_seen[s], seen[s] & 1), ++seen[s];
         }
-        if (has_v) {
-          if (i == 0 || j == 0) {  // O of the part before has been read
-            if (parts) wait(&bar.o_free[g], (parts - 1) & 1);
-            ++parts;
-          }
-          wait(&bar.p_full[g], uses & 1);
-          ++uses;
-        }
-        wait(&bar.turn[g], (i + 1) & 1);
+        if (has_v) wait2(&bar.turn[g], (i + 1) & 1, &bar.p_full[g], uses & 1), ++uses;
+        else wait(&bar.turn[g], (i + 1) & 1);
         tc_after_sync();
         if (has_v) {
+          if (sixteens == PT / 16) {
 #pragma unroll
-          for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
-            tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+            for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
+              tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < sixteens; ++k) tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+          }
           if (j + 1 == tiles || !has_k) tc_commit_warp(&bar.o_done[g]);
         }
+        sixteens = prompt_sixteens(next, next.j);
         if (has_k) {
+          const auto off = [](int k) -> uint64_t { return ((k >> 2) * 16384 + (k & 3) * 32) >> 4; };  // 32 bytes of the rows at a time, 16384 between panels
+          if (sixteens == PT / 16) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {  // 32 bytes of the rows at a time, 16384 between panels
-            const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            tc_mma_ss_warp(tS, dQ + off, dK + off, ID_S, k > 0);
+            for (int k = 0; k < D / 16; ++k) tc_mma_ss_warp(tS, dQ + off(k), dK + off(k), ID_S | (PT / 8) << 17, k > 0);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) tc_mma_ss_warp(tS, dQ + off(k), dK + off(k), ID_S | static_cast<uint32_t>(2 * sixteens) << 17, k > 0);
           }
         }
         mbar_arrive_warp(&bar.turn[g ^ 1]);
@@ -675,10 +706,14 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
         lazy_wait(&bar.v_full[s], ph);
         if (u.j >= prompt_first_edge(p, u)) {
           unsigned char *const tile = psm + L::V + s * L::OP;
+          // rows that are not seen by all, up to where the products stop
+          const int r0 = max(0, 2 * u.r * p.tile + 1 - u.j * PT), r1 = 16 * prompt_sixteens(u, u.j);
           uint32_t most = 0;
-#pragma unroll 8
-          for (int k = 0; k < L::OP / 512; ++k) {
-            const uint4 x = lds128(tile + (k * 32 + lane) * 16);
+          const unsigned char *from = tile + lane / 8 % (D / 64) * 16384 + lane % 8 * 16;
+          constexpr int STEP = 256 / D;  // rows at a time
+#pragma unroll 4
+          for (int row = r0 + lane / (D / 8); row < r1; row += STEP) {
+            const uint4 x = lds128(from + row * 128);
             asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.x & 0x7fff7fffu));
             asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.y & 0x7fff7fffu));
             asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(x.z & 0x7fff7fffu));
@@ -687,7 +722,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           if (__any_sync(0xffffffffu, (most & 0xffffu) >= EXP || (most >> 16) >= EXP)) {
             volatile int *const marked = &bar.marked, *const ended = bar.ended;
             if (*marked != seg + 1) {  // the marks of an earlier segment may still be read
-              for (int polls = 0; !lost && !__all_sync(0xffffffffu, ended[lane % (P_OUT / 32)] >= seg); ++polls) {
+              for (int polls = 0; !lost && !__all_sync(0xffffffffu, ended[lane % (P_SOFT / 32)] >= seg); ++polls) {
                 __nanosleep(100);
                 lost = polls > 1 << 18;
               }
@@ -731,7 +766,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   if (lost) atomicOr(p.status, ST_TIMEOUT);
   tc_before_sync();
   __syncthreads();
-  if (warp == (P_SOFT + P_OUT) / 32) {
+  if (warp == P_SOFT / 32) {
     tc_after_sync();
     tmem_free(tmem, 512);
   }
