@@ -35,6 +35,7 @@ constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
 constexpr float P_UP = 8.f, P_MOST = 60000.f;
+constexpr int P_SHORT = 16;          // token tiles of segments that are not shared between CTAs
 constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
 
 struct PromptParams {
@@ -182,8 +183,8 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   using L = PromptLayout<D>;
   extern __shared__ __align__(1024) unsigned char psm[];
   __shared__ unsigned s_scan[P_NT / 32];
-  __shared__ int s_seq, s_last[2];
-  __shared__ unsigned s_base;
+  __shared__ int s_seq[2], s_last[2];
+  __shared__ unsigned s_base[2];
   PromptBars &bar = *reinterpret_cast<PromptBars *>(psm + L::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float NINF = __uint_as_float(0xff800000u), QNAN = __uint_as_float(0x7fc00000u);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   pdl_launch_dependents();
 
   // ---- the list of all work, and this CTA's stretch of it
-  int wrong = 0;
+  int wrong = 0, longer = 0;
   const auto work_of = [&](int b) -> unsigned {
     if (b >= p.B) return 0;
     const int s = p.starts[b], e = p.starts[b + 1];
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       wrong = 1;
       return 0;
     }
+    longer |= e - s > P_SHORT * PT;
     return prompt_head_tiles(p, e - s) * p.heads;
   };
   unsigned total = 0, w = 0, upto = 0;  // upto: of all sequences up to this thread's (of the last block of them)
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   }
   if (p.B == 0 && (p.starts[0] < 0 || p.starts[0] > p.T)) wrong = 1;
   wrong = __syncthreads_or(wrong);
+  const bool shared = __syncthreads_or(longer);
   {  // rows of no sequence
     const long long row = static_cast<long long>(p.Hq) * D / 8, lo = wrong ? 0 : p.starts[0], hi = wrong ? 0 : p.starts[p.B];
     const float v = wrong ? QNAN : 0.f, x[8] = {v, v, v, v, v, v, v, v};
@@ -226,8 +229,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   const unsigned nc = wrong ? 0 : min(gridDim.x, total);
   if (blockIdx.x >= nc) return;
   const Share share(total, nc);
-  const unsigned my0 = share.start(blockIdx.x);
-  const int count = static_cast<int>(share.start(blockIdx.x + 1) - my0);
+  const unsigned cut[2] = {share.start(blockIdx.x), share.start(blockIdx.x + 1)};
   unsigned before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += P_NT) {
@@ -237,8 +239,48 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       upto = before + block_scan<P_NT / 32>(w, s_scan, sum);
       before += sum;
     }
-    if (my0 < upto && my0 >= upto - w) s_seq = b0 + tid, s_base = upto - w;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (cut[e] < upto && cut[e] >= upto - w) s_seq[e] = b0 + tid, s_base[e] = upto - w;
   }
+  __syncthreads();
+  const auto place_of = [&](int b, unsigned r) {  // tile r of sequence b's
+    PromptPlace u;
+    u.b = b;
+    prompt_enter(p, u);
+    const unsigned head = prompt_head_tiles(p, u.len);
+    u.h = static_cast<int>(r / head);
+    r -= u.h * head;
+    int lo = 0, hi = (u.len + 2 * p.tile - 1) / (2 * p.tile);  // the last pair that starts at or before tile r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prompt_tiles_before(p, mid) <= r) lo = mid;
+      else hi = mid;
+    }
+    u.r = lo;
+    u.n = prompt_pair_tiles(p, u.len, lo);
+    u.j = static_cast<int>(r - prompt_tiles_before(p, lo));
+    return u;
+  };
+  // Where all segments are short they stay whole, each with the CTA that has
+  // most of it: pieces and their joining cost about ten token tiles.  (One
+  // prompt of 2048 tokens @S2048, of 512 @S512.)
+  PromptPlace at = place_of(s_seq[0], cut[0] - s_base[0]);
+  unsigned my0 = cut[0], my1 = cut[1];
+  if (!shared) {
+    if (cut[1] < total) {
+      const PromptPlace u = place_of(s_seq[1], cut[1] - s_base[1]);
+      my1 = cut[1] - u.j + (2 * u.j >= u.n && u.j ? u.n : 0);
+    }
+    if (at.j) {
+      const bool on = 2 * at.j >= at.n;
+      my0 += (on ? at.n : 0) - at.j;
+      if (on && my0 < my1) prompt_next(p, at);
+      at.j = 0;
+    }
+    if (my0 >= my1) return;
+  }
+  const int count = static_cast<int>(my1 - my0);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2);
@@ -257,24 +299,6 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   tc_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&bar.tmem);
 
-  PromptPlace at;
-  at.b = s_seq;
-  prompt_enter(p, at);
-  {
-    unsigned r = my0 - s_base;
-    const unsigned head = prompt_head_tiles(p, at.len);
-    at.h = static_cast<int>(r / head);
-    r -= at.h * head;
-    int lo = 0, hi = (at.len + 2 * p.tile - 1) / (2 * p.tile);  // the last pair that starts at or before tile r
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prompt_tiles_before(p, mid) <= r) lo = mid;
-      else hi = mid;
-    }
-    at.r = lo;
-    at.n = prompt_pair_tiles(p, at.len, lo);
-    at.j = static_cast<int>(r - prompt_tiles_before(p, lo));
-  }
   // a wait that ran out: the role goes on without waiting, its loops end, and
   // the call reports a timeout
   bool lost = false;
