@@ -206,15 +206,24 @@ AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   return bf ? choose_attn<64, KIND_I8, DT_BF16>(rows) : choose_attn<64, KIND_I8, DT_F16>(rows);
 }
 
-template <int D>
-const void *pick_weights(int kind, int dtype) {
-  const bool bf = dtype == SPEC_BF16;
-  if (kind == SPEC_E4M3) return bf ? reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_E4M3, DT_BF16>)
-                                   : reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_E4M3, DT_F16>);
-  return bf ? reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_I8, DT_BF16>)
-            : reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND_I8, DT_F16>);
+// Up to 24 rows a warp's own matrix instructions keep up with the memory;
+// beyond, the tensor cores with accumulators in tensor memory.  (@WR)
+struct WeightsChoice {
+  const void *fn;
+  int chunk, smem;
+};
+template <int D, int KIND, int DT>
+WeightsChoice choose_weights(long long rows) {
+  if (rows > 24) return {reinterpret_cast<const void *>(&cache_weights_tile_kernel<D, KIND, DT>), WR, WeightsLayout<D>::SMEM};
+  const int chunk = static_cast<int>((rows + 7) / 8 * 8);
+  return {reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND, DT>), chunk, chunk * (D * 2 + 8)};
 }
-const void *pick_weights(int D, int kind, int dtype) { return D == 128 ? pick_weights<128>(kind, dtype) : pick_weights<64>(kind, dtype); }
+template <int D>
+WeightsChoice choose_weights(int kind, int dtype, long long rows) {
+  const bool bf = dtype == SPEC_BF16;
+  if (kind == SPEC_E4M3) return bf ? choose_weights<D, KIND_E4M3, DT_BF16>(rows) : choose_weights<D, KIND_E4M3, DT_F16>(rows);
+  return bf ? choose_weights<D, KIND_I8, DT_BF16>(rows) : choose_weights<D, KIND_I8, DT_F16>(rows);
+}
 
 }  // namespace
 }  // namespace spec
@@ -407,18 +416,17 @@ int spec_cache_weights(const spec_cache_t *cache, const int32_t *page_table, int
   p.q_vec = vectors(*q, 2);
   const long long rows = static_cast<long long>(N) * p.G;
   if (rows > INT_MAX / 2) return fail(SPEC_ERR_ARG, "N * Hq / kv_heads is too large");
-  p.chunk = static_cast<int>(std::min<long long>((rows + 7) / 8 * 8, WMAX));
+  const WeightsChoice k = p.c.D == 128 ? choose_weights<128>(p.c.kind, dtype, rows) : choose_weights<64>(p.c.kind, dtype, rows);
+  p.chunk = k.chunk;
   const double tiles = std::ceil(static_cast<double>(pages_per_seq) * p.c.page / WTOK);
   if (static_cast<double>(B) * p.c.Hk * tiles >= 2147483648.0) return fail(SPEC_ERR_ARG, "B * kv_heads * pages_per_seq is too large");
-  const void *fn = pick_weights(p.c.D, p.c.kind, dtype);
-  const int smem = p.chunk * (p.c.D * 2 + 8);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, WMAX * (p.c.D * 2 + 8));
+  const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic smem)");
   Workspace *w = nullptr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if ((st = get_ws(stream, 1, &w))) return st;
   p.status = w->status;
-  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * num_sms())), WT, smem, stream, &p, "cache_weights_kernel launch");
+  return launch_dependent(k.fn, dim3(static_cast<unsigned>(2 * num_sms())), WT, k.smem, stream, &p, "cache_weights_kernel launch");
 }
 
 int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int pages_per_seq, const int32_t *ctx_len, float *weights,

@@ -4,7 +4,7 @@
 
 #include <cstdint>
 
-#include "attention.cuh"
+#include "attention_tile.cuh"
 
 namespace spec {
 
@@ -214,6 +214,291 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
       do s = sequence(p, ++b);
       while (s.cnt <= 0);
     }
+  }
+}
+
+// Many rows per kv head: the same sums with the products on the tensor cores,
+// keys as the 128 rows of A and queries as the columns of B, so that a thread
+// has a token and adds up what it reads of tensor memory.  While a tile is
+// weighed, the next one's codes become fp16 operands and its products run; two
+// CTAs per SM fill one another's waits.  Two threads per token take half of the
+// rows each and join a tile later.  What bounds it are the instructions of the
+// weights (a multiply-add, an exponential and an addition each).
+constexpr int WR = 128;  // most rows of a chunk
+template <int D>
+struct WeightsLayout {
+  static constexpr int OP = 128 * D * 2;                 // an operand
+  static constexpr int K = 0, Q = 2 * OP;                // two tiles of keys, the queries
+  static constexpr int F = Q + OP;                       // [WR] each: factors, -lse log2e, nodes
+  static constexpr int PART = F + 3 * WR * 4;            // [2][128] sums of the second threads
+  static constexpr int SCALE = PART + 2 * 128 * 4;       // [4][8] of sixteen tokens: a thread may still read those of two tiles before
+  static constexpr int BARS = SCALE + 128;
+  static constexpr int SMEM = BARS + 32;
+};
+
+template <int D, int KIND, int DT>
+__global__ void __launch_bounds__(WT, 2) cache_weights_tile_kernel(const __grid_constant__ WeightsParams p) {
+  using L = WeightsLayout<D>;
+  constexpr int PER = D / 16, STEP = WT / PER, LOADS = 128 / STEP;  // 16-code pieces of a row; rows at a time
+  const float NINF = __uint_as_float(0xff800000u);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ unsigned s_scan[WT / 32];
+  __shared__ int s_seq;
+  __shared__ unsigned s_base;
+  float *const s_fac = reinterpret_cast<float *>(smem + L::F), *const s_nl = s_fac + WR;
+  int *const s_node = reinterpret_cast<int *>(s_nl + WR);
+  float *const s_part = reinterpret_cast<float *>(smem + L::PART), *const s_scale = reinterpret_cast<float *>(smem + L::SCALE);
+  uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + L::BARS);
+  uint32_t *const s_tmem = reinterpret_cast<uint32_t *>(smem + L::BARS + 16);
+  const CacheView &c = p.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const auto work_of = [&](int b) -> unsigned {
+    if (b >= p.B) return 0;
+    const Seq s = sequence(p, b);
+    if (s.cnt < 0 && blockIdx.x == 0) atomicOr(p.status, ST_SLOTS);
+    return s.cnt > 0 ? static_cast<unsigned>(c.Hk) * ((s.ctx + s.cnt + WTOK - 1) / WTOK) : 0;
+  };
+  unsigned total = 0, w = 0, upto = 0;
+  for (int b0 = 0; b0 < p.B; b0 += WT) {
+    unsigned sum;
+    w = work_of(b0 + tid);
+    upto = total + block_scan<WT / 32>(w, s_scan, sum);
+    total += sum;
+  }
+  const unsigned nc = min(gridDim.x, total);
+  if (blockIdx.x >= nc) return;
+  const Share share(total, nc);
+  const unsigned my0 = share.start(blockIdx.x);
+  int left = static_cast<int>(share.start(blockIdx.x + 1) - my0);
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += WT) {
+    if (p.B > WT) {
+      unsigned sum;
+      w = work_of(b0 + tid);
+      upto = before + block_scan<WT / 32>(w, s_scan, sum);
+      before += sum;
+    }
+    if (my0 < upto && my0 >= upto - w) s_seq = b0 + tid, s_base = upto - w;
+  }
+  if (tid == 0) {
+    mbar_init(bar, 1), mbar_init(bar + 1, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(s_tmem, 256);
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
+  const uint32_t base = smem_u32(smem);
+
+  int b = s_seq, h, j;  // of the stretch's next tile
+  Seq s = sequence(p, b);
+  {
+    const unsigned tiles = (s.ctx + s.cnt + WTOK - 1) / WTOK, r = my0 - s_base;
+    h = static_cast<int>(r / tiles);
+    j = static_cast<int>(r - h * tiles);
+  }
+  const long long S = static_cast<long long>(c.per) * c.page;
+  bool lost = false;
+  uint32_t uses = 0;  // tiles so far, all chunks: buffer uses & 1, phase (uses >> 1) & 1
+  for (;;) {
+    const int len = s.ctx + s.cnt, tiles = (len + WTOK - 1) / WTOK, end = min(tiles, j + left), rows = s.cnt * p.G;
+    float *const out = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
+    const int32_t *const table = c.table + static_cast<long long>(b) * c.per;
+    for (int r0 = 0; r0 < rows; r0 += WR) {
+      const int here = min(WR, rows - r0), columns = (here + 31) & ~31;
+      __syncthreads();  // the chunk before has been used
+      // queries: half a row to a thread, as fp16 under a power of two per row
+      {
+        const int r = tid >> 1, half = tid & 1, row = r0 + r;
+        bool live = r < here;
+        const int node = row / p.G, head = h * p.G + row % p.G;
+        const float lse = live ? p.lse[(static_cast<long long>(b) * p.N + node) * (c.Hk * p.G) + head] : NINF;
+        live = lse != NINF;
+        const long long at = live ? b * p.q_sb + node * p.q_sn + head * p.q_sh + half * (D / 2) : 0;
+        Raw8<DT> raw[D / 16];
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          raw[k].v[0] = make_uint4(0, 0, 0, 0);
+          if (live) raw[k] = p.q_vec ? load8<DT, true>(p.q, at + 8 * k) : load8<DT, false>(p.q, at + 8 * k);
+          float x[8];
+          unpack8<DT>(raw[k], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);  // amax * 2^-e lies in [1, 2)
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+        if (half == 0) {
+          s_fac[r] = live ? f : 0.f;
+          s_nl[r] = live ? lse * -1.4426950408889634f : NINF;
+          s_node[r] = min(node, p.N - 1);
+        }
+        if (r < columns)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            float x[8];
+            unpack8<DT>(raw[k], x);
+            const int chunk = half * (D / 16) + k;  // of 8 elements
+            *reinterpret_cast<uint4 *>(smem + L::Q + (chunk >> 3) * 16384 + r * 128 + ((chunk & 7) ^ (r & 7)) * 16) =
+                make_uint4(f32_to_f16x2(x[0] * down, x[1] * down), f32_to_f16x2(x[2] * down, x[3] * down),
+                           f32_to_f16x2(x[4] * down, x[5] * down), f32_to_f16x2(x[6] * down, x[7] * down));
+          }
+      }
+      // codes of a tile: LOADS pieces of 16 to a thread, STEP rows apart
+      const int piece = tid % PER, row0 = tid / PER;
+      int page[LOADS], scale_page = -1;
+      uint4 raw[LOADS];
+      float scale = -1.f;  // of this thread's sixteen tokens (the first 8 threads)
+      const auto find = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          const int tok = i * WTOK + row0 + k * STEP;
+          page[k] = i < end && tok < len ? table[tok >> c.log_page] : -1;
+        }
+        if (tid < 8) scale_page = i < end && i * WTOK + 16 * tid < len ? table[(i * WTOK + 16 * tid) >> c.log_page] : -1;
+      };
+      const auto load = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          const int tok = i * WTOK + row0 + k * STEP;
+          const bool ok = static_cast<unsigned>(page[k]) < static_cast<unsigned>(c.pages);
+          raw[k] = make_uint4(0, 0, 0, 0);
+          if (ok) raw[k] = ldg_na(reinterpret_cast<const uint4 *>(c.k + ((static_cast<long long>(page[k]) * c.Hk + h) * c.page + (tok & (c.page - 1))) * D + 16 * piece));
+        }
+        if (tid < 8) {
+          const bool ok = static_cast<unsigned>(scale_page) < static_cast<unsigned>(c.pages);
+          if (!ok && i < end && i * WTOK + 16 * tid < len) atomicOr(p.status, ST_PAGE);
+          scale = ok ? c.k_scale[static_cast<long long>(scale_page) * c.Hk + h] : -1.f;
+        }
+      };
+      const auto convert = [&](uint32_t use) {
+        const int buf = use & 1;
+        const int panel = piece >> 2;
+        unsigned char *to = smem + L::K + buf * L::OP + panel * 16384;
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          const int row = row0 + k * STEP;
+          uint4 lo, hi;
+          codes_to_f16<KIND, false>(raw[k], lo, hi);
+          *reinterpret_cast<uint4 *>(to + row * 128 + (((2 * piece) & 7) ^ (row & 7)) * 16) = lo;
+          *reinterpret_cast<uint4 *>(to + row * 128 + (((2 * piece + 1) & 7) ^ (row & 7)) * 16) = hi;
+        }
+        if (tid < 8) s_scale[8 * (use & 3) + tid] = scale;
+        fence_async_smem();
+      };
+      const auto issue = [&](int buf) {
+        if (warp != 0) return;
+        tc_after_sync();
+        const uint64_t dK = tc_desc(base + L::K + buf * L::OP, 0), dQ = tc_desc(base + L::Q, 0);
+        const uint32_t id = 1u << 4 | static_cast<uint32_t>(columns / 8) << 17 | (128 / 16) << 24;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          tc_mma_ss_warp(tmem + buf * WR, dK + off, dQ + off, id, k > 0);
+        }
+        tc_commit_warp(bar + buf);
+      };
+      find(j);
+      load(j);
+      convert(uses);
+      find(j + 1);
+      load(j + 1);
+      find(j + 2);
+      tc_before_sync();
+      __syncthreads();
+      issue(uses & 1);
+      const int token = 32 * (warp & 3) + lane, second = warp >> 2;
+      float mine = 0.f, old = 0.f;  // the first thread's sum of the tile before, and the weight so far
+      bool done = false;
+      const auto finish = [&](int i, int buf) {  // both threads' sums of tile i
+        const int tok = i * WTOK + token;
+        if (second || !done) return;
+        out[tok] = old + (mine + s_part[128 * buf + token]);
+      };
+      for (int i = j; i < end; ++i, ++uses) {
+        const int buf = uses & 1;
+        if (i + 1 < end) {
+          convert(uses + 1);
+          load(i + 2);
+          find(i + 3);
+        }
+        tc_before_sync();
+        __syncthreads();  // the next tile's operand; the second threads' sums of the tile before
+        if (i + 1 < end) issue(buf ^ 1);
+        if (i > j) finish(i - 1, buf ^ 1);
+        old = !second && i * WTOK + token < len && (i * WTOK + token < s.ctx || r0 > 0) ? out[i * WTOK + token] : 0.f;
+        if (!lost && !__all_sync(0xffffffffu, tile_wait<0>(bar + buf, (uses >> 1) & 1))) lost = true;
+        tc_after_sync();
+        const int tok = i * WTOK + token, n = tok - s.ctx;
+        const float ks = s_scale[8 * (uses & 3) + (token >> 4)];
+        const bool edge = (i + 1) * WTOK > s.ctx;
+        float2 sum = make_float2(0.f, 0.f), other = sum;
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + buf * WR;
+        // 32 rows at a time, in turn with the other thread
+        if (__builtin_expect(edge, 0)) {
+#pragma unroll 1
+          for (int q = second * 32; q < columns; q += 64) {
+            uint32_t x[32];
+            tmem_ld32(at + q, x);
+            tc_wait_ld32(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int node = s_node[q + e];
+              bool seen = n < 0;
+              if (n >= 0 && n < s.cnt)
+                seen = p.mask ? (p.mask[(static_cast<long long>(b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
+              if (seen) sum.x += ex2(fmaf(__uint_as_float(x[e]) * ks, s_fac[q + e], s_nl[q + e]));
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int q = second * 32; q < columns; q += 64) {
+            uint32_t x[32];
+            tmem_ld32(at + q, x);
+            tc_wait_ld32(x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(s_fac + q + e), l = *reinterpret_cast<const float4 *>(s_nl + q + e);
+              float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(ks, ks), make_float2(0.f, 0.f));
+              y = fma2(y, make_float2(f.x, f.y), make_float2(l.x, l.y));
+              sum = add2(sum, make_float2(ex2(y.x), ex2(y.y)));
+              y = fma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(ks, ks), make_float2(0.f, 0.f));
+              y = fma2(y, make_float2(f.z, f.w), make_float2(l.z, l.w));
+              other = add2(other, make_float2(ex2(y.x), ex2(y.y)));
+            }
+          }
+          sum = add2(sum, other);
+        }
+        mine = sum.x + sum.y;
+        done = ks >= 0.f && tok < len;  // a bad page's slots stay as they are
+        if (second) s_part[128 * buf + token] = mine;
+      }
+      tc_before_sync();
+      __syncthreads();
+      finish(end - 1, (uses - 1) & 1);
+    }
+    left -= end - j;
+    if (left <= 0) break;
+    j = 0;
+    if (++h == c.Hk) {
+      h = 0;
+      do s = sequence(p, ++b);
+      while (s.cnt <= 0);
+    }
+  }
+  if (lost) atomicOr(p.status, ST_TIMEOUT);
+  tc_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc_after_sync();
+    tmem_free(tmem, 256);
   }
 }
 
