@@ -675,10 +675,14 @@ def spec_prompt_attention(q, k, v, starts, *, scale=None, out=None, want_lse=Fal
     T, Hq, D = q.shape
     Hk, device = k.shape[1], q.device
     code = _code(q, "q")
-    qs = _heads(q[None], "q", q.dtype, 1, T, Hq, D)
-    ks, vs = (_heads(t[None], name, q.dtype, 1, T, Hk, D) for t, name in ((k, "k"), (v, "v")))
-    if k.device != device or v.device != device:
-        raise ValueError("q, k and v must be on one device")
+    structs = []
+    for t, name, H in ((q, "q", Hq), (k, "k", Hk), (v, "v", Hk)):
+        if not t.is_cuda or t.dtype != q.dtype or t.device != device:
+            raise TypeError(f"{name} must be a tensor of {q.dtype} on the GPU of q, got {t.dtype} on {t.device}")
+        sn, sh, sd = t.stride()
+        if t.shape != (T, H, D) or sd != 1 and D > 1:
+            raise ValueError(f"{name} must be [{T}, {H}, {D}] with contiguous heads, got {list(t.shape)}")
+        structs.append(ctypes.byref(HeadsStruct(t.data_ptr(), 0, sn, sh)))
     if starts is None or starts.dim() != 1 or starts.shape[0] < 1:
         raise ValueError("starts must be [B + 1]")
     B = starts.shape[0] - 1
@@ -687,8 +691,7 @@ def spec_prompt_attention(q, k, v, starts, *, scale=None, out=None, want_lse=Fal
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != device:
         raise ValueError("out must be contiguous, on the device of q, and of the shape and dtype of q")
     lse = torch.empty((T, Hq), dtype=torch.float32, device=device) if want_lse else None
-    _call(lib.spec_prompt_attention, "spec_prompt_attention", device, stream, ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs),
-          _index(starts, "starts", (B + 1,), device), B, T, Hq, Hk, D, code, D ** -0.5 if scale is None else scale, out.data_ptr(),
+    _call(lib.spec_prompt_attention, "spec_prompt_attention", device, stream, *structs, _index(starts, "starts", (B + 1,), device), B, T, Hq, Hk, D, code, D ** -0.5 if scale is None else scale, out.data_ptr(),
           None if lse is None else lse.data_ptr())
     return out, lse
 

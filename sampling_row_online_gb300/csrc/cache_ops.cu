@@ -206,17 +206,19 @@ AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
   return bf ? choose_attn<64, KIND_I8, DT_BF16>(rows) : choose_attn<64, KIND_I8, DT_F16>(rows);
 }
 
-// Up to 24 rows a warp's own matrix instructions keep up with the memory;
-// beyond, the tensor cores with accumulators in tensor memory.  (@WR)
+// Up to 48 rows a warp's own matrix instructions; beyond, the tensor cores with
+// accumulators in tensor memory, 128 rows at a time.  (Sequences of up to 8192
+// tokens, 8 kv heads, e4m3: 64 of them with 16, 24 and 32 rows 91, 104 and 119 us,
+// the tile kernel 151 to 153; 32 with 64 rows 96 and 91.)
 struct WeightsChoice {
   const void *fn;
-  int chunk, smem;
+  int most, smem;
 };
 template <int D, int KIND, int DT>
 WeightsChoice choose_weights(long long rows) {
-  if (rows > 24) return {reinterpret_cast<const void *>(&cache_weights_tile_kernel<D, KIND, DT>), WR, WeightsLayout<D>::SMEM};
-  const int chunk = static_cast<int>((rows + 7) / 8 * 8);
-  return {reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND, DT>), chunk, chunk * (D * 2 + 8)};
+  if (rows > 48) return {reinterpret_cast<const void *>(&cache_weights_tile_kernel<D, KIND, DT>), WR, WeightsLayout<D>::SMEM};
+  const int most = static_cast<int>((rows + 7) / 8 * 8);
+  return {reinterpret_cast<const void *>(&cache_weights_kernel<D, KIND, DT>), most, most * (D * 2 + 8)};
 }
 template <int D>
 WeightsChoice choose_weights(int kind, int dtype, long long rows) {
@@ -417,7 +419,7 @@ int spec_cache_weights(const spec_cache_t *cache, const int32_t *page_table, int
   const long long rows = static_cast<long long>(N) * p.G;
   if (rows > INT_MAX / 2) return fail(SPEC_ERR_ARG, "N * Hq / kv_heads is too large");
   const WeightsChoice k = p.c.D == 128 ? choose_weights<128>(p.c.kind, dtype, rows) : choose_weights<64>(p.c.kind, dtype, rows);
-  p.chunk = k.chunk;
+  p.most = k.most;
   const double tiles = std::ceil(static_cast<double>(pages_per_seq) * p.c.page / WTOK);
   if (static_cast<double>(B) * p.c.Hk * tiles >= 2147483648.0) return fail(SPEC_ERR_ARG, "B * kv_heads * pages_per_seq is too large");
   const cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);

@@ -16,19 +16,18 @@ namespace spec {
 // slot's sum is finished by the warp that reads its key.
 struct WeightsParams : AttnParams {  // lse is read
   float *weights;                    // [B, Hk, per * page]
-  int chunk;                         // rows that are in shared memory together, a multiple of 8
+  int most;                          // rows of a kv head, rounded up to a multiple of 8
 };
 
 // The list of all (sequence, kv head, tile of 128 tokens) is cut into equal
 // stretches, one per CTA; a warp takes 16 tokens of every tile.  Tokens are the
 // 16 rows of the m16n8k16 products, query rows their 8 columns, in the fragment
-// order of attn_stream_kernel: the key codes are converted once for all rows of
-// a chunk, and the queries lie in shared memory as finished fragments.  A
+// order of attn_stream_kernel: the key codes are converted once for all rows,
+// and the queries lie in shared memory as finished fragments.  A
 // lane's sums are those of its two tokens, over its two rows of each tile of 8;
 // four lanes join them at the end.  The next tile's keys are on their way
 // meanwhile.
 constexpr int WT = 256, WTOK = 128;  // threads, tokens of a tile
-constexpr int WMAX = 256;            // most rows of a chunk
 
 template <int D, int KIND, int DT>
 __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_constant__ WeightsParams p) {
@@ -39,7 +38,7 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
   __shared__ int s_seq;
   __shared__ unsigned s_base;
   uint4 *const s_q = reinterpret_cast<uint4 *>(dyn);                      // [row tile][CH][2][lane]
-  float2 *const s_f = reinterpret_cast<float2 *>(dyn + p.chunk * D * 2);  // [row]: factor, -lse log2e
+  float2 *const s_f = reinterpret_cast<float2 *>(dyn + p.most * D * 2);  // [row]: factor, -lse log2e
   const CacheView &c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -88,11 +87,11 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
     const int len = s.ctx + s.cnt, tiles = (len + WTOK - 1) / WTOK, end = min(tiles, j + left), rows = s.cnt * p.G;
     float *const out = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
     const int32_t *const table = c.table + static_cast<long long>(b) * c.per;
-    for (int r0 = 0; r0 < rows; r0 += p.chunk) {
-      const int here = min(p.chunk, (rows - r0 + 7) & ~7);
-      __syncthreads();  // the chunk before has been used
+    {
+      const int here = (rows + 7) & ~7;
+      __syncthreads();  // the queries before have been used
       for (int rt = warp; rt < here / 8; rt += WT / 32) {
-        const int r = r0 + 8 * rt + g;
+        const int r = 8 * rt + g;
         bool live = r < rows;
         const long long lse_at = (static_cast<long long>(b) * p.N + r / p.G) * (c.Hk * p.G) + h * p.G + r % p.G;
         const float lse = live ? p.lse[lse_at] : NINF;
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
         // lanes 0 and 1 of a group of four write tokens g and g + 8
         const int mine = tok + g + 8 * t;
         float old = 0.f;
-        if (t < 2 && mine < len && (mine < s.ctx || r0 > 0)) old = out[mine];
+        if (t < 2 && mine < s.ctx) old = out[mine];
         const bool edge = tok + 16 > s.ctx;
         float sum[2] = {0.f, 0.f};
 #pragma unroll 2
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
           if (edge) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int node = min((r0 + 8 * rt + 2 * t + (k & 1)) / p.G, p.N - 1), n = tok + g + 8 * (k >> 1) - s.ctx;
+              const int node = min((8 * rt + 2 * t + (k & 1)) / p.G, p.N - 1), n = tok + g + 8 * (k >> 1) - s.ctx;
               bool seen = n < 0;
               if (n >= 0 && n < s.cnt)
                 seen = p.mask ? (p.mask[(static_cast<long long>(b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
