@@ -734,6 +734,8 @@ __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_con
     unpack8<DT>(load8<DT, true>(p.weight[w], at), g[0]);
     if (two) unpack8<DT>(load8<DT, true>(p.weight[w], at + half), g[1]);
   }
+  // with several axes every angle has a position to load: four at a time
+#pragma unroll(std::is_same_v<P, NormRopeAxesParams> ? 4 : 1)
   for (int i = threadIdx.x; i < here * half; i += 256) {
     const int tk = i / half, tok = first + tk, b = tok / p.N;
     if (!same) freq = p.freq[i - tk * half], axis = axis_of(p, i - tk * half);

@@ -36,6 +36,7 @@ constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
 constexpr float P_UP = 8.f, P_MOST = 60000.f;
 constexpr int P_SHORT = 16;          // token tiles of segments that are not shared between CTAs
+constexpr int P_EXTRA = 2;           // token tiles that take as long as a segment's begin and end
 constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
 
 struct PromptParams {
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   extern __shared__ __align__(1024) unsigned char psm[];
   __shared__ unsigned s_scan[P_NT / 32];
   __shared__ int s_seq[2], s_last[2];
-  __shared__ unsigned s_base[2];
+  __shared__ unsigned s_base[2], s_segs[2];
   PromptBars &bar = *reinterpret_cast<PromptBars *>(psm + L::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float NINF = __uint_as_float(0xff800000u), QNAN = __uint_as_float(0x7fc00000u);
@@ -193,15 +194,24 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
 
   // ---- the list of all work, and this CTA's stretch of it
   int wrong = 0, longer = 0;
-  const auto work_of = [&](int b) -> unsigned {
-    if (b >= p.B) return 0;
-    const int s = p.starts[b], e = p.starts[b + 1];
-    if (s < 0 || e < s || e > p.T) {
-      wrong = 1;
-      return 0;
-    }
+#pragma unroll 1
+  for (int b = tid; b <= p.B; b += P_NT) {
+    const int s = p.starts[b], e = b < p.B ? p.starts[b + 1] : s;
+    wrong |= s < 0 || e < s || e > p.T;
     longer |= e - s > P_SHORT * PT;
-    return prompt_head_tiles(p, e - s) * p.heads;
+  }
+  wrong = __syncthreads_or(wrong);
+  const bool shared = __syncthreads_or(longer);
+  // Work is counted in token tiles.  Where all segments are short they stay
+  // whole, each with the CTA that has most of it, and count their begin and end
+  // too: pieces and their joining cost about ten token tiles.  (One prompt of
+  // 2048 tokens @S2048, of 512 @S512.)
+  const int extra = shared ? 0 : P_EXTRA;
+  const auto pairs_of = [&](int len) -> unsigned { return (len + 2 * p.tile - 1) / (2 * p.tile); };
+  const auto length_of = [&](int b) { return b < p.B && !wrong ? p.starts[b + 1] - p.starts[b] : 0; };
+  const auto work_of = [&](int b) -> unsigned {
+    const int len = length_of(b);
+    return (prompt_head_tiles(p, len) + extra * pairs_of(len)) * p.heads;
   };
   unsigned total = 0, w = 0, upto = 0;  // upto: of all sequences up to this thread's (of the last block of them)
   for (int b0 = 0; b0 < p.B; b0 += P_NT) {
@@ -210,9 +220,6 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
     upto = total + block_scan<P_NT / 32>(w, s_scan, sum);
     total += sum;
   }
-  if (p.B == 0 && (p.starts[0] < 0 || p.starts[0] > p.T)) wrong = 1;
-  wrong = __syncthreads_or(wrong);
-  const bool shared = __syncthreads_or(longer);
   {  // rows of no sequence
     const long long row = static_cast<long long>(p.Hq) * D / 8, lo = wrong ? 0 : p.starts[0], hi = wrong ? 0 : p.starts[p.B];
     const float v = wrong ? QNAN : 0.f, x[8] = {v, v, v, v, v, v, v, v};
@@ -230,56 +237,62 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   if (blockIdx.x >= nc) return;
   const Share share(total, nc);
   const unsigned cut[2] = {share.start(blockIdx.x), share.start(blockIdx.x + 1)};
-  unsigned before = 0;
+  unsigned before = 0, segs_before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += P_NT) {
+    unsigned sum, segs = 0;
     if (p.B > P_NT) {
-      unsigned sum;
       w = work_of(b0 + tid);
       upto = before + block_scan<P_NT / 32>(w, s_scan, sum);
       before += sum;
     }
+    if (!shared) {
+      const unsigned mine = pairs_of(length_of(b0 + tid)) * p.heads;
+      segs = segs_before + block_scan<P_NT / 32>(mine, s_scan, sum) - mine;
+      segs_before += sum;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (cut[e] < upto && cut[e] >= upto - w) s_seq[e] = b0 + tid, s_base[e] = upto - w;
+      if (cut[e] < upto && cut[e] >= upto - w) s_seq[e] = b0 + tid, s_base[e] = upto - w, s_segs[e] = segs;
   }
   __syncthreads();
-  const auto place_of = [&](int b, unsigned r) {  // tile r of sequence b's
+  // The place of cut e, and how many token tiles of all sequences come before.
+  const auto place_of = [&](int e, unsigned &tiles) {
     PromptPlace u;
-    u.b = b;
+    u.b = s_seq[e];
     prompt_enter(p, u);
-    const unsigned head = prompt_head_tiles(p, u.len);
+    unsigned r = cut[e] - s_base[e];
+    const unsigned pairs = pairs_of(u.len), head = prompt_head_tiles(p, u.len) + extra * pairs;
     u.h = static_cast<int>(r / head);
     r -= u.h * head;
-    int lo = 0, hi = (u.len + 2 * p.tile - 1) / (2 * p.tile);  // the last pair that starts at or before tile r
+    unsigned lo = 0, hi = pairs;  // the last pair that starts at or before r
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prompt_tiles_before(p, mid) <= r) lo = mid;
+      const unsigned mid = (lo + hi) >> 1;
+      if (prompt_tiles_before(p, mid) + extra * mid <= r) lo = mid;
       else hi = mid;
     }
-    u.r = lo;
-    u.n = prompt_pair_tiles(p, u.len, lo);
-    u.j = static_cast<int>(r - prompt_tiles_before(p, lo));
+    u.r = static_cast<int>(lo);
+    u.n = prompt_pair_tiles(p, u.len, u.r);
+    u.j = static_cast<int>(r - prompt_tiles_before(p, lo) - extra * lo);
+    tiles = cut[e];
+    if (!shared) {
+      tiles -= u.j + extra * (s_segs[e] + u.h * pairs + lo);
+      if (u.j && 2 * u.j >= u.n + extra) {  // from the next segment on
+        tiles += u.n;
+        u.j = u.n;
+      } else {
+        u.j = 0;
+      }
+    }
     return u;
   };
-  // Where all segments are short they stay whole, each with the CTA that has
-  // most of it: pieces and their joining cost about ten token tiles.  (One
-  // prompt of 2048 tokens @S2048, of 512 @S512.)
-  PromptPlace at = place_of(s_seq[0], cut[0] - s_base[0]);
-  unsigned my0 = cut[0], my1 = cut[1];
-  if (!shared) {
-    if (cut[1] < total) {
-      const PromptPlace u = place_of(s_seq[1], cut[1] - s_base[1]);
-      my1 = cut[1] - u.j + (2 * u.j >= u.n && u.j ? u.n : 0);
-    }
-    if (at.j) {
-      const bool on = 2 * at.j >= at.n;
-      my0 += (on ? at.n : 0) - at.j;
-      if (on && my0 < my1) prompt_next(p, at);
-      at.j = 0;
-    }
-    if (my0 >= my1) return;
-  }
+  unsigned my0, my1;
+  PromptPlace at = place_of(0, my0);
+  if (shared) my1 = cut[1];
+  else if (cut[1] < total) place_of(1, my1);
+  else my1 = total - extra * segs_before;
+  if (my0 >= my1) return;
+  if (at.j == at.n) prompt_next(p, at);
   const int count = static_cast<int>(my1 - my0);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
