@@ -510,8 +510,9 @@ struct EvictParams {
   int32_t *out_index, *out_ctx;
   int32_t *status;
 };
-constexpr int EV_NT = 512, EV_BINS = 2048;       // threads, bins
-constexpr int EV_SLICE = 8192;                   // slots of a CTA at a time
+constexpr int EV_NT = 1024, EV_BINS = 2048;      // threads, bins
+constexpr int EV_SLICE = 40960;                  // slots of a CTA at a time
+static_assert(EV_NT == 1024, "full_scan");
 constexpr int EV_SMEM = (EV_SLICE + 2 * EV_BINS) * 4;
 
 // Weights as whole numbers of the same order: NaN below everything, both zeros
@@ -522,6 +523,27 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float key_weight(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
+
+// As block_scan, for a full CTA: every warp adds the warps' sums up by itself (a
+// loop over 32 of them takes a thousand clocks).
+__device__ __forceinline__ unsigned full_scan(unsigned x, unsigned *s, unsigned &sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto scan = [&](unsigned y) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    return y;
+  };
+  x = scan(x);
+  __syncthreads();  // the previous use of s is over
+  if (lane == 31) s[warp] = x;
+  __syncthreads();
+  const unsigned y = scan(s[lane]), below = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+  sum = __shfl_sync(0xffffffffu, y, 31);
+  return warp ? x + below : x;
+}
 
 // A cluster per kv head and sequence finds the k-th largest weight by its
 // digits, 11, 11 and 10 bits from the top (a histogram each, added up through
@@ -618,9 +640,11 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       if (joint) cluster_sync();
       else __syncthreads();
       // four bins to a thread, from the top
-      const unsigned *mine = &hist[EV_BINS - 4 - 4 * tid];
-      uint4 n = *reinterpret_cast<const uint4 *>(mine);
-      if (joint) {
+      const bool has = tid < EV_BINS / 4;
+      const unsigned *mine = &hist[has ? EV_BINS - 4 - 4 * tid : 0];
+      uint4 n = make_uint4(0, 0, 0, 0);
+      if (has) n = *reinterpret_cast<const uint4 *>(mine);
+      if (joint && has) {
 #pragma unroll 2
         for (int i = 1; i < C; ++i) {
           const uint4 x = dsmem_ld_v4(dsmem_addr(mine, (rank + i) & (C - 1)));
@@ -629,8 +653,8 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       }
       const unsigned four = n.x + n.y + n.z + n.w, each[4] = {n.w, n.z, n.y, n.x};
       unsigned sum;
-      unsigned above = block_scan<EV_NT / 32>(four, s_scan, sum) - four;
-      if (above < rem && above + four >= rem) {
+      unsigned above = full_scan(four, s_scan, sum) - four;
+      if (has && above < rem && above + four >= rem) {
         int e = 0;
         while (above + each[e] < rem) above += each[e++];
         s_digit = EV_BINS - 1 - 4 * tid - e, s_rem = rem - above;
@@ -667,7 +691,7 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       both += __popc(__ballot_sync(0xffffffffu, more)) | __popc(__ballot_sync(0xffffffffu, same)) << 16;
     }
     unsigned sum;
-    const unsigned upto = block_scan<EV_NT / 32>(lane == 0 ? both : 0, s_scan, sum);  // the stretch's weights have been read
+    const unsigned upto = full_scan(lane == 0 ? both : 0, s_scan, sum);  // the stretch's weights have been read
     if (joint) {
       if (tid == 0) s_total = sum;
       cluster_sync();

@@ -167,6 +167,12 @@ def test_evict_many_slots_and_blocks():
     evict("e4m3", 40, 1, 64, 16, [33 + 7 * b for b in range(40)], 48, 2, 2, seed=3)
 
 
+def test_evict_more_slots_than_shared_memory_holds():
+    """Slots that no cluster holds together, and a short context behind the same wide table."""
+    evict("int8", 2, 1, 64, 128, [350001, 600], 20000, 3, 1000, seed=4)
+    evict("e4m3", 2, 1, 64, 128, [50003, 49000], 300, 0, 0, seed=5)   # two to four CTAs' slices
+
+
 def test_evict_orders_any_weights():
     """Infinities, NaN, negative and equal weights, both zeros, neighbours in the last bit, and numbers whose digits are equal up
     to any of the three histograms."""
