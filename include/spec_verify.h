@@ -37,8 +37,10 @@
  *   - The library keeps one grow-only device workspace per (device, stream)
  *     pair: 16 bytes per row, 16 KB of the row and consumer warp in a
  *     verification, up to 21 MB for spec_cache_attention (it depends on Hq * N /
- *     kv_heads, head_dim and the number of SMs, not on the lengths), a few ints
- *     per sequence otherwise.  Growing it (to twice its size at least) calls
+ *     kv_heads, head_dim and the number of SMs, not on the lengths), 21 or 41 MB
+ *     (head_dim 64 or 128) for spec_prompt_attention and the size of those of
+ *     its inputs that are not 16-byte aligned throughout, a few ints per sequence
+ *     otherwise.  Growing it (to twice its size at least) calls
  *     cudaMalloc, so the first call of a new size on a stream should not be
  *     inside a CUDA graph capture.
  *     What a call has outgrown stays allocated, so a graph captured earlier can
@@ -568,11 +570,20 @@ int spec_qk_norm_rope_axes(const spec_heads_t *q, const spec_heads_t *k, const s
  * over the rows j <= i of i's own sequence.  Query head h uses kv head
  * h / (Hq / Hk).
  *   q             [T, Hq, D], k and v [T, Hk, D] as spec_heads_t (stride_b is
- *                 not used), SPEC_BF16 or SPEC_F16, D 64 or 128
+ *                 not used), SPEC_BF16 or SPEC_F16, D 64 or 128; a tensor whose
+ *                 rows are not 16-byte aligned, or whose strides are not
+ *                 positive, is copied first
  *   starts        [B + 1] int32, ascending, in [0, T]
- *   out           [T, Hq, D] contiguous, 16-byte aligned, dtype
+ *   out           [T, Hq, D] contiguous, 16-byte aligned, dtype; no input's
+ *                 memory
  *   lse           [T, Hq] float or NULL: the natural logarithm of the sum of
  *                 exp(scale * q_i . k_j)
+ * Scores, sums and the output are held in fp32; softmax weights are rounded to
+ * dtype where they meet the values (half a step, 2^-8 of the weight for bf16 and
+ * 2^-11 for fp16), the sum takes the unrounded ones.  Results do not depend on
+ * timing.  The call counts pieces of 128 x 128 (rows of a kv head x tokens) of
+ * the upper half of T x T in 31 bits (SPEC_ERR_ARG beyond; about a million
+ * tokens with 64 heads).
  * Rows of no sequence (before starts[0], from starts[B] on) are not read; out
  * is 0 and lse -inf there.  A row does not depend on what later rows or other
  * sequences hold, be it infinities or NaN.  starts that are not ascending, or

@@ -467,7 +467,7 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   const long long heads = static_cast<long long>(Hk) * batch, slots = static_cast<long long>(p.c.per) * p.c.page;
   // One CTA as far as its shared memory holds the slots, and more where few heads
   // leave SMs idle.  (64 heads of up to 32768 slots, the whole call: one CTA 66 us,
-  // four of 512 threads 81; 8 heads of 32768 @E1.)
+  // four of 512 threads 81; 8 heads of 32768: one 34 us, four 26.)
   unsigned n = 1;
   while (n < 8 && (static_cast<long long>(n) * EV_SLICE < slots || (n * 8192ll < slots && 4 * n * heads <= num_sms()))) n *= 2;
   if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, EV_SMEM, stream, &p, "evict_select_kernel launch", n))) return st;

@@ -174,11 +174,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // index order, so results do not depend on timing.
 //
 //   copies    Q of both row tiles, K and V tiles, as swizzled operands (TMA)
-//   products  S = Q K^T, O += P V (P in tensor memory, over S)
-//   softmax   a thread per row: S -> P under the running offset, the output
+//   products  S = Q K^T, O += P V (P in tensor memory, over S), A and B in turn
+//   softmax   a thread per row: S -> P under the running offset; the output
 //   values    looks for values that are not finite where some row does not see
 //             all of the tile: 0 * inf is not 0.  They are taken out, and marked
 //             with their token, and rows that see them get them at the end.
+//
+// What bounds it is a row tile's chain: scores to weights 1130 clocks (512 of
+// exponentials), 130 to 250 to the products' warp, 900 for the issue of 16
+// products, 400 until the scores are there; two row tiles share it, a pair of
+// tiles every 2600 clocks, of which the products need 2048.  One prompt of 16384
+// tokens, 32 heads on 8: 1499 to 1519 us, 1448 to 1467 TFLOP/s; 8 of 2048: 257 us,
+// 1070 TFLOP/s; head size 64 has half of the products under the same chain: 1350 us,
+// 815 TFLOP/s.  A segment's begin and end cost about two token tiles.
+// Measured and dropped (the prompt of 16384, us): output threads of their own,
+// 512 threads of 128 registers, 1656; half of the weights stored and multiplied
+// at a time 1806; all of a tile's scores in registers 1932 (spills).
 template <int D, int DT>
 __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using L = PromptLayout<D>;
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
   // Work is counted in token tiles.  Where all segments are short they stay
   // whole, each with the CTA that has most of it, and count their begin and end
   // too: pieces and their joining cost about ten token tiles.  (One prompt of
-  // 2048 tokens @S2048, of 512 @S512.)
+  // 512 tokens 16 us, 32 shared; of 2048 tokens 54 and 67.)
   const int extra = shared ? 0 : P_EXTRA;
   const auto pairs_of = [&](int len) -> unsigned { return (len + 2 * p.tile - 1) / (2 * p.tile); };
   const auto length_of = [&](int b) { return b < p.B && !wrong ? p.starts[b + 1] - p.starts[b] : 0; };
