@@ -174,7 +174,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // index order, so results do not depend on timing.
 //
 //   copies    Q of both row tiles, K and V tiles, as swizzled operands (TMA)
-//   products  S = Q K^T, O += P V (P in tensor memory, over S), A and B in turn
+//   products  S = Q K^T, O += P V (P in tensor memory; head size 128: over S), A and B in turn
 //   softmax   a thread per row: S -> P under the running offset; the output
 //   values    looks for values that are not finite where some row does not see
 //             all of the tile: 0 * inf is not 0.  They are taken out, and marked
@@ -185,14 +185,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // products, 400 until the scores are there; two row tiles share it, a pair of
 // tiles every 2600 clocks, of which the products need 2048.  One prompt of 16384
 // tokens, 32 heads on 8: 1499 to 1519 us, 1448 to 1467 TFLOP/s; 8 of 2048: 257 us,
-// 1070 TFLOP/s; head size 64 has half of the products under the same chain: 1350 us,
-// 815 TFLOP/s.  A segment's begin and end cost about two token tiles.
+// 1070 TFLOP/s.  Head size 64 has half of the products, but the same softmax; its
+// weights have columns of their own, and the next scores are multiplied before
+// them: 1225 to 1239 us, 898 TFLOP/s (weights over the scores as for 128: 1350).  A segment's
+// begin and end cost about two token tiles.
 // Measured and dropped (the prompt of 16384, us): output threads of their own,
 // 512 threads of 128 registers, 1656; half of the weights stored and multiplied
-// at a time 1806; all of a tile's scores in registers 1932 (spills).
+// at a time 1806; all of a tile's scores in registers 1932 (spills).  For head size
+// 64: two score buffers of 64 tokens a row tile 1627 (twice the steps), the next
+// scores already under the last quarter of the weights 1279 to 1336 (spills), no
+// turns 1449.
 template <int D, int DT>
 __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using L = PromptLayout<D>;
+  // Head size 64 leaves tensor memory for weights of their own (64 columns a row
+  // tile), so the next scores come before the weights' product, not after it.
+  constexpr bool APART = D == 64;
   extern __shared__ __align__(1024) unsigned char psm[];
   __shared__ unsigned s_scan[P_NT / 32];
   __shared__ int s_seq[2], s_last[2];
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
     more_registers<P_REG_SOFT>();
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field of the addresses
-    const uint32_t tS = tmem + lanes + g * PT, tO = tmem + lanes + 256 + g * PT;
+    const uint32_t tS = tmem + lanes + g * PT, tO = tmem + lanes + 256 + g * D, tP = APART ? tmem + lanes + 384 + g * 64 : tS;
     const int tok_in = r / p.G, head_in = r - tok_in * p.G, first_in = 32 * (warp & 3) / p.G;  // first_in: of the warp's first row
     // scores times f; a scale of zero as the least number, so that a hidden
     // column's infinite score stays infinite
@@ -591,8 +599,12 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           }
         }
         l += sum;
+        if (APART && uses) {  // the weights before these have been multiplied
+          wait(&bar.o_done[g], (uses - 1) & 1);
+          tc_after_sync();
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_st16(tS + 16 * q, pk + 16 * q);  // weights over scores that have been read
+        for (int q = 0; q < 4; ++q) tmem_st16(tP + 16 * q, pk + 16 * q);  // weights, if not apart over scores that have been read
         tc_wait_st();
         tc_before_sync();
         }
@@ -673,7 +685,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
     } else if (role <= 2) {
       // ---------------------------------------------------------- products
       // A warp for each row tile.  They take turns: PV of a tile and S of the
-      // next tile for A, then for B, so that one row tile's softmax runs under
+      // next tile (with P apart the other way round) for A, then for B, so that one row tile's softmax runs under
       // the other's products; without turns the products mix, both row tiles
       // wait for both, and their softmaxes run at the same time.  What a warp
       // waits for, and its arrivals, pass under the other's products.
@@ -681,7 +693,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       constexpr uint32_t ID_S = TYPE | 1u << 4 | (PT / 16) << 24;  // without the columns
       constexpr uint32_t ID_O = TYPE | 1u << 4 | 1u << 16 | (D / 8) << 17 | (PT / 16) << 24;  // values run along the tokens
       const int g = role - 1;
-      const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * PT;
+      const uint32_t sm = smem_u32(psm), tS = tmem + g * PT, tO = tmem + 256 + g * D, tP = APART ? tmem + 384 + g * 64 : tS;
       const uint64_t dQ = tc_desc(sm + L::Q + g * L::OP, 0), dK0 = tc_desc(sm + L::K, 0), dV0 = tc_desc(sm + L::V, 16384);
       uint32_t uses = 0, q_uses = 0, seen[2] = {0, 0};
       PromptPlace next = at;
@@ -700,19 +712,19 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
         if (has_v) wait2(&bar.turn[g], (i + 1) & 1, &bar.p_full[g], uses & 1), ++uses;
         else wait(&bar.turn[g], (i + 1) & 1);
         tc_after_sync();
-        if (has_v) {
-          if (sixteens == PT / 16) {
+        const int six_v = sixteens;
+        sixteens = prompt_sixteens(next, next.j);
+        const auto weighted = [&]() {
+          if (six_v == PT / 16) {
 #pragma unroll
             for (int k = 0; k < PT / 16; ++k)  // 16 tokens at a time
-              tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+              tc_mma_ts_warp(tO, tP + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
           } else {
 #pragma unroll 1
-            for (int k = 0; k < sixteens; ++k) tc_mma_ts_warp(tO, tS + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
+            for (int k = 0; k < six_v; ++k) tc_mma_ts_warp(tO, tP + 8 * k, dV + (k * 2048 >> 4), ID_O, k > 0 || (i > 0 && j > 0));
           }
-          if (j + 1 == tiles || !has_k) tc_commit_warp(&bar.o_done[g]);
-        }
-        sixteens = prompt_sixteens(next, next.j);
-        if (has_k) {
+        };
+        const auto scores = [&]() {
           const auto off = [](int k) -> uint64_t { return ((k >> 2) * 16384 + (k & 3) * 32) >> 4; };  // 32 bytes of the rows at a time, 16384 between panels
           if (sixteens == PT / 16) {
 #pragma unroll
@@ -721,21 +733,36 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
 #pragma unroll 1
             for (int k = 0; k < D / 16; ++k) tc_mma_ss_warp(tS, dQ + off(k), dK + off(k), ID_S | static_cast<uint32_t>(2 * sixteens) << 17, k > 0);
           }
+        };
+        const auto scores_end = [&]() {
+          if (has_k) {
+            tc_commit_warp(&bar.s_full[g]);
+            tc_commit_warp(&bar.k_empty[t]);
+            if (next.j + 1 == coming) tc_commit_warp(&bar.q_empty[g]);
+          } else if (more) {
+            mbar_arrive_warp(&bar.k_empty[t]);
+          }
+        };
+        if (APART) {
+          if (has_k) scores();
+          scores_end();
+          if (has_v) {
+            weighted();
+            tc_commit_warp(&bar.o_done[g]);
+          }
+          mbar_arrive_warp(&bar.turn[g ^ 1]);
+        } else {
+          if (has_v) {
+            weighted();
+            if (j + 1 == tiles || !has_k) tc_commit_warp(&bar.o_done[g]);
+          }
+          if (has_k) scores();
+          mbar_arrive_warp(&bar.turn[g ^ 1]);
+          scores_end();
+          if (has_v && j + 1 != tiles && has_k) tc_commit_warp(&bar.o_done[g]);
         }
-        mbar_arrive_warp(&bar.turn[g ^ 1]);
-        if (has_k) {
-          tc_commit_warp(&bar.s_full[g]);
-          tc_commit_warp(&bar.k_empty[t]);
-          if (next.j + 1 == coming) tc_commit_warp(&bar.q_empty[g]);
-        } else if (more) {
-          mbar_arrive_warp(&bar.k_empty[t]);
-        }
-        if (has_v) {
-          if (j + 1 != tiles && has_k) tc_commit_warp(&bar.o_done[g]);
-          tc_commit_warp(&bar.v_empty[s]);
-        } else if (i >= 0) {
-          mbar_arrive_warp(&bar.v_empty[s]);
-        }
+        if (has_v) tc_commit_warp(&bar.v_empty[s]);
+        else if (i >= 0) mbar_arrive_warp(&bar.v_empty[s]);
         j = next.j, tiles = coming, edge = coming_edge;
         if (++next.j == next.n && i + 2 < count) {
           prompt_next(p, next);
