@@ -469,7 +469,7 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   // leave SMs idle.  (64 heads of up to 32768 slots, the whole call: one CTA 66 us,
   // four of 512 threads 81; 8 heads of 32768: one 34 us, four 26.)
   unsigned n = 1;
-  while (n < 8 && (static_cast<long long>(n) * EV_SLICE < slots || (n * 8192ll < slots && 4 * n * heads <= num_sms()))) n *= 2;
+  while (n < 8 && (static_cast<long long>(n) * EV_SLICE < slots || (n * 8192ll < slots && 2 * n * heads <= num_sms()))) n *= 2;
   if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, EV_SMEM, stream, &p, "evict_select_kernel launch", n))) return st;
   const int rows = EM_BYTES / p.c.D;
   n = cluster((keep + rows - 1) / rows, 2 * heads, 8);

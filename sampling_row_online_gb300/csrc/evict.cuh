@@ -577,18 +577,26 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
   if (!joint) slice = ctx;
   const int s0 = joint ? min(rank * slice, ctx) : 0, s1 = joint ? min(s0 + slice, ctx) : ctx;
   float *const wts = p.weights + (static_cast<long long>(b) * c.Hk + h) * S;
-  const auto load = [&](int from) {
-    const int n = min(EV_SLICE, s1 - from);
+  const int lo = p.first, hi = ctx - p.last;  // of the slots between these the largest are kept
+  const auto load = [&](int from, bool count) {  // keys; counts of their first digit
+    const int n = min(EV_SLICE, s1 - from), first = max(lo - from, 0), end = min(hi - from, n);
 #pragma unroll 2
     for (int i = 4 * tid; i < n; i += 4 * EV_NT) {
       const float4 x = *reinterpret_cast<const float4 *>(wts + from + i);
-      *reinterpret_cast<uint4 *>(s_key + i) = make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+      const uint32_t u[4] = {weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w)};
+      *reinterpret_cast<uint4 *>(s_key + i) = make_uint4(u[0], u[1], u[2], u[3]);
+      if (!count) continue;
+      const bool all = i >= first && i + 4 <= end;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (all || (i + k >= first && i + k < end)) atomicAdd(&s_hist[u[k] >> 21], 1u);
     }
   };
   const bool one = s1 - s0 <= EV_SLICE;
   int bad = 0;
+  __syncthreads();  // counts are zero
   if (moves) {
-    if (one) load(s0);
+    if (one) load(s0, true);
     const int blocks = (ctx + c.page - 1) >> c.log_page;
 #pragma unroll 1
     for (int i = tid; i < blocks; i += EV_NT)
@@ -608,7 +616,6 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
   }
   if (!joint && rank > 0) return;
 
-  const int lo = p.first, hi = ctx - p.last;
   unsigned rem = p.keep - p.first - p.last;  // of hi - lo, which are more
   uint32_t key = 0;                          // the digits found so far, at their place
   const bool some = rem > 0;
@@ -624,17 +631,26 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
         __syncthreads();
       }
 #pragma unroll 1
-      for (int from = s0; from < s1; from += EV_SLICE) {
+      for (int from = s0; from < s1 && !(one && pass == 0); from += EV_SLICE) {
         if (!one) {
           __syncthreads();
-          load(from);
+          load(from, pass == 0);
+          if (pass == 0) continue;
           __syncthreads();
         }
         const int first = max(lo - from, 0), end = min(min(hi, s1) - from, EV_SLICE);
-#pragma unroll 4
-        for (int i = first + tid; i < end; i += EV_NT) {
-          const uint32_t u = s_key[i];
-          if (pass == 0 || u >> up == key >> up) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
+        const auto count = [&](uint32_t u) {
+          if (u >> up == key >> up) atomicAdd(&hist[u >> down & ((1u << bits) - 1)], 1u);
+        };
+#pragma unroll 2
+        for (int i = (first & ~3) + 4 * tid; i < end; i += 4 * EV_NT) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(s_key + i);
+          if (i >= first && i + 4 <= end) {
+            count(u.x), count(u.y), count(u.z), count(u.w);
+          } else {
+#pragma unroll 1
+            for (int k = max(i, first); k < min(i + 4, end); ++k) count(s_key[k]);
+          }
         }
       }
       if (joint) cluster_sync();
@@ -665,31 +681,39 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
       up = down;
     }
   }
-  // in order: all above the key, and the first `rem` of those that equal it; a
-  // warp's slots are neighbours
+  // Slots between the given ones in order: all above the key, and the first `rem`
+  // of those that equal it.  Four to a lane; a warp's are neighbours.
   unsigned n_more = 0, n_same = 0;  // before this stretch of slots
 #pragma unroll 1
   for (int from = s0; from < max(s1, s0 + 1); from += EV_SLICE) {
     if (!one) {
       __syncthreads();
-      load(from);
+      load(from, false);
       __syncthreads();
     }
-    const int n = min(EV_SLICE, s1 - from), part = (n + EV_NT - 1) / EV_NT * 32, w0 = (tid >> 5) * part, w1 = min(w0 + part, n);
-    const auto look = [&](int i, bool &more, bool &same) {
-      const int s = from + i;
-      const uint32_t u = i < w1 ? s_key[i] : 0;
-      const bool given = s < lo || s >= hi;
-      more = i < w1 && (given || (some && u > key));
-      same = i < w1 && !given && some && u == key;
+    const int n = min(EV_SLICE, s1 - from), first = max(lo - from, 0), end = some ? min(hi - from, n) : 0;
+    const int part = (max(end - (first & ~3), 0) + 4 * EV_NT - 1) / (4 * EV_NT) * 128;
+    const int w0 = (first & ~3) + (tid >> 5) * part, w1 = min(w0 + part, end);
+    const auto look = [&](int i, uint32_t (&u)[4], unsigned &more, unsigned &same) {  // a bit for each of slots i to i + 3
+      more = same = 0;
+      if (i >= w1) return;
+      const uint4 x = *reinterpret_cast<const uint4 *>(s_key + i);
+      u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) more |= (u[k] > key) << k, same |= (u[k] == key) << k;
+      if (i < first || i + 4 > end) {
+        const unsigned in = (i < first ? 15u << (first - i) : 15u) & (i + 4 > end ? (1u << (end - i)) - 1 : 15u);
+        more &= in, same &= in;
+      }
     };
-    unsigned both = 0;  // of the warp
+    uint32_t u[4];
+    unsigned more, same, both = 0;  // of the warp
 #pragma unroll 1
-    for (int i = w0; i < w1; i += 32) {
-      bool more, same;
-      look(i + lane, more, same);
-      both += __popc(__ballot_sync(0xffffffffu, more)) | __popc(__ballot_sync(0xffffffffu, same)) << 16;
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+      look(i, u, more, same);
+      both += __popc(more) | __popc(same) << 16;
     }
+    both = __reduce_add_sync(0xffffffffu, both);
     unsigned sum;
     const unsigned upto = full_scan(lane == 0 ? both : 0, s_scan, sum);  // the stretch's weights have been read
     if (joint) {
@@ -701,20 +725,42 @@ __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_consta
         n_more += x & 0xffffu, n_same += x >> 16;
       }
     }
+    // the first slots stay where they are, the last ones follow all others
+#pragma unroll 1
+    for (int i = from + tid; i < min(lo, from + n); i += EV_NT) index[i] = i;
+#pragma unroll 1
+    for (int i = max(hi, from) + tid; i < from + n; i += EV_NT) {
+      const int pos = p.keep - p.last + i - hi;
+      index[pos] = i;
+      wts[pos] = key_weight(s_key[i - from]);
+    }
     const unsigned start = __shfl_sync(0xffffffffu, upto, 0) - both;
     unsigned m = n_more + (start & 0xffffu), e = n_same + (start >> 16);
 #pragma unroll 1
-    for (int i = w0; i < w1; i += 32) {
-      bool more, same;
-      look(i + lane, more, same);
-      const unsigned bm = __ballot_sync(0xffffffffu, more), be = __ballot_sync(0xffffffffu, same), below = (1u << lane) - 1;
-      const unsigned mm = m + __popc(bm & below), ee = e + __popc(be & below);
-      if (more || (same && ee < rem)) {
-        const unsigned pos = mm + min(ee, rem);
-        index[pos] = from + i + lane;
-        wts[pos] = key_weight(s_key[i + lane]);
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      const int i = i0 + 4 * lane;
+      look(i, u, more, same);
+      const unsigned mine = __popc(more) | __popc(same) << 16;
+      unsigned before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
       }
-      m += __popc(bm), e += __popc(be);
+      const unsigned all = __shfl_sync(0xffffffffu, before, 31);
+      before -= mine;
+      unsigned mm = m + (before & 0xffffu), ee = e + (before >> 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool above = more >> k & 1, equal = same >> k & 1;
+        if (above || (equal && ee < rem)) {
+          const unsigned pos = lo + mm + min(ee, rem);
+          index[pos] = from + i + k;
+          wts[pos] = key_weight(u[k]);
+        }
+        mm += above, ee += equal;
+      }
+      m += all & 0xffffu, e += all >> 16;
     }
     n_more += sum & 0xffffu, n_same += sum >> 16;
   }
@@ -741,7 +787,7 @@ __device__ __forceinline__ uint32_t magnitudes(int kind, uint32_t w, uint32_t so
 // largest magnitude of each block gives its scale, and the codes are written
 // once the whole cluster has read.  A row never moves to a later block, so
 // whatever later rounds take is still there.
-constexpr int EM_NT = 256, EM_BYTES = 32768, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
+constexpr int EM_NT = 512, EM_BYTES = 32768, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
 constexpr int EM_SMEM = EM_BYTES + EM_ROWS * 12;
 __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];  // rows; where they come from; their scales
@@ -766,10 +812,8 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
   for (int round = 0; round < p.keep; round += most * C) {
     const int r0 = round + rank * most, rows = max(0, min(most, p.keep - r0));
     const int vectors = rows << log_row, blocks = (rows + c.page - 1) >> c.log_page;
-#pragma unroll
-    for (int i = 0; i < EM_ROWS / EM_NT; ++i) {
-      const int row = tid + i * EM_NT;
-      if (row >= rows) continue;
+#pragma unroll 1
+    for (int row = tid; row < rows; row += EM_NT) {
       const int slot = index[r0 + row];
       const long long id = static_cast<long long>(table[slot >> c.log_page]) * c.Hk + h;
       s_from[row] = scales[id];
