@@ -221,8 +221,12 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_kernel(const __grid_const
 // has a token and adds up what it reads of tensor memory.  While a tile is
 // weighed, the next one's codes become fp16 operands and its products run; two
 // CTAs per SM fill one another's waits.  Two threads per token take half of the
-// rows each and join a tile later.  What bounds it are the instructions of the
-// weights (a multiply-add, an exponential and an addition each).
+// rows each and join a tile later.  What bounds it is shared memory, which the
+// products' operands, their conversion and the rows' lse (read by every warp)
+// share: 8 x 32 tokens over up to 32768 slots, 128 rows: 93 us.  So rows whose
+// magnitudes are alike have one factor, in a register (with a factor for each row
+// 103).  Measured and dropped: conversion and weights in warps of their own 91, but
+// 1024 rows 217 (203 here); with codes by bulk copies 102.
 constexpr int WR = 128;  // most rows of a chunk
 template <int D>
 struct WeightsLayout {
@@ -244,6 +248,7 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_tile_kernel(const __grid_
   __shared__ unsigned s_scan[WT / 32];
   __shared__ int s_seq;
   __shared__ unsigned s_base;
+  __shared__ int s_most[WT / 32], s_least[WT / 32];
   float *const s_fac = reinterpret_cast<float *>(smem + L::F), *const s_nl = s_fac + WR;
   int *const s_node = reinterpret_cast<int *>(s_nl + WR);
   float *const s_part = reinterpret_cast<float *>(smem + L::PART), *const s_scale = reinterpret_cast<float *>(smem + L::SCALE);
@@ -311,7 +316,10 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_tile_kernel(const __grid_
     for (int r0 = 0; r0 < rows; r0 += WR) {
       const int here = min(WR, rows - r0), columns = (here + 31) & ~31;
       __syncthreads();  // the chunk before has been used
-      // queries: half a row to a thread, as fp16 under a power of two per row
+      // queries: half a row to a thread, as fp16 under a power of two: one for all
+      // rows of the chunk, unless their magnitudes lie too far apart
+      bool alike;
+      float common;
       {
         const int r = tid >> 1, half = tid & 1, row = r0 + r;
         bool live = r < here;
@@ -331,7 +339,17 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_tile_kernel(const __grid_
           for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);  // amax * 2^-e lies in [1, 2)
+        int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);  // amax * 2^-e lies in [1, 2)
+        int most = __reduce_max_sync(0xffffffffu, amax > 0.f ? e : -127), least = __reduce_min_sync(0xffffffffu, amax > 0.f ? e : 127);
+        if (lane == 0) s_most[warp] = most, s_least[warp] = least;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < WT / 32; ++k) most = max(most, s_most[k]), least = min(least, s_least[k]);
+        // The largest in [2^14, 2^15): a row whose largest is 2^14 below it is rounded
+        // as under its own power.
+        alike = most - least <= 14;
+        if (alike) e = max(most - 14, -126);
+        common = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
         if (half == 0) {
@@ -441,21 +459,46 @@ __global__ void __launch_bounds__(WT, 2) cache_weights_tile_kernel(const __grid_
         float2 sum = make_float2(0.f, 0.f), other = sum;
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + buf * WR;
         // 32 rows at a time, in turn with the other thread
+        const float kf = ks * common;
+        const bool easy = alike && !__any_sync(0xffffffffu, !(fabsf(kf) < INFINITY));
         if (__builtin_expect(edge, 0)) {
+#pragma unroll 1
+          for (int q = second * 32; q < columns; q += 64) {
+            uint32_t bits = n < 0 ? ~0u : 0u;  // the rows that see the slot
+            if (n >= 0 && n < s.cnt) {
+              if (!p.mask) {  // those of its own node and later ones
+                const int before = n * p.G - r0 - q;
+                bits = before <= 0 ? ~0u : before < 32 ? ~0u << before : 0u;
+              } else {
+#pragma unroll 8
+                for (int e = 0; e < 32; ++e)
+                  bits |= ((p.mask[(static_cast<long long>(b) * p.N + s_node[q + e]) * p.W + (n >> 5)] >> (n & 31)) & 1) << e;
+              }
+            }
+            __syncwarp();
+            uint32_t x[32];
+            tmem_ld32(at + q, x);
+            tc_wait_ld32(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (bits >> e & 1) sum.x += ex2(fmaf(__uint_as_float(x[e]) * ks, s_fac[q + e], s_nl[q + e]));
+          }
+        } else if (easy) {
 #pragma unroll 1
           for (int q = second * 32; q < columns; q += 64) {
             uint32_t x[32];
             tmem_ld32(at + q, x);
             tc_wait_ld32(x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int node = s_node[q + e];
-              bool seen = n < 0;
-              if (n >= 0 && n < s.cnt)
-                seen = p.mask ? (p.mask[(static_cast<long long>(b) * p.N + node) * p.W + (n >> 5)] >> (n & 31)) & 1 : n <= node;
-              if (seen) sum.x += ex2(fmaf(__uint_as_float(x[e]) * ks, s_fac[q + e], s_nl[q + e]));
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l = *reinterpret_cast<const float4 *>(s_nl + q + e);
+              float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(kf, kf), make_float2(l.x, l.y));
+              sum = add2(sum, make_float2(ex2(y.x), ex2(y.y)));
+              y = fma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(kf, kf), make_float2(l.z, l.w));
+              other = add2(other, make_float2(ex2(y.x), ex2(y.y)));
             }
           }
+          sum = add2(sum, other);
         } else {
 #pragma unroll 1
           for (int q = second * 32; q < columns; q += 64) {
