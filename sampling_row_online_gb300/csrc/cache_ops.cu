@@ -466,13 +466,13 @@ int spec_cache_evict(const spec_cache_t *cache, const int32_t *page_table, int p
   const unsigned Hk = static_cast<unsigned>(p.c.Hk), batch = static_cast<unsigned>(B);
   const long long heads = static_cast<long long>(Hk) * batch, slots = static_cast<long long>(p.c.per) * p.c.page;
   // One CTA as far as its shared memory holds the slots, and more where few heads
-  // leave SMs idle.  (64 heads of up to 32768 slots, the whole call: one CTA 66 us,
-  // four of 512 threads 81; 8 heads of 32768: one 34 us, four 26.)
+  // leave SMs idle.  (64 heads of up to 32768 slots, the whole call: one CTA 54 us,
+  // two 52; 8 heads of 32768: one 34 us, four 25.)
   unsigned n = 1;
   while (n < 8 && (static_cast<long long>(n) * EV_SLICE < slots || (n * 8192ll < slots && 2 * n * heads <= num_sms()))) n *= 2;
   if ((st = launch_dependent(select, dim3(Hk * n, batch), EV_NT, EV_SMEM, stream, &p, "evict_select_kernel launch", n))) return st;
   const int rows = EM_BYTES / p.c.D;
-  n = cluster((keep + rows - 1) / rows, 2 * heads, 8);
+  n = cluster((keep + rows - 1) / rows, 2 * heads, 4);
   return launch_dependent(move, dim3(2 * Hk * n, batch), EM_NT, EM_SMEM, stream, &p, "evict_move_kernel launch", n);
 }
 

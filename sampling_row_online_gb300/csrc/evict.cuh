@@ -597,7 +597,8 @@ __device__ __forceinline__ unsigned full_scan(unsigned x, unsigned *s, unsigned 
 // CTA, which reads them once for each digit and once more: a slot never moves
 // up, so it too overwrites only what it has read.  What bounds it is the chain
 // of counts, barriers and scans, and the fetch of code that runs a few times:
-// all loops are short.
+// all loops are short.  64 heads of up to 32768 slots: 19 us (a slot to a lane, with
+// ballots, and the first digit counted after loading: 27).
 __global__ void __launch_bounds__(EV_NT) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ unsigned s_scan[EV_NT / 32], s_digit, s_rem, s_total;
@@ -829,7 +830,9 @@ __device__ __forceinline__ uint32_t magnitudes(int kind, uint32_t w, uint32_t so
 // blocks to a CTA at a time: their rows are gathered in shared memory, the
 // largest magnitude of each block gives its scale, and the codes are written
 // once the whole cluster has read.  A row never moves to a later block, so
-// whatever later rounds take is still there.
+// whatever later rounds take is still there.  What bounds it are its instructions
+// (60 % of issue) and the barriers of a round.  64 heads to 4096 slots: 33 us, 4 TB/s
+// (256 threads 40, 1024 53; rows in registers 33 to 41).
 constexpr int EM_NT = 512, EM_BYTES = 32768, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
 constexpr int EM_SMEM = EM_BYTES + EM_ROWS * 12;
 __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant__ EvictParams p) {
