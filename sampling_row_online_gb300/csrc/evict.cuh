@@ -831,21 +831,23 @@ __device__ __forceinline__ uint32_t magnitudes(int kind, uint32_t w, uint32_t so
 // largest magnitude of each block gives its scale, and the codes are written
 // once the whole cluster has read.  A row never moves to a later block, so
 // whatever later rounds take is still there.  What bounds it are its instructions
-// (60 % of issue) and the barriers of a round.  64 heads to 4096 slots: 33 us, 4 TB/s
-// (256 threads 40, 1024 53; rows in registers 33 to 41).
+// and the barriers of a round, which four CTAs on an SM hide: 64 heads to 4096
+// slots, the whole call 50 us (three CTAs 57, two 64; 1024 threads 71; rows in
+// registers 52 to 60).
 constexpr int EM_NT = 512, EM_BYTES = 32768, EM_ROWS = EM_BYTES / 64, EM_BLOCKS = EM_ROWS / 16;
 constexpr int EM_SMEM = EM_BYTES + EM_ROWS * 12;
-__global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant__ EvictParams p) {
+constexpr int EM_V = EM_BYTES / 16 / EM_NT;      // vectors of a thread
+constexpr float EM_SAME = 0.f, EM_ANY = -1.f;    // instead of a power of two that codes are multiplied by
+__global__ void __launch_bounds__(EM_NT, 4) evict_move_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];  // rows; where they come from; their scales
   __shared__ unsigned s_amax[EM_BLOCKS];
-  __shared__ long long s_to[EM_BLOCKS];
-  __shared__ float2 s_scale[EM_BLOCKS];  // and its inverse
+  __shared__ unsigned char *s_to[EM_BLOCKS];
   const CacheView &c = p.c;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int b = blockIdx.y, h = blockIdx.x / C >> 1, tensor = blockIdx.x / C & 1, tid = threadIdx.x, lane = tid & 31;
   uint4 *const s_row = reinterpret_cast<uint4 *>(dyn);
   const uint4 **const s_at = reinterpret_cast<const uint4 **>(dyn + EM_BYTES);
-  float *const s_from = reinterpret_cast<float *>(dyn + EM_BYTES + EM_ROWS * 8);
+  float *const s_from = reinterpret_cast<float *>(dyn + EM_BYTES + EM_ROWS * 8), *const s_ratio = reinterpret_cast<float *>(s_at);
   pdl_wait();
   pdl_launch_dependents();
   if (p.ctx[b] <= p.keep || p.out_ctx[b] != p.keep) return;  // nothing to move, or an error
@@ -867,21 +869,25 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
     }
     if (tid < blocks) {
       s_amax[tid] = 0;
-      s_to[tid] = static_cast<long long>(table[(r0 >> c.log_page) + tid]) * c.Hk + h;
+      s_to[tid] = codes + ((static_cast<long long>(table[(r0 >> c.log_page) + tid]) * c.Hk + h) << (c.log_page + log_row + 4));
     }
     __syncthreads();
 #pragma unroll 8
     for (int k = tid; k < vectors; k += EM_NT) cp_async16(s_row + k, s_at[k >> log_row] + (k & last));
     cp_async_wait_all();
     __syncthreads();
-#pragma unroll 2
-    for (int k0 = tid - lane; k0 < vectors; k0 += EM_NT) {  // a warp's vectors belong to one block
-      const int k = k0 + lane;
-      float m = 0.f;
+    // a warp's vectors are neighbours, some sixteens of rows
+    const int k0 = (tid - lane) * EM_V + lane;
+    float most_here = 0.f;
+#pragma unroll
+    for (int v = 0; v < EM_V; ++v) {
+      const int k = k0 + 32 * v, blk = (k - lane) >> log_row >> c.log_page;
+      if (k - lane >= vectors) break;
       if (k < vectors) {
         const uint4 w = s_row[k];
         uint32_t x = magnitudes(c.kind, w.w, magnitudes(c.kind, w.z, magnitudes(c.kind, w.y, magnitudes(c.kind, w.x, 0))));
         x = max(x & 0xffffu, x >> 16) >> 8;
+        float m;
         if (c.kind == KIND_E4M3) {
           float y[4];
           decode4(KIND_E4M3, x, y);
@@ -889,33 +895,39 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
         } else {
           m = static_cast<float>(x);
         }
-        m *= s_from[k >> log_row];
+        most_here = fmaxf(most_here, m * s_from[k >> log_row]);
       }
-      const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-      if (lane == 0) atomicMax(&s_amax[k0 >> log_row >> c.log_page], largest);
+      if (v + 1 == EM_V || k - lane + 32 >= vectors || (k - lane + 32) >> log_row >> c.log_page != blk) {  // the block's last
+        const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(most_here));
+        if (lane == 0) atomicMax(&s_amax[blk], largest);
+        most_here = 0.f;
+      }
     }
     __syncthreads();
-    if (tid < blocks) {
-      const float scale = scale_for(c.kind, s_amax[tid]);
-      s_scale[tid] = make_float2(scale, 1.f / scale);
+    // What a row's codes are multiplied by.  The same scale, the same codes (-128 is
+    // not among them: its block's scale is larger).  A power of two: e4m3 in fp16,
+    // where codes times 2^-14 to 2^15 are exact as far as their rounding to e4m3 can
+    // tell; conversions between 8 and 32 bits would bound the kernel.
+    const auto inverse = [&](int blk) { return 1.f / scale_for(c.kind, s_amax[blk]); };
+#pragma unroll 1
+    for (int row = tid; row < rows; row += EM_NT) {
+      const float from = s_from[row], ratio = from * inverse(row >> c.log_page);
+      const bool two = ((__float_as_uint(from) | __float_as_uint(ratio)) & 0x7fffffu) == 0 && from >= 0x1p-126f && ratio >= 0x1p-14f && ratio <= 0x1p15f;
+      s_ratio[row] = !two ? EM_ANY : ratio == 1.f ? EM_SAME : ratio;
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
-    if (tid < blocks) scales[s_to[tid]] = s_scale[tid].x;
-#pragma unroll 2
-    for (int k = tid; k < vectors; k += EM_NT) {
+    if (tid < blocks) scales[(s_to[tid] - codes) >> (c.log_page + log_row + 4)] = scale_for(c.kind, s_amax[tid]);
+#pragma unroll
+    for (int v = 0; v < EM_V; ++v) {
+      const int k = k0 + 32 * v;
+      if (k >= vectors) break;
       const int row = k >> log_row, blk = row >> c.log_page;
-      const float inv = s_scale[blk].y, from = s_from[row];
+      const float ratio = s_ratio[row];
       const uint4 w = s_row[k];
       uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      // The same scale, the same codes (-128 is not among them: its block's scale
-      // is larger).  A power of two: e4m3 in fp16, where codes times 2^-14 to 2^15
-      // are exact as far as their rounding to e4m3 can tell; conversions between
-      // 8 and 32 bits would bound the kernel.
-      const float ratio = from * inv;
-      const bool two = ((__float_as_uint(from) | __float_as_uint(ratio)) & 0x7fffffu) == 0 && from >= 0x1p-126f && ratio >= 0x1p-14f && ratio <= 0x1p15f;
-      if (two && ratio == 1.f) {
-      } else if (two && c.kind == KIND_E4M3) {
+      if (ratio == EM_SAME) {
+      } else if (ratio > 0.f && c.kind == KIND_E4M3) {
         const uint32_t r2 = f32_to_f16x2(ratio, ratio);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -926,16 +938,16 @@ __global__ void __launch_bounds__(EM_NT) evict_move_kernel(const __grid_constant
               : "r"(r2));
         }
       } else {
+        const float from = s_from[row], inv = inverse(blk);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x[4];
           decode4(c.kind, u[j], x);
-          if (two) u[j] = encode4_finite(c.kind, x[0], x[1], x[2], x[3], ratio);
+          if (ratio > 0.f) u[j] = encode4_finite(c.kind, x[0], x[1], x[2], x[3], ratio);
           else u[j] = encode4(c.kind, x[0] * from * inv, x[1] * from * inv, x[2] * from * inv, x[3] * from * inv);
         }
       }
-      const long long id = s_to[blk];
-      reinterpret_cast<uint4 *>(codes + (id * c.page + (row & (c.page - 1))) * c.D)[k & last] = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4 *>(s_to[blk] + ((row & (c.page - 1)) << (log_row + 4)) + ((k & last) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
     __syncthreads();
   }
