@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
     const float f = p.scale_log2 == 0.f ? __uint_as_float(1u) : p.scale_log2;
     const uint32_t flip = f < 0.f ? 0x80000000u : 0u, hidden = 0xff800000u ^ flip;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-    uint32_t uses = 0;  // tiles of this group
+    uint32_t uses = 0, outs = 0;  // tiles of this group, its segments whose output has been awaited
     // The output of a segment waits for its last products, so it is read only
     // after the next segment's first weights have been made, and written while
     // the products with them run.
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       const bool any = last.any;  // it had tiles
       const int *mark = reinterpret_cast<const int *>(psm + L::MARKS);
       if (any) {
-        wait(&bar.o_done[g], (uses - 1) & 1);
+        wait(&bar.o_done[g], (APART ? uses - 1 : outs) & 1);
+        ++outs;
         tc_after_sync();
       }
       const bool marked = *reinterpret_cast<const volatile int *>(&bar.marked) == last.seg + 1;
@@ -584,8 +585,10 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           l *= a;
           m = nm, base = nb;
           if (uses != uses0) {  // O holds the products of this segment's earlier tiles
-            wait(&bar.o_done[g], (uses - 1) & 1);
-            tc_after_sync();
+            if (APART) {  // elsewhere they are done before the scores
+              wait(&bar.o_done[g], (uses - 1) & 1);
+              tc_after_sync();
+            }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               uint32_t o[32];
@@ -752,6 +755,9 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           }
           mbar_arrive_warp(&bar.turn[g ^ 1]);
         } else {
+          // o_done: once a segment, for its output.  A phase for every tile could be
+          // taken for the one after it, since the softmax does not wait for the tiles
+          // before: those products are done when the scores issued after them are.
           if (has_v) {
             weighted();
             if (j + 1 == tiles || !has_k) tc_commit_warp(&bar.o_done[g]);
@@ -759,7 +765,6 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           if (has_k) scores();
           mbar_arrive_warp(&bar.turn[g ^ 1]);
           scores_end();
-          if (has_v && j + 1 != tiles && has_k) tc_commit_warp(&bar.o_done[g]);
         }
         if (has_v) tc_commit_warp(&bar.v_empty[s]);
         else if (i >= 0) mbar_arrive_warp(&bar.v_empty[s]);
