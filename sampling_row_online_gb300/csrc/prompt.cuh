@@ -6,9 +6,15 @@
 // In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  m is
 // 8 below the maximum of x over a row's first tile, and moves to 8 below the
 // maximum again where the weights of a later tile come to more than 60000
-// together.  So the largest weight of a row lies in [2^8, 60000], fp16 keeps full
+// together.  So the largest weight of a row lies in [2^7.9, 60000], fp16 keeps full
 // precision down to 2^-22 of it, and a tile's maximum is looked for only where m
 // moves: its sum tells.
+// One number of 32 bits holds the offset to a sixteenth up to 2^20, but from 2^27
+// on it is off by more than the 8, and weights would pass 60000 under any of them.
+// So beyond 2^20 it is two numbers, the maximum as rounded and the rest, every
+// tile's maximum is looked for, and exponents are taken from both before they are
+// weighed: the largest weight is 2^8 whatever the scores (1 beyond 2^40, where
+// weights are 1 or 0).
 // What is rounded: weights to the inputs' type before they meet the values (one
 // instruction takes one type; half a step, 2^-8 relative for bf16 and 2^-11 for
 // fp16), and the output, once.  Sums (of the unrounded weights), maxima,
@@ -35,6 +41,7 @@ constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
 constexpr float P_UP = 8.f, P_MOST = 60000.f;
+constexpr float P_FAR = 1 << 20;     // offsets beyond are two numbers
 constexpr int P_SHORT = 16;          // token tiles of segments that are not shared between CTAs
 constexpr int P_EXTRA = 2;           // token tiles that take as long as a segment's begin and end
 constexpr int P_STEPS = 64;          // most row pairs after which their ends fall on token tiles alike again
@@ -58,7 +65,7 @@ struct PromptParams {
 struct PromptLast {  // of the segment whose output is still to be read
   long long row;
   int tok, any, live, whole, seg, first, n, which;  // not whole: first CTA of the segment, number of CTAs, the piece's place
-  float m, l;
+  float m, lo, l;
 };
 
 template <int D>
@@ -68,7 +75,7 @@ struct PromptLayout {
   static constexpr int LAST = MARKS + 3 * D * 4;  // [P_SOFT] PromptLast
   static constexpr int BARS = LAST + P_SOFT * sizeof(PromptLast);  // MARKS: first tokens with NaN, +inf, -inf in each column
   static constexpr int SMEM = BARS + 256;
-  static constexpr int PIECE = PT * D + 2 * PT;  // floats: out, offset, sum
+  static constexpr int PIECE = PT * D + 3 * PT;  // floats: out, offset, sum, the offset's second number
 };
 
 struct PromptBars {
@@ -443,11 +450,11 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       float *const piece = p.pieces + ((static_cast<long long>(blockIdx.x) * 2 + last.which) * 2 + g) * L::PIECE;
       if (last.live) {
         if (last.whole) {
-          if (p.lse) p.lse[last.row] = (last.m + log2f(last.l)) * 0.6931471805599453f;
+          if (p.lse) p.lse[last.row] = (last.m + (last.lo + log2f(last.l))) * 0.6931471805599453f;
         } else {
           if (!any)  // nothing that this row tile sees
             for (int k = 0; k < D / 4; ++k) reinterpret_cast<float4 *>(piece)[k * PT + r] = make_float4(0.f, 0.f, 0.f, 0.f);
-          piece[PT * D + r] = last.m, piece[PT * D + PT + r] = last.l;
+          piece[PT * D + r] = last.m, piece[PT * D + PT + r] = last.l, piece[PT * D + 2 * PT + r] = last.lo;
         }
       }
       if (!last.whole) {
@@ -464,9 +471,15 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           __threadfence();
           if (last.live) {
             const auto part = [&](int e) { return p.pieces + ((static_cast<long long>(c0 + e) * 2 + (e == 0 ? 1 : 0)) * 2 + g) * L::PIECE; };
-            float M = NINF, sum = 0.f;
+            float M = NINF, low = 0.f, sum = 0.f;
 #pragma unroll 4
             for (int e = 0; e < n; ++e) M = fmaxf(M, __ldcg(part(e) + PT * D + r));
+            const bool far = fabsf(M) > P_FAR / 2;  // otherwise a piece whose offset is two numbers counts nothing
+            if (__builtin_expect(far, 0)) {  // the largest second number beside the first one
+              low = NINF;
+              for (int e = 0; e < n; ++e)
+                if (__ldcg(part(e) + PT * D + r) == M) low = fmaxf(low, __ldcg(part(e) + PT * D + 2 * PT + r));
+            }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {  // 32 columns at a time: eight loads a piece, of two pieces, on their way together
               float4 z[8];
@@ -476,7 +489,9 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
 #pragma unroll 2
               for (int e = 0; e < n; ++e) {
                 const float *from = part(e);
-                const float a = ex2(__ldcg(from + PT * D + r) - M), le = __ldcg(from + PT * D + PT + r);  // M: every row sees a token
+                float x0 = __ldcg(from + PT * D + r) - M;  // every row sees a token
+                if (__builtin_expect(far, 0)) x0 += __ldcg(from + PT * D + 2 * PT + r) - low;
+                const float a = ex2(x0), le = __ldcg(from + PT * D + PT + r);
                 float4 x[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(from) + (8 * q + k) * PT + r);
@@ -493,7 +508,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
               for (int k = 0; k < 8; ++k) y[2 * k] = pack2<DT>(z[k].x * over, z[k].y * over), y[2 * k + 1] = pack2<DT>(z[k].z * over, z[k].w * over);
               store64(static_cast<uint16_t *>(p.out) + last.row * D + 32 * q, y, wide);
             }
-            if (p.lse) p.lse[last.row] = (M + log2f(sum)) * 0.6931471805599453f;
+            if (p.lse) p.lse[last.row] = (M + (low + log2f(sum))) * 0.6931471805599453f;
           }
           if (r == 0) p.done[2 * c0 + g] = 0;  // zero again for the next call
         }
@@ -511,7 +526,9 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       const int s0 = over ? 0 : at.j, end = over ? 0 : min(at.n, s0 + count - i), mine = over ? 0 : min(end, prompt_group_tiles(p, at, g));
       const int from = prompt_from(p, at, g), tok = from + tok_in;
       const bool live = tok_in < p.tile && tok < at.len;
-      float m = NINF, base = 0.f, l = 0.f;
+      float m = NINF, lo = 0.f, l = 0.f;  // offset (two numbers beyond P_FAR), sum
+      float less = 0.f;                   // exponents are score * f - less
+      bool look = true;                   // at the first tile, and while some row's offset is beyond P_FAR
       const uint32_t uses0 = uses;
       for (int j = s0; j < mine || there; ++j) {
         const auto weighed = [&]() {
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
               if (!(bits >> e & 1)) s[e] = hidden;
           }
         };
-        const auto largest = [&]() {  // exponent
+        const auto largest = [&]() {  // of the scores, turned around for a negative scale
           float top = NINF;
 #pragma unroll 1
           for (int q = 0; 32 * q < at.len - j * PT && q < 4; ++q) {
@@ -540,20 +557,56 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
             tmem_ld32(tS + 32 * q, s);
             tc_wait_ld32(s);
             hide(s, q);
-            if (flip) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e] ^ 0x80000000u));
-            } else {
+            for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[e] ^ flip)), __uint_as_float(s[e + 1] ^ flip));
+          }
+          return top;
+        };
+        // The offset to P_UP below the tile's largest exponent, if that is above it.
+        const auto rise = [&]() {
+          const float size = fabsf(f), top = largest();
+          float nm = top * size, nl = 0.f, a = 1.f;
+          if (fabsf(nm) > P_FAR && nm != NINF) {  // the product, and what it was rounded by
+            nl = fmaf(top, size, -nm);
+            if (fabsf(nl) < P_FAR / 16) nl -= P_UP;  // beyond, all weights are 1 or 0
+          } else {
+            nm -= P_UP;
+          }
+          const float up = (nm - m) + (nl - lo);
+          if (nm > NINF && !(up <= 0.f)) a = ex2(-up), m = nm, lo = nl;  // NaN for an infinite score
+          l *= a;
+          if (uses != uses0) {  // O holds the products of this segment's earlier tiles
+            if (APART) {  // elsewhere they are done before the scores
+              wait(&bar.o_done[g], (uses - 1) & 1);
+              tc_after_sync();
+            }
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * q, o);
+              tc_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st16(tO + 16 * q, o);
             }
           }
-          return top * fabsf(f);
+          look = __any_sync(0xffffffffu, live && fabsf(m) > P_FAR && m != NINF);
+          less = m == NINF ? 0.f : m;
+          if (__builtin_expect(!look, 1)) return;
+          // the tile's exponents, over f, take its scores' place
+          const float over = 1.f / f;
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            uint32_t s[16];
+            tmem_ld16(tS + 16 * q, s);
+            tc_wait_ld(s);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = __float_as_uint((fmaf(__uint_as_float(s[e]), f, -less) - lo) * over);
+            tmem_st16(tS + 16 * q, s);
+          }
+          tc_wait_st();
+          less = 0.f;
         };
-        if (j == s0) {
-          m = largest() - P_UP;
-          base = m == NINF ? 0.f : m;
-        }
         uint32_t pk[64];
         float sum;
         const auto weights = [&]() {
@@ -567,7 +620,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
             hide(s[q & 1], q);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float2 x = fma2(make_float2(__uint_as_float(s[q & 1][e]), __uint_as_float(s[q & 1][e + 1])), make_float2(f, f), make_float2(-base, -base));
+              float2 x = fma2(make_float2(__uint_as_float(s[q & 1][e]), __uint_as_float(s[q & 1][e + 1])), make_float2(f, f), make_float2(-less, -less));
               x.x = ex2(x.x), x.y = ex2(x.y);
               part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], x);
               pk[16 * q + e / 2] = pack2<DT>(x.x, x.y);
@@ -576,30 +629,26 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           const float2 both = add2(part[0], part[1]);
           sum = both.x + both.y;
         };
+        // The offset is found in a row's first tile, and moves where a sum tells that
+        // some weight is above 2^8.8, or in every tile where offsets are two numbers.
+        // After that no sum is looked at: there is no third pass.
+        float limit = P_MOST;
+        if (look) {
+          const float top = j == s0 ? largest() * fabsf(f) - P_UP : m;
+          look = __any_sync(0xffffffffu, live && fabsf(top) > P_FAR / 2 && top != NINF);
+          if (__builtin_expect(look, 0)) {
+            limit = -1.f;
+          } else {
+            m = top;
+            less = m == NINF ? 0.f : m;
+          }
+        }
 #pragma unroll 1
         for (;;) {
           weights();
-          if (__builtin_expect(!__any_sync(0xffffffffu, live && sum > P_MOST), 1)) break;
-          // some weight is above 2^8.8: the offset moves
-          const float nm = fmaxf(m, largest() - P_UP), nb = nm == NINF ? 0.f : nm, a = ex2(m - nb);
-          l *= a;
-          m = nm, base = nb;
-          if (uses != uses0) {  // O holds the products of this segment's earlier tiles
-            if (APART) {  // elsewhere they are done before the scores
-              wait(&bar.o_done[g], (uses - 1) & 1);
-              tc_after_sync();
-            }
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(tO + 32 * q, o);
-              tc_wait_ld32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tmem_st16(tO + 32 * q, o);
-              tmem_st16(tO + 32 * q + 16, o + 16);
-            }
-          }
+          if (__builtin_expect(!__any_sync(0xffffffffu, live && sum > limit), 1)) break;
+          rise();
+          limit = INFINITY;
         }
         l += sum;
         if (APART && uses) {  // the weights before these have been multiplied
@@ -623,7 +672,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       // ---- the end of the segment
       last.any = mine > s0, last.live = live, last.whole = s0 == 0 && end == at.n;
       last.seg = seg, last.tok = tok, last.which = s0 > 0 ? 0 : 1;
-      last.m = m, last.l = l;
+      last.m = m, last.lo = lo, last.l = l;
       last.row = static_cast<long long>(at.start + tok) * p.Hq + at.h * p.G + head_in;
       if (!last.whole) {
         const unsigned f0 = my0 + i - s0;
