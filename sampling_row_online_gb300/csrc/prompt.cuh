@@ -4,11 +4,11 @@
 //   out_i = sum_{j <= i} softmax(scale q_i . k_j) v_j   in i's own sequence.
 //
 // In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  m is
-// 8 below the maximum of x over a row's first tile, and moves to 8 below the
-// maximum again where the weights of a later tile come to more than 60000
-// together.  So the largest weight of a row lies in [2^7.9, 60000], fp16 keeps full
-// precision down to 2^-22 of it, and a tile's maximum is looked for only where m
-// moves: its sum tells.
+// 8 below the maximum of x over the first tile where that is above -inf, and
+// moves to 8 below the maximum again where the weights of a later tile come to
+// more than 60000 together.  So the largest weight of a row lies in [2^7.9, 60000],
+// fp16 keeps full precision down to 2^-22 of it, and a tile's maximum is looked for
+// only where m moves: its sum tells.
 // One number of 32 bits holds the offset to a sixteenth up to 2^20, but from 2^27
 // on it is off by more than the 8, and weights would pass 60000 under any of them.
 // So beyond 2^20 it is two numbers, the maximum as rounded and the rest, every
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
       const bool live = tok_in < p.tile && tok < at.len;
       float m = NINF, lo = 0.f, l = 0.f;  // offset (two numbers beyond P_FAR), sum
       float less = 0.f;                   // exponents are score * f - less
-      bool look = true;                   // at the first tile, and while some row's offset is beyond P_FAR
+      bool look = true;                   // while some row has no offset yet, or one beyond P_FAR
       const uint32_t uses0 = uses;
       for (int j = s0; j < mine || there; ++j) {
         const auto weighed = [&]() {
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
               tmem_st16(tO + 16 * q, o);
             }
           }
-          look = __any_sync(0xffffffffu, live && fabsf(m) > P_FAR && m != NINF);
+          look = __any_sync(0xffffffffu, live && !(fabsf(m) <= P_FAR));
           less = m == NINF ? 0.f : m;
           if (__builtin_expect(!look, 1)) return;
           // the tile's exponents, over f, take its scores' place
@@ -629,18 +629,20 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           const float2 both = add2(part[0], part[1]);
           sum = both.x + both.y;
         };
-        // The offset is found in a row's first tile, and moves where a sum tells that
-        // some weight is above 2^8.8, or in every tile where offsets are two numbers.
-        // After that no sum is looked at: there is no third pass.
+        // The offset is found in the first tile where a row has a score above -inf, and
+        // moves where a sum tells that some weight is above 2^8.8, or in every tile
+        // where offsets are two numbers.  After that no sum is looked at: there is no
+        // third pass.
         float limit = P_MOST;
         if (look) {
-          const float top = j == s0 ? largest() * fabsf(f) - P_UP : m;
+          const float here = largest() * fabsf(f) - P_UP, top = m == NINF ? here : m;
           look = __any_sync(0xffffffffu, live && fabsf(top) > P_FAR / 2 && top != NINF);
           if (__builtin_expect(look, 0)) {
             limit = -1.f;
           } else {
             m = top;
             less = m == NINF ? 0.f : m;
+            look = __any_sync(0xffffffffu, live && m == NINF);
           }
         }
 #pragma unroll 1

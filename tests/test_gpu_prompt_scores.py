@@ -1,5 +1,5 @@
-"""The attention over whole prompts at scores of any size, against a plain 64-bit restatement.  Every score here is an exact
-32-bit number (two products of short numbers, or one), so that the softmax of scores far apart is well defined."""
+"""The attention over whole prompts at scores of any size, against a plain 64-bit restatement.  Scores are two products of
+short numbers, or one, and nearly all of them exact 32-bit numbers, so that the softmax of scores far apart is well defined."""
 import math
 
 import pytest
@@ -51,7 +51,8 @@ def column(kind, T, u, few):
     return low, few
 
 
-def check(q, k, v, starts, scale):
+def check(q, k, v, starts, scale, first=0):
+    """first: a sequence's first row that is compared."""
     on = torch.tensor(starts, dtype=torch.int32, device="cuda")
     out, lse = binding.spec_prompt_attention(q, k, v, on, scale=scale, want_lse=True)
     assert binding.spec_get_status() == 0
@@ -59,8 +60,8 @@ def check(q, k, v, starts, scale):
     for lo, hi in zip(starts, starts[1:]):
         later = torch.ones((hi - lo, hi - lo), dtype=torch.bool, device="cuda").triu(1)
         for h in range(q.shape[1]):
-            s = q[lo:hi, h].double() @ k[lo:hi, h // G].double().T * scale
-            s = s.masked_fill(later, -math.inf)
+            products = q[lo:hi, h].double() @ k[lo:hi, h // G].double().T
+            s = (products * scale).masked_fill(later, -math.inf)
             z, vv = torch.logsumexp(s, -1), v[lo:hi, h // G].double()
             top = s.amax(-1, keepdim=True)
             w = (s - top).exp()
@@ -71,14 +72,19 @@ def check(q, k, v, starts, scale):
             # 126 apart).  The exponential and the sums: 2^-20.  So a weight is off by less than 2^-14 of it, and so is their
             # sum
             tol = (half + 2.0 ** -13) * spread
+            # a score that 32 bits do not hold is off by a last place at most (one addition, rounded or cut off), so a weight
+            # by a factor of e to that, and so is their sum
+            seen = products[s.isfinite()]
+            place = 0.0 if torch.equal(seen.float().double(), seen) else 2.0 ** -23 * seen.abs().max().item() * abs(scale)
+            tol += math.expm1(2 * place) * spread
             if q.dtype == F16:  # fp16's least step, half of which is 2^-25 where the largest weight is 2^7.9 (1 beyond 2^40)
                 least = 2.0 ** -25 if abs(scale) >= 2.0 ** 24 else 2.0 ** -32
                 tol += least * w.amax(-1, keepdim=True) * ((~later).double() @ vv.abs())
             off = (out[lo:hi, h].double() - want).abs()
-            assert (off <= tol + half * want.abs() * 1.01 + half * tol).all(), (h, off.max().item())
+            assert (off <= tol + half * want.abs() * 1.01 + half * tol)[first:].all(), (h, off.max().item())
             # the logarithm: the factor of the scores, the offset, its product with ln 2, each to half a last place
             off = (lse[lo:hi, h].double() - z).abs()
-            assert (off <= 2.0 ** -13 + 2.0 ** -22 * z.abs()).all(), (h, off.max().item())
+            assert (off <= 2.0 ** -13 + 2.0 ** -22 * z.abs() + place)[first:].all(), (h, off.max().item())
 
 
 KINDS = ["alike", "different", "near", "negative", "rising", "falling", "late", "below"]
@@ -120,3 +126,28 @@ def test_large_elements(D):
         check(q, k.to(dtype), v, [0, T], D ** -0.5)
         k[..., 0] = b
         check(q, k.to(dtype), v, [0, T], D ** -0.5)
+
+
+@pytest.mark.parametrize("rest", ["near zero", "far below", "beyond", "whole"])
+@pytest.mark.parametrize("keys", [(0, 127), (0, 128), (0, 300), (256, 384), (130, 690)], ids=str)
+@pytest.mark.parametrize("Hq,Hk,D,dtype,T", [(4, 2, 128, BF16, 700), (4, 2, 64, F16, 700), (6, 2, 128, F16, 700), (2, 1, 128, BF16, 4500),
+                                             (3, 1, 64, F16, 4500)])
+def test_keys_that_count_nothing(Hq, Hk, D, dtype, T, keys, rest):
+    """Some keys' scores are -inf, by an infinite element: a row's softmax is that over the others, wherever they stand."""
+    q, k, v, u, few = inputs(T, Hq, Hk, D, dtype, keys[1])
+    k[..., 1] = few
+    if rest == "far below":
+        k[..., 0] = -1                       # scores of -256
+    if rest == "beyond":
+        k[..., 0] = -2.0 ** 15               # of -2^23 and some eighths, which 32 bits do not hold
+    if rest == "whole":
+        k[..., 0], k[..., 1] = -2.0 ** 14, few.round()
+    q[..., 2] = 1
+    lo, hi = (x * T // 700 for x in keys)
+    k[lo:hi, :, 2] = -math.inf
+    q, k = q.to(dtype), k.to(dtype)
+    if lo == 0:                              # rows that see no other key have no softmax
+        on = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        out, lse = binding.spec_prompt_attention(q, k, v, on, scale=1.0, want_lse=True)
+        assert out[:hi].isnan().all() and not lse[:hi].isfinite().any()
+    check(q, k, v, [0, T], 1.0, hi if lo == 0 else 0)

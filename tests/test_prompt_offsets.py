@@ -33,13 +33,12 @@ def row(scores, scale, two=True):
         for at in range(0, len(scores), TILE):
             s, limit, passes = scores[at:at + TILE], MOST, 0
             top = (s if f >= 0 else -s).max()
-            if at == 0:
-                m = less = F(top * size - UP)
-                hard = two and abs(m) > FAR / F(2)
-                if hard:
-                    m = NINF
-            if hard:
-                limit = F(-1)
+            if m == NINF or hard:
+                first = F(top * size - UP) if m == NINF else m
+                if two and abs(first) > FAR / F(2) and first != NINF:
+                    limit = F(-1)
+                else:
+                    m, less = first, F(0) if first == NINF else first
             while True:
                 passes += 1
                 w = ex2(fma(s, f, -less))
@@ -48,14 +47,14 @@ def row(scores, scale, two=True):
                 if passes == 4:
                     return None
                 nm, nl, a = F(top * size), F(0), F(1)
-                if two and abs(nm) > FAR:
+                if two and abs(nm) > FAR and nm != NINF:
                     nl = F(fma(top, size, -nm))
                     if abs(nl) < FAR / F(16):
                         nl = F(nl - UP)
                 else:
                     nm = F(nm - UP)
                 up = F(F(nm - m) + F(nl - lo))
-                if not up <= 0:
+                if nm > NINF and not up <= 0:
                     a, m, lo = ex2(-up), nm, nl
                 total, weights = F(total * a), (weights * a).astype(F)
                 hard, less = two and abs(m) > FAR, m
@@ -86,6 +85,9 @@ def cases(size, seed):
     x = (x - F(size)).astype(F)                                                      # far below, then near zero
     x[200:] = g.normal(size=n - 200)
     yield x
+    x = (size * g.uniform(0.5, 1, n)).astype(F)                                      # none in the first tiles, and one among others
+    x[:g.integers(129, 300)] = x[390] = -math.inf
+    yield x
 
 
 SIZES = [2.0 ** e for e in (0, 6, 10, 16, 19, 19.99, 20, 20.01, 21, 24, 26, 27, 28, 29, 30, 33, 36, 39, 40, 41, 50, 51, 52, 60, 100)]
@@ -96,11 +98,11 @@ SIZES = [2.0 ** e for e in (0, 6, 10, 16, 19, 19.99, 20, 20.01, 21, 24, 26, 27, 
 def test_weights_are_held_and_right(size, scale):
     for seed in range(8):
         for scores in cases(size, seed):
-            weights, total, (m, lo), most = row(scores, scale)
+            weights, total, (m, lo), most = row(scores if scale > 0 else -scores, scale)
             assert most <= 2
             assert (2.0 ** 7.9 if size < 2.0 ** 36 else 1) <= weights.max() <= MOST
             f = np.float64(F(scale * 1.4426950408889634))
-            x = scores.astype(np.float64) * f
+            x = scores.astype(np.float64) * (f if f > 0 else -f)
             want = np.exp2(x - x.max())
             want /= want.sum()
             # exponents are off by half a last place of numbers up to 126, three times (2^-16), and of the offset's rest; where
