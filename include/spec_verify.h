@@ -580,8 +580,10 @@ int spec_qk_norm_rope_axes(const spec_heads_t *q, const spec_heads_t *k, const s
  *                 exp(scale * q_i . k_j)
  * Scores, sums and the output are held in fp32; softmax weights are rounded to
  * dtype where they meet the values (half a step, 2^-8 of the weight for bf16 and
- * 2^-11 for fp16), the sum takes the unrounded ones.  Results do not depend on
- * timing.  The call counts pieces of 128 x 128 (rows of a kv head x tokens) of
+ * 2^-11 for fp16), the sum takes the unrounded ones.  Weights are scaled so that
+ * finite values have finite sums, whatever their size (where scores pass 2^40,
+ * bf16 values have to stay below 2^128 over the number of tokens).  Results do
+ * not depend on timing.  The call counts pieces of 128 x 128 (rows of a kv head x tokens) of
  * the upper half of T x T in 31 bits (SPEC_ERR_ARG beyond; about a million
  * tokens with 64 heads).
  * Rows of no sequence (before starts[0], from starts[B] on) are not read; out

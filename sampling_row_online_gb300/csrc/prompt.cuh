@@ -3,18 +3,20 @@
 //
 //   out_i = sum_{j <= i} softmax(scale q_i . k_j) v_j   in i's own sequence.
 //
-// In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  m is
-// 8 below the maximum of x over the first tile where that is above -inf, and
+// In base 2 and with x = s * scale * log2e the weights are w = 2^(x - m).  For fp16
+// m is 8 below the maximum of x over the first tile where that is above -inf, and
 // moves to 8 below the maximum again where the weights of a later tile come to
 // more than 60000 together.  So the largest weight of a row lies in [2^7.9, 60000],
 // fp16 keeps full precision down to 2^-22 of it, and a tile's maximum is looked for
-// only where m moves: its sum tells.
+// only where m moves: its sum tells.  bf16 has the range of 32 bits, and so may its
+// values: all its weights are 2^-33 of that, which keeps the sums of 2^17 tiles of
+// them below 1, and the output's below the largest value.
 // One number of 32 bits holds the offset to a sixteenth up to 2^20, but from 2^27
-// on it is off by more than the 8, and weights would pass 60000 under any of them.
-// So beyond 2^20 it is two numbers, the maximum as rounded and the rest, every
-// tile's maximum is looked for, and exponents are taken from both before they are
-// weighed: the largest weight is 2^8 whatever the scores (1 beyond 2^40, where
-// weights are 1 or 0).
+// on it is off by more than the 8, and weights would pass the limit under any of
+// them.  So beyond 2^20 it is two numbers, the maximum as rounded and the rest,
+// every tile's maximum is looked for, and exponents are taken from both before they
+// are weighed: the largest weight is the same whatever the scores (1 beyond 2^40,
+// where weights are 1 or 0).
 // What is rounded: weights to the inputs' type before they meet the values (one
 // instruction takes one type; half a step, 2^-8 relative for bf16 and 2^-11 for
 // fp16), and the output, once.  Sums (of the unrounded weights), maxima,
@@ -40,7 +42,10 @@ constexpr int P_NT = P_SOFT + 128;   // and a warp each for copies, A's products
 // Registers: 168 a thread at launch, then 256 * 208 + 128 * 88 = 384 * 168.
 constexpr int P_REG = 168, P_REG_SOFT = 208, P_REG_REST = 88;
 static_assert(P_SOFT * P_REG_SOFT + 128 * P_REG_REST <= P_NT * P_REG, "register split");
-constexpr float P_UP = 8.f, P_MOST = 60000.f;
+template <int DT>
+constexpr float P_UP = DT == DT_BF16 ? 8.f - 33.f : 8.f;  // the largest weight where the offset has moved
+template <int DT>
+constexpr float P_MOST = DT == DT_BF16 ? 60000.f / (1ll << 33) : 60000.f;
 constexpr float P_FAR = 1 << 20;     // offsets beyond are two numbers
 constexpr int P_SHORT = 16;          // token tiles of segments that are not shared between CTAs
 constexpr int P_EXTRA = 2;           // token tiles that take as long as a segment's begin and end
@@ -568,9 +573,9 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           float nm = top * size, nl = 0.f, a = 1.f;
           if (fabsf(nm) > P_FAR && nm != NINF) {  // the product, and what it was rounded by
             nl = fmaf(top, size, -nm);
-            if (fabsf(nl) < P_FAR / 16) nl -= P_UP;  // beyond, all weights are 1 or 0
+            if (fabsf(nl) < P_FAR / 16) nl -= P_UP<DT>;  // beyond, all weights are 1 or 0
           } else {
-            nm -= P_UP;
+            nm -= P_UP<DT>;
           }
           const float up = (nm - m) + (nl - lo);
           if (nm > NINF && !(up <= 0.f)) a = ex2(-up), m = nm, lo = nl;  // NaN for an infinite score
@@ -630,12 +635,12 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           sum = both.x + both.y;
         };
         // The offset is found in the first tile where a row has a score above -inf, and
-        // moves where a sum tells that some weight is above 2^8.8, or in every tile
+        // moves where a sum tells that some weight is above 2^8.8 (2^-24.2), or in every tile
         // where offsets are two numbers.  After that no sum is looked at: there is no
         // third pass.
-        float limit = P_MOST;
+        float limit = P_MOST<DT>;
         if (look) {
-          const float here = largest() * fabsf(f) - P_UP, top = m == NINF ? here : m;
+          const float here = largest() * fabsf(f) - P_UP<DT>, top = m == NINF ? here : m;
           look = __any_sync(0xffffffffu, live && fabsf(top) > P_FAR / 2 && top != NINF);
           if (__builtin_expect(look, 0)) {
             limit = -1.f;

@@ -151,3 +151,15 @@ def test_keys_that_count_nothing(Hq, Hk, D, dtype, T, keys, rest):
         out, lse = binding.spec_prompt_attention(q, k, v, on, scale=1.0, want_lse=True)
         assert out[:hi].isnan().all() and not lse[:hi].isfinite().any()
     check(q, k, v, [0, T], 1.0, hi if lo == 0 else 0)
+
+
+@pytest.mark.parametrize("size", [1e-25, 1e30, 1e36, 3.3895313892515355e38])
+@pytest.mark.parametrize("Hq,Hk,D,T", [(4, 2, 64, 700), (4, 2, 128, 700), (2, 1, 128, 4500), (3, 1, 64, 4500)])
+def test_values_of_any_size(Hq, Hk, D, T, size):
+    """An average of bf16 values is finite, however large they are: up to the type's largest."""
+    q, k, v, u, few = inputs(T, Hq, Hk, D, BF16, 4)
+    for scores in (0 * few, few):
+        k[..., 1] = scores
+        sign = torch.where(torch.rand(v.shape, device="cuda") < 0.9, 1.0, -1.0)
+        check(q, k.to(BF16), (sign * size).to(BF16), [0, 100, T], 1.0)
+        check(q, k.to(BF16), torch.full_like(v, size), [0, T], 1.0)

@@ -1,13 +1,15 @@
 """The offsets of the prompt attention's weights in 32-bit arithmetic, restated on the CPU: a row's scores come in tiles of 128,
-weights are powers of two under an offset near the largest score so far, and fp16 has to hold them.  The restatement follows
-csrc/prompt.cuh's arithmetic step by step, with an offset of one number as well, for what that cannot do."""
+weights are powers of two under an offset near the largest score so far, and fp16 has to hold them (for bf16 their sums have
+to stay below 1).  The restatement follows csrc/prompt.cuh's arithmetic step by step, with an offset of one number as well,
+for what that cannot do."""
 import math
 
 import numpy as np
 import pytest
 
 F = np.float32
-UP, MOST, FAR, TILE = F(8), F(60000), F(2 ** 20), 128
+TYPES = {"f16": (F(8), F(60000)), "bf16": (F(-25), F(60000 / 2 ** 33))}  # the largest weight's exponent, a tile's most
+FAR, TILE = F(2 ** 20), 128
 NINF = F(-math.inf)
 
 
@@ -24,8 +26,9 @@ def ex2(x):
     return np.where(y < F(2.0 ** -126), F(0), y)
 
 
-def row(scores, scale, two=True):
+def row(scores, scale, kind, two=True):
     """(weights, sum, offset as (number, rest), most passes over a tile), or None if a tile's passes do not end."""
+    UP, MOST = TYPES[kind]
     f = F(scale * 1.4426950408889634)
     size, over = F(abs(f)), F(1) / f
     m, lo, total, weights, most, hard, less = NINF, F(0), F(0), np.zeros(0, F), 0, False, F(0)
@@ -93,14 +96,16 @@ def cases(size, seed):
 SIZES = [2.0 ** e for e in (0, 6, 10, 16, 19, 19.99, 20, 20.01, 21, 24, 26, 27, 28, 29, 30, 33, 36, 39, 40, 41, 50, 51, 52, 60, 100)]
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("scale", [1.0, -1.0, 0.0883883461356163])
 @pytest.mark.parametrize("size", SIZES)
-def test_weights_are_held_and_right(size, scale):
+def test_weights_are_held_and_right(size, scale, kind):
     for seed in range(8):
         for scores in cases(size, seed):
-            weights, total, (m, lo), most = row(scores if scale > 0 else -scores, scale)
+            weights, total, (m, lo), most = row(scores if scale > 0 else -scores, scale, kind)
             assert most <= 2
-            assert (2.0 ** 7.9 if size < 2.0 ** 36 else 1) <= weights.max() <= MOST
+            up, limit = TYPES[kind]
+            assert (2.0 ** (up - 0.1) if size < 2.0 ** 36 else min(1, 2.0 ** up)) <= weights.max() <= max(limit, 1)
             f = np.float64(F(scale * 1.4426950408889634))
             x = scores.astype(np.float64) * (f if f > 0 else -f)
             want = np.exp2(x - x.max())
@@ -108,8 +113,9 @@ def test_weights_are_held_and_right(size, scale):
             # exponents are off by half a last place of numbers up to 126, three times (2^-16), and of the offset's rest; where
             # that is above 2^9, neighbouring scores lie more than 126 apart, and all exponents that count have the same error
             # (below: half a last place of 2^9, 2^-15), of no more than 2^-9, which the logarithm has.  Weights and sums: 2^-21
+            # exponentials below 2^-126 are 0
             off = np.abs(weights.astype(np.float64) / total - want)
-            assert (off <= want * 2.0 ** -13 + 2.0 ** -126).all(), (off / np.maximum(want, 1e-30)).max()
+            assert (off <= want * 2.0 ** -13 + 2.0 ** (-125 - min(0, up))).all(), (off / np.maximum(want, 1e-30)).max()
             lse = np.float64(m) + (np.float64(lo) + math.log2(total))
             exact = x.max() + math.log2(np.exp2(x - x.max()).sum())
             assert abs(lse - exact) <= 2.0 ** -8 + 2.0 ** -40 * abs(exact)
@@ -117,7 +123,7 @@ def test_weights_are_held_and_right(size, scale):
 
 def test_one_number_does_not_do():
     """An offset of one number stays too low for good, from scores of about 2^24 on."""
-    never = {e: sum(row(np.full(256, F(2.0 ** e * u)), 1.0, two=False) is None for u in np.random.default_rng(e).uniform(0.5, 1, 200))
+    never = {e: sum(row(np.full(256, F(2.0 ** e * u)), 1.0, "f16", two=False) is None for u in np.random.default_rng(e).uniform(0.5, 1, 200))
              for e in (18, 20, 25, 29, 32, 36)}
     assert never[18] == never[20] == 0
     assert never[25] > 10 and never[29] > 50 and never[32] > 50 and never[36] > 50
