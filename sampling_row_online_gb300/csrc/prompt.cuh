@@ -567,18 +567,22 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           }
           return top;
         };
-        // The offset to P_UP below the tile's largest exponent, if that is above it.
+        float sum = 0.f;
+        const auto exponent = [&](float top) { return __fmul_rn(top, fabsf(f)); };
+        // The offset to P_UP below the tile's largest exponent, if that is above it and
+        // the row's own sum or offset asks for it: no row changes another's bits.
         const auto rise = [&]() {
-          const float size = fabsf(f), top = largest();
-          float nm = top * size, nl = 0.f, a = 1.f;
+          const float top = largest();
+          float nm = exponent(top), nl = 0.f, a = 1.f;
           if (fabsf(nm) > P_FAR && nm != NINF) {  // the product, and what it was rounded by
-            nl = fmaf(top, size, -nm);
+            nl = fmaf(top, fabsf(f), -nm);
             if (fabsf(nl) < P_FAR / 16) nl -= P_UP<DT>;  // beyond, all weights are 1 or 0
           } else {
-            nm -= P_UP<DT>;
+            nm = __fsub_rn(nm, P_UP<DT>);
           }
           const float up = (nm - m) + (nl - lo);
-          if (nm > NINF && !(up <= 0.f)) a = ex2(-up), m = nm, lo = nl;  // NaN for an infinite score
+          const bool own = !(sum <= P_MOST<DT>) || fabsf(m) > P_FAR;
+          if (own && nm > NINF && !(up <= 0.f)) a = ex2(-up), m = nm, lo = nl;  // NaN for an infinite score
           l *= a;
           if (uses != uses0) {  // O holds the products of this segment's earlier tiles
             if (APART) {  // elsewhere they are done before the scores
@@ -598,22 +602,23 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           look = __any_sync(0xffffffffu, live && !(fabsf(m) <= P_FAR));
           less = m == NINF ? 0.f : m;
           if (__builtin_expect(!look, 1)) return;
-          // the tile's exponents, over f, take its scores' place
+          // where offsets are two numbers, exponents, over f, take the scores' place
           const float over = 1.f / f;
+          const bool two = fabsf(m) > P_FAR;
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
             uint32_t s[16];
             tmem_ld16(tS + 16 * q, s);
             tc_wait_ld(s);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = __float_as_uint((fmaf(__uint_as_float(s[e]), f, -less) - lo) * over);
+            for (int e = 0; e < 16; ++e)
+              if (two) s[e] = __float_as_uint((fmaf(__uint_as_float(s[e]), f, -less) - lo) * over);
             tmem_st16(tS + 16 * q, s);
           }
           tc_wait_st();
-          less = 0.f;
+          if (two) less = 0.f;
         };
-        uint32_t pk[64];
-        float sum;
+        uint32_t pk[64];  // in the inputs' type
         const auto weights = [&]() {
           float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t s[2][32];
@@ -635,12 +640,12 @@ __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__
           sum = both.x + both.y;
         };
         // The offset is found in the first tile where a row has a score above -inf, and
-        // moves where a sum tells that some weight is above 2^8.8 (2^-24.2), or in every tile
-        // where offsets are two numbers.  After that no sum is looked at: there is no
-        // third pass.
+        // moves where a sum tells that some weight is above 2^8.8 (2^-24.2 for bf16), or
+        // in every tile where offsets are two numbers.  After that no sum is looked at:
+        // there is no third pass.
         float limit = P_MOST<DT>;
         if (look) {
-          const float here = largest() * fabsf(f) - P_UP<DT>, top = m == NINF ? here : m;
+          const float here = __fsub_rn(exponent(largest()), P_UP<DT>), top = m == NINF ? here : m;
           look = __any_sync(0xffffffffu, live && fabsf(top) > P_FAR / 2 && top != NINF);
           if (__builtin_expect(look, 0)) {
             limit = -1.f;

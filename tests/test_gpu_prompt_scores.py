@@ -163,3 +163,21 @@ def test_values_of_any_size(Hq, Hk, D, T, size):
         sign = torch.where(torch.rand(v.shape, device="cuda") < 0.9, 1.0, -1.0)
         check(q, k.to(BF16), (sign * size).to(BF16), [0, 100, T], 1.0)
         check(q, k.to(BF16), torch.full_like(v, size), [0, T], 1.0)
+
+
+@pytest.mark.parametrize("junk", [30.0, 2.0 ** 14, -2.0 ** 14, math.inf, math.nan])
+@pytest.mark.parametrize("Hq,Hk,D,dtype,T", [(4, 1, 128, BF16, 700), (4, 1, 64, F16, 700), (6, 2, 64, BF16, 700), (2, 1, 128, F16, 4500)])
+def test_later_queries_change_nothing(Hq, Hk, D, dtype, T, junk):
+    """A row's result, to the last bit, is its own: whatever the queries, keys and values of later rows are."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn((T, H, D), generator=g, device="cuda").to(dtype) for H in (Hq, Hk, Hk))
+    on = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    clean = binding.spec_prompt_attention(q, k, v, on, want_lse=True)
+    for t in (1, 130, 277, T - 3):
+        for which in ((0,), (0, 1, 2)):
+            x = [y.clone() for y in (q, k, v)]
+            for i in which:
+                x[i][t:] = x[i][t:] * junk if i == 0 and math.isfinite(junk) else junk
+            out, lse = binding.spec_prompt_attention(*x, on, want_lse=True)
+            assert torch.equal(out[:t], clean[0][:t]) and torch.equal(lse[:t], clean[1][:t])
+    assert binding.spec_get_status() == 0
