@@ -593,12 +593,13 @@ def _call(fn, where, device, stream, *args):
 
 
 def _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k):
-    """What spec_qk_norm_rope and spec_qk_norm_rope_axes share: (tensors, weights, head counts, outputs, inv_freq, rot)."""
+    """What spec_qk_norm_rope and spec_qk_norm_rope_axes share: (device, pointers of tensors and weights, sizes and dtype's
+    code, outputs, pointer of inv_freq, rot)."""
     x = q if q is not None else k
     if x is None or x.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, head_dim]")
     B, N, _, D = x.shape
-    _code(x, "q" if q is not None else "k")
+    code, dtype, device = _code(x, "q" if q is not None else "k"), x.dtype, x.device
     heads, srcs, dsts, outs, weights = [0, 0], [None, None], [None, None], [None, None], [None, None]
     for i, (t, out, w, name) in enumerate(((q, out_q, q_weight, "q"), (k, out_k, k_weight, "k"))):
         if t is None:
@@ -606,27 +607,27 @@ def _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k):
         if t.dim() != 4:
             raise ValueError(f"{name} must be [B, N, heads, head_dim]")
         H = t.shape[2]
-        if t.device != x.device:
+        if t.device != device:
             raise ValueError("q and k must be on one device")
-        src = _heads(t, name, x.dtype, B, N, H, D)
+        src = _heads(t, name, dtype, B, N, H, D)
         if out is None:
-            out = torch.empty((B, N, H, D), dtype=t.dtype, device=t.device)
+            out = torch.empty((B, N, H, D), dtype=dtype, device=device)
             dst = HeadsStruct(out.data_ptr(), N * H * D, H * D, D)
         else:
-            if out.device != x.device:
+            if out.device != device:
                 raise ValueError(f"out_{name} must be on the device of {name}")
-            dst = _heads(out, "out_" + name, x.dtype, B, N, H, D)
+            dst = _heads(out, "out_" + name, dtype, B, N, H, D)
         if w is not None:
-            if w.dtype != x.dtype or tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != x.device:
-                raise ValueError(f"{name}_weight must be a contiguous [{D}] tensor of {x.dtype} on {x.device}")
+            if w.dtype != dtype or tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != device:
+                raise ValueError(f"{name}_weight must be a contiguous [{D}] tensor of {dtype} on {device}")
             weights[i] = w.data_ptr()
-        heads[i], srcs[i], dsts[i], outs[i] = H, src, dst, out
+        heads[i], srcs[i], dsts[i], outs[i] = H, ctypes.byref(src), ctypes.byref(dst), out
     freq, rot = None, 0
     if inv_freq is not None:
         if inv_freq.device.type != "cpu" or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-d float64 tensor on the host")
         freq, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    return [None if s is None else ctypes.byref(s) for s in srcs + dsts], weights, heads, outs, freq, rot
+    return device, (*srcs, *dsts, *weights), (B, N, *heads, D, code), tuple(outs), freq, rot
 
 
 def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True, q_weight=None, k_weight=None,
@@ -637,12 +638,11 @@ def spec_qk_norm_rope(q, k, inv_freq=None, *, base=None, offset=None, norm=True,
     contiguous head; weights [D] of the same dtype or None.  inv_freq: float64 host tensor [rot / 2] or None (no
     rotation); the position of token (b, n) is base[b] + offset[b, n] (int32; None: 0 and n).  pairs: neighbouring
     elements are rotated together, not the two halves.  Returns (out_q, out_k); out_q may be q, out_k may be k."""
-    ref, weights, heads, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
-    x = outs[0] if outs[0] is not None else outs[1]
-    B, N, _, D = x.shape
-    _call(library().spec_qk_norm_rope, "spec_qk_norm_rope", x.device, stream, *ref, *weights, _index(base, "base", (B,), x.device),
-          _index(offset, "offset", (B, N), x.device), B, N, heads[0], heads[1], D, _DTYPES[x.dtype], int(norm), eps, freq, rot, int(pairs))
-    return tuple(outs)
+    device, tensors, sizes, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
+    B, N = sizes[:2]
+    _call(library().spec_qk_norm_rope, "spec_qk_norm_rope", device, stream, *tensors, _index(base, "base", (B,), device),
+          _index(offset, "offset", (B, N), device), *sizes, int(norm), eps, freq, rot, int(pairs))
+    return outs
 
 
 def spec_qk_norm_rope_axes(q, k, inv_freq, axis, positions, *, base=None, norm=True, q_weight=None, k_weight=None, eps=1e-6,
@@ -650,18 +650,16 @@ def spec_qk_norm_rope_axes(q, k, inv_freq, axis, positions, *, base=None, norm=T
     """As spec_qk_norm_rope for positions with several axes (time, height and width of an image's or a video's tokens):
     positions [B, N, axes] int32; pair i turns by (base[b] + positions[b, n, axis[i]]) * inv_freq[i].  inv_freq: float64,
     axis: int32, both host tensors [rot / 2].  Returns (out_q, out_k)."""
-    ref, weights, heads, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
-    x = outs[0] if outs[0] is not None else outs[1]
-    B, N, _, D = x.shape
+    device, tensors, sizes, outs, freq, rot = _rope_arguments(q, k, inv_freq, q_weight, k_weight, out_q, out_k)
+    B, N = sizes[:2]
     if positions is None or positions.dim() != 3:
         raise ValueError("positions must be [B, N, axes]")
     if axis is None or axis.device.type != "cpu" or axis.dtype != torch.int32 or not axis.is_contiguous() or axis.shape != (rot // 2,):
         raise ValueError("axis must be a contiguous int32 tensor of the length of inv_freq, on the host")
     axes = positions.shape[2]
-    _call(library().spec_qk_norm_rope_axes, "spec_qk_norm_rope_axes", x.device, stream, *ref, *weights,
-          _index(base, "base", (B,), x.device), _index(positions, "positions", (B, N, axes), x.device), axes, B, N, heads[0], heads[1],
-          D, _DTYPES[x.dtype], int(norm), eps, freq, axis.data_ptr(), rot, int(pairs))
-    return tuple(outs)
+    _call(library().spec_qk_norm_rope_axes, "spec_qk_norm_rope_axes", device, stream, *tensors, _index(base, "base", (B,), device),
+          _index(positions, "positions", (B, N, axes), device), axes, *sizes, int(norm), eps, freq, axis.data_ptr(), rot, int(pairs))
+    return outs
 
 
 def spec_prompt_attention(q, k, v, starts, *, scale=None, out=None, want_lse=False, stream=None):
