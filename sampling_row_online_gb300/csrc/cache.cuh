@@ -699,8 +699,9 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
 // instructions (about 85 a vector), so nothing is divided or looked up per
 // row.  16380 tokens, 40 heads of 128, bf16: half of the head rotated in
 // neighbouring pairs 66.5 us, 5.0 TB/s, bound by issue (the kernel above took
-// 112); the whole head in two halves 72.7 us, 4.6 TB/s, with two units of a row to a
-// thread and 52 bytes of spills each way (fp32: 12).
+// 112); the whole head in two halves 71.9 us, 4.7 TB/s, with two units of a row to a
+// thread and 36 bytes of spills each way (fp32: 104.9 us, 12 bytes).  With three axes
+// 68.6 and 75.5 us (52 bytes; fp32 106.6).
 template <int DT, bool PAIRS, class P = NormRopeParams>
 __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_constant__ P p) {
   extern __shared__ float2 s_trig[];  // [per_cta][rot / 2]
@@ -734,7 +735,8 @@ __global__ void __launch_bounds__(256, 4) norm_rope_rows_kernel(const __grid_con
     unpack8<DT>(load8<DT, true>(p.weight[w], at), g[0]);
     if (two) unpack8<DT>(load8<DT, true>(p.weight[w], at + half), g[1]);
   }
-  // with several axes every angle has a position to load: four at a time
+  // with several axes every angle has a position to load: four at a time; otherwise
+  // one (two halves 71.9 us, 384 tokens 5.6; by the compiler's choice 72.5 and 5.8)
 #pragma unroll(std::is_same_v<P, NormRopeAxesParams> ? 4 : 1)
   for (int i = threadIdx.x; i < here * half; i += 256) {
     const int tk = i / half, tok = first + tk, b = tok / p.N;

@@ -207,9 +207,11 @@ AttnChoice choose_attn(int D, int kind, int dtype, long long rows) {
 }
 
 // Up to 48 rows a warp's own matrix instructions; beyond, the tensor cores with
-// accumulators in tensor memory, 128 rows at a time.  (Sequences of up to 8192
-// tokens, 8 kv heads, e4m3: 64 of them with 16, 24 and 32 rows 91, 104 and 119 us,
-// the tile kernel 151 to 153; 32 with 64 rows 96 and 91.)
+// accumulators in tensor memory, 128 rows at a time.  (64 sequences of up to 8192
+// tokens, 8 kv heads, e4m3, head size 128: 16, 32, 48, 56 and 64 rows 88, 114, 148,
+// 167 and 180 us, the tile kernel 147, 148, 162, 162 and 163; head size 64: 48 and 56
+// rows 102 and 115, the tile kernel 106 and 107.  8 of up to 32768: 72 and 81, the
+// tile kernel 80 and 80.)
 struct WeightsChoice {
   const void *fn;
   int most, smem;

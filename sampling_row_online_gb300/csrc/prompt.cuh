@@ -196,17 +196,20 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 // exponentials), 130 to 250 to the products' warp, 900 for the issue of 16
 // products, 400 until the scores are there; two row tiles share it, a pair of
 // tiles every 2600 clocks, of which the products need 2048.  One prompt of 16384
-// tokens, 32 heads on 8: 1499 to 1519 us, 1448 to 1467 TFLOP/s; 8 of 2048: 257 us,
-// 1070 TFLOP/s.  Head size 64 has half of the products, but the same softmax; its
-// weights have columns of their own, and the next scores are multiplied before
-// them: 1225 to 1239 us, 898 TFLOP/s (weights over the scores as for 128: 1350).  A segment's
-// begin and end cost about two token tiles.
+// tokens, 32 heads on 8: 1535 to 1640 us with the power limit of the card, 1340 to
+// 1433 TFLOP/s; 8 of 2048: 254 to 278 us, 990 to 1083 TFLOP/s.  Head size 64 has half
+// of the products, but the same softmax; its weights have columns of their own, and
+// the next scores are multiplied before them: 1254 to 1282 us, 858 to 877 TFLOP/s.
+// (1217 to 1225 with offsets of one number, which do not do for large scores; 1350
+// beside that with weights over the scores as for 128.)  12 bytes a thread are
+// stored to local memory and 104 loaded.  A segment's begin and end cost about two
+// token tiles.
 // Measured and dropped (the prompt of 16384, us): output threads of their own,
 // 512 threads of 128 registers, 1656; half of the weights stored and multiplied
 // at a time 1806; all of a tile's scores in registers 1932 (spills).  For head size
-// 64: two score buffers of 64 tokens a row tile 1627 (twice the steps), the next
-// scores already under the last quarter of the weights 1279 to 1336 (spills), no
-// turns 1449.
+// 64, beside 1225: two score buffers of 64 tokens a row tile 1627 (twice the steps),
+// the next scores already under the last quarter of the weights 1279 to 1336
+// (spills), no turns 1449.
 template <int D, int DT>
 __global__ void __launch_bounds__(P_NT, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
   using L = PromptLayout<D>;

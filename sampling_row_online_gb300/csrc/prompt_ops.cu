@@ -30,7 +30,7 @@ struct Rows {
   int64_t sn, sh;  // strides in elements
   int H;
 };
-// The copies need 16-byte aligned rows whose strides grow.
+// The copies need 16-byte aligned rows with positive strides, in any order.
 bool fits(const Rows &x, int T) {
   const auto stride = [](int64_t s) { return s > 0 && s % 8 == 0 && s < (1ll << 38); };
   return (reinterpret_cast<uintptr_t>(x.data) & 15u) == 0 && (T == 1 || stride(x.sn)) && (x.H == 1 || (stride(x.sh) && stride(x.sh * x.H)));

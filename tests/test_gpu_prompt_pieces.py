@@ -31,3 +31,16 @@ def test_long_and_short_sequences(Hq, Hk, D, dtype):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
     lo, hi = starts[7], starts[8]
     check(q[lo:hi], k[lo:hi], v[lo:hi], [0, hi - lo])
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 1, 128), (4, 4, 64)])
+def test_as_many_sequences_as_can_be(Hq, Hk, D):
+    """65535 of them, nearly all empty."""
+    lengths = [0] * 65535
+    lengths[3], lengths[40000], lengths[40001], lengths[65534] = 5, 150, 1, 33
+    q, k, v = tensors(sum(lengths) + 2, Hq, Hk, D, BF16, D)
+    on = torch.tensor(starts_of(lengths, first=1), dtype=torch.int32, device="cuda")
+    out, lse = binding.spec_prompt_attention(q, k, v, on, want_lse=True)
+    few = check(q, k, v, [1, 6, 156, 157, 190])
+    assert torch.equal(out, few[0]) and torch.equal(lse, few[1])
+    assert binding.spec_get_status() == 0
