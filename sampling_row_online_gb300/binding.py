@@ -665,8 +665,9 @@ def spec_qk_norm_rope_axes(q, k, inv_freq, axis, positions, *, base=None, norm=T
 def spec_prompt_attention(q, k, v, starts, *, scale=None, out=None, want_lse=False, stream=None):
     """Causal attention among the tokens of whole prompts that stand packed one behind the other: q [T, Hq, head_dim],
     k and v [T, Hk, head_dim] (bfloat16 or float16, any strides with a contiguous head), sequence b in the rows starts[b]
-    ... starts[b + 1] - 1 (int32 [B + 1], ascending).  scale: head_dim ** -0.5 by default.  Returns (out [T, Hq, head_dim],
-    lse [T, Hq] float32 or None); rows of no sequence are 0 and -inf."""
+    ... starts[b + 1] - 1 (int32 [B + 1], ascending).  scale: head_dim ** -0.5 by default.  out: a tensor like a contiguous
+    q, in none of the inputs' memory.  Returns (out [T, Hq, head_dim], lse [T, Hq] float32 or None); rows of no sequence
+    are 0 and -inf."""
     lib = library()
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [T, Hq, head_dim], k and v [T, Hk, head_dim]")
